@@ -364,6 +364,151 @@ typedef struct {
 
 ssd_status ssd_conv1d_silu(const ssd_conv_args *args, void *stream);
 
+/*
+ * The gated delta rule: a matrix-state recurrence with the heads, groups, gates,
+ * packing and states of the SSD above, whose update first removes from the state
+ * what it holds for the new token's key.  Per batch row, head h (group
+ * j = h*G/H) and token t, with the state S kept as [P][N]:
+ *
+ *     u_t = v_t - e^{g_t} S_{t-1} k_t
+ *     S_t = e^{g_t} S_{t-1} + beta_t u_t k_t^T
+ *     y_t = scale * S_t q_t
+ *
+ * so v, k and q stand where x, B and C stand in the SSD.  k and q come as the
+ * layer made them (usually of unit length; nothing here normalises them).  g is
+ * the log of the decay, g <= 0; a value below -64, -inf among them, acts as -64
+ * (e^-64 = 1.6e-28).  beta is any finite number, usually in [0, 1].
+ *
+ * ssd_gdr_fwd computes y and the final states in chunks of 64 tokens; ssd_gdr_bwd
+ * every gradient; ssd_gdr_step one token per batch row.  Supported: batch >= 1,
+ * seqlen >= 0, H % G == 0, P % 16 == 0, N % 16 == 0, N <= 256, P <= 4096.
+ * Results do not change from call to call: every sum has a fixed order.  g, beta
+ * and their gradients need only the alignment of their elements (a token's gates
+ * of a few heads may start anywhere).
+ *
+ * bf16 problems hold the states (S and its gradient) in fp32 throughout and feed
+ * them to the matrix cores as sums of two bf16 numbers, so that final_states and
+ * dinitial_states are as exact as fp32 storage asks for; y and the other
+ * gradients are rounded to bf16 once, from products with operands of 8 bits.
+ *
+ * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0,
+ * nseq), not checked here: see ssd_check_seq_idx; an invalid stream gives wrong
+ * results and leaves tokens of ids out of range unwritten, but nothing outside
+ * the buffers is touched).  Unlike ssd_fwd every segment has an initial state of
+ * its own: initial_states is [nseq,H,P,N], so a stream of prompts can continue
+ * nseq carried states.  A segment without tokens has its initial state as its
+ * final state.
+ */
+typedef struct {
+    int64_t batch, seqlen, nheads, headdim, dstate, ngroups; /* b, T, H, P, N, G */
+    int32_t dtype;                /* ssd_dtype of q, k, v, g, beta, y and their gradients */
+    float scale;                  /* factor of y, e.g. 1 / sqrt(N) */
+    const void *q;                /* [b,T,G,N] dtype */
+    const void *k;                /* [b,T,G,N] dtype */
+    const void *v;                /* [b,T,H,P] dtype */
+    const void *g;                /* [b,T,H]   dtype, log decay */
+    const void *beta;             /* [b,T,H]   dtype */
+    const float *initial_states;  /* [b,H,P,N] (with seq_idx [nseq,H,P,N]) fp32, or NULL for zeros */
+    const int32_t *seq_idx;       /* [T] int32 segment ids, or NULL */
+    int64_t nseq;                 /* number of segment ids when seq_idx != NULL */
+    void *y;                      /* [b,T,H,P] dtype, out (ssd_gdr_fwd; not read or written by ssd_gdr_bwd) */
+    float *final_states;          /* shape of initial_states, fp32, out, or NULL (ssd_gdr_fwd) */
+    void *workspace;              /* device scratch, >= ssd_gdr_fwd_workspace_size (ssd_gdr_fwd) */
+    size_t workspace_bytes;
+} ssd_gdr_args;
+
+/* Workspace bytes of ssd_gdr_fwd and of ssd_gdr_bwd for these shapes (only the
+ * shape and dtype fields, seq_idx != NULL and nseq are read). */
+ssd_status ssd_gdr_fwd_workspace_size(const ssd_gdr_args *args, size_t *bytes);
+ssd_status ssd_gdr_bwd_workspace_size(const ssd_gdr_args *args, size_t *bytes);
+
+/* y and final_states. */
+ssd_status ssd_gdr_fwd(const ssd_gdr_args *args, void *stream);
+
+/* The gradients of L = sum(y * dy) + sum(final_states * dfinal_states) with
+ * respect to every input.  `args` describes the forward's inputs; what the
+ * forward computed is formed again from them.  dq and dk are summed over the
+ * heads of a group in a fixed order.  All outputs are overwritten. */
+typedef struct {
+    const void *dy;               /* [b,T,H,P] dtype */
+    const float *dfinal_states;   /* shape of the final states, fp32, or NULL for zero */
+    void *dq;                     /* [b,T,G,N] dtype, out */
+    void *dk;                     /* [b,T,G,N] dtype, out */
+    void *dv;                     /* [b,T,H,P] dtype, out */
+    void *dg;                     /* [b,T,H]   dtype, out */
+    void *dbeta;                  /* [b,T,H]   dtype, out */
+    float *dinitial_states;       /* shape of the initial states, fp32, out, or NULL */
+    void *workspace;              /* device scratch, >= ssd_gdr_bwd_workspace_size */
+    size_t workspace_bytes;
+} ssd_gdr_bwd_args;
+
+ssd_status ssd_gdr_bwd(const ssd_gdr_args *args, const ssd_gdr_bwd_args *grads, void *stream);
+
+/* One token of every batch row: q, k [b,G,N], v, y [b,H,P], g, beta [b,H] dtype,
+ * the state [b,H,P,N] fp32 read and overwritten.  Steps over tokens 0..T-1 from
+ * the initial states give ssd_gdr_fwd's y and final states. */
+typedef struct {
+    int64_t batch, nheads, headdim, dstate, ngroups; /* b, H, P, N, G */
+    int32_t dtype;
+    float scale;
+    const void *q, *k, *v, *g, *beta;
+    float *state;
+    void *y;
+} ssd_gdr_step_args;
+
+ssd_status ssd_gdr_step(const ssd_gdr_step_args *args, void *stream);
+
+/*
+ * Layer norm, the step in front of the block: over the last axis of x
+ * [rows, dim],
+ *
+ *     y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps)
+ *
+ * with mean and var (the mean square around the mean) in fp32 from two passes
+ * over the row held on chip.  weight and bias are fp32, like the block's other
+ * parameters, and may each be NULL (1 and 0).  mean and rstd [rows] fp32 are
+ * outputs that the backward reads; NULL if no backward follows.
+ * Supported: rows >= 0, 1 <= dim <= 65536, rows * dim <= 2^40, any dim (odd ones
+ * take narrower accesses).  mean and rstd need 4-byte alignment.  y may be x itself, not overlap it otherwise.
+ */
+typedef struct {
+    int64_t rows, dim;
+    int32_t dtype;                /* ssd_dtype of x and y */
+    float eps;
+    const void *x;                /* [rows,dim] dtype */
+    const float *weight;          /* [dim] fp32, or NULL */
+    const float *bias;            /* [dim] fp32, or NULL */
+    void *y;                      /* [rows,dim] dtype, out */
+    float *mean, *rstd;           /* [rows] fp32, out, or NULL */
+} ssd_norm_args;
+
+ssd_status ssd_layer_norm_fwd(const ssd_norm_args *args, void *stream);
+
+/* With xhat = (x - mean) rstd and w = dy * weight (dy without weight):
+ *
+ *     dx = rstd (w - avg(w) - xhat avg(w xhat)),
+ *     dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy
+ *
+ * The two sums over rows are formed in fp32 in a fixed order through the
+ * workspace.  dx may be dy itself. */
+typedef struct {
+    int64_t rows, dim;
+    int32_t dtype;                /* ssd_dtype of x, dy and dx */
+    int32_t reserved;
+    const void *x;                /* [rows,dim] dtype */
+    const void *dy;               /* [rows,dim] dtype */
+    const float *mean, *rstd;     /* [rows] fp32, as the forward left them */
+    const float *weight;          /* [dim] fp32, or NULL */
+    void *dx;                     /* [rows,dim] dtype, out */
+    float *dweight;               /* [dim] fp32, out, or NULL */
+    float *dbias;                 /* [dim] fp32, out, or NULL */
+    void *workspace;              /* >= ssd_layer_norm_bwd_workspace_size; unused without dweight and dbias */
+    size_t workspace_bytes;
+} ssd_norm_bwd_args;
+
+ssd_status ssd_layer_norm_bwd_workspace_size(const ssd_norm_bwd_args *args, size_t *bytes);
+ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,410 @@
+// gdr_api.hip -- host side of the gated delta rule (ssd_gdr_* in include/ssd.h):
+// argument validation, workspace layout and launches.  Validation is host-only and
+// runs before any HIP call; nothing here allocates, frees or synchronises.
+#include "ssd.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "gdr_kernels.hpp"
+
+using namespace ssd;
+using namespace ssd::gdr;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;
+
+struct Shape {
+    int64_t b, T, H, P, N, G, nseq;
+    int64_t nc;       // chunks per batch row
+    int64_t nct;      // chunks in all (an upper bound for packed streams)
+    int64_t chains;   // batch rows or segments
+    int64_t NT, Pp, np;
+    int dtype;
+    size_t esz;
+    bool packed;
+};
+
+struct Range {
+    const void *p;
+    size_t n;
+};
+bool overlaps(Range a, Range b)
+{
+    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a0 < b0 + b.n && b0 < a0 + a.n;
+}
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// g, beta and their gradients are read and written one element at a time
+bool aligned_to(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == SSD_DTYPE_BF16 ? 1u : 3u)) == 0; }
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+ssd_status launched() { return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+
+// P, N, heads and groups, common to the chunked calls and the step.
+ssd_status check_dims(int64_t b, int64_t H, int64_t P, int64_t N, int64_t G, int dtype)
+{
+    if (dtype != SSD_DTYPE_F32 && dtype != SSD_DTYPE_BF16) return SSD_ERR_BAD_DTYPE;
+    if (b < 1 || H < 1 || P < 16 || N < 16 || G < 1) return SSD_ERR_BAD_SHAPE;
+    if (P % 16 != 0 || N % 16 != 0 || N > kMaxStateDim || P > 4096) return SSD_ERR_BAD_SHAPE;
+    if (b > kMaxDim || H > kMaxDim || b * H > INT32_MAX) return SSD_ERR_BAD_SHAPE;
+    if (H % G != 0) return SSD_ERR_GROUPS;
+    return SSD_OK;
+}
+
+ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
+{
+    if (!a) return SSD_ERR_NULL_POINTER;
+    const ssd_status r = check_dims(a->batch, a->nheads, a->headdim, a->dstate, a->ngroups, a->dtype);
+    if (r != SSD_OK) return r;
+    if (a->seqlen < 0 || a->seqlen > kMaxDim) return SSD_ERR_BAD_SHAPE;
+    if (a->seq_idx && (a->batch != 1 || a->nseq < 1 || a->nseq > kMaxDim)) return SSD_ERR_SEQ_IDX;
+    s->b = a->batch;
+    s->T = a->seqlen;
+    s->H = a->nheads;
+    s->P = a->headdim;
+    s->N = a->dstate;
+    s->G = a->ngroups;
+    s->dtype = a->dtype;
+    s->esz = a->dtype == SSD_DTYPE_BF16 ? 2 : 4;
+    s->packed = a->seq_idx != nullptr;
+    s->nseq = s->packed ? a->nseq : 0;
+    s->nc = (s->T + kC - 1) / kC;
+    // every segment starts a chunk of its own: a bound that the host knows
+    s->nct = s->packed ? s->T / kC + (s->nseq < s->T ? s->nseq : s->T) : s->b * s->nc;
+    s->chains = s->packed ? s->nseq : s->b;
+    s->NT = s->N <= 64 ? 64 : s->N <= 128 ? 128 : 256;
+    s->Pp = (s->P + 31) / 32 * 32;
+    s->np = (s->Pp + kC - 1) / kC;
+    // grids and int32 indices
+    if (s->chains > INT32_MAX / s->H / s->np / 2 || s->nct > INT32_MAX / s->H / 2 || s->nct * kC > INT32_MAX)
+        return SSD_ERR_BAD_SHAPE;
+    // byte counts stay far below 2^63
+    if (s->nct * s->H > ((int64_t)1 << 40) / (s->P * s->NT) * 64 || s->chains * s->H > ((int64_t)1 << 44) / (s->P * s->N))
+        return SSD_ERR_BAD_SHAPE;
+    return SSD_OK;
+}
+
+struct Sizes {
+    size_t kq, v, gate, states, seq;
+};
+Sizes sizes_of(const Shape &s)
+{
+    Sizes z;
+    z.kq = (size_t)(s.b * s.T * s.G * s.N) * s.esz;
+    z.v = (size_t)(s.b * s.T * s.H * s.P) * s.esz;
+    z.gate = (size_t)(s.b * s.T * s.H) * s.esz;
+    z.states = (size_t)(s.chains * s.H * s.P * s.N) * 4;
+    z.seq = s.packed ? (size_t)s.T * 4 : 0;
+    return z;
+}
+
+// The heads of a group go to `hsplit` workgroups of the gradient kernel when the
+// chunks and groups alone would leave the GPU short of them (about 1024 wanted);
+// every split adds fp32 sums of dq and dk to write and read back.
+int64_t head_split(const Shape &s)
+{
+    const int64_t tiles = s.nct * s.G, hpg = s.H / s.G;
+    int64_t k = tiles ? (1024 + tiles - 1) / tiles : 1;
+    return k > hpg ? hpg : k < 1 ? 1 : k;
+}
+
+struct Workspace {
+    size_t cmap, chain, range, kq, vec, tri, sst, ust, dst, hst, part, total;
+};
+Workspace layout(const Shape &s, bool bwd)
+{
+    Workspace w{};
+    size_t o = 0;
+    auto take = [&](size_t n) { const size_t at = o; o = align256(o + n); return at; };
+    if (s.packed) {
+        w.cmap = take((size_t)s.nct * 8);
+        w.chain = take((size_t)s.nseq * 8);
+        w.range = take((size_t)s.nseq * 8);
+    }
+    const size_t u = (size_t)(s.nct * s.H);
+    const int tri = s.dtype == SSD_DTYPE_BF16 ? tri_elems<bf16>(bwd) : tri_elems<float>(bwd);
+    w.kq = take((size_t)(s.nct * s.G) * (bwd ? 4 : 3) * kC * (size_t)s.NT * s.esz);
+    w.vec = take(u * kVec * 4);
+    w.tri = take(u * (size_t)tri * s.esz);
+    if (bwd) {
+        w.sst = take(u * (size_t)(s.NT * s.Pp) * s.esz);
+        w.ust = take(u * kC * (size_t)s.Pp * s.esz);
+        w.dst = take(u * (size_t)(s.NT * s.Pp) * s.esz);
+        w.hst = take(u * kC * (size_t)s.Pp * s.esz);
+        const int64_t hs = head_split(s);
+        w.part = take(hs > 1 ? (size_t)(s.nct * s.G * hs) * 2 * kC * (size_t)s.NT * 4 : 0);
+    }
+    w.total = o;
+    return w;
+}
+
+template <typename F> ssd_status with_nt(int64_t NT, F &&f)
+{
+    if (NT == 64) return f(std::integral_constant<int, 64>{});
+    if (NT == 128) return f(std::integral_constant<int, 128>{});
+    return f(std::integral_constant<int, 256>{});
+}
+
+// What both directions form first: the chunk map, the operand copies, the triangles.
+template <typename E, bool BWD>
+ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Workspace &w, Chunks *m, hipStream_t st)
+{
+    *m = Chunks{nullptr, nullptr, (int)s.T, (int)s.nc};
+    if (s.packed) {
+        int2 *cmap = reinterpret_cast<int2 *>(ws + w.cmap), *chain = reinterpret_cast<int2 *>(ws + w.chain);
+        hipLaunchKernelGGL(k_gdr_map, dim3(1), dim3(kMapThreads), 0, st, a->seq_idx,
+                           reinterpret_cast<int2 *>(ws + w.range), chain, cmap, (int)s.T, (int)s.nseq, (int)s.nct);
+        m->cmap = cmap;
+        m->chain = chain;
+        if (launched() != SSD_OK) return SSD_ERR_HIP;
+    }
+    return with_nt(s.NT, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        E *kq = reinterpret_cast<E *>(ws + w.kq);
+        hipLaunchKernelGGL((k_gdr_frags<E, NT>), dim3((unsigned)(s.nct * s.G), 2), dim3(kThreads), 0, st,
+                           (const E *)a->k, (const E *)a->q, kq, *m, (int)s.G, (int)s.N, BWD ? 4 : 3);
+        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)(s.nct * s.H)), dim3(kThreads), 0, st,
+                           (const E *)kq, (const E *)a->g, (const E *)a->beta, reinterpret_cast<float *>(ws + w.vec),
+                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, a->scale);
+        return launched();
+    });
+}
+
+template <typename E> ChainArgs chain_args(const Shape &s, const ssd_gdr_args *a, char *ws, const Workspace &w, const Chunks &m)
+{
+    ChainArgs c{};
+    c.kq = ws + w.kq;
+    c.tri = ws + w.tri;
+    c.vec = reinterpret_cast<const float *>(ws + w.vec);
+    c.v = a->v;
+    c.s0 = a->initial_states;
+    c.m = m;
+    c.H = (int)s.H;
+    c.G = (int)s.G;
+    c.P = (int)s.P;
+    c.N = (int)s.N;
+    c.Pp = (int)s.Pp;
+    c.np = (int)s.np;
+    c.units = (int)(s.chains * s.H * s.np);
+    c.scale = a->scale;
+    return c;
+}
+
+template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_gdr_args *a, hipStream_t st)
+{
+    const Workspace w = layout(s, false);
+    char *ws = static_cast<char *>(a->workspace);
+    Chunks m;
+    ssd_status r = prepare<E, false>(s, a, ws, w, &m, st);
+    if (r != SSD_OK) return r;
+    ChainArgs c = chain_args<E>(s, a, ws, w, m);
+    c.y = a->y;
+    c.s1 = a->final_states;
+    return with_nt(s.NT, [&](auto nt) {
+        hipLaunchKernelGGL((k_gdr_chain<E, decltype(nt)::value / 16>), dim3((unsigned)c.units), dim3(kThreads), 0, st, c);
+        return launched();
+    });
+}
+
+template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a, const ssd_gdr_bwd_args *g, hipStream_t st)
+{
+    const Workspace w = layout(s, true);
+    char *ws = static_cast<char *>(g->workspace);
+    Chunks m;
+    ssd_status r = prepare<E, true>(s, a, ws, w, &m, st);
+    if (r != SSD_OK) return r;
+    ChainArgs c = chain_args<E>(s, a, ws, w, m);
+    c.dy = g->dy;
+    c.dv = g->dv;
+    c.d1 = g->dfinal_states;
+    c.d0 = g->dinitial_states;
+    c.sst = ws + w.sst;
+    c.ust = ws + w.ust;
+    c.dst = ws + w.dst;
+    c.hst = ws + w.hst;
+    const int64_t hs = head_split(s);
+    GradArgs ga{};
+    ga.kq = c.kq;
+    ga.k = a->k;
+    ga.q = a->q;
+    ga.dy = g->dy;
+    ga.sst = c.sst;
+    ga.ust = c.ust;
+    ga.dst = c.dst;
+    ga.hst = c.hst;
+    ga.vec = c.vec;
+    ga.dq = g->dq;
+    ga.dk = g->dk;
+    ga.dg = g->dg;
+    ga.dbeta = g->dbeta;
+    ga.part = reinterpret_cast<float *>(ws + w.part);
+    ga.m = m;
+    ga.H = c.H;
+    ga.G = c.G;
+    ga.P = c.P;
+    ga.N = c.N;
+    ga.Pp = c.Pp;
+    ga.hsplit = (int)hs;
+    ga.scale = a->scale;
+    return with_nt(s.NT, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((k_gdr_chains<E, NT / 16>), dim3(2u * (unsigned)c.units), dim3(kThreads), 0, st, c);
+        hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kThreads), 0, st, ga);
+        if (hs > 1)
+            hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G)), dim3(kThreads), 0, st,
+                               (const float *)ga.part, (E *)g->dq, (E *)g->dk, m, (int)s.G, (int)s.N, (int)hs);
+        return launched();
+    });
+}
+
+void copy_states(float *dst, const float *src, const Shape &s, hipStream_t st)
+{
+    const int64_t n = s.chains * s.H * s.P * s.N;
+    if (dst)
+        hipLaunchKernelGGL(k_gdr_copy, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, dst, src, n);
+}
+
+// Inputs of the chunked calls: present, aligned.
+ssd_status check_inputs(const ssd_gdr_args *a, const Shape &s)
+{
+    if (s.T > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta)) return SSD_ERR_NULL_POINTER;
+    const void *ptrs[] = {a->q, a->k, a->v, a->initial_states, a->seq_idx};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return SSD_ERR_MISALIGNED;
+    if (!aligned_to(a->g, s.dtype) || !aligned_to(a->beta, s.dtype)) return SSD_ERR_MISALIGNED;
+    return SSD_OK;
+}
+
+template <size_t NO, size_t NI> bool clash(const Range (&outs)[NO], const Range (&ins)[NI])
+{
+    for (size_t i = 0; i < NO; ++i) {
+        for (const Range &in : ins)
+            if (overlaps(outs[i], in)) return true;
+        for (size_t j = i + 1; j < NO; ++j)
+            if (overlaps(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+template <typename E> ssd_status run_step(const ssd_gdr_step_args *a, hipStream_t st)
+{
+    const int N = (int)a->dstate, P = (int)a->headdim;
+    auto launch = [&](auto nl) {
+        constexpr int NL = decltype(nl)::value;
+        constexpr int rows = kThreads / NL * kStepRows;
+        const dim3 grid((unsigned)(a->batch * a->nheads), (unsigned)((P + rows - 1) / rows));
+        hipLaunchKernelGGL((k_gdr_step<E, NL>), grid, dim3(kThreads), 0, st, (const E *)a->q, (const E *)a->k,
+                           (const E *)a->v, (const E *)a->g, (const E *)a->beta, a->state, (E *)a->y, (int)a->nheads,
+                           (int)a->ngroups, P, N, a->scale);
+        return launched();
+    };
+    const int need = N / 4;   // lanes per state row
+    if (need <= 4) return launch(std::integral_constant<int, 4>{});
+    if (need <= 8) return launch(std::integral_constant<int, 8>{});
+    if (need <= 16) return launch(std::integral_constant<int, 16>{});
+    if (need <= 32) return launch(std::integral_constant<int, 32>{});
+    return launch(std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_gdr_fwd_workspace_size(const ssd_gdr_args *args, size_t *bytes)
+{
+    Shape s;
+    const ssd_status r = parse_shape(args, &s);
+    if (r != SSD_OK) return r;
+    if (!bytes) return SSD_ERR_NULL_POINTER;
+    *bytes = layout(s, false).total;
+    return SSD_OK;
+}
+
+ssd_status ssd_gdr_bwd_workspace_size(const ssd_gdr_args *args, size_t *bytes)
+{
+    Shape s;
+    const ssd_status r = parse_shape(args, &s);
+    if (r != SSD_OK) return r;
+    if (!bytes) return SSD_ERR_NULL_POINTER;
+    *bytes = layout(s, true).total;
+    return SSD_OK;
+}
+
+ssd_status ssd_gdr_fwd(const ssd_gdr_args *a, void *stream)
+{
+    Shape s;
+    ssd_status r = parse_shape(a, &s);
+    if (r != SSD_OK) return r;
+    if ((r = check_inputs(a, s)) != SSD_OK) return r;
+    const bool empty = s.T == 0;
+    if (!empty && (!a->y || !a->workspace)) return SSD_ERR_NULL_POINTER;
+    if (!aligned16(a->y) || !aligned16(a->final_states) || !aligned16(a->workspace)) return SSD_ERR_MISALIGNED;
+    const size_t wtotal = layout(s, false).total;
+    if (!empty && a->workspace_bytes < wtotal) return SSD_ERR_WORKSPACE_TOO_SMALL;
+    const Sizes z = sizes_of(s);
+    const Range ins[] = {{a->q, z.kq}, {a->k, z.kq}, {a->v, z.v}, {a->g, z.gate}, {a->beta, z.gate},
+                         {a->initial_states, z.states}, {a->seq_idx, z.seq}};
+    const Range outs[] = {{a->y, z.v}, {a->final_states, z.states}, {empty ? nullptr : a->workspace, wtotal}};
+    if (clash(outs, ins)) return SSD_ERR_ALIASING;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (empty) {
+        copy_states(a->final_states, a->initial_states, s, st);
+        return launched();
+    }
+    return s.dtype == SSD_DTYPE_BF16 ? fwd_typed<bf16>(s, a, st) : fwd_typed<float>(s, a, st);
+}
+
+ssd_status ssd_gdr_bwd(const ssd_gdr_args *a, const ssd_gdr_bwd_args *g, void *stream)
+{
+    Shape s;
+    ssd_status r = parse_shape(a, &s);
+    if (r != SSD_OK) return r;
+    if (!g) return SSD_ERR_NULL_POINTER;
+    if ((r = check_inputs(a, s)) != SSD_OK) return r;
+    const bool empty = s.T == 0;
+    if (!empty && (!g->dy || !g->dq || !g->dk || !g->dv || !g->dg || !g->dbeta || !g->workspace))
+        return SSD_ERR_NULL_POINTER;
+    const void *ptrs[] = {g->dy, g->dfinal_states, g->dq, g->dk, g->dv, g->dinitial_states, g->workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return SSD_ERR_MISALIGNED;
+    if (!aligned_to(g->dg, s.dtype) || !aligned_to(g->dbeta, s.dtype)) return SSD_ERR_MISALIGNED;
+    const size_t wtotal = layout(s, true).total;
+    if (!empty && g->workspace_bytes < wtotal) return SSD_ERR_WORKSPACE_TOO_SMALL;
+    const Sizes z = sizes_of(s);
+    const Range ins[] = {{a->q, z.kq}, {a->k, z.kq}, {a->v, z.v}, {a->g, z.gate}, {a->beta, z.gate},
+                         {a->initial_states, z.states}, {a->seq_idx, z.seq}, {g->dy, z.v}, {g->dfinal_states, z.states}};
+    const Range outs[] = {{g->dq, z.kq}, {g->dk, z.kq}, {g->dv, z.v}, {g->dg, z.gate}, {g->dbeta, z.gate},
+                          {g->dinitial_states, z.states}, {empty ? nullptr : g->workspace, wtotal}};
+    if (clash(outs, ins)) return SSD_ERR_ALIASING;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (empty) {
+        copy_states(g->dinitial_states, g->dfinal_states, s, st);
+        return launched();
+    }
+    return s.dtype == SSD_DTYPE_BF16 ? bwd_typed<bf16>(s, a, g, st) : bwd_typed<float>(s, a, g, st);
+}
+
+ssd_status ssd_gdr_step(const ssd_gdr_step_args *a, void *stream)
+{
+    if (!a) return SSD_ERR_NULL_POINTER;
+    const ssd_status r = check_dims(a->batch, a->nheads, a->headdim, a->dstate, a->ngroups, a->dtype);
+    if (r != SSD_OK) return r;
+    if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->state || !a->y) return SSD_ERR_NULL_POINTER;
+    const void *ptrs[] = {a->q, a->k, a->v, a->state, a->y};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return SSD_ERR_MISALIGNED;
+    if (!aligned_to(a->g, a->dtype) || !aligned_to(a->beta, a->dtype)) return SSD_ERR_MISALIGNED;
+    const size_t esz = a->dtype == SSD_DTYPE_BF16 ? 2 : 4;
+    const size_t bh = (size_t)(a->batch * a->nheads), kq = (size_t)(a->batch * a->ngroups * a->dstate) * esz;
+    const Range ins[] = {{a->q, kq}, {a->k, kq}, {a->v, bh * a->headdim * esz}, {a->g, bh * esz}, {a->beta, bh * esz}};
+    const Range outs[] = {{a->state, bh * a->headdim * a->dstate * 4}, {a->y, bh * a->headdim * esz}};
+    if (clash(outs, ins)) return SSD_ERR_ALIASING;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return a->dtype == SSD_DTYPE_BF16 ? run_step<bf16>(a, st) : run_step<float>(a, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,1062 @@
+// gdr_kernels.hpp -- the gated delta rule for gfx950: chunked forward, backward
+// and the one-token step.
+//
+// Per head (keys and queries are shared by the heads of a group), state S [N][P]:
+//
+//   u_t = v_t - e^{g_t} S_{t-1}^T k_t,   S_t = e^{g_t} S_{t-1} + beta_t k_t u_t^T,
+//   y_t = scale S_t^T q_t
+//
+// Over a chunk of 64 tokens with entering state S, cs = the inclusive prefix sum
+// of g, Gam[t][s] = e^{cs_t - cs_s} (s <= t) and A = the strictly lower part of
+// Gam o K K^T, the 64 u's solve the unit lower triangular system
+//
+//   (I + A Db) U = R,   R = V - e^{cs} o (K S),   Db = diag(beta)
+//
+// and with N = (I + A Db)^-1 A (strictly lower, defined for beta = 0 too)
+//
+//   U = R - N (beta o R)
+//   Y = scale (e^{cs} o (Q S) + (Gam o Q K^T) (beta o U))
+//   S' = e^{cs_last} S + K^T (e^{cs_last - cs} o beta o U).
+//
+// The gradient runs the same chain backwards: with D = dL/dS' and
+// W = scale (Gam o Q K^T)^T dY + e^{cs_last - cs} o (K D),
+//
+//   H = W - N^T (beta o W)       (= dL/d(beta u)),   dV = beta o H
+//   dL/dS = e^{cs_last} D + scale Q^T (e^{cs} o dY) - K^T (e^{cs} o beta o H),
+//
+// which needs no state, so both chains run at the same time.  Everything that no
+// state enters (N, Gam o Q K^T, the operand copies) is formed first, for all
+// chunks in parallel; the gradients of q, k, g and beta are formed last, again
+// for all chunks in parallel, from the stored S, U, D and H of every chunk.
+//
+// Register layout of a chain.  A wave owns 16 value columns of one head and all
+// of their state: N / 16 accumulators S[nb], lane l holding rows n = 16 nb +
+// 4 (l/16) + r of column p = l % 16.  A matrix-core product contracts over 32
+// slots, 8 per lane group l/16, and does not care which row a slot stands for as
+// long as both operands agree: with slot j of lane group g standing for row
+// 4g + j (j < 4) or 16 + 4g + j - 4 (j >= 4) of a 32-row block, two accumulators
+// ARE the second operand of the next product.  So the chain K S -> U -> S' runs
+// from registers to registers, without a shuffle or a barrier between products;
+// only the first operands (K, K^T, Q, N, Gam o Q K^T) come from memory, laid out
+// once per chunk in that slot order ("slot order" below).
+//
+// Numerics.  Inputs are exact in their type.  For bf16 problems the chain carries
+// S, U and D in fp32 and hands them to the matrix cores as a sum of two bf16
+// numbers (16 bits of significand; the error of a product is about 2^-18 of its
+// size), so states and dV are as good as fp32 storage of them needs; the
+// products that end in bf16 outputs without feeding the chain (Q S, (Gam o Q
+// K^T) U, and those of dq and dk) take one bf16 number for S, U, D and H.
+// fp32 problems use the fp32 matrix instructions throughout.
+#pragma once
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+namespace gdr {
+
+constexpr int kC = 64;            // tokens per chunk
+constexpr int kTri = 6;           // 16 x 32 operand blocks in a triangle of 64 x 64
+constexpr int kVec = 6 * kC;      // floats of per-token scalars per (chunk, head)
+// their order
+constexpr int kSince = 0, kBeta = kC, kTill = 2 * kC, kCsHi = 3 * kC, kCsLo = 4 * kC;
+constexpr double kLog2eD = 1.4426950408889634;
+constexpr float kMinLogDecay = -64.f;   // e^-64 = 1.6e-28: smaller decays act as this one
+
+// Planes of a split operand: a bf16 chain value is the sum of two bf16 numbers.
+template <typename E> constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
+
+// ---------------------------------------------------------------------------
+// chunks and chains
+// ---------------------------------------------------------------------------
+// A chain is one batch row, or one segment of a packed stream; its chunks are
+// consecutive.  Packed streams: cmap[c] = {first token, token count} and
+// chain[i] = {first chunk, chunks} are built on the device from seq_idx (every
+// segment starts a chunk of its own); otherwise both are null and arithmetic.
+struct Chunks {
+    const int2 *cmap, *chain;
+    int T, nc;   // tokens and chunks per batch row (not packed)
+};
+
+__device__ __forceinline__ void chunk_at(const Chunks &m, int c, int64_t &t0, int &count)
+{
+    if (m.cmap) {
+        const int2 v = m.cmap[c];
+        t0 = v.x;
+        count = v.y;
+    } else {
+        const int row = c / m.nc, i = c - row * m.nc;
+        t0 = (int64_t)row * m.T + (int64_t)i * kC;
+        count = m.T - i * kC < kC ? m.T - i * kC : kC;
+    }
+}
+
+__device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n)
+{
+    if (m.chain) {
+        const int2 v = m.chain[i];
+        c0 = v.x;
+        n = v.y;
+    } else {
+        c0 = i * m.nc;
+        n = m.nc;
+    }
+}
+
+// The chunk map of a packed stream, by one workgroup.  `range` [nseq] is scratch.
+// Ids outside [0, nseq) are skipped and nothing is written past ncmax chunks, so
+// an invalid stream gives wrong chunks but no access out of bounds.
+constexpr int kMapThreads = 1024;
+__global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restrict__ seq_idx, int2 *__restrict__ range,
+                                                         int2 *__restrict__ chain, int2 *__restrict__ cmap, int T,
+                                                         int nseq, int ncmax)
+{
+    __shared__ int wsum[kMapThreads / 64], base;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    for (int i = tid; i < nseq; i += kMapThreads) range[i] = int2{0, 0};
+    if (tid == 0) base = 0;
+    __syncthreads();
+    // range[id] = {start, end}: the words of one id are written by the threads of
+    // its first and its last token
+    int *words = reinterpret_cast<int *>(range);
+    for (int t = tid; t < T; t += kMapThreads) {
+        const int id = seq_idx[t];
+        if (id < 0 || id >= nseq) continue;
+        if (t == 0 || seq_idx[t - 1] != id) words[2 * id] = t;
+        if (t == T - 1 || seq_idx[t + 1] != id) words[2 * id + 1] = t + 1;
+    }
+    __syncthreads();
+    for (int i0 = 0; i0 < nseq; i0 += kMapThreads) {
+        const int i = i0 + tid;
+        const int2 r = i < nseq ? range[i] : int2{0, 0};
+        const int len = r.y > r.x ? r.y - r.x : 0, n = (len + kC - 1) / kC;
+        int s = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        if (lane == 63) wsum[wv] = s;
+        __syncthreads();
+        int before = base;
+        for (int w = 0; w < wv; ++w) before += wsum[w];
+        const int c0 = before + s - n;
+        if (i < nseq) {
+            const int lo = c0 < ncmax ? c0 : ncmax;
+            chain[i] = int2{lo, c0 + n <= ncmax ? n : ncmax - lo};
+        }
+        __syncthreads();
+        if (tid == kMapThreads - 1) base = before + s;
+        __syncthreads();
+    }
+    // one wave per segment writes its chunks
+    for (int i = wv; i < nseq; i += kMapThreads / 64) {
+        const int2 r = range[i], ch = chain[i];
+        for (int j = lane; j < ch.y; j += 64) {
+            const int left = r.y - r.x - j * kC;
+            cmap[ch.x + j] = int2{r.x + j * kC, left < kC ? left : kC};
+        }
+    }
+    for (int c = base + tid; c < ncmax; c += kMapThreads) cmap[c] = int2{0, 0};
+}
+
+// ---------------------------------------------------------------------------
+// operand blocks
+// ---------------------------------------------------------------------------
+// An operand block is 16 rows x 32 slots, 512 elements, lane l's 8 slots at
+// element 8 l: one coalesced 16-byte (fp32: 32-byte) load per lane feeds one
+// product.  The position in a 32-row block of slot j of lane group g:
+__device__ __forceinline__ int slot_row(int g, int j) { return j < 4 ? 4 * g + j : 16 + 4 * g + j - 4; }
+// Blocks of a lower triangle (rows t, slots s <= t) and of an upper one (rows s,
+// slots t >= s) of a 64 x 64 matrix, 32-slot block kb of row block b.
+__device__ __forceinline__ int lower_block(int b, int kb) { return b < 2 ? b : 2 + 2 * (b - 2) + kb; }
+__device__ __forceinline__ int upper_block(int b, int kb) { return b < 2 ? 2 * b + kb : 4 + (b - 2); }
+
+// Two accumulators (32 rows of 16 columns) as a second operand, hi + lo.
+__device__ __forceinline__ void split_pair(const floatx4 &a, const floatx4 &b, bf16x8 &hi, bf16x8 &lo)
+{
+    const floatx8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    hi = __builtin_convertvector(v, bf16x8);   // nearest even; the remainder is exact in fp32
+    lo = __builtin_convertvector(v - __builtin_convertvector(hi, floatx8), bf16x8);
+}
+__device__ __forceinline__ void split_pair(const floatx4 &a, const floatx4 &b, floatx8 &hi, floatx8 &)
+{
+    hi = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <typename E> __device__ __forceinline__ frag_t<E> round_pair(const floatx4 &a, const floatx4 &b)
+{
+    return from_f32<frag_t<E>>(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Four consecutive slots of a split matrix into its planes (`plane` elements apart).
+__device__ __forceinline__ void store_split4(bf16 *p, int64_t plane, const floatx4 &v)
+{
+    const bf16x4 hi = __builtin_convertvector(v, bf16x4);
+    *reinterpret_cast<bf16x4 *>(p) = hi;
+    *reinterpret_cast<bf16x4 *>(p + plane) = __builtin_convertvector(v - __builtin_convertvector(hi, floatx4), bf16x4);
+}
+__device__ __forceinline__ void store_split4(float *p, int64_t, const floatx4 &v) { *reinterpret_cast<floatx4 *>(p) = v; }
+__device__ __forceinline__ void store_round4(bf16 *p, const floatx4 &v)
+{
+    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
+}
+__device__ __forceinline__ void store_round4(float *p, const floatx4 &v) { *reinterpret_cast<floatx4 *>(p) = v; }
+
+// K and Q of one chunk and group as operand blocks in slot order: rows (64 tokens,
+// slots over N: 4 x NT/32 blocks) and transposed (NT rows n, slots over tokens:
+// NT/16 x 2 blocks).  Tokens past the chunk's count and columns past N are zero.
+// `out` [which] : 0 = K rows, 1 = K^T, 2 = Q rows, 3 = Q^T (backward only).
+template <typename E, int NT>
+__global__ __launch_bounds__(kThreads) void k_gdr_frags(const E *__restrict__ k, const E *__restrict__ q,
+                                                        E *__restrict__ out, Chunks m, int G, int N, int nmat)
+{
+    constexpr int LD = NT + 16 / (int)sizeof(E);   // LDS row stride: 16 bytes of padding
+    __shared__ __attribute__((aligned(16))) E tile[kC * LD];
+    const int c = blockIdx.x / G, grp = blockIdx.x % G, src = blockIdx.y;   // src: 0 = k, 1 = q
+    int64_t t0;
+    int count;
+    chunk_at(m, c, t0, count);
+    if (count <= 0) return;
+    constexpr int V = kVec16<E>;
+    const E *in = (src ? q : k) + (t0 * G + grp) * N;
+    const int64_t ld = (int64_t)G * N;
+    for (int i = threadIdx.x; i < kC * NT / V; i += kThreads) {
+        const int t = i / (NT / V), n = (i % (NT / V)) * V;
+        uint4 v = uint4{0, 0, 0, 0};
+        if (t < count && n < N) v = *reinterpret_cast<const uint4 *>(in + t * ld + n);
+        *reinterpret_cast<uint4 *>(&tile[t * LD + n]) = v;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    E *o = out + ((int64_t)c * G + grp) * nmat * kC * NT + (int64_t)(2 * src) * kC * NT;
+    for (int b = wv; b < 4 * (NT / 32); b += kThreads / 64) {
+        const E *row = &tile[(16 * (b / (NT / 32)) + l) * LD + 32 * (b % (NT / 32)) + 4 * g];
+        frag_t<E> f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = row[j];
+            f[4 + j] = row[16 + j];
+        }
+        store_frag(o + b * 512 + 8 * lane, f);
+    }
+    if (2 * src + 1 >= nmat) return;
+    o += kC * NT;
+    for (int b = wv; b < 2 * (NT / 16); b += kThreads / 64) {
+        frag_t<E> f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = tile[(32 * (b & 1) + slot_row(g, j)) * LD + 16 * (b >> 1) + l];
+        store_frag(o + b * 512 + 8 * lane, f);
+    }
+}
+
+// Elements of one (chunk, head) of the prepared triangles: N (its planes), Gam o
+// Q K^T rounded; for the backward also N^T and (Gam o Q K^T)^T (their planes).
+template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
+{
+    return 512 * kTri * (bwd ? 3 * kPlanes<E> + 1 : kPlanes<E> + 1);
+}
+
+// Everything of one chunk and head that no state enters.  One wave per block of
+// 16 tokens.  cs is summed in 64 bits, since Gam takes differences of it; A in
+// fp32 in LDS.  The inverse goes by blocks of 16: the diagonal blocks' inverses
+// Tm = (I + Db A)^-1 by substitution (a wave each, a column per lane), then block
+// row i of N from right to left,
+//   N_ij = (A_ij - sum_{j < k <= i} N_ik (Db A)_kj) Tm_jj,
+// transposed, so that the accumulators are the next product's second operand and
+// hold four consecutive slots of N's operand blocks.  fp32 matrix instructions.
+template <typename E, int NT, bool BWD>
+__global__ __launch_bounds__(kThreads) void k_gdr_prep(const E *__restrict__ kq, const E *__restrict__ gate,
+                                                       const E *__restrict__ beta, float *__restrict__ vec,
+                                                       E *__restrict__ tri, Chunks m, int H, int G, float scale)
+{
+    constexpr int LD = kC + 4, NK = NT / 32, kMat = kC * NT;
+    __shared__ __attribute__((aligned(16))) float A[kC * LD];
+    __shared__ __attribute__((aligned(16))) float Tm[4][16][17];
+    __shared__ double csd[kC];
+    __shared__ float bt[kC];
+    const int c = blockIdx.x / H, h = blockIdx.x % H;
+    int64_t t0;
+    int count;
+    chunk_at(m, c, t0, count);
+    if (count <= 0) return;
+    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    const int64_t unit = (int64_t)c * H + h;
+    if (i == 0) {
+        float gv = 0.f, bv = 0.f;
+        if (lane < count) {
+            gv = to_float(gate[(t0 + lane) * H + h]);
+            bv = to_float(beta[(t0 + lane) * H + h]);
+        }
+        double s = gv < kMinLogDecay ? kMinLogDecay : gv;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        csd[lane] = s;
+        bt[lane] = bv;
+        const double last = __shfl(s, 63);
+        float *vo = vec + unit * kVec;
+        const float hi = (float)s;
+        vo[kSince + lane] = exp2_((float)(s * kLog2eD));
+        vo[kBeta + lane] = bv;
+        vo[kTill + lane] = exp2_((float)((last - s) * kLog2eD));
+        vo[kCsHi + lane] = hi;
+        vo[kCsLo + lane] = (float)(s - (double)hi);
+        vo[5 * kC + lane] = 0.f;
+    }
+    __syncthreads();
+    const E *kf = kq + ((int64_t)c * G + h / (H / G)) * (BWD ? 4 : 3) * kMat, *qf = kf + 2 * kMat;
+    E *tri_o = tri + unit * tri_elems<E>(BWD);
+    constexpr int64_t PL = 512 * kTri;
+    E *n_o = tri_o, *p_o = tri_o + kPlanes<E> * PL, *nt_o = p_o + PL, *pt_o = nt_o + kPlanes<E> * PL;
+
+    // blocks (i, j) of K K^T and Q K^T, j <= i, with rows s and columns t
+    frag_t<E> ki[NK], qi[NK];
+#pragma unroll
+    for (int kb = 0; kb < NK; ++kb) {
+        ki[kb] = load_frag(kf + (i * NK + kb) * 512 + 8 * lane);
+        qi[kb] = load_frag(qf + (i * NK + kb) * 512 + 8 * lane);
+    }
+    const int t = 16 * i + l;
+    for (int j = 0; j <= (i | 1); ++j) {
+        floatx4 a = floatx4{0, 0, 0, 0}, p = a, pt = a;
+        if (j <= i) {
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb) {
+                const frag_t<E> kj = load_frag(kf + (j * NK + kb) * 512 + 8 * lane);
+                mma(a, kj, ki[kb]);
+                mma(p, kj, qi[kb]);
+                if (BWD) mma(pt, qi[kb], kj);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int s = 16 * j + 4 * g + r;
+                const float gam = exp2_((float)((csd[t] - csd[s]) * kLog2eD));
+                a[r] = s < t ? gam * a[r] : 0.f;
+                p[r] = s <= t ? scale * gam * p[r] : 0.f;
+                if (BWD) {   // rows t, columns s
+                    const int tt = 16 * i + 4 * g + r, ss = 16 * j + l;
+                    pt[r] = ss <= tt ? scale * exp2_((float)((csd[tt] - csd[ss]) * kLog2eD)) * pt[r] : 0.f;
+                }
+            }
+            *reinterpret_cast<floatx4 *>(&A[t * LD + 16 * j + 4 * g]) = a;
+        }
+        store_round4(p_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), p);
+        if (BWD) store_split4(pt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, pt);
+    }
+    __syncthreads();
+    {
+        // column l of Tm_ii (the four lane groups do the same work)
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < r; ++e) s += A[(16 * i + r) * LD + 16 * i + e] * x[e];
+            x[r] = (r == l ? 1.f : 0.f) - bt[16 * i + r] * s;
+        }
+        if (g == 0)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) Tm[i][r][l] = x[r];
+    }
+    __syncthreads();
+    floatx4 nt[4];   // N^T_ji: rows s of block j, columns t of block i
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+        floatx4 x = floatx4{0, 0, 0, 0}, n = x;
+        if (j <= i) {
+            x = *reinterpret_cast<const floatx4 *>(&A[t * LD + 16 * j + 4 * g]);
+#pragma unroll
+            for (int k = j + 1; k < 4; ++k)
+                if (k <= i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int kt = 16 * k + 4 * g + r;
+                        x = __builtin_amdgcn_mfma_f32_16x16x4f32(-bt[kt] * A[kt * LD + 16 * j + l], nt[k][r], x, 0, 0, 0);
+                    }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                n = __builtin_amdgcn_mfma_f32_16x16x4f32(Tm[j][4 * g + r][l], x[r], n, 0, 0, 0);
+        }
+        nt[j] = n;
+        if (j <= (i | 1)) store_split4(n_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), PL, n);
+    }
+    if (!BWD) return;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j <= i) *reinterpret_cast<floatx4 *>(&A[t * LD + 16 * j + 4 * g]) = nt[j];
+    __syncthreads();
+    for (int j = 0; j <= (i | 1); ++j) {
+        floatx4 v = floatx4{0, 0, 0, 0};
+        if (j <= i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = A[(16 * i + 4 * g + r) * LD + 16 * j + l];
+        store_split4(nt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the chains
+// ---------------------------------------------------------------------------
+struct ChainArgs {
+    const void *kq, *tri;        // operand blocks per (chunk, group) and (chunk, head)
+    const float *vec;
+    const void *v, *dy;          // values; output gradients (backward)
+    void *y, *dv;                // outputs of the forward / backward chain
+    const float *s0, *d1;        // [chains,H,P,N] initial state, gradient of the final state, or null
+    float *s1, *d0;              // final state, gradient of the initial state, or null
+    void *sst, *ust, *dst, *hst; // backward only: S, U, D, H of every (chunk, head)
+    Chunks m;
+    int H, G, P, N, Pp, np;      // Pp: P rounded up to 32; np: workgroups per head
+    int units;                   // chains * H * np
+    float scale;
+};
+
+// The state of 16 columns as second operands.
+template <typename E, int NB> struct StateOps {
+    frag_t<E> hi[NB / 2], lo[NB / 2];
+    __device__ __forceinline__ void of(const floatx4 (&s)[NB])
+    {
+#pragma unroll
+        for (int kb = 0; kb < NB / 2; ++kb) split_pair(s[2 * kb], s[2 * kb + 1], hi[kb], lo[kb]);
+    }
+};
+
+template <typename E, int NB>
+__device__ __forceinline__ void load_state(const float *src, floatx4 (&s)[NB], int p, int g, int P, int N)
+{
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int n = 16 * nb + 4 * g;
+        s[nb] = floatx4{0, 0, 0, 0};
+        if (src && p < P && n < N) s[nb] = *reinterpret_cast<const floatx4 *>(src + (int64_t)p * N + n);
+    }
+}
+template <int NB>
+__device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], int p, int g, int P, int N)
+{
+    if (!dst || p >= P) return;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int n = 16 * nb + 4 * g;
+        if (n < N) *reinterpret_cast<floatx4 *>(dst + (int64_t)p * N + n) = s[nb];
+    }
+}
+
+// The state's columns as rows of [n][Pp] (p contiguous) in E: the state's operand,
+// read as a first operand, is its transpose, and a product with rows of the
+// identity moves it to accumulators exactly.
+template <typename E, int NB>
+__device__ __forceinline__ void store_state_rows(E *dst, const frag_t<E> (&hi)[NB / 2], int p0, int Pp, int lane)
+{
+    const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        frag_t<E> sel;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sel[j] = from_float<E>(slot_row(g, j) == 16 * (nb & 1) + l ? 1.f : 0.f);
+        floatx4 d = floatx4{0, 0, 0, 0};
+        mma(d, hi[nb >> 1], sel);
+        store_round4(dst + (int64_t)(16 * nb + l) * Pp + p0 + 4 * g, d);
+    }
+}
+
+// The lane's 16 elements of a [64 tokens][16 columns] tile: token 16 tb + 4 g + r.
+template <typename E>
+__device__ __forceinline__ void load_tile(const E *src, int64_t ld, E (&x)[16], int g, int count, bool on)
+{
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * tb + 4 * g + r;
+            x[4 * tb + r] = from_float<E>(0.f);
+            if (on && t < count) x[4 * tb + r] = src[t * ld];
+        }
+}
+template <typename E>
+__device__ __forceinline__ void store_tile(E *dst, int64_t ld, const floatx4 (&x)[4], int g, int count, bool on)
+{
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * tb + 4 * g + r;
+            if (on && t < count) dst[t * ld] = from_float<E>(x[tb][r]);
+        }
+}
+
+__device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
+
+// One forward chain.  KEEP: for the backward, which wants S and U of every chunk
+// and not y.
+template <typename E, int NB, bool KEEP>
+__device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
+{
+    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
+    constexpr int64_t PL = 512 * kTri;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    const int pt = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = pt * kC + 16 * wv, p = p0 + l;
+    if (p0 >= a.Pp) return;
+    const bool on = p < a.P;
+    int c0, n;
+    chain_at(a.m, ch, c0, n);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
+    floatx4 S[NB];
+    load_state<E, NB>(a.s0 ? a.s0 + so : nullptr, S, p, g, a.P, a.N);
+    const int64_t ld = (int64_t)a.H * a.P;
+    const int grp = h / (a.H / a.G);
+    for (int c = c0; c < c0 + n; ++c) {
+        int64_t t0;
+        int count;
+        chunk_at(a.m, c, t0, count);
+        const int64_t u = (int64_t)c * a.H + h;
+        const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * (KEEP ? 4 : 3) * kMat + 8 * lane;
+        const E *ktf = kf + kMat, *qf = kf + 2 * kMat;
+        const E *nf = (const E *)a.tri + u * tri_elems<E>(KEEP) + 8 * lane, *pf = nf + kPlanes<E> * PL;
+        const float *vec = a.vec + u * kVec;
+        E v[16];
+        load_tile((const E *)a.v + (t0 * a.H + h) * a.P + p, ld, v, g, count, on);
+        StateOps<E, NB> so_;
+        so_.of(S);
+        if (KEEP) store_state_rows<E, NB>((E *)a.sst + u * NT * a.Pp, so_.hi, p0, a.Pp, lane);
+        floatx4 ks[4], qs[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb) {
+                const frag_t<E> f = load_frag(kf + (tb * NK + kb) * 512);
+                mma(ks[tb], f, so_.hi[kb]);
+                if (kPlanes<E> == 2) mma(ks[tb], f, so_.lo[kb]);
+                if (!KEEP) mma(qs[tb], load_frag(qf + (tb * NK + kb) * 512), so_.hi[kb]);
+            }
+        }
+        floatx4 since[4], bt[4], R[4], X[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            since[tb] = vec4(vec + kSince + 16 * tb + 4 * g);
+            bt[tb] = vec4(vec + kBeta + 16 * tb + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) R[tb][r] = to_float(v[4 * tb + r]) - since[tb][r] * ks[tb][r];
+            X[tb] = bt[tb] * R[tb];
+        }
+        frag_t<E> xh[2], xl[2];
+        split_pair(X[0], X[1], xh[0], xl[0]);
+        split_pair(X[2], X[3], xh[1], xl[1]);
+        floatx4 W[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            floatx4 d = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb <= tb / 2; ++kb) {
+                const frag_t<E> f = load_frag(nf + lower_block(tb, kb) * 512);
+                mma(d, f, xh[kb]);
+                if (kPlanes<E> == 2) {
+                    mma(d, f, xl[kb]);
+                    mma(d, load_frag(nf + PL + lower_block(tb, kb) * 512), xh[kb]);
+                }
+            }
+            R[tb] -= d;   // U
+            W[tb] = bt[tb] * R[tb];
+        }
+        if (KEEP) {
+            store_tile((E *)a.ust + u * kC * a.Pp + p, a.Pp, R, g, kC, true);
+        } else {
+            const frag_t<E> w0 = round_pair<E>(W[0], W[1]), w1 = round_pair<E>(W[2], W[3]);
+            floatx4 y[4];
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                y[tb] = (a.scale * since[tb]) * qs[tb];
+                mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w0);
+                if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w1);
+            }
+            store_tile((E *)a.y + (t0 * a.H + h) * a.P + p, ld, y, g, count, on);
+        }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
+        split_pair(W[0], W[1], xh[0], xl[0]);
+        split_pair(W[2], W[3], xh[1], xl[1]);
+        const float whole = vec[kSince + kC - 1];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            S[nb] *= whole;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const frag_t<E> f = load_frag(ktf + (2 * nb + kb) * 512);
+                mma(S[nb], f, xh[kb]);
+                if (kPlanes<E> == 2) mma(S[nb], f, xl[kb]);
+            }
+        }
+    }
+    save_state<NB>(a.s1 ? a.s1 + so : nullptr, S, p, g, a.P, a.N);
+}
+
+// One backward chain: D of every chunk (the gradient of the state that leaves it),
+// H, and dv.
+template <typename E, int NB>
+__device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit)
+{
+    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
+    constexpr int64_t PL = 512 * kTri;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    const int pt = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = pt * kC + 16 * wv, p = p0 + l;
+    if (p0 >= a.Pp) return;
+    const bool on = p < a.P;
+    int c0, n;
+    chain_at(a.m, ch, c0, n);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
+    floatx4 D[NB];
+    load_state<E, NB>(a.d1 ? a.d1 + so : nullptr, D, p, g, a.P, a.N);
+    const int64_t ld = (int64_t)a.H * a.P;
+    const int grp = h / (a.H / a.G);
+    for (int c = c0 + n - 1; c >= c0; --c) {
+        int64_t t0;
+        int count;
+        chunk_at(a.m, c, t0, count);
+        const int64_t u = (int64_t)c * a.H + h;
+        const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat + 8 * lane;
+        const E *ktf = kf + kMat, *qtf = kf + 3 * kMat;
+        const E *nt = (const E *)a.tri + u * tri_elems<E>(true) + (kPlanes<E> + 1) * PL + 8 * lane;
+        const E *ptf = nt + kPlanes<E> * PL;
+        const float *vec = a.vec + u * kVec;
+        E dy[16];
+        load_tile((const E *)a.dy + (t0 * a.H + h) * a.P + p, ld, dy, g, count, on);
+        StateOps<E, NB> dop;
+        dop.of(D);
+        store_state_rows<E, NB>((E *)a.dst + u * NT * a.Pp, dop.hi, p0, a.Pp, lane);
+        floatx4 yt[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) yt[tb][r] = to_float(dy[4 * tb + r]);
+        const frag_t<E> y0 = round_pair<E>(yt[0], yt[1]), y1 = round_pair<E>(yt[2], yt[3]);   // exact
+        floatx4 W[4], X[4], bt[4], since[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            W[tb] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb) {
+                const frag_t<E> f = load_frag(kf + (tb * NK + kb) * 512);
+                mma(W[tb], f, dop.hi[kb]);
+                if (kPlanes<E> == 2) mma(W[tb], f, dop.lo[kb]);
+            }
+            W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
+            bt[tb] = vec4(vec + kBeta + 16 * tb + 4 * g);
+            since[tb] = vec4(vec + kSince + 16 * tb + 4 * g);
+#pragma unroll
+            for (int kb = tb / 2; kb < 2; ++kb)
+#pragma unroll
+                for (int pl = 0; pl < kPlanes<E>; ++pl)
+                    mma(W[tb], load_frag(ptf + pl * PL + upper_block(tb, kb) * 512), kb ? y1 : y0);
+            X[tb] = bt[tb] * W[tb];
+        }
+        frag_t<E> xh[2], xl[2];
+        split_pair(X[0], X[1], xh[0], xl[0]);
+        split_pair(X[2], X[3], xh[1], xl[1]);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            floatx4 d = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = tb / 2; kb < 2; ++kb) {
+                const frag_t<E> f = load_frag(nt + upper_block(tb, kb) * 512);
+                mma(d, f, xh[kb]);
+                if (kPlanes<E> == 2) {
+                    mma(d, f, xl[kb]);
+                    mma(d, load_frag(nt + PL + upper_block(tb, kb) * 512), xh[kb]);
+                }
+            }
+            W[tb] -= d;             // H
+            X[tb] = bt[tb] * W[tb]; // dv
+        }
+        store_tile((E *)a.hst + u * kC * a.Pp + p, a.Pp, W, g, kC, true);
+        store_tile((E *)a.dv + (t0 * a.H + h) * a.P + p, ld, X, g, count, on);
+        frag_t<E> yh[2], yl[2];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            yt[tb] *= a.scale * since[tb];
+            X[tb] *= -since[tb];
+        }
+        split_pair(yt[0], yt[1], yh[0], yl[0]);
+        split_pair(yt[2], yt[3], yh[1], yl[1]);
+        split_pair(X[0], X[1], xh[0], xl[0]);
+        split_pair(X[2], X[3], xh[1], xl[1]);
+        const float whole = vec[kSince + kC - 1];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            D[nb] *= whole;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const frag_t<E> f = load_frag(ktf + (2 * nb + kb) * 512);
+                const frag_t<E> fq = load_frag(qtf + (2 * nb + kb) * 512);
+                mma(D[nb], fq, yh[kb]);
+                if (kPlanes<E> == 2) mma(D[nb], fq, yl[kb]);
+                mma(D[nb], f, xh[kb]);
+                if (kPlanes<E> == 2) mma(D[nb], f, xl[kb]);
+            }
+        }
+    }
+    save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p, g, a.P, a.N);
+}
+
+template <typename E, int NB>
+__global__ __launch_bounds__(kThreads) void k_gdr_chain(ChainArgs a)
+{
+    chain_fwd<E, NB, false>(a, blockIdx.x);
+}
+
+// The backward's two chains in one launch: neither needs the other.
+template <typename E, int NB>
+__global__ __launch_bounds__(kThreads) void k_gdr_chains(ChainArgs a)
+{
+    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB>(a, blockIdx.x);
+    else chain_fwd<E, NB, true>(a, blockIdx.x - a.units);
+}
+
+// ---------------------------------------------------------------------------
+// gradients of q, k, g and beta
+// ---------------------------------------------------------------------------
+// With W_ts = scale Gam_ts beta_s (dy_t . u_s) (s <= t) and Z_ts = Gam_ts beta_t
+// beta_s (H_t . u_s) (s < t), per head
+//   dq = scale e^{cs} o (dY S^T) + W K
+//   dk = -e^{cs} beta o (H S^T) + e^{cs_last - cs} beta o (U D^T) + W^T Q - (Z + Z^T) K
+//   dbeta_t = H_t . u_t
+// and dq, dk are summed over the heads of the group, in order.  For dg_t every
+// path from before t to at or after t counts once: with
+//   X_ts = W_ts q_t.k_s - Z_ts k_t.k_s,
+//   a_t = q_t . scale e^{cs_t} S dy_t - k_t . e^{cs_t} beta_t S H_t,
+//   b_s = k_s . e^{cs_last - cs_s} beta_s D u_s,
+//   dg_t = sum_{u >= t} (sum_s X_us - sum_s X_su + a_u - b_u) + sum_s b_s + e^{cs_last} <D, S>.
+// The pairs on one side of t cancel, and do so to fp32 whatever U, H, S and D were
+// rounded to, because both sums take the same X.  (q.dq - v.dv, the shorter form of
+// the same sum, would need dq and dv far beyond bf16: 9e-3 against 2e-3 of dg.)
+struct GradArgs {
+    const void *kq, *k, *q, *dy, *sst, *ust, *dst, *hst;
+    const float *vec;
+    void *dq, *dk, *dg, *dbeta;
+    float *part;                 // hsplit > 1: fp32 sums of dq and dk per split
+    Chunks m;
+    int H, G, P, N, Pp, hsplit;
+    float scale;
+};
+
+template <typename E, int NB>
+__global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
+{
+    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
+    __shared__ __attribute__((aligned(16))) float vs[kVec];
+    __shared__ float dcs[kC], red[8];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    int x = blockIdx.x;
+    const int sp = x % a.hsplit;
+    x /= a.hsplit;
+    const int grp = x % a.G, c = x / a.G;
+    int64_t t0;
+    int count;
+    chunk_at(a.m, c, t0, count);
+    if (count <= 0) return;
+    const int hpg = a.H / a.G;
+    const int h0 = grp * hpg + (int)((int64_t)hpg * sp / a.hsplit), h1 = grp * hpg + (int)((int64_t)hpg * (sp + 1) / a.hsplit);
+    const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat + 8 * lane;
+    const E *ktf = kf + kMat, *qf = kf + 2 * kMat, *qtf = kf + 3 * kMat;
+
+    // q.k and k.k of the wave's 16 tokens against all (rows j, columns w)
+    floatx4 qkT[4], qkN[4], kk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        qkT[j] = qkN[j] = kk[j] = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            const frag_t<E> kj = load_frag(kf + (j * NK + kb) * 512), kw = load_frag(kf + (w * NK + kb) * 512);
+            mma(kk[j], kj, kw);
+            if (j <= w) mma(qkT[j], kj, load_frag(qf + (w * NK + kb) * 512));   // rows s, columns t
+            if (j >= w) mma(qkN[j], load_frag(qf + (j * NK + kb) * 512), kw);   // rows t, columns s
+        }
+    }
+    // the wave's q and k rows in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
+    E qe[NB][4], ke[NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * w + 4 * g + r, n = 16 * nb + l;
+            qe[nb][r] = ke[nb][r] = from_float<E>(0.f);
+            if (t < count && n < a.N) {
+                const int64_t at = ((t0 + t) * a.G + grp) * a.N + n;
+                qe[nb][r] = ((const E *)a.q)[at];
+                ke[nb][r] = ((const E *)a.k)[at];
+            }
+        }
+    floatx4 dq[NB], dk[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
+
+    const int KP = a.Pp / 32;
+    const int64_t yld = (int64_t)a.H * a.P;
+    for (int h = h0; h < h1; ++h) {
+        const int64_t u = (int64_t)c * a.H + h;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kVec; i += kThreads) vs[i] = a.vec[u * kVec + i];
+        __syncthreads();
+        const E *U = (const E *)a.ust + u * kC * a.Pp, *Hh = (const E *)a.hst + u * kC * a.Pp;
+        const E *S = (const E *)a.sst + u * NT * a.Pp, *D = (const E *)a.dst + u * NT * a.Pp;
+        const E *dy = (const E *)a.dy + (t0 * a.H + h) * a.P;
+        auto dyf = [&](int tb, int kb) {   // rows past the count and columns past P are zero
+            frag_t<E> f;
+            const int t = 16 * tb + l, pp = 32 * kb + 8 * g;
+            if (t < count && pp < a.P) f = load_frag(dy + t * yld + pp);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = from_float<E>(0.f);
+            return f;
+        };
+        auto rowf = [&](const E *base, int row0, int kb) {
+            return load_frag(base + (int64_t)(row0 + l) * a.Pp + 32 * kb + 8 * g);
+        };
+        // the pair products, in both orientations
+        floatx4 wT[4], wN[4], zT[4], zN[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wT[j] = wN[j] = zT[j] = zN[j] = floatx4{0, 0, 0, 0};
+        float db = 0.f;
+        for (int kb = 0; kb < KP; ++kb) {
+            const frag_t<E> uw = rowf(U, 16 * w, kb), hw = rowf(Hh, 16 * w, kb), yw = dyf(w, kb);
+            const floatx8 uf = to_f32(uw), hf = to_f32(hw);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) db += uf[j] * hf[j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j <= w) {
+                    const frag_t<E> uj = rowf(U, 16 * j, kb);
+                    mma(wT[j], uj, yw);   // rows s, columns t
+                    mma(zT[j], uj, hw);
+                }
+                if (j >= w) {
+                    mma(wN[j], dyf(j, kb), uw);   // rows t, columns s
+                    mma(zN[j], rowf(Hh, 16 * j, kb), uw);
+                }
+            }
+        }
+        db += __shfl_xor(db, 16);
+        db += __shfl_xor(db, 32);
+        if (g == 0 && 16 * w + l < count)
+            ((E *)a.dbeta)[(t0 + 16 * w + l) * a.H + h] = from_float<E>(db);
+        float rowX = 0.f, colX = 0.f;   // of token 16 w + l, this lane's share
+        const int tl = 16 * w + l;
+        const float bl = vs[kBeta + tl];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int o = 16 * j + 4 * g + r;
+                const float bo = vs[kBeta + o];
+                const float dh = vs[kCsHi + tl] - vs[kCsHi + o], dl = vs[kCsLo + tl] - vs[kCsLo + o];
+                if (j <= w) {   // t = tl, s = o
+                    const float gam = o <= tl ? exp2_((dh + dl) * kLog2e) * bo : 0.f;
+                    wT[j][r] = a.scale * gam * wT[j][r];
+                    zT[j][r] = o < tl ? gam * bl * zT[j][r] : 0.f;
+                    if (o > tl) wT[j][r] = 0.f;
+                    rowX += wT[j][r] * qkT[j][r] - zT[j][r] * kk[j][r];
+                }
+                if (j >= w) {   // t = o, s = tl
+                    const float gam = tl <= o ? exp2_(-(dh + dl) * kLog2e) * bl : 0.f;
+                    wN[j][r] = a.scale * gam * wN[j][r];
+                    zN[j][r] = tl < o ? gam * bo * zN[j][r] : 0.f;
+                    if (tl > o) wN[j][r] = 0.f;
+                    colX += wN[j][r] * qkN[j][r] - zN[j][r] * kk[j][r];
+                }
+            }
+        float dx = rowX - colX;
+        dx += __shfl_xor(dx, 16);
+        dx += __shfl_xor(dx, 32);
+        // the state products
+        floatx4 since = vec4(vs + kSince + 16 * w + 4 * g), bt = vec4(vs + kBeta + 16 * w + 4 * g);
+        const floatx4 cq = a.scale * since, ch = since * bt, cd = vec4(vs + kTill + 16 * w + 4 * g) * bt;
+        floatx4 ab = floatx4{0, 0, 0, 0}, bs = ab;
+        float sd = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
+            for (int kb = 0; kb < KP; ++kb) {
+                const frag_t<E> sf = rowf(S, 16 * nb, kb), df = rowf(D, 16 * nb, kb);
+                mma(ys, dyf(w, kb), sf);
+                mma(hs, rowf(Hh, 16 * w, kb), sf);
+                mma(ud, rowf(U, 16 * w, kb), df);
+                if ((nb & 3) == w) {
+                    const floatx8 s8 = to_f32(sf), d8 = to_f32(df);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sd += s8[j] * d8[j];
+                }
+            }
+            ys *= cq;
+            hs *= ch;
+            ud *= cd;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float qv = to_float(qe[nb][r]), kv = to_float(ke[nb][r]);
+                ab[r] += qv * ys[r] - kv * hs[r];
+                bs[r] += kv * ud[r];
+            }
+            dq[nb] += ys;
+            dk[nb] += ud - hs;
+        }
+        // W K, W^T Q and (Z + Z^T) K
+        floatx4 zs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) zs[j] = j < w ? -zT[j] : j > w ? -zN[j] : -(zT[j] + zN[j]);
+        const frag_t<E> a0 = round_pair<E>(wT[0], wT[1]), a1 = round_pair<E>(wT[2], wT[3]);
+        const frag_t<E> b0 = round_pair<E>(wN[0], wN[1]), b1 = round_pair<E>(wN[2], wN[3]);
+        const frag_t<E> z0 = round_pair<E>(zs[0], zs[1]), z1 = round_pair<E>(zs[2], zs[3]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const frag_t<E> k0 = load_frag(ktf + 2 * nb * 512), k1 = load_frag(ktf + (2 * nb + 1) * 512);
+            const frag_t<E> q0 = load_frag(qtf + 2 * nb * 512), q1 = load_frag(qtf + (2 * nb + 1) * 512);
+            mma(dq[nb], a0, k0);
+            mma(dq[nb], a1, k1);
+            mma(dk[nb], b0, q0);
+            mma(dk[nb], b1, q1);
+            mma(dk[nb], z0, k0);
+            mma(dk[nb], z1, k1);
+        }
+        // dg
+        ab -= bs;
+        float sb = bs[0] + bs[1] + bs[2] + bs[3];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ab[r] += __shfl_xor(ab[r], d);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            sb += __shfl_xor(sb, d);
+            sd += __shfl_xor(sd, d);
+        }
+        if (g == 0) dcs[16 * w + l] = dx;
+        if (lane == 0) {
+            red[w] = sb;
+            red[4 + w] = sd;
+        }
+        __syncthreads();
+        if (l == 0)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dcs[16 * w + 4 * g + r] += ab[r];
+        __syncthreads();
+        if (w == 0) {
+            float s = dcs[63 - lane];
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const float o = __shfl_up(s, d);
+                if (lane >= d) s += o;
+            }
+            s += red[0] + red[1] + red[2] + red[3] +
+                 vs[kSince + kC - 1] * (red[4] + red[5] + red[6] + red[7]);
+            if (63 - lane < count) ((E *)a.dg)[(t0 + 63 - lane) * a.H + h] = from_float<E>(s);
+        }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * w + 4 * g + r, n = 16 * nb + l;
+            if (a.hsplit > 1) {
+                float *o = a.part + (((int64_t)c * a.G + grp) * a.hsplit + sp) * 2 * kMat + (int64_t)t * NT + n;
+                o[0] = dq[nb][r];
+                o[kMat] = dk[nb][r];
+            } else if (t < count && n < a.N) {
+                const int64_t at = ((t0 + t) * a.G + grp) * a.N + n;
+                ((E *)a.dq)[at] = from_float<E>(dq[nb][r]);
+                ((E *)a.dk)[at] = from_float<E>(dk[nb][r]);
+            }
+        }
+}
+
+// dq and dk of one chunk and group from their parts, added in order of the split.
+template <typename E, int NT>
+__global__ __launch_bounds__(kThreads) void k_gdr_grad_sum(const float *__restrict__ part, E *__restrict__ dq,
+                                                           E *__restrict__ dk, Chunks m, int G, int N, int hsplit)
+{
+    constexpr int kMat = kC * NT;
+    const int c = blockIdx.x / G, grp = blockIdx.x % G;
+    int64_t t0;
+    int count;
+    chunk_at(m, c, t0, count);
+    const float *p = part + ((int64_t)c * G + grp) * hsplit * 2 * kMat;
+    for (int i = threadIdx.x; i < 2 * kMat / 4; i += kThreads) {
+        const int which = i / (kMat / 4), e = 4 * (i % (kMat / 4)), t = e / NT, n = e % NT;
+        if (t >= count || n >= N) continue;
+        floatx4 s = floatx4{0, 0, 0, 0};
+        for (int k = 0; k < hsplit; ++k) s += vec4(p + (int64_t)(2 * k + which) * kMat + e);
+        store_round4((which ? dk : dq) + ((t0 + t) * G + grp) * N + n, s);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one token
+// ---------------------------------------------------------------------------
+// One step of the recurrence for every (batch row, head), the state [P][N] in
+// fp32, read and written once.  NL lanes share a row of the state (four
+// consecutive n each, 16-byte accesses); the two sums over n (with k before the
+// update, with q after it) are reduced inside those lanes.  Bound by the state's
+// bytes, like any step of a recurrence.
+constexpr int kStepRows = 4;   // rows in flight per thread
+template <typename E, int NL>
+__global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, const E *__restrict__ k,
+                                                       const E *__restrict__ v, const E *__restrict__ gate,
+                                                       const E *__restrict__ beta, float *__restrict__ state,
+                                                       E *__restrict__ y, int H, int G, int P, int N, float scale)
+{
+    const int bh = blockIdx.x, b = bh / H, h = bh - b * H, grp = h / (H / G);
+    const int ln = threadIdx.x % NL, row = threadIdx.x / NL, n = 4 * ln;
+    constexpr int RPB = kThreads / NL;
+    const bool in = n < N;
+    const int64_t kq = ((int64_t)b * G + grp) * N + n;
+    float kv[4] = {0, 0, 0, 0}, qv[4] = {0, 0, 0, 0};
+    const int p0 = blockIdx.y * RPB * kStepRows + row;
+    float *st = state + (int64_t)bh * P * N;
+    floatx4 s[kStepRows];
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int p = p0 + i * RPB;
+        s[i] = floatx4{0, 0, 0, 0};
+        if (in && p < P) s[i] = *reinterpret_cast<const floatx4 *>(st + (int64_t)p * N + n);
+    }
+    if (in) {
+        load4_f32(k + kq, kv);
+        load4_f32(q + kq, qv);
+    }
+    float gv = to_float(gate[bh]);
+    gv = gv < kMinLogDecay ? kMinLogDecay : gv;
+    const float al = exp2_(gv * kLog2e), bt = to_float(beta[bh]);
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int p = p0 + i * RPB;
+        s[i] *= al;
+        float d = s[i][0] * kv[0] + s[i][1] * kv[1] + s[i][2] * kv[2] + s[i][3] * kv[3];
+#pragma unroll
+        for (int o = 1; o < NL; o <<= 1) d += __shfl_xor(d, o);
+        const float u = p < P ? bt * (to_float(v[(int64_t)bh * P + p]) - d) : 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[i][e] += u * kv[e];
+            o += s[i][e] * qv[e];
+        }
+#pragma unroll
+        for (int x = 1; x < NL; x <<= 1) o += __shfl_xor(o, x);
+        if (p < P) {
+            if (in) *reinterpret_cast<floatx4 *>(st + (int64_t)p * N + n) = s[i];
+            if (ln == 0) y[(int64_t)bh * P + p] = from_float<E>(scale * o);
+        }
+    }
+}
+
+// final_states = initial_states (or zero): no tokens.
+__global__ __launch_bounds__(kThreads) void k_gdr_copy(float *__restrict__ dst, const float *__restrict__ src, int64_t n)
+{
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i < n) *reinterpret_cast<floatx4 *>(dst + i) = src ? vec4(src + i) : floatx4{0, 0, 0, 0};
+}
+
+}  // namespace gdr
+}  // namespace ssd

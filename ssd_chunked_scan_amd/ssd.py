@@ -9,7 +9,9 @@ is missing the first call raises, there is no fallback.
 Names follow the C ABI: ``fwd`` (= ``ssd_fwd``), the per-step entry points
 ``chunk_cumsum``, ``chunk_cb``, ``chunk_state``, ``state_passing``,
 ``seq_final_states``, ``chunk_scan``, the decode step ``step`` (= ``ssd_step``)
-and the backward ``bwd`` (= ``ssd_bwd``).
+and the backward ``bwd`` (= ``ssd_bwd``); the gated delta rule ``gdr_fwd``,
+``gdr_bwd`` and ``gdr_step``; layer norm ``layer_norm_fwd`` and
+``layer_norm_bwd``.
 """
 from __future__ import annotations
 
@@ -27,7 +29,9 @@ _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 EXPORTED = ["ssd_abi_version", "ssd_status_string", "ssd_fwd_workspace_size", "ssd_fwd",
             "ssd_chunk_cumsum", "ssd_chunk_cb", "ssd_chunk_state", "ssd_state_passing",
             "ssd_seq_final_states", "ssd_chunk_scan", "ssd_step", "ssd_bwd_workspace_size", "ssd_bwd",
-            "ssd_fwd_gated", "ssd_conv1d_silu", "ssd_fwd_noalloc", "ssd_bwd_stage_times", "ssd_check_seq_idx"]
+            "ssd_fwd_gated", "ssd_conv1d_silu", "ssd_fwd_noalloc", "ssd_bwd_stage_times", "ssd_check_seq_idx",
+            "ssd_gdr_fwd_workspace_size", "ssd_gdr_bwd_workspace_size", "ssd_gdr_fwd", "ssd_gdr_bwd", "ssd_gdr_step",
+            "ssd_layer_norm_fwd", "ssd_layer_norm_bwd_workspace_size", "ssd_layer_norm_bwd"]
 
 # SSD_BWD_MAX_STAGES in include/ssd.h
 BWD_MAX_STAGES = 24
@@ -85,6 +89,57 @@ class ConvArgs(ctypes.Structure):
     ]
 
 
+class GdrArgs(ctypes.Structure):
+    """Mirror of ``ssd_gdr_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+        ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
+        ("beta", ctypes.c_void_p), ("initial_states", ctypes.c_void_p), ("seq_idx", ctypes.c_void_p),
+        ("nseq", ctypes.c_int64), ("y", ctypes.c_void_p), ("final_states", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GdrBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_gdr_bwd_args``."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("dfinal_states", ctypes.c_void_p), ("dq", ctypes.c_void_p),
+        ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("dg", ctypes.c_void_p), ("dbeta", ctypes.c_void_p),
+        ("dinitial_states", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GdrStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_gdr_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+        ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
+        ("beta", ctypes.c_void_p), ("state", ctypes.c_void_p), ("y", ctypes.c_void_p),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of ``ssd_norm_args``."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class NormBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_norm_bwd_args``."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class SSDError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -122,6 +177,16 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_fwd_gated.argtypes = [P, vp, vp]
     lib.ssd_conv1d_silu.argtypes = [ctypes.POINTER(ConvArgs), vp]
     lib.ssd_fwd_noalloc.argtypes = [P, vp]
+    # the structures below are passed by address (ctypes.addressof): a call per token
+    # should not pay for the pointer objects
+    lib.ssd_gdr_fwd_workspace_size.argtypes = [vp, vp]
+    lib.ssd_gdr_bwd_workspace_size.argtypes = [vp, vp]
+    lib.ssd_gdr_fwd.argtypes = [vp, vp]
+    lib.ssd_gdr_bwd.argtypes = [vp, vp, vp]
+    lib.ssd_gdr_step.argtypes = [vp, vp]
+    lib.ssd_layer_norm_fwd.argtypes = [vp, vp]
+    lib.ssd_layer_norm_bwd_workspace_size.argtypes = [vp, vp]
+    lib.ssd_layer_norm_bwd.argtypes = [vp, vp]
     for name in EXPORTED[2:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -529,3 +594,253 @@ def bwd(x, dt, A, B, C, chunk, y, dy, D=None, initial_states=None, dfinal_states
         raise SSDError(rc, "ssd_bwd_stage_times")
     stage_times.extend((names[i].decode(), float(ms[i])) for i in range(n.value))
     return g
+
+
+# ---------------------------------------------------------------------------
+# the gated delta rule and layer norm
+# ---------------------------------------------------------------------------
+
+def _same(t, name, dtype, shape, dev):
+    """``_check`` with the common case first: everything as it should be."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous() and t.is_cuda):
+        return
+    _check(t, name, dtype, shape, dev)
+
+
+class _Launch:
+    """Device and stream of one call.  Within it the tensors' device is current and,
+    for a stream of the caller's, what is allocated belongs to that stream (memory of
+    the current stream could be handed out again while the other still uses it)."""
+
+    def __init__(self, dev, stream):
+        cur = torch.cuda.current_stream(dev).cuda_stream
+        self.stream = cur if stream is None else int(stream)
+        self.ctx = []
+        if self.stream != cur:
+            self.ctx.append(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=dev)))
+        elif torch.cuda.current_device() != dev.index:
+            self.ctx.append(torch.cuda.device(dev))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _run(name, rc):
+    if rc != 0:
+        raise SSDError(rc, name)
+
+
+def _bytes_of(name, args):
+    n = ctypes.c_size_t(0)
+    _run(name, getattr(load_library(), name)(ctypes.addressof(args), ctypes.addressof(n)))
+    return n.value
+
+
+def _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq):
+    """Validated ``GdrArgs`` (no outputs), and the shape of the states."""
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must be [batch, seqlen, nheads, headdim]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, seqlen, ngroups, dstate]")
+    b, T, H, P = v.shape
+    G, N = q.shape[2:]
+    dtype, dev = v.dtype, v.device
+    if dtype not in _DTYPES:
+        raise TypeError("v must be float32 or bfloat16")
+    _same(v, "v", dtype, v.shape, dev)
+    _same(q, "q", dtype, (b, T, G, N), dev)
+    _same(k, "k", dtype, (b, T, G, N), dev)
+    _same(g, "g", dtype, (b, T, H), dev)
+    _same(beta, "beta", dtype, (b, T, H), dev)
+    if seq_idx is not None:
+        _same(seq_idx, "seq_idx", torch.int32, (T,), dev)
+        if nseq is None:
+            raise ValueError("nseq is required with seq_idx (no device->host read)")
+    n = 0 if seq_idx is None else int(nseq)
+    states = (b if seq_idx is None else n, H, P, N)
+    if initial_states is not None:
+        _same(initial_states, "initial_states", torch.float32, states, dev)
+    a = GdrArgs(b, T, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale, q.data_ptr(), k.data_ptr(),
+                v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(initial_states), _ptr(seq_idx), n)
+    return a, states
+
+
+def gdr_fwd_workspace_bytes(q, k, v, g, beta, seq_idx=None, nseq=None) -> int:
+    """Bytes of the ``workspace`` that ``gdr_fwd`` takes for these shapes."""
+    return _bytes_of("ssd_gdr_fwd_workspace_size", _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)[0])
+
+
+def gdr_bwd_workspace_bytes(q, k, v, g, beta, seq_idx=None, nseq=None) -> int:
+    """Bytes of the ``workspace`` that ``gdr_bwd`` takes for these shapes."""
+    return _bytes_of("ssd_gdr_bwd_workspace_size", _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)[0])
+
+
+def gdr_fwd(q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, nseq=None, y=None, final_states=None,
+            workspace=None, stream=None, want_final=True):
+    """y, final_states = the gated delta rule over whole sequences (``ssd_gdr_fwd``):
+    q, k [b,T,G,N], v [b,T,H,P], g (log decay, <= 0) and beta [b,T,H], all fp32 or
+    bf16; ``scale`` multiplies y (default 1).  States are [b,H,P,N] fp32, with
+    ``seq_idx`` (packed streams, batch 1) [nseq,H,P,N], one per segment.  ``y``,
+    ``final_states`` and ``workspace`` (uint8) may be passed pre-allocated."""
+    a, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
+    dev = v.device
+    with _Launch(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(v)
+        else:
+            _same(y, "y", v.dtype, v.shape, dev)
+        if final_states is None:
+            if want_final:
+                final_states = torch.empty(states, dtype=torch.float32, device=dev)
+        else:
+            _same(final_states, "final_states", torch.float32, states, dev)
+        if workspace is None:
+            workspace = torch.empty(_bytes_of("ssd_gdr_fwd_workspace_size", a), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", torch.uint8, None, dev)
+        a.y, a.final_states = y.data_ptr(), _ptr(final_states)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _run("ssd_gdr_fwd", load_library().ssd_gdr_fwd(ctypes.addressof(a), st))
+    return y, final_states
+
+
+def gdr_bwd(q, k, v, g, beta, dy, scale=None, initial_states=None, dfinal_states=None, seq_idx=None, nseq=None,
+            grads=None, workspace=None, stream=None, want_dinit=True):
+    """Gradients of sum(y * dy) + sum(final_states * dfinal_states) (``ssd_gdr_bwd``):
+    a dict with dq, dk, dv, dg, dbeta and dinitial_states (None unless
+    ``want_dinit``); ``grads`` may pass those tensors pre-allocated."""
+    a, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
+    dev, dtype = v.device, v.dtype
+    _same(dy, "dy", dtype, v.shape, dev)
+    if dfinal_states is not None:
+        _same(dfinal_states, "dfinal_states", torch.float32, states, dev)
+    out = dict(grads or {})
+    with _Launch(dev, stream) as st:
+        for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
+            if out.get(name) is None:
+                out[name] = torch.empty_like(like)
+            else:
+                _same(out[name], name, dtype, like.shape, dev)
+        if out.get("dinitial_states") is not None:
+            _same(out["dinitial_states"], "dinitial_states", torch.float32, states, dev)
+        else:
+            out["dinitial_states"] = torch.empty(states, dtype=torch.float32, device=dev) if want_dinit else None
+        if workspace is None:
+            workspace = torch.empty(_bytes_of("ssd_gdr_bwd_workspace_size", a), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", torch.uint8, None, dev)
+        ga = GdrBwdArgs(dy.data_ptr(), _ptr(dfinal_states), out["dq"].data_ptr(), out["dk"].data_ptr(),
+                        out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(),
+                        _ptr(out["dinitial_states"]), workspace.data_ptr(), workspace.numel())
+        _run("ssd_gdr_bwd", load_library().ssd_gdr_bwd(ctypes.addressof(a), ctypes.addressof(ga), st))
+    return out
+
+
+def gdr_step(q, k, v, g, beta, state, scale=None, y=None, stream=None):
+    """y = one token of every batch row (``ssd_gdr_step``): q, k [b,G,N], v [b,H,P],
+    g, beta [b,H]; ``state`` [b,H,P,N] fp32 is updated in place."""
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v must be [batch, nheads, headdim]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [batch, ngroups, dstate]")
+    b, H, P = v.shape
+    G, N = q.shape[1:]
+    dtype, dev = v.dtype, v.device
+    if dtype not in _DTYPES:
+        raise TypeError("v must be float32 or bfloat16")
+    _same(v, "v", dtype, v.shape, dev)
+    _same(q, "q", dtype, (b, G, N), dev)
+    _same(k, "k", dtype, (b, G, N), dev)
+    _same(g, "g", dtype, (b, H), dev)
+    _same(beta, "beta", dtype, (b, H), dev)
+    _same(state, "state", torch.float32, (b, H, P, N), dev)
+    with _Launch(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(v)
+        else:
+            _same(y, "y", dtype, v.shape, dev)
+        a = GdrStepArgs(b, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale, q.data_ptr(), k.data_ptr(),
+                        v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), y.data_ptr())
+        _run("ssd_gdr_step", load_library().ssd_gdr_step(ctypes.addressof(a), st))
+    return y
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None, want_stats=True):
+    """y, mean, rstd = layer norm over the last axis of x [..., dim] fp32/bf16
+    (``ssd_layer_norm_fwd``); weight and bias [dim] fp32 or None.  mean and rstd
+    (fp32, the leading shape of x) are what the backward reads; None unless
+    ``want_stats``.  ``y`` may be ``x``."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    dtype, dev, lead, dim = x.dtype, x.device, x.shape[:-1], x.shape[-1]
+    if dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16")
+    _same(x, "x", dtype, x.shape, dev)
+    if weight is not None:
+        _same(weight, "weight", torch.float32, (dim,), dev)
+    if bias is not None:
+        _same(bias, "bias", torch.float32, (dim,), dev)
+    with _Launch(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _same(y, "y", dtype, x.shape, dev)
+        if want_stats:
+            mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else mean
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
+            _same(mean, "mean", torch.float32, lead, dev)
+            _same(rstd, "rstd", torch.float32, lead, dev)
+        else:
+            mean = rstd = None
+        a = NormArgs(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], eps, x.data_ptr(), _ptr(weight), _ptr(bias),
+                     y.data_ptr(), _ptr(mean), _ptr(rstd))
+        _run("ssd_layer_norm_fwd", load_library().ssd_layer_norm_fwd(ctypes.addressof(a), st))
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, dy, mean, rstd, weight=None, grads=None, workspace=None, stream=None, want_params=None):
+    """Gradients of sum(y * dy) through ``layer_norm_fwd`` (``ssd_layer_norm_bwd``): a
+    dict with dx and, when ``want_params`` (default: if a weight is given), dweight
+    and dbias [dim] fp32; ``grads`` may pass those tensors pre-allocated (dx may be
+    ``dy``)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    dtype, dev, lead, dim = x.dtype, x.device, x.shape[:-1], x.shape[-1]
+    if dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16")
+    _same(x, "x", dtype, x.shape, dev)
+    _same(dy, "dy", dtype, x.shape, dev)
+    _same(mean, "mean", torch.float32, lead, dev)
+    _same(rstd, "rstd", torch.float32, lead, dev)
+    if weight is not None:
+        _same(weight, "weight", torch.float32, (dim,), dev)
+    params = weight is not None if want_params is None else want_params
+    out = dict(grads or {})
+    with _Launch(dev, stream) as st:
+        if out.get("dx") is None:
+            out["dx"] = torch.empty_like(x)
+        else:
+            _same(out["dx"], "dx", dtype, x.shape, dev)
+        for name in ("dweight", "dbias"):
+            if out.get(name) is not None:
+                _same(out[name], name, torch.float32, (dim,), dev)
+            elif params:
+                out[name] = torch.empty(dim, dtype=torch.float32, device=dev)
+        dw, db = out.get("dweight"), out.get("dbias")
+        a = NormBwdArgs(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], 0, x.data_ptr(), dy.data_ptr(),
+                        mean.data_ptr(), rstd.data_ptr(), _ptr(weight), out["dx"].data_ptr(), _ptr(dw), _ptr(db))
+        if workspace is not None:
+            _check(workspace, "workspace", torch.uint8, None, dev)
+        elif dw is not None or db is not None:
+            workspace = torch.empty(_bytes_of("ssd_layer_norm_bwd_workspace_size", a), dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _run("ssd_layer_norm_bwd", load_library().ssd_layer_norm_bwd(ctypes.addressof(a), st))
+    return out
