@@ -79,6 +79,8 @@ ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
     s->NT = s->N <= 64 ? 64 : s->N <= 128 ? 128 : 256;
     s->Pp = (s->P + 31) / 32 * 32;
     s->np = (s->Pp + kC - 1) / kC;
+    // a chunk's rows of all heads or groups are addressed with 31-bit byte offsets
+    if (s->H * s->P > (1 << 22) || s->G * s->N > (1 << 22)) return SSD_ERR_BAD_SHAPE;
     // grids and int32 indices
     if (s->chains > INT32_MAX / s->H / s->np / 2 || s->nct > INT32_MAX / s->H / 2 || s->nct * kC > INT32_MAX)
         return SSD_ERR_BAD_SHAPE;

@@ -217,13 +217,19 @@ __global__ __launch_bounds__(kThreads) void k_gdr_frags(const E *__restrict__ k,
     chunk_at(m, c, t0, count);
     if (count <= 0) return;
     constexpr int V = kVec16<E>;
-    const E *in = (src ? q : k) + (t0 * G + grp) * N;
-    const int64_t ld = (int64_t)G * N;
-    for (int i = threadIdx.x; i < kC * NT / V; i += kThreads) {
-        const int t = i / (NT / V), n = (i % (NT / V)) * V;
-        uint4 v = uint4{0, 0, 0, 0};
-        if (t < count && n < N) v = *reinterpret_cast<const uint4 *>(in + t * ld + n);
-        *reinterpret_cast<uint4 *>(&tile[t * LD + n]) = v;
+    const uint32_t ld = (uint32_t)(G * N) * sizeof(E);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc((src ? q : k) + (t0 * G + grp) * N, ((int64_t)(count - 1) * G + 1) * N * (int64_t)sizeof(E));
+    constexpr int IT = kC * NT / V / kThreads;
+    uint4 v[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int e = i * kThreads + threadIdx.x, t = e / (NT / V), n = (e % (NT / V)) * V;
+        v[i] = bload16(rs, n < N ? t * ld + n * sizeof(E) : kOffNone);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int e = i * kThreads + threadIdx.x, t = e / (NT / V), n = (e % (NT / V)) * V;
+        *reinterpret_cast<uint4 *>(&tile[t * LD + n]) = v[i];
     }
     __syncthreads();
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
@@ -462,78 +468,212 @@ __device__ __forceinline__ void store_state_rows(E *dst, const frag_t<E> (&hi)[N
     }
 }
 
-// The lane's 16 elements of a [64 tokens][16 columns] tile: token 16 tb + 4 g + r.
+// One element through a buffer resource: out of range reads are zero and writes are
+// dropped, so ragged tiles need no branches (a branch around each of 16 loads makes
+// each wait for its own).
+template <typename E> __device__ __forceinline__ E bload_elem(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    if constexpr (sizeof(E) == 2)
+        return __builtin_bit_cast(E, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    else return __builtin_bit_cast(E, (unsigned int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+template <typename E> __device__ __forceinline__ void bstore_elem(__amdgpu_buffer_rsrc_t r, uint32_t off, E v)
+{
+    if constexpr (sizeof(E) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), r, off, 0, 0);
+}
+// The buffer of one head's rows of a chunk: `count` rows of P elements, `ld` apart
+// (the host keeps 64 ld elements below 2^31 bytes).
+template <typename E> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const E *base, int count, int64_t ld, int P)
+{
+    return make_rsrc(base, ((count - 1) * ld + P) * (int64_t)sizeof(E));
+}
+// The lane's 16 elements of a [64 tokens][16 columns] tile: token 16 tb + 4 g + r,
+// column p (off: kOffNone for a column past P).
 template <typename E>
-__device__ __forceinline__ void load_tile(const E *src, int64_t ld, E (&x)[16], int g, int count, bool on)
+__device__ __forceinline__ void load_tile(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, E (&x)[16], int g)
 {
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * tb + 4 * g + r;
-            x[4 * tb + r] = from_float<E>(0.f);
-            if (on && t < count) x[4 * tb + r] = src[t * ld];
-        }
+        for (int r = 0; r < 4; ++r) x[4 * tb + r] = bload_elem<E>(rs, off + (16 * tb + 4 * g + r) * ld);
 }
 template <typename E>
-__device__ __forceinline__ void store_tile(E *dst, int64_t ld, const floatx4 (&x)[4], int g, int count, bool on)
+__device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, const floatx4 (&x)[4], int g)
 {
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * tb + 4 * g + r;
-            if (on && t < count) dst[t * ld] = from_float<E>(x[tb][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+            bstore_elem<E>(rs, off + (16 * tb + 4 * g + r) * ld, from_float<E>(x[tb][r]));
 }
 
 __device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
 
+// ---- operands of a chain's step, staged through LDS ----
+// The waves of a workgroup own different columns and read the same first operands, 44
+// to 72 KB a step at N = 128.  They come straight from memory into LDS (16 bytes per
+// lane, no registers), in two regions: while a step computes from one, the other one's
+// next contents are in flight.  Phase 1 of a step reads what meets the entering state
+// (K, and Q or the pair matrix), phase 2 the rest.  One barrier before each phase says
+// both that its operands are there and that the other region is free.  Larger sets (fp32
+// at N = 256) do not fit 160 KB and are read from global memory by every wave.
+template <typename E, int NT> constexpr bool kStaged = sizeof(E) * NT <= 512;
+
+// KIND 0: the forward (y), 1: the forward for the backward (S and U), 2: the backward
+template <typename E, int NB, int KIND> struct Regions {
+    static constexpr int kMat = 4 * NB / 2;   // blocks of K, K^T, Q or Q^T (64 x NT)
+    static constexpr int kN = kTri * kPlanes<E>;
+    // phase 1: K | Q (KIND 0) or the transposed pair matrix (KIND 2)
+    static constexpr int kOne = kMat + (KIND == 0 ? kMat : KIND == 2 ? kN : 0);
+    // phase 2: N or N^T | the pair matrix (KIND 0) | K^T | Q^T (KIND 2)
+    static constexpr int kTwo = kN + (KIND == 0 ? kTri : 0) + kMat + (KIND == 2 ? kMat : 0);
+    static constexpr int kBytes = kStaged<E, 16 * NB> ? (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * 1024 : 16;
+};
+
+typedef __attribute__((address_space(1))) const void *gptr_t;
+typedef __attribute__((address_space(3))) void *lptr_t;
+
+// `n` operand blocks from memory to LDS, a wave every fourth block.
+template <typename E, int n> __device__ __forceinline__ void stage(const E *src, E *dst, int wv, int lane)
+{
+    constexpr int V = kVec16<E>;
+#pragma unroll
+    for (int b0 = 0; b0 < n; b0 += 4) {
+        const int b = b0 + wv;
+        if (n % 4 == 0 || b < n)
+#pragma unroll
+            for (int j = 0; j < 512; j += 64 * V)
+                __builtin_amdgcn_global_load_lds((gptr_t)(src + b * 512 + j + V * lane), (lptr_t)(dst + b * 512 + j), 16,
+                                                 0, 0);
+    }
+}
+// Every load of this wave has arrived; then the workgroup meets.
+__device__ __forceinline__ void arrive()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    __syncthreads();
+}
+
+// A step's operand pointers: in LDS at fixed places, or in memory.
+template <typename E, int NB, int KIND> struct Operands {
+    using R = Regions<E, NB, KIND>;
+    static constexpr int kMatE = kC * 16 * NB;
+    static constexpr bool LDS = kStaged<E, 16 * NB>;
+    E *one, *two;
+    float *vecs;
+    const E *kq, *tri;
+    const float *vec;
+    int wv, lane, turn;
+
+    __device__ __forceinline__ void init(char *smem, int wv_, int lane_)
+    {
+        one = reinterpret_cast<E *>(smem);
+        two = one + R::kOne * 512;
+        vecs = reinterpret_cast<float *>(two + R::kTwo * 512);
+        wv = wv_;
+        lane = lane_;
+        turn = 0;
+    }
+    // where chunk c's operands are in memory
+    __device__ __forceinline__ void at(const ChainArgs &a, int c, int h, int grp)
+    {
+        const int64_t u = (int64_t)c * a.H + h;
+        kq = (const E *)a.kq + ((int64_t)c * a.G + grp) * (KIND == 0 ? 3 : 4) * kMatE;
+        tri = (const E *)a.tri + u * tri_elems<E>(KIND != 0);
+        vec = a.vec + u * kVec;
+    }
+    // N | Gam QK^T | N^T | (Gam QK^T)^T in `tri`; K | K^T | Q | Q^T in `kq`
+    static constexpr int kPL = 512 * kTri, kNt = (kPlanes<E> + 1) * kPL, kPt = (2 * kPlanes<E> + 1) * kPL;
+    __device__ __forceinline__ void stage_one()
+    {
+        if constexpr (LDS) {
+            stage<E, R::kMat>(kq, one, wv, lane);
+            if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, one + kMatE, wv, lane);
+            if (KIND == 2) stage<E, R::kN>(tri + kPt, one + kMatE, wv, lane);
+            if (wv == 3)
+                __builtin_amdgcn_global_load_lds((gptr_t)(vec + 4 * lane), (lptr_t)(vecs + 256 * turn), 16, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void stage_two()
+    {
+        if constexpr (LDS) {
+            stage<E, R::kN>(tri + (KIND == 2 ? kNt : 0), two, wv, lane);
+            E *o = two + R::kN * 512;
+            if (KIND == 0) {
+                stage<E, kTri>(tri + kPlanes<E> * kPL, o, wv, lane);
+                o += kTri * 512;
+            }
+            stage<E, R::kMat>(kq + kMatE, o, wv, lane);
+            if (KIND == 2) stage<E, R::kMat>(kq + 3 * kMatE, o + kMatE, wv, lane);
+        }
+    }
+    __device__ __forceinline__ const E *k() const { return (LDS ? one : kq) + 8 * lane; }
+    __device__ __forceinline__ const E *q() const { return (LDS ? one + kMatE : kq + 2 * kMatE) + 8 * lane; }
+    __device__ __forceinline__ const E *pt() const { return (LDS ? one + kMatE : tri + kPt) + 8 * lane; }
+    __device__ __forceinline__ const E *n() const { return (LDS ? two : tri + (KIND == 2 ? kNt : 0)) + 8 * lane; }
+    __device__ __forceinline__ const E *p() const { return (LDS ? two + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane; }
+    __device__ __forceinline__ const E *kt() const
+    {
+        return (LDS ? two + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
+    }
+    __device__ __forceinline__ const E *qt() const { return (LDS ? two + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane; }
+    __device__ __forceinline__ const float *scalars() const { return LDS ? vecs + 256 * turn : vec; }
+};
+
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
 // and not y.
 template <typename E, int NB, bool KEEP>
-__device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
+__device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *smem)
 {
-    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
-    constexpr int64_t PL = 512 * kTri;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
-    const int pt = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
-    const int p0 = pt * kC + 16 * wv, p = p0 + l;
-    if (p0 >= a.Pp) return;
-    const bool on = p < a.P;
+    constexpr int NT = 16 * NB, NK = NT / 32, KIND = KEEP ? 1 : 0;
+    constexpr int PL = 512 * kTri;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = ptile * kC + 16 * wv, p = p0 + l;
+    const bool on = p < a.P, keep = p0 < a.Pp;
     int c0, n;
     chain_at(a.m, ch, c0, n);
     const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
     floatx4 S[NB];
     load_state<E, NB>(a.s0 ? a.s0 + so : nullptr, S, p, g, a.P, a.N);
     const int64_t ld = (int64_t)a.H * a.P;
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), pldb = a.Pp * sizeof(E);
+    const uint32_t poff = on ? p * sizeof(E) : kOffNone, koff = keep ? p * sizeof(E) : kOffNone;
     const int grp = h / (a.H / a.G);
+    Operands<E, NB, KIND> op;
+    op.init(smem, wv, lane);
+    int64_t t0 = 0;
+    int count = 0;
+    E v[16];
+    if (n > 0) {
+        chunk_at(a.m, c0, t0, count);
+        op.at(a, c0, h, grp);
+        op.stage_one();
+        load_tile<E>(rows_rsrc((const E *)a.v + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, v, g);
+    }
     for (int c = c0; c < c0 + n; ++c) {
-        int64_t t0;
-        int count;
-        chunk_at(a.m, c, t0, count);
         const int64_t u = (int64_t)c * a.H + h;
-        const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * (KEEP ? 4 : 3) * kMat + 8 * lane;
-        const E *ktf = kf + kMat, *qf = kf + 2 * kMat;
-        const E *nf = (const E *)a.tri + u * tri_elems<E>(KEEP) + 8 * lane, *pf = nf + kPlanes<E> * PL;
-        const float *vec = a.vec + u * kVec;
-        E v[16];
-        load_tile((const E *)a.v + (t0 * a.H + h) * a.P + p, ld, v, g, count, on);
+        if (Operands<E, NB, KIND>::LDS) arrive();
+        op.stage_two();
+        const float *vec = op.scalars();
         StateOps<E, NB> so_;
         so_.of(S);
-        if (KEEP) store_state_rows<E, NB>((E *)a.sst + u * NT * a.Pp, so_.hi, p0, a.Pp, lane);
+        if (KEEP && keep) store_state_rows<E, NB>((E *)a.sst + u * NT * a.Pp, so_.hi, p0, a.Pp, lane);
         floatx4 ks[4], qs[4];
+        const E *kf = op.k(), *qf = op.q();
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
+        for (int tb = 0; tb < 4; ++tb) ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb) {
+        for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
                 const frag_t<E> f = load_frag(kf + (tb * NK + kb) * 512);
                 mma(ks[tb], f, so_.hi[kb]);
                 if (kPlanes<E> == 2) mma(ks[tb], f, so_.lo[kb]);
                 if (!KEEP) mma(qs[tb], load_frag(qf + (tb * NK + kb) * 512), so_.hi[kb]);
             }
-        }
         floatx4 since[4], bt[4], R[4], X[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
@@ -546,6 +686,17 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
+        if (Operands<E, NB, KIND>::LDS) arrive();
+        const int64_t yt0 = t0;
+        const int ycount = count;
+        const E *nf = op.n(), *pf = op.p(), *ktf = op.kt();
+        if (c + 1 < c0 + n) {
+            chunk_at(a.m, c + 1, t0, count);
+            op.at(a, c + 1, h, grp);
+            op.turn ^= 1;
+            op.stage_one();
+            load_tile<E>(rows_rsrc((const E *)a.v + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, v, g);
+        }
         floatx4 W[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
@@ -563,7 +714,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
             W[tb] = bt[tb] * R[tb];
         }
         if (KEEP) {
-            store_tile((E *)a.ust + u * kC * a.Pp + p, a.Pp, R, g, kC, true);
+            store_tile<E>(rows_rsrc((E *)a.ust + u * kC * a.Pp, kC, a.Pp, a.Pp), pldb, koff, R, g);
         } else {
             const frag_t<E> w0 = round_pair<E>(W[0], W[1]), w1 = round_pair<E>(W[2], W[3]);
             floatx4 y[4];
@@ -573,7 +724,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
                 mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w0);
                 if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w1);
             }
-            store_tile((E *)a.y + (t0 * a.H + h) * a.P + p, ld, y, g, count, on);
+            store_tile<E>(rows_rsrc((E *)a.y + (yt0 * a.H + h) * a.P, ycount, ld, a.P), ldb, poff, y, g);
         }
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
@@ -581,15 +732,15 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
         split_pair(W[2], W[3], xh[1], xl[1]);
         const float whole = vec[kSince + kC - 1];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            S[nb] *= whole;
+        for (int nb = 0; nb < NB; ++nb) S[nb] *= whole;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 const frag_t<E> f = load_frag(ktf + (2 * nb + kb) * 512);
                 mma(S[nb], f, xh[kb]);
                 if (kPlanes<E> == 2) mma(S[nb], f, xl[kb]);
             }
-        }
     }
     save_state<NB>(a.s1 ? a.s1 + so : nullptr, S, p, g, a.P, a.N);
 }
@@ -597,53 +748,62 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit)
 // One backward chain: D of every chunk (the gradient of the state that leaves it),
 // H, and dv.
 template <typename E, int NB>
-__device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit)
+__device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *smem)
 {
-    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
-    constexpr int64_t PL = 512 * kTri;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
-    const int pt = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
-    const int p0 = pt * kC + 16 * wv, p = p0 + l;
-    if (p0 >= a.Pp) return;
-    const bool on = p < a.P;
+    constexpr int NT = 16 * NB, NK = NT / 32;
+    constexpr int PL = 512 * kTri;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = ptile * kC + 16 * wv, p = p0 + l;
+    const bool on = p < a.P, keep = p0 < a.Pp;
     int c0, n;
     chain_at(a.m, ch, c0, n);
     const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
     floatx4 D[NB];
     load_state<E, NB>(a.d1 ? a.d1 + so : nullptr, D, p, g, a.P, a.N);
     const int64_t ld = (int64_t)a.H * a.P;
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), pldb = a.Pp * sizeof(E);
+    const uint32_t poff = on ? p * sizeof(E) : kOffNone, koff = keep ? p * sizeof(E) : kOffNone;
     const int grp = h / (a.H / a.G);
+    Operands<E, NB, 2> op;
+    op.init(smem, wv, lane);
+    int64_t t0 = 0;
+    int count = 0;
+    E dy[16];
+    if (n > 0) {
+        chunk_at(a.m, c0 + n - 1, t0, count);
+        op.at(a, c0 + n - 1, h, grp);
+        op.stage_one();
+        load_tile<E>(rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, dy, g);
+    }
     for (int c = c0 + n - 1; c >= c0; --c) {
-        int64_t t0;
-        int count;
-        chunk_at(a.m, c, t0, count);
         const int64_t u = (int64_t)c * a.H + h;
-        const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat + 8 * lane;
-        const E *ktf = kf + kMat, *qtf = kf + 3 * kMat;
-        const E *nt = (const E *)a.tri + u * tri_elems<E>(true) + (kPlanes<E> + 1) * PL + 8 * lane;
-        const E *ptf = nt + kPlanes<E> * PL;
-        const float *vec = a.vec + u * kVec;
-        E dy[16];
-        load_tile((const E *)a.dy + (t0 * a.H + h) * a.P + p, ld, dy, g, count, on);
+        if (Operands<E, NB, 2>::LDS) arrive();
+        op.stage_two();
+        const float *vec = op.scalars();
         StateOps<E, NB> dop;
         dop.of(D);
-        store_state_rows<E, NB>((E *)a.dst + u * NT * a.Pp, dop.hi, p0, a.Pp, lane);
+        if (keep) store_state_rows<E, NB>((E *)a.dst + u * NT * a.Pp, dop.hi, p0, a.Pp, lane);
         floatx4 yt[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) yt[tb][r] = to_float(dy[4 * tb + r]);
         const frag_t<E> y0 = round_pair<E>(yt[0], yt[1]), y1 = round_pair<E>(yt[2], yt[3]);   // exact
+        const E *kf = op.k(), *ptf = op.pt();
         floatx4 W[4], X[4], bt[4], since[4];
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            W[tb] = floatx4{0, 0, 0, 0};
+        for (int tb = 0; tb < 4; ++tb) W[tb] = floatx4{0, 0, 0, 0};
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb) {
+        for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
                 const frag_t<E> f = load_frag(kf + (tb * NK + kb) * 512);
                 mma(W[tb], f, dop.hi[kb]);
                 if (kPlanes<E> == 2) mma(W[tb], f, dop.lo[kb]);
             }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
             W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
             bt[tb] = vec4(vec + kBeta + 16 * tb + 4 * g);
             since[tb] = vec4(vec + kSince + 16 * tb + 4 * g);
@@ -657,6 +817,25 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit)
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
+        if (Operands<E, NB, 2>::LDS) arrive();
+        const int64_t yt0 = t0;
+        const int ycount = count;
+        const E *nt = op.n(), *ktf = op.kt(), *qtf = op.qt();
+        if (c > c0) {
+            chunk_at(a.m, c - 1, t0, count);
+            op.at(a, c - 1, h, grp);
+            op.turn ^= 1;
+            op.stage_one();
+            load_tile<E>(rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, dy, g);
+        }
+        const float whole = vec[kSince + kC - 1];
+        frag_t<E> yh[2], yl[2];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) yt[tb] *= a.scale * since[tb];
+        split_pair(yt[0], yt[1], yh[0], yl[0]);
+        split_pair(yt[2], yt[3], yh[1], yl[1]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) D[nb] *= whole;
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             floatx4 d = floatx4{0, 0, 0, 0};
@@ -672,32 +851,28 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit)
             W[tb] -= d;             // H
             X[tb] = bt[tb] * W[tb]; // dv
         }
-        store_tile((E *)a.hst + u * kC * a.Pp + p, a.Pp, W, g, kC, true);
-        store_tile((E *)a.dv + (t0 * a.H + h) * a.P + p, ld, X, g, count, on);
-        frag_t<E> yh[2], yl[2];
+        store_tile<E>(rows_rsrc((E *)a.hst + u * kC * a.Pp, kC, a.Pp, a.Pp), pldb, koff, W, g);
+        store_tile<E>(rows_rsrc((E *)a.dv + (yt0 * a.H + h) * a.P, ycount, ld, a.P), ldb, poff, X, g);
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            yt[tb] *= a.scale * since[tb];
-            X[tb] *= -since[tb];
-        }
-        split_pair(yt[0], yt[1], yh[0], yl[0]);
-        split_pair(yt[2], yt[3], yh[1], yl[1]);
+        for (int tb = 0; tb < 4; ++tb) X[tb] *= -since[tb];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
-        const float whole = vec[kSince + kC - 1];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            D[nb] *= whole;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                const frag_t<E> f = load_frag(ktf + (2 * nb + kb) * 512);
                 const frag_t<E> fq = load_frag(qtf + (2 * nb + kb) * 512);
                 mma(D[nb], fq, yh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], fq, yl[kb]);
+            }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const frag_t<E> f = load_frag(ktf + (2 * nb + kb) * 512);
                 mma(D[nb], f, xh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], f, xl[kb]);
             }
-        }
     }
     save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p, g, a.P, a.N);
 }
@@ -705,15 +880,17 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit)
 template <typename E, int NB>
 __global__ __launch_bounds__(kThreads) void k_gdr_chain(ChainArgs a)
 {
-    chain_fwd<E, NB, false>(a, blockIdx.x);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0>::kBytes];
+    chain_fwd<E, NB, false>(a, blockIdx.x, smem);
 }
 
 // The backward's two chains in one launch: neither needs the other.
 template <typename E, int NB>
 __global__ __launch_bounds__(kThreads) void k_gdr_chains(ChainArgs a)
 {
-    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB>(a, blockIdx.x);
-    else chain_fwd<E, NB, true>(a, blockIdx.x - a.units);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2>::kBytes];   // the larger of both
+    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB>(a, blockIdx.x, smem);
+    else chain_fwd<E, NB, true>(a, blockIdx.x - a.units, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -778,17 +955,18 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
     }
     // the wave's q and k rows in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
     E qe[NB][4], ke[NB][4];
+    const int64_t kq0 = (t0 * a.G + grp) * a.N;
+    const uint32_t kqld = (uint32_t)(a.G * a.N) * sizeof(E);
+    const __amdgpu_buffer_rsrc_t qrs = rows_rsrc((const E *)a.q + kq0, count, (int64_t)a.G * a.N, a.N);
+    const __amdgpu_buffer_rsrc_t krs = rows_rsrc((const E *)a.k + kq0, count, (int64_t)a.G * a.N, a.N);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int t = 16 * w + 4 * g + r, n = 16 * nb + l;
-            qe[nb][r] = ke[nb][r] = from_float<E>(0.f);
-            if (t < count && n < a.N) {
-                const int64_t at = ((t0 + t) * a.G + grp) * a.N + n;
-                qe[nb][r] = ((const E *)a.q)[at];
-                ke[nb][r] = ((const E *)a.k)[at];
-            }
+            const uint32_t off = n < a.N ? t * kqld + n * sizeof(E) : kOffNone;
+            qe[nb][r] = bload_elem<E>(qrs, off);
+            ke[nb][r] = bload_elem<E>(krs, off);
         }
     floatx4 dq[NB], dk[NB];
 #pragma unroll
@@ -803,14 +981,11 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
         __syncthreads();
         const E *U = (const E *)a.ust + u * kC * a.Pp, *Hh = (const E *)a.hst + u * kC * a.Pp;
         const E *S = (const E *)a.sst + u * NT * a.Pp, *D = (const E *)a.dst + u * NT * a.Pp;
-        const E *dy = (const E *)a.dy + (t0 * a.H + h) * a.P;
+        const __amdgpu_buffer_rsrc_t dyrs = rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, yld, a.P);
         auto dyf = [&](int tb, int kb) {   // rows past the count and columns past P are zero
             frag_t<E> f;
             const int t = 16 * tb + l, pp = 32 * kb + 8 * g;
-            if (t < count && pp < a.P) f = load_frag(dy + t * yld + pp);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = from_float<E>(0.f);
+            bload_frag(dyrs, pp < a.P ? (t * (uint32_t)yld + pp) * (uint32_t)sizeof(E) : kOffNone, f);
             return f;
         };
         auto rowf = [&](const E *base, int row0, int kb) {
