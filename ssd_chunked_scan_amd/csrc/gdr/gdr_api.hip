@@ -114,6 +114,8 @@ int64_t head_split(const Shape &s)
     return k > hpg ? hpg : k < 1 ? 1 : k;
 }
 
+constexpr int64_t kTwiceUpTo = 256;   // workgroups: one per CU
+
 struct Workspace {
     size_t cmap, chain, range, kq, vec, tri, sst, ust, dst, hst, part, total;
 };
@@ -124,7 +126,7 @@ Workspace layout(const Shape &s, bool bwd)
     auto take = [&](size_t n) { const size_t at = o; o = align256(o + n); return at; };
     if (s.packed) {
         w.cmap = take((size_t)s.nct * 8);
-        w.chain = take((size_t)s.nseq * 8);
+        w.chain = take((size_t)s.nseq * 16);
         w.range = take((size_t)s.nseq * 8);
     }
     const size_t u = (size_t)(s.nct * s.H);
@@ -151,13 +153,24 @@ template <typename F> ssd_status with_nt(int64_t NT, F &&f)
     return f(std::integral_constant<int, 256>{});
 }
 
+// How the chains' operands are staged: twice where a workgroup per CU is all there
+// is (its own loads then hide behind its own steps), once where several share a CU.
+template <typename E, int NT, typename F> void with_flow(int64_t workgroups, F &&f)
+{
+    if constexpr (!kStaged<E, NT>) f(std::integral_constant<int, 0>{});
+    else if constexpr (!kTwice<E, NT>) f(std::integral_constant<int, 1>{});
+    else if (workgroups <= kTwiceUpTo) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 1>{});
+}
+
 // What both directions form first: the chunk map, the operand copies, the triangles.
 template <typename E, bool BWD>
 ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Workspace &w, Chunks *m, hipStream_t st)
 {
     *m = Chunks{nullptr, nullptr, (int)s.T, (int)s.nc};
     if (s.packed) {
-        int2 *cmap = reinterpret_cast<int2 *>(ws + w.cmap), *chain = reinterpret_cast<int2 *>(ws + w.chain);
+        int2 *cmap = reinterpret_cast<int2 *>(ws + w.cmap);
+        int4 *chain = reinterpret_cast<int4 *>(ws + w.chain);
         hipLaunchKernelGGL(k_gdr_map, dim3(1), dim3(kMapThreads), 0, st, a->seq_idx,
                            reinterpret_cast<int2 *>(ws + w.range), chain, cmap, (int)s.T, (int)s.nseq, (int)s.nct);
         m->cmap = cmap;
@@ -207,7 +220,11 @@ template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_gdr_args *a
     c.y = a->y;
     c.s1 = a->final_states;
     return with_nt(s.NT, [&](auto nt) {
-        hipLaunchKernelGGL((k_gdr_chain<E, decltype(nt)::value / 16>), dim3((unsigned)c.units), dim3(kThreads), 0, st, c);
+        constexpr int NT = decltype(nt)::value;
+        with_flow<E, NT>(c.units, [&](auto flow) {
+            hipLaunchKernelGGL((k_gdr_chain<E, NT / 16, decltype(flow)::value>), dim3((unsigned)c.units), dim3(kThreads), 0,
+                               st, c);
+        });
         return launched();
     });
 }
@@ -254,7 +271,10 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
     ga.scale = a->scale;
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        hipLaunchKernelGGL((k_gdr_chains<E, NT / 16>), dim3(2u * (unsigned)c.units), dim3(kThreads), 0, st, c);
+        with_flow<E, NT>(2 * (int64_t)c.units, [&](auto flow) {
+            hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, decltype(flow)::value>), dim3(2u * (unsigned)c.units),
+                               dim3(kThreads), 0, st, c);
+        });
         hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kThreads), 0, st, ga);
         if (hs > 1)
             hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G)), dim3(kThreads), 0, st,

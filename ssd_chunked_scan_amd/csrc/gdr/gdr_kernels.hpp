@@ -56,9 +56,11 @@ namespace gdr {
 
 constexpr int kC = 64;            // tokens per chunk
 constexpr int kTri = 6;           // 16 x 32 operand blocks in a triangle of 64 x 64
-constexpr int kVec = 6 * kC;      // floats of per-token scalars per (chunk, head)
-// their order
-constexpr int kSince = 0, kBeta = kC, kTill = 2 * kC, kCsHi = 3 * kC, kCsLo = 4 * kC;
+// Per-token scalars of a (chunk, head), 64 floats each: e^{cs}, beta, scale e^{cs},
+// beta e^{cs_last - cs}, e^{cs_last - cs}, -beta e^{cs}, and cs as a sum of two floats.
+constexpr int kVec = 8 * kC;
+constexpr int kSince = 0, kBeta = kC, kScaled = 2 * kC, kTillBeta = 3 * kC, kTill = 4 * kC, kErase = 5 * kC,
+              kCsHi = 6 * kC, kCsLo = 7 * kC;
 constexpr double kLog2eD = 1.4426950408889634;
 constexpr float kMinLogDecay = -64.f;   // e^-64 = 1.6e-28: smaller decays act as this one
 
@@ -70,10 +72,12 @@ template <typename E> constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
 // ---------------------------------------------------------------------------
 // A chain is one batch row, or one segment of a packed stream; its chunks are
 // consecutive.  Packed streams: cmap[c] = {first token, token count} and
-// chain[i] = {first chunk, chunks} are built on the device from seq_idx (every
-// segment starts a chunk of its own); otherwise both are null and arithmetic.
+// chain[i] = {first chunk, chunks, first token, tokens} are built on the device from
+// seq_idx (every segment starts a chunk of its own); otherwise both are null and
+// arithmetic.
 struct Chunks {
-    const int2 *cmap, *chain;
+    const int2 *cmap;
+    const int4 *chain;
     int T, nc;   // tokens and chunks per batch row (not packed)
 };
 
@@ -81,8 +85,8 @@ __device__ __forceinline__ void chunk_at(const Chunks &m, int c, int64_t &t0, in
 {
     if (m.cmap) {
         const int2 v = m.cmap[c];
-        t0 = v.x;
-        count = v.y;
+        t0 = __builtin_amdgcn_readfirstlane(v.x);
+        count = __builtin_amdgcn_readfirstlane(v.y);
     } else {
         const int row = c / m.nc, i = c - row * m.nc;
         t0 = (int64_t)row * m.T + (int64_t)i * kC;
@@ -90,15 +94,19 @@ __device__ __forceinline__ void chunk_at(const Chunks &m, int c, int64_t &t0, in
     }
 }
 
-__device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n)
+__device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n, int64_t &t0, int &len)
 {
     if (m.chain) {
-        const int2 v = m.chain[i];
-        c0 = v.x;
-        n = v.y;
+        const int4 v = m.chain[i];
+        c0 = __builtin_amdgcn_readfirstlane(v.x);
+        n = __builtin_amdgcn_readfirstlane(v.y);
+        t0 = __builtin_amdgcn_readfirstlane(v.z);
+        len = __builtin_amdgcn_readfirstlane(v.w);
     } else {
         c0 = i * m.nc;
         n = m.nc;
+        t0 = (int64_t)i * m.T;
+        len = m.T;
     }
 }
 
@@ -107,7 +115,7 @@ __device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n
 // an invalid stream gives wrong chunks but no access out of bounds.
 constexpr int kMapThreads = 1024;
 __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restrict__ seq_idx, int2 *__restrict__ range,
-                                                         int2 *__restrict__ chain, int2 *__restrict__ cmap, int T,
+                                                         int4 *__restrict__ chain, int2 *__restrict__ cmap, int T,
                                                          int nseq, int ncmax)
 {
     __shared__ int wsum[kMapThreads / 64], base;
@@ -142,7 +150,7 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
         const int c0 = before + s - n;
         if (i < nseq) {
             const int lo = c0 < ncmax ? c0 : ncmax;
-            chain[i] = int2{lo, c0 + n <= ncmax ? n : ncmax - lo};
+            chain[i] = int4{lo, c0 + n <= ncmax ? n : ncmax - lo, r.x, len};
         }
         __syncthreads();
         if (tid == kMapThreads - 1) base = before + s;
@@ -150,7 +158,8 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
     }
     // one wave per segment writes its chunks
     for (int i = wv; i < nseq; i += kMapThreads / 64) {
-        const int2 r = range[i], ch = chain[i];
+        const int2 r = range[i];
+        const int4 ch = chain[i];
         for (int j = lane; j < ch.y; j += 64) {
             const int left = r.y - r.x - j * kC;
             cmap[ch.x + j] = int2{r.x + j * kC, left < kC ? left : kC};
@@ -171,12 +180,20 @@ __device__ __forceinline__ int slot_row(int g, int j) { return j < 4 ? 4 * g + j
 __device__ __forceinline__ int lower_block(int b, int kb) { return b < 2 ? b : 2 + 2 * (b - 2) + kb; }
 __device__ __forceinline__ int upper_block(int b, int kb) { return b < 2 ? 2 * b + kb : 4 + (b - 2); }
 
-// Two accumulators (32 rows of 16 columns) as a second operand, hi + lo.
+// Two accumulators (32 rows of 16 columns) as a second operand, hi + lo: both
+// rounded to nearest even, the remainder x - hi exact in fp32.  Pairwise, so that one
+// conversion serves the operand and the remainder.
 __device__ __forceinline__ void split_pair(const floatx4 &a, const floatx4 &b, bf16x8 &hi, bf16x8 &lo)
 {
-    const floatx8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    hi = __builtin_convertvector(v, bf16x8);   // nearest even; the remainder is exact in fp32
-    lo = __builtin_convertvector(v - __builtin_convertvector(hi, floatx8), bf16x8);
+    uint32_t h[4], o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+        h[i] = pack_bf16x2(x, y);
+        o[i] = pack_bf16x2(x - __uint_as_float(h[i] << 16), y - __uint_as_float(h[i] & 0xffff0000u));
+    }
+    hi = __builtin_bit_cast(bf16x8, uint4{h[0], h[1], h[2], h[3]});
+    lo = __builtin_bit_cast(bf16x8, uint4{o[0], o[1], o[2], o[3]});
 }
 __device__ __forceinline__ void split_pair(const floatx4 &a, const floatx4 &b, floatx8 &hi, floatx8 &)
 {
@@ -254,11 +271,11 @@ __global__ __launch_bounds__(kThreads) void k_gdr_frags(const E *__restrict__ k,
     }
 }
 
-// Elements of one (chunk, head) of the prepared triangles: N (its planes), Gam o
-// Q K^T rounded; for the backward also N^T and (Gam o Q K^T)^T (their planes).
+// Elements of one (chunk, head) of the prepared triangles: N (its planes) and Gam o
+// Q K^T rounded; for the backward N, N^T and (Gam o Q K^T)^T (their planes).
 template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 {
-    return 512 * kTri * (bwd ? 3 * kPlanes<E> + 1 : kPlanes<E> + 1);
+    return 512 * kTri * (bwd ? 3 * kPlanes<E> : kPlanes<E> + 1);
 }
 
 // Everything of one chunk and head that no state enters.  One wave per block of
@@ -303,18 +320,22 @@ __global__ __launch_bounds__(kThreads) void k_gdr_prep(const E *__restrict__ kq,
         const double last = __shfl(s, 63);
         float *vo = vec + unit * kVec;
         const float hi = (float)s;
-        vo[kSince + lane] = exp2_((float)(s * kLog2eD));
+        const float since = exp2_((float)(s * kLog2eD)), till = exp2_((float)((last - s) * kLog2eD));
+        vo[kSince + lane] = since;
         vo[kBeta + lane] = bv;
-        vo[kTill + lane] = exp2_((float)((last - s) * kLog2eD));
+        vo[kScaled + lane] = scale * since;
+        vo[kTillBeta + lane] = till * bv;
+        vo[kTill + lane] = till;
+        vo[kErase + lane] = -bv * since;
         vo[kCsHi + lane] = hi;
         vo[kCsLo + lane] = (float)(s - (double)hi);
-        vo[5 * kC + lane] = 0.f;
     }
     __syncthreads();
     const E *kf = kq + ((int64_t)c * G + h / (H / G)) * (BWD ? 4 : 3) * kMat, *qf = kf + 2 * kMat;
     E *tri_o = tri + unit * tri_elems<E>(BWD);
     constexpr int64_t PL = 512 * kTri;
-    E *n_o = tri_o, *p_o = tri_o + kPlanes<E> * PL, *nt_o = p_o + PL, *pt_o = nt_o + kPlanes<E> * PL;
+    E *n_o = tri_o, *p_o = tri_o + kPlanes<E> * PL;
+    E *nt_o = tri_o + kPlanes<E> * PL, *pt_o = nt_o + kPlanes<E> * PL;   // backward
 
     // blocks (i, j) of K K^T and Q K^T, j <= i, with rows s and columns t
     frag_t<E> ki[NK], qi[NK];
@@ -331,24 +352,24 @@ __global__ __launch_bounds__(kThreads) void k_gdr_prep(const E *__restrict__ kq,
             for (int kb = 0; kb < NK; ++kb) {
                 const frag_t<E> kj = load_frag(kf + (j * NK + kb) * 512 + 8 * lane);
                 mma(a, kj, ki[kb]);
-                mma(p, kj, qi[kb]);
                 if (BWD) mma(pt, qi[kb], kj);
+                else mma(p, kj, qi[kb]);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int s = 16 * j + 4 * g + r;
                 const float gam = exp2_((float)((csd[t] - csd[s]) * kLog2eD));
                 a[r] = s < t ? gam * a[r] : 0.f;
-                p[r] = s <= t ? scale * gam * p[r] : 0.f;
-                if (BWD) {   // rows t, columns s
+                if (!BWD) p[r] = s <= t ? scale * gam * p[r] : 0.f;
+                else {   // rows t, columns s
                     const int tt = 16 * i + 4 * g + r, ss = 16 * j + l;
                     pt[r] = ss <= tt ? scale * exp2_((float)((csd[tt] - csd[ss]) * kLog2eD)) * pt[r] : 0.f;
                 }
             }
             *reinterpret_cast<floatx4 *>(&A[t * LD + 16 * j + 4 * g]) = a;
         }
-        store_round4(p_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), p);
-        if (BWD) store_split4(pt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, pt);
+        if (!BWD) store_round4(p_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), p);
+        else store_split4(pt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, pt);
     }
     __syncthreads();
     {
@@ -450,21 +471,37 @@ __device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], i
     }
 }
 
-// The state's columns as rows of [n][Pp] (p contiguous) in E: the state's operand,
-// read as a first operand, is its transpose, and a product with rows of the
-// identity moves it to accumulators exactly.
-template <typename E, int NB>
-__device__ __forceinline__ void store_state_rows(E *dst, const frag_t<E> (&hi)[NB / 2], int p0, int Pp, int lane)
+// Rows of the identity as a second operand: slot row (g, j) of a 32-row block against
+// column 16 HALF + l.  An operand read as a first operand is its transpose; a product
+// with these moves it to accumulators, exactly, with rows and columns exchanged.  That
+// is how tiles enter and leave a chain with four consecutive elements per lane instead
+// of one (4 accesses of 8 bytes instead of 16 of 2).
+template <typename E> struct Select {
+    frag_t<E> half[2];
+    __device__ __forceinline__ void init(int lane)
+    {
+        const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) half[h][j] = from_float<E>(slot_row(g, j) == 16 * h + l ? 1.f : 0.f);
+    }
+};
+// Where lane (g, l) puts four consecutive columns p0 + 4 g .. + 3 of row l of row block
+// `b` of a matrix kept as operand blocks with its Pp columns as slots (in order, 8 per
+// lane): one wave's 16 x 16 piece is 512 contiguous bytes of bf16.
+__device__ __forceinline__ int64_t piece(int b, int p0, int Pp, int g, int l)
 {
-    const int g = lane >> 4, l = lane & 15;
+    return ((int64_t)(b * (Pp >> 5) + (p0 >> 5)) * 64 + l + 16 * (((p0 & 31) >> 3) + (g >> 1))) * 8 + 4 * (g & 1);
+}
+template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *dst, const frag_t<E> (&f)[NF],
+                                                                           const Select<E> &sel, int p0, int Pp, int lane)
+{
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        frag_t<E> sel;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sel[j] = from_float<E>(slot_row(g, j) == 16 * (nb & 1) + l ? 1.f : 0.f);
+    for (int b = 0; b < 2 * NF; ++b) {
         floatx4 d = floatx4{0, 0, 0, 0};
-        mma(d, hi[nb >> 1], sel);
-        store_round4(dst + (int64_t)(16 * nb + l) * Pp + p0 + 4 * g, d);
+        mma(d, f[b >> 1], sel.half[b & 1]);
+        store_round4(dst + piece(b, p0, Pp, lane >> 4, lane & 15), d);
     }
 }
 
@@ -489,24 +526,56 @@ template <typename E> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsr
 {
     return make_rsrc(base, ((count - 1) * ld + P) * (int64_t)sizeof(E));
 }
-// The lane's 16 elements of a [64 tokens][16 columns] tile: token 16 tb + 4 g + r,
-// column p (off: kOffNone for a column past P).
+// A [64 tokens][16 columns] tile of a caller's tensor: lane (g, l) moves columns
+// 4 g .. 4 g + 3 of token 16 tb + l (`off`: byte offset of column p0 + 4 g, kOffNone past P).
+template <typename E> struct Tile {
+    typedef E vec __attribute__((ext_vector_type(4)));
+    vec x[4];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, int l)
+    {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const uint32_t o = off + (16 * tb + l) * ld;
+            if constexpr (sizeof(E) == 2)
+                x[tb] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b64(rs, o, 0, 0));
+            else x[tb] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+        }
+    }
+    // to accumulators: rows t = 16 tb + 4 g + r, column p0 + l
+    __device__ __forceinline__ void rows(floatx4 (&o)[4], const Select<E> &sel) const
+    {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            frag_t<E> f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[j] = x[tb][j];
+                f[4 + j] = from_float<E>(0.f);
+            }
+            o[tb] = floatx4{0, 0, 0, 0};
+            mma(o[tb], f, sel.half[0]);
+        }
+    }
+};
 template <typename E>
-__device__ __forceinline__ void load_tile(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, E (&x)[16], int g)
+__device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, const floatx4 (&x)[4],
+                                           const Select<E> &sel, int l)
 {
+    const frag_t<E> f[2] = {round_pair<E>(x[0], x[1]), round_pair<E>(x[2], x[3])};
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[4 * tb + r] = bload_elem<E>(rs, off + (16 * tb + 4 * g + r) * ld);
-}
-template <typename E>
-__device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t ld, uint32_t off, const floatx4 (&x)[4], int g)
-{
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            bstore_elem<E>(rs, off + (16 * tb + 4 * g + r) * ld, from_float<E>(x[tb][r]));
+    for (int tb = 0; tb < 4; ++tb) {
+        floatx4 d = floatx4{0, 0, 0, 0};
+        mma(d, f[tb >> 1], sel.half[tb & 1]);
+        const uint32_t o = off + (16 * tb + l) * ld;
+        if constexpr (sizeof(E) == 2) {
+            const uint2 v = uint2{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])};
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(__attribute__((__vector_size__(8))) unsigned int, v),
+                                                  rs, o, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(__attribute__((__vector_size__(16))) unsigned int, d), rs, o, 0, 0);
+        }
+    }
 }
 
 __device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
@@ -514,22 +583,26 @@ __device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_ca
 // ---- operands of a chain's step, staged through LDS ----
 // The waves of a workgroup own different columns and read the same first operands, 44
 // to 72 KB a step at N = 128.  They come straight from memory into LDS (16 bytes per
-// lane, no registers), in two regions: while a step computes from one, the other one's
-// next contents are in flight.  Phase 1 of a step reads what meets the entering state
-// (K, and Q or the pair matrix), phase 2 the rest.  One barrier before each phase says
-// both that its operands are there and that the other region is free.  Larger sets (fp32
-// at N = 256) do not fit 160 KB and are read from global memory by every wave.
+// lane, no registers), in two regions: phase 1 of a step reads what meets the entering
+// state (K, and Q or the pair matrix), phase 2 the rest.
+//   FLOW 1: while a phase computes from one region, the other one's next contents are
+//   in flight; one barrier before each phase says both that its operands are there and
+//   that the other region is free.
+//   FLOW 2: both regions twice (where 160 KB hold them); a whole step's operands are in
+//   flight while the step before it computes, with one barrier a step.
+//   FLOW 0: larger sets (fp32 at N = 256) are read from global memory by every wave.
 template <typename E, int NT> constexpr bool kStaged = sizeof(E) * NT <= 512;
+template <typename E, int NT> constexpr bool kTwice = sizeof(E) * NT <= 256;
 
 // KIND 0: the forward (y), 1: the forward for the backward (S and U), 2: the backward
-template <typename E, int NB, int KIND> struct Regions {
+template <typename E, int NB, int KIND, int FLOW> struct Regions {
     static constexpr int kMat = 4 * NB / 2;   // blocks of K, K^T, Q or Q^T (64 x NT)
     static constexpr int kN = kTri * kPlanes<E>;
     // phase 1: K | Q (KIND 0) or the transposed pair matrix (KIND 2)
     static constexpr int kOne = kMat + (KIND == 0 ? kMat : KIND == 2 ? kN : 0);
     // phase 2: N or N^T | the pair matrix (KIND 0) | K^T | Q^T (KIND 2)
     static constexpr int kTwo = kN + (KIND == 0 ? kTri : 0) + kMat + (KIND == 2 ? kMat : 0);
-    static constexpr int kBytes = kStaged<E, 16 * NB> ? (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * 1024 : 16;
+    static constexpr int kBytes = FLOW ? FLOW * (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVec * 4 : 16;
 };
 
 typedef __attribute__((address_space(1))) const void *gptr_t;
@@ -549,29 +622,26 @@ template <typename E, int n> __device__ __forceinline__ void stage(const E *src,
                                                  0, 0);
     }
 }
-// Every load of this wave has arrived; then the workgroup meets.
-__device__ __forceinline__ void arrive()
-{
-    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
-    __syncthreads();
-}
+// This wave's loads have arrived.  Called before a step's stores are issued, so that
+// the next barrier does not wait for them.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
 
-// A step's operand pointers: in LDS at fixed places, or in memory.
-template <typename E, int NB, int KIND> struct Operands {
-    using R = Regions<E, NB, KIND>;
+// A step's operand pointers: in LDS, or in memory.
+template <typename E, int NB, int KIND, int FLOW> struct Operands {
+    using R = Regions<E, NB, KIND, FLOW>;
     static constexpr int kMatE = kC * 16 * NB;
-    static constexpr bool LDS = kStaged<E, 16 * NB>;
+    static constexpr bool LDS = FLOW != 0;
     E *one, *two;
     float *vecs;
     const E *kq, *tri;
     const float *vec;
-    int wv, lane, turn;
+    int wv, lane, turn;   // turn: which copy of what is kept twice is being staged
 
     __device__ __forceinline__ void init(char *smem, int wv_, int lane_)
     {
         one = reinterpret_cast<E *>(smem);
-        two = one + R::kOne * 512;
-        vecs = reinterpret_cast<float *>(two + R::kTwo * 512);
+        two = one + (FLOW == 2 ? 2 : 1) * R::kOne * 512;
+        vecs = reinterpret_cast<float *>(two + (FLOW == 2 ? 2 : 1) * R::kTwo * 512);
         wv = wv_;
         lane = lane_;
         turn = 0;
@@ -584,23 +654,28 @@ template <typename E, int NB, int KIND> struct Operands {
         tri = (const E *)a.tri + u * tri_elems<E>(KIND != 0);
         vec = a.vec + u * kVec;
     }
-    // N | Gam QK^T | N^T | (Gam QK^T)^T in `tri`; K | K^T | Q | Q^T in `kq`
-    static constexpr int kPL = 512 * kTri, kNt = (kPlanes<E> + 1) * kPL, kPt = (2 * kPlanes<E> + 1) * kPL;
+    // in `tri`: N | Gam QK^T, or N | N^T | (Gam QK^T)^T; in `kq`: K | K^T | Q | Q^T
+    static constexpr int kPL = 512 * kTri, kNt = kPlanes<E> * kPL, kPt = 2 * kPlanes<E> * kPL;
+    __device__ __forceinline__ E *one_at(int t) const { return one + (FLOW == 2 ? t * R::kOne * 512 : 0); }
+    __device__ __forceinline__ E *two_at(int t) const { return two + (FLOW == 2 ? t * R::kTwo * 512 : 0); }
     __device__ __forceinline__ void stage_one()
     {
         if constexpr (LDS) {
-            stage<E, R::kMat>(kq, one, wv, lane);
-            if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, one + kMatE, wv, lane);
-            if (KIND == 2) stage<E, R::kN>(tri + kPt, one + kMatE, wv, lane);
-            if (wv == 3)
-                __builtin_amdgcn_global_load_lds((gptr_t)(vec + 4 * lane), (lptr_t)(vecs + 256 * turn), 16, 0, 0);
+            E *o = one_at(turn);
+            stage<E, R::kMat>(kq, o, wv, lane);
+            if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, o + kMatE, wv, lane);
+            if (KIND == 2) stage<E, R::kN>(tri + kPt, o + kMatE, wv, lane);
+            if (wv >= 2)   // kVec floats: two loads
+                __builtin_amdgcn_global_load_lds((gptr_t)(vec + 256 * (wv - 2) + 4 * lane),
+                                                 (lptr_t)(vecs + kVec * turn + 256 * (wv - 2)), 16, 0, 0);
         }
     }
     __device__ __forceinline__ void stage_two()
     {
         if constexpr (LDS) {
-            stage<E, R::kN>(tri + (KIND == 2 ? kNt : 0), two, wv, lane);
-            E *o = two + R::kN * 512;
+            E *o = two_at(turn);
+            stage<E, R::kN>(tri + (KIND == 2 ? kNt : 0), o, wv, lane);
+            o += R::kN * 512;
             if (KIND == 0) {
                 stage<E, kTri>(tri + kPlanes<E> * kPL, o, wv, lane);
                 o += kTri * 512;
@@ -609,60 +684,81 @@ template <typename E, int NB, int KIND> struct Operands {
             if (KIND == 2) stage<E, R::kMat>(kq + 3 * kMatE, o + kMatE, wv, lane);
         }
     }
-    __device__ __forceinline__ const E *k() const { return (LDS ? one : kq) + 8 * lane; }
-    __device__ __forceinline__ const E *q() const { return (LDS ? one + kMatE : kq + 2 * kMatE) + 8 * lane; }
-    __device__ __forceinline__ const E *pt() const { return (LDS ? one + kMatE : tri + kPt) + 8 * lane; }
-    __device__ __forceinline__ const E *n() const { return (LDS ? two : tri + (KIND == 2 ? kNt : 0)) + 8 * lane; }
-    __device__ __forceinline__ const E *p() const { return (LDS ? two + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane; }
-    __device__ __forceinline__ const E *kt() const
+    // the operands of the step whose turn is t
+    __device__ __forceinline__ const E *k(int t) const { return (LDS ? one_at(t) : kq) + 8 * lane; }
+    __device__ __forceinline__ const E *q(int t) const { return (LDS ? one_at(t) + kMatE : kq + 2 * kMatE) + 8 * lane; }
+    __device__ __forceinline__ const E *pt(int t) const { return (LDS ? one_at(t) + kMatE : tri + kPt) + 8 * lane; }
+    __device__ __forceinline__ const E *n(int t) const { return (LDS ? two_at(t) : tri + (KIND == 2 ? kNt : 0)) + 8 * lane; }
+    __device__ __forceinline__ const E *p(int t) const
     {
-        return (LDS ? two + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
+        return (LDS ? two_at(t) + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane;
     }
-    __device__ __forceinline__ const E *qt() const { return (LDS ? two + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane; }
-    __device__ __forceinline__ const float *scalars() const { return LDS ? vecs + 256 * turn : vec; }
+    __device__ __forceinline__ const E *kt(int t) const
+    {
+        return (LDS ? two_at(t) + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
+    }
+    __device__ __forceinline__ const E *qt(int t) const
+    {
+        return (LDS ? two_at(t) + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane;
+    }
+    __device__ __forceinline__ const float *scalars(int t) const { return LDS ? vecs + kVec * t : vec; }
 };
 
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
 // and not y.
-template <typename E, int NB, bool KEEP>
+template <typename E, int NB, bool KEEP, int FLOW>
 __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *smem)
 {
-    constexpr int NT = 16 * NB, NK = NT / 32, KIND = KEEP ? 1 : 0;
-    constexpr int PL = 512 * kTri;
+    constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
-    const int p0 = ptile * kC + 16 * wv, p = p0 + l;
-    const bool on = p < a.P, keep = p0 < a.Pp;
-    int c0, n;
-    chain_at(a.m, ch, c0, n);
-    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
+    const int p0 = ptile * kC + 16 * wv;
+    const bool keep = p0 < a.Pp;
+    int c0, n, len;
+    int64_t t0;
+    chain_at(a.m, ch, c0, n, t0, len);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N, ld = (int64_t)a.H * a.P;
     floatx4 S[NB];
-    load_state<E, NB>(a.s0 ? a.s0 + so : nullptr, S, p, g, a.P, a.N);
-    const int64_t ld = (int64_t)a.H * a.P;
-    const uint32_t ldb = (uint32_t)ld * sizeof(E), pldb = a.Pp * sizeof(E);
-    const uint32_t poff = on ? p * sizeof(E) : kOffNone, koff = keep ? p * sizeof(E) : kOffNone;
+    load_state<E, NB>(a.s0 ? a.s0 + so : nullptr, S, p0 + l, g, a.P, a.N);
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), poff = p0 < a.P ? (p0 + 4 * g) * sizeof(E) : kOffNone;
     const int grp = h / (a.H / a.G);
-    Operands<E, NB, KIND> op;
+    auto rows_of = [&](const void *base, int i) {   // the head's rows of the chain's chunk i
+        const int left = len - i * kC;
+        return rows_rsrc((const E *)base + ((t0 + i * kC) * a.H + h) * a.P, left < kC ? left : kC, ld, a.P);
+    };
+    Select<E> sel;
+    sel.init(lane);
+    Operands<E, NB, KEEP ? 1 : 0, FLOW> op;
     op.init(smem, wv, lane);
-    int64_t t0 = 0;
-    int count = 0;
-    E v[16];
+    Tile<E> v;
     if (n > 0) {
-        chunk_at(a.m, c0, t0, count);
         op.at(a, c0, h, grp);
         op.stage_one();
-        load_tile<E>(rows_rsrc((const E *)a.v + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, v, g);
+        if (FLOW == 2) op.stage_two();
+        v.load(rows_of(a.v, 0), ldb, poff, l);
     }
-    for (int c = c0; c < c0 + n; ++c) {
-        const int64_t u = (int64_t)c * a.H + h;
-        if (Operands<E, NB, KIND>::LDS) arrive();
-        op.stage_two();
-        const float *vec = op.scalars();
+    for (int i = 0; i < n; ++i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        const int turn = op.turn;
+        if (FLOW) {
+            if (i == 0) loads_done();
+            __syncthreads();
+        }
+        if (FLOW == 1) op.stage_two();
+        floatx4 R[4], X[4];
+        v.rows(R, sel);
+        if (FLOW == 2 && i + 1 < n) {
+            op.at(a, c0 + i + 1, h, grp);
+            op.turn ^= 1;
+            op.stage_one();
+            op.stage_two();
+            v.load(rows_of(a.v, i + 1), ldb, poff, l);
+        }
+        const float *vec = op.scalars(turn);
         StateOps<E, NB> so_;
         so_.of(S);
-        if (KEEP && keep) store_state_rows<E, NB>((E *)a.sst + u * NT * a.Pp, so_.hi, p0, a.Pp, lane);
         floatx4 ks[4], qs[4];
-        const E *kf = op.k(), *qf = op.q();
+        const E *kf = op.k(turn), *qf = op.q(turn);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
 #pragma unroll
@@ -674,30 +770,27 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 if (kPlanes<E> == 2) mma(ks[tb], f, so_.lo[kb]);
                 if (!KEEP) mma(qs[tb], load_frag(qf + (tb * NK + kb) * 512), so_.hi[kb]);
             }
-        floatx4 since[4], bt[4], R[4], X[4];
+        floatx4 bt[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            since[tb] = vec4(vec + kSince + 16 * tb + 4 * g);
             bt[tb] = vec4(vec + kBeta + 16 * tb + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[tb][r] = to_float(v[4 * tb + r]) - since[tb][r] * ks[tb][r];
+            R[tb] -= vec4(vec + kSince + 16 * tb + 4 * g) * ks[tb];
             X[tb] = bt[tb] * R[tb];
         }
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
-        if (Operands<E, NB, KIND>::LDS) arrive();
-        const int64_t yt0 = t0;
-        const int ycount = count;
-        const E *nf = op.n(), *pf = op.p(), *ktf = op.kt();
-        if (c + 1 < c0 + n) {
-            chunk_at(a.m, c + 1, t0, count);
-            op.at(a, c + 1, h, grp);
+        if (FLOW == 1) {
+            loads_done();
+            __syncthreads();
+        }
+        const E *nf = op.n(turn), *pf = op.p(turn), *ktf = op.kt(turn);
+        if (FLOW != 2 && i + 1 < n) {
+            op.at(a, c0 + i + 1, h, grp);
             op.turn ^= 1;
             op.stage_one();
-            load_tile<E>(rows_rsrc((const E *)a.v + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, v, g);
+            v.load(rows_of(a.v, i + 1), ldb, poff, l);
         }
-        floatx4 W[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             floatx4 d = floatx4{0, 0, 0, 0};
@@ -711,25 +804,16 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 }
             }
             R[tb] -= d;   // U
-            W[tb] = bt[tb] * R[tb];
+            X[tb] = vec4(vec + kTillBeta + 16 * tb + 4 * g) * R[tb];
         }
-        if (KEEP) {
-            store_tile<E>(rows_rsrc((E *)a.ust + u * kC * a.Pp, kC, a.Pp, a.Pp), pldb, koff, R, g);
-        } else {
-            const frag_t<E> w0 = round_pair<E>(W[0], W[1]), w1 = round_pair<E>(W[2], W[3]);
-            floatx4 y[4];
+        // beta U for y, or U itself for the backward
+        frag_t<E> w[2];
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                y[tb] = (a.scale * since[tb]) * qs[tb];
-                mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w0);
-                if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w1);
-            }
-            store_tile<E>(rows_rsrc((E *)a.y + (yt0 * a.H + h) * a.P, ycount, ld, a.P), ldb, poff, y, g);
-        }
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
-        split_pair(W[0], W[1], xh[0], xl[0]);
-        split_pair(W[2], W[3], xh[1], xl[1]);
+        for (int j = 0; j < 2; ++j)
+            w[j] = KEEP ? round_pair<E>(R[2 * j], R[2 * j + 1])
+                        : round_pair<E>(bt[2 * j] * R[2 * j], bt[2 * j + 1] * R[2 * j + 1]);
+        split_pair(X[0], X[1], xh[0], xl[0]);
+        split_pair(X[2], X[3], xh[1], xl[1]);
         const float whole = vec[kSince + kC - 1];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] *= whole;
@@ -741,57 +825,83 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 mma(S[nb], f, xh[kb]);
                 if (kPlanes<E> == 2) mma(S[nb], f, xl[kb]);
             }
+        if (KEEP) {
+            if (FLOW) loads_done();
+            if (keep) {
+                store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, a.Pp, lane);
+                store_pieces<E>((E *)a.ust + u * kC * a.Pp, w, sel, p0, a.Pp, lane);
+            }
+        } else {
+            floatx4 y[4];
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                y[tb] = vec4(vec + kScaled + 16 * tb + 4 * g) * qs[tb];
+                mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w[0]);
+                if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w[1]);
+            }
+            if (FLOW) loads_done();
+            store_tile<E>(rows_of(a.y, i), ldb, poff, y, sel, l);
+        }
     }
-    save_state<NB>(a.s1 ? a.s1 + so : nullptr, S, p, g, a.P, a.N);
+    save_state<NB>(a.s1 ? a.s1 + so : nullptr, S, p0 + l, g, a.P, a.N);
 }
 
 // One backward chain: D of every chunk (the gradient of the state that leaves it),
 // H, and dv.
-template <typename E, int NB>
+template <typename E, int NB, int FLOW>
 __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *smem)
 {
-    constexpr int NT = 16 * NB, NK = NT / 32;
-    constexpr int PL = 512 * kTri;
+    constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
-    const int p0 = ptile * kC + 16 * wv, p = p0 + l;
-    const bool on = p < a.P, keep = p0 < a.Pp;
-    int c0, n;
-    chain_at(a.m, ch, c0, n);
-    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N;
+    const int p0 = ptile * kC + 16 * wv;
+    const bool keep = p0 < a.Pp;
+    int c0, n, len;
+    int64_t t0;
+    chain_at(a.m, ch, c0, n, t0, len);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N, ld = (int64_t)a.H * a.P;
     floatx4 D[NB];
-    load_state<E, NB>(a.d1 ? a.d1 + so : nullptr, D, p, g, a.P, a.N);
-    const int64_t ld = (int64_t)a.H * a.P;
-    const uint32_t ldb = (uint32_t)ld * sizeof(E), pldb = a.Pp * sizeof(E);
-    const uint32_t poff = on ? p * sizeof(E) : kOffNone, koff = keep ? p * sizeof(E) : kOffNone;
+    load_state<E, NB>(a.d1 ? a.d1 + so : nullptr, D, p0 + l, g, a.P, a.N);
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), poff = p0 < a.P ? (p0 + 4 * g) * sizeof(E) : kOffNone;
     const int grp = h / (a.H / a.G);
-    Operands<E, NB, 2> op;
+    auto rows_of = [&](const void *base, int i) {
+        const int left = len - i * kC;
+        return rows_rsrc((const E *)base + ((t0 + i * kC) * a.H + h) * a.P, left < kC ? left : kC, ld, a.P);
+    };
+    Select<E> sel;
+    sel.init(lane);
+    Operands<E, NB, 2, FLOW> op;
     op.init(smem, wv, lane);
-    int64_t t0 = 0;
-    int count = 0;
-    E dy[16];
+    Tile<E> dy;
     if (n > 0) {
-        chunk_at(a.m, c0 + n - 1, t0, count);
         op.at(a, c0 + n - 1, h, grp);
         op.stage_one();
-        load_tile<E>(rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, dy, g);
+        if (FLOW == 2) op.stage_two();
+        dy.load(rows_of(a.dy, n - 1), ldb, poff, l);
     }
-    for (int c = c0 + n - 1; c >= c0; --c) {
-        const int64_t u = (int64_t)c * a.H + h;
-        if (Operands<E, NB, 2>::LDS) arrive();
-        op.stage_two();
-        const float *vec = op.scalars();
+    for (int i = n - 1; i >= 0; --i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        const int turn = op.turn;
+        if (FLOW) {
+            if (i == n - 1) loads_done();
+            __syncthreads();
+        }
+        if (FLOW == 1) op.stage_two();
+        floatx4 yt[4];
+        dy.rows(yt, sel);
+        if (FLOW == 2 && i > 0) {
+            op.at(a, c0 + i - 1, h, grp);
+            op.turn ^= 1;
+            op.stage_one();
+            op.stage_two();
+            dy.load(rows_of(a.dy, i - 1), ldb, poff, l);
+        }
+        const float *vec = op.scalars(turn);
         StateOps<E, NB> dop;
         dop.of(D);
-        if (keep) store_state_rows<E, NB>((E *)a.dst + u * NT * a.Pp, dop.hi, p0, a.Pp, lane);
-        floatx4 yt[4];
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) yt[tb][r] = to_float(dy[4 * tb + r]);
         const frag_t<E> y0 = round_pair<E>(yt[0], yt[1]), y1 = round_pair<E>(yt[2], yt[3]);   // exact
-        const E *kf = op.k(), *ptf = op.pt();
-        floatx4 W[4], X[4], bt[4], since[4];
+        const E *kf = op.k(turn), *ptf = op.pt(turn);
+        floatx4 W[4], X[4], bt[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) W[tb] = floatx4{0, 0, 0, 0};
 #pragma unroll
@@ -806,7 +916,6 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
         for (int tb = 0; tb < 4; ++tb) {
             W[tb] *= vec4(vec + kTill + 16 * tb + 4 * g);
             bt[tb] = vec4(vec + kBeta + 16 * tb + 4 * g);
-            since[tb] = vec4(vec + kSince + 16 * tb + 4 * g);
 #pragma unroll
             for (int kb = tb / 2; kb < 2; ++kb)
 #pragma unroll
@@ -817,25 +926,23 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
-        if (Operands<E, NB, 2>::LDS) arrive();
-        const int64_t yt0 = t0;
-        const int ycount = count;
-        const E *nt = op.n(), *ktf = op.kt(), *qtf = op.qt();
-        if (c > c0) {
-            chunk_at(a.m, c - 1, t0, count);
-            op.at(a, c - 1, h, grp);
+        if (FLOW == 1) {
+            loads_done();
+            __syncthreads();
+        }
+        const E *nt = op.n(turn), *ktf = op.kt(turn), *qtf = op.qt(turn);
+        if (FLOW != 2 && i > 0) {
+            op.at(a, c0 + i - 1, h, grp);
             op.turn ^= 1;
             op.stage_one();
-            load_tile<E>(rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, ld, a.P), ldb, poff, dy, g);
+            dy.load(rows_of(a.dy, i - 1), ldb, poff, l);
         }
         const float whole = vec[kSince + kC - 1];
         frag_t<E> yh[2], yl[2];
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) yt[tb] *= a.scale * since[tb];
+        for (int tb = 0; tb < 4; ++tb) yt[tb] *= vec4(vec + kScaled + 16 * tb + 4 * g);
         split_pair(yt[0], yt[1], yh[0], yl[0]);
         split_pair(yt[2], yt[3], yh[1], yl[1]);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) D[nb] *= whole;
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             floatx4 d = floatx4{0, 0, 0, 0};
@@ -851,12 +958,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
             W[tb] -= d;             // H
             X[tb] = bt[tb] * W[tb]; // dv
         }
-        store_tile<E>(rows_rsrc((E *)a.hst + u * kC * a.Pp, kC, a.Pp, a.Pp), pldb, koff, W, g);
-        store_tile<E>(rows_rsrc((E *)a.dv + (yt0 * a.H + h) * a.P, ycount, ld, a.P), ldb, poff, X, g);
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) X[tb] *= -since[tb];
-        split_pair(X[0], X[1], xh[0], xl[0]);
-        split_pair(X[2], X[3], xh[1], xl[1]);
+        for (int nb = 0; nb < NB; ++nb) D[nb] *= whole;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -865,6 +968,11 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
                 mma(D[nb], fq, yh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], fq, yl[kb]);
             }
+        const frag_t<E> hf[2] = {round_pair<E>(W[0], W[1]), round_pair<E>(W[2], W[3])};
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) W[tb] *= vec4(vec + kErase + 16 * tb + 4 * g);
+        split_pair(W[0], W[1], xh[0], xl[0]);
+        split_pair(W[2], W[3], xh[1], xl[1]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -873,24 +981,30 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
                 mma(D[nb], f, xh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], f, xl[kb]);
             }
+        if (FLOW) loads_done();
+        store_tile<E>(rows_of(a.dv, i), ldb, poff, X, sel, l);
+        if (keep) {
+            store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, a.Pp, lane);
+            store_pieces<E>((E *)a.hst + u * kC * a.Pp, hf, sel, p0, a.Pp, lane);
+        }
     }
-    save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p, g, a.P, a.N);
+    save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N);
 }
 
-template <typename E, int NB>
-__global__ __launch_bounds__(kThreads) void k_gdr_chain(ChainArgs a)
+template <typename E, int NB, int FLOW>
+__global__ __launch_bounds__(kThreads, 2) void k_gdr_chain(ChainArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0>::kBytes];
-    chain_fwd<E, NB, false>(a, blockIdx.x, smem);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0, FLOW>::kBytes];
+    chain_fwd<E, NB, false, FLOW>(a, blockIdx.x, smem);
 }
 
 // The backward's two chains in one launch: neither needs the other.
-template <typename E, int NB>
-__global__ __launch_bounds__(kThreads) void k_gdr_chains(ChainArgs a)
+template <typename E, int NB, int FLOW>
+__global__ __launch_bounds__(kThreads, 2) void k_gdr_chains(ChainArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2>::kBytes];   // the larger of both
-    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB>(a, blockIdx.x, smem);
-    else chain_fwd<E, NB, true>(a, blockIdx.x - a.units, smem);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2, FLOW>::kBytes];   // the larger of both
+    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, FLOW>(a, blockIdx.x, smem);
+    else chain_fwd<E, NB, true, FLOW>(a, blockIdx.x - a.units, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -989,7 +1103,7 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
             return f;
         };
         auto rowf = [&](const E *base, int row0, int kb) {
-            return load_frag(base + (int64_t)(row0 + l) * a.Pp + 32 * kb + 8 * g);
+            return load_frag(base + ((int64_t)(row0 / 16 * KP + kb) * 64 + lane) * 8);
         };
         // the pair products, in both orientations
         floatx4 wT[4], wN[4], zT[4], zN[4];
