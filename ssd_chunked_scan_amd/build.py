@@ -27,6 +27,12 @@ FLAGS = [
 ]
 
 
+# The gated delta rule's kernels hold their products' accumulators in the general
+# registers; given a whole register file the compiler would put them into the
+# accumulation registers and copy them out for every use.
+EXTRA = {"gdr_api.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
+
 def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
@@ -45,7 +51,7 @@ def build_library(verbose: bool = False, extra_flags=()) -> str:
     with tempfile.TemporaryDirectory() as obj:
         objects = [os.path.join(obj, os.path.basename(s) + ".o") for s in SOURCES]
         with ThreadPoolExecutor(len(SOURCES)) as pool:
-            jobs = [pool.submit(_run, [HIPCC, *FLAGS, *extra_flags, "-c", s, "-o", o], verbose)
+            jobs = [pool.submit(_run, [HIPCC, *FLAGS, *EXTRA.get(os.path.basename(s), []), *extra_flags, "-c", s, "-o", o], verbose)
                     for s, o in zip(SOURCES, objects)]
             for j in jobs:
                 j.result()

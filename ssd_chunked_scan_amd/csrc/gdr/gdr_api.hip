@@ -77,7 +77,8 @@ ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
     s->nct = s->packed ? s->T / kC + (s->nseq < s->T ? s->nseq : s->T) : s->b * s->nc;
     s->chains = s->packed ? s->nseq : s->b;
     s->NT = s->N <= 64 ? 64 : s->N <= 128 ? 128 : 256;
-    s->Pp = (s->P + 31) / 32 * 32;
+    const int64_t cols = a->dtype == SSD_DTYPE_BF16 ? 32 * kColBlocks<bf16> : 32 * kColBlocks<float>;
+    s->Pp = (s->P + cols - 1) / cols * cols;
     s->np = (s->Pp + kC - 1) / kC;
     // a chunk's rows of all heads or groups are addressed with 31-bit byte offsets
     if (s->H * s->P > (1 << 22) || s->G * s->N > (1 << 22)) return SSD_ERR_BAD_SHAPE;
@@ -275,7 +276,7 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
             hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, decltype(flow)::value>), dim3(2u * (unsigned)c.units),
                                dim3(kThreads), 0, st, c);
         });
-        hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kThreads), 0, st, ga);
+        hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kGradThreads), 0, st, ga);
         if (hs > 1)
             hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G)), dim3(kThreads), 0, st,
                                (const float *)ga.part, (E *)g->dq, (E *)g->dk, m, (int)s.G, (int)s.N, (int)hs);

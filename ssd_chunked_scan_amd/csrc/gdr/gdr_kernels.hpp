@@ -49,6 +49,8 @@
 // fp32 problems use the fp32 matrix instructions throughout.
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_device.hpp"
 
 namespace ssd {
@@ -435,7 +437,7 @@ struct ChainArgs {
     float *s1, *d0;              // final state, gradient of the initial state, or null
     void *sst, *ust, *dst, *hst; // backward only: S, U, D, H of every (chunk, head)
     Chunks m;
-    int H, G, P, N, Pp, np;      // Pp: P rounded up to 32; np: workgroups per head
+    int H, G, P, N, Pp, np;      // Pp: P rounded up to 32 kColBlocks; np: workgroups per head
     int units;                   // chains * H * np
     float scale;
 };
@@ -487,21 +489,26 @@ template <typename E> struct Select {
             for (int j = 0; j < 8; ++j) half[h][j] = from_float<E>(slot_row(g, j) == 16 * h + l ? 1.f : 0.f);
     }
 };
-// Where lane (g, l) puts four consecutive columns p0 + 4 g .. + 3 of row l of row block
-// `b` of a matrix kept as operand blocks with its Pp columns as slots (in order, 8 per
-// lane): one wave's 16 x 16 piece is 512 contiguous bytes of bf16.
-__device__ __forceinline__ int64_t piece(int b, int p0, int Pp, int g, int l)
+// S, U, D and H of a chunk and head are kept as operand blocks with their columns p as
+// slots (in order, 8 per lane), kColBlocks blocks of 32 columns for each row block, the
+// columns after these after all rows: what the gradient kernel takes at a time is
+// contiguous.  Where lane (g, l) puts columns p0 + 4 g .. + 3 of row l of row block b (a
+// wave's 16 x 16 piece is 512 contiguous bytes of bf16):
+template <typename E> constexpr int kColBlocks = sizeof(E) == 2 ? 2 : 1;
+template <typename E> __device__ __forceinline__ int64_t piece(int b, int rows, int p0, int g, int l)
 {
-    return ((int64_t)(b * (Pp >> 5) + (p0 >> 5)) * 64 + l + 16 * (((p0 & 31) >> 3) + (g >> 1))) * 8 + 4 * (g & 1);
+    constexpr int KB = kColBlocks<E>;
+    const int block = (p0 / (32 * KB) * rows + b) * KB + (p0 >> 5) % KB;
+    return ((int64_t)block * 64 + l + 16 * (((p0 & 31) >> 3) + (g >> 1))) * 8 + 4 * (g & 1);
 }
 template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *dst, const frag_t<E> (&f)[NF],
-                                                                           const Select<E> &sel, int p0, int Pp, int lane)
+                                                                           const Select<E> &sel, int p0, int lane)
 {
 #pragma unroll
     for (int b = 0; b < 2 * NF; ++b) {
         floatx4 d = floatx4{0, 0, 0, 0};
         mma(d, f[b >> 1], sel.half[b & 1]);
-        store_round4(dst + piece(b, p0, Pp, lane >> 4, lane & 15), d);
+        store_round4(dst + piece<E>(b, 2 * NF, p0, lane >> 4, lane & 15), d);
     }
 }
 
@@ -828,8 +835,8 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
         if (KEEP) {
             if (FLOW) loads_done();
             if (keep) {
-                store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, a.Pp, lane);
-                store_pieces<E>((E *)a.ust + u * kC * a.Pp, w, sel, p0, a.Pp, lane);
+                store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane);
+                store_pieces<E>((E *)a.ust + u * kC * a.Pp, w, sel, p0, lane);
             }
         } else {
             floatx4 y[4];
@@ -984,8 +991,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
         if (FLOW) loads_done();
         store_tile<E>(rows_of(a.dv, i), ldb, poff, X, sel, l);
         if (keep) {
-            store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, a.Pp, lane);
-            store_pieces<E>((E *)a.hst + u * kC * a.Pp, hf, sel, p0, a.Pp, lane);
+            store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, lane);
+            store_pieces<E>((E *)a.hst + u * kC * a.Pp, hf, sel, p0, lane);
         }
     }
     save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N);
@@ -1034,13 +1041,33 @@ struct GradArgs {
     float scale;
 };
 
+// One workgroup per (chunk, group, part of the group's heads), 8 waves: wave (tb, half)
+// owns 16 tokens and half of the columns n of dq and dk, in registers over all heads.
+// What a head brings (S, D, U, H and dy, 64 columns p at a time) comes into LDS as
+// operand blocks without passing through registers, for the next head while this one
+// computes where LDS holds it twice (TWICE).
+constexpr int kGradThreads = 512;
+template <typename E, int NB> struct GradPlan {
+    static constexpr int KPC = kColBlocks<E>;                   // 32-column blocks per stage
+    static constexpr int kBlocks = (2 * NB + 12) * KPC;         // S | D | U | H | dy
+    static constexpr int kStage = kBlocks * 512 * (int)sizeof(E);
+    static constexpr int kMats = 2 * 2 * NB * 512 * (int)sizeof(E);   // K^T and Q^T
+    static constexpr int kRest = 2 * kVec * 4 + 1024;
+    static constexpr bool TWICE = 2 * kStage + kMats + kRest <= 160 * 1024;
+    static constexpr bool MATS = kStage + kMats + kRest <= 160 * 1024;   // K^T and Q^T in LDS as well
+};
+
 template <typename E, int NB>
-__global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
+__global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 {
-    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT;
-    __shared__ __attribute__((aligned(16))) float vs[kVec];
-    __shared__ float dcs[kC], red[8];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+    using PL = GradPlan<E, NB>;
+    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT, KPC = PL::KPC, HB = NB / 2, V = kVec16<E>;
+    __shared__ __attribute__((aligned(16))) E stage_m[(PL::TWICE ? 2 : 1) * PL::kBlocks * 512];
+    __shared__ __attribute__((aligned(16))) E mats[PL::MATS ? 2 * kMat : 8];
+    __shared__ __attribute__((aligned(16))) float vs2[2 * kVec];
+    __shared__ float dcs[3][kC], red[16];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    const int w = wv & 3, half = wv >> 2;
     int x = blockIdx.x;
     const int sp = x % a.hsplit;
     x /= a.hsplit;
@@ -1051,167 +1078,265 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
     if (count <= 0) return;
     const int hpg = a.H / a.G;
     const int h0 = grp * hpg + (int)((int64_t)hpg * sp / a.hsplit), h1 = grp * hpg + (int)((int64_t)hpg * (sp + 1) / a.hsplit);
-    const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat + 8 * lane;
-    const E *ktf = kf + kMat, *qf = kf + 2 * kMat, *qtf = kf + 3 * kMat;
+    const int NPC = a.Pp / (32 * KPC), J = (h1 - h0) * NPC;
+    const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat;
+    const E *ktg = kf + kMat, *qf = kf + 2 * kMat, *qtg = kf + 3 * kMat;
+    const int64_t yld = (int64_t)a.H * a.P;
 
-    // q.k and k.k of the wave's 16 tokens against all (rows j, columns w)
-    floatx4 qkT[4], qkN[4], kk[4];
+    // stage j: head h0 + j / NPC, columns 32 KPC (j % NPC) ...
+    const int mine = wv * 64 * V + V * lane;
+    auto run = [&](const E *src, E *dst, auto n) {   // n blocks, 1 KiB at a time from wave to wave
+        constexpr int kParts = decltype(n)::value * 512 / (64 * V);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        qkT[j] = qkN[j] = kk[j] = floatx4{0, 0, 0, 0};
+        for (int i = 0; i < kParts; i += 8)
+            if (kParts % 8 == 0 || i + wv < kParts)
+                __builtin_amdgcn_global_load_lds((gptr_t)(src + mine + i * 64 * V), (lptr_t)(dst + (i + wv) * 64 * V), 16, 0, 0);
+    };
+    auto issue = [&](int j) {
+        const int hi = j / NPC, pc = j - hi * NPC, h = h0 + hi;
+        const int64_t u = (int64_t)c * a.H + h;
+        E *dst = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kBlocks * 512;
+        const int64_t so = u * NT * a.Pp + pc * (NB * KPC * 512), uo = u * kC * a.Pp + pc * (4 * KPC * 512);
+        using BS = std::integral_constant<int, NB * KPC>;
+        using BU = std::integral_constant<int, 4 * KPC>;
+        run((const E *)a.sst + so, dst, BS{});
+        run((const E *)a.dst + so, dst + NB * KPC * 512, BS{});
+        dst += 2 * NB * KPC * 512;
+        run((const E *)a.ust + uo, dst, BU{});
+        run((const E *)a.hst + uo, dst + 4 * KPC * 512, BU{});
+        dst += 8 * KPC * 512;
+        // dy, 8 KiB, a KiB per wave.  Rows past the count and columns past P: any element of
+        // the row's own data (masked below; columns past P meet zeros of S, U and H)
+        {
+            const int r = mine / (512 * KPC), kk = mine / 512 % KPC, e = mine % 512;
+            const int t = 16 * r + (e >> 3) % 16, pp = 32 * (pc * KPC + kk) + 8 * (e >> 7) + (e & 7);
+            const E *dy = (const E *)a.dy + (t0 * a.H + h) * a.P;
+            __builtin_amdgcn_global_load_lds((gptr_t)(dy + (int64_t)(t < count ? t : count - 1) * yld + (pp < a.P ? pp : 0)),
+                                             (lptr_t)(dst + wv * 64 * V), 16, 0, 0);
+        }
+        if (pc == 0 && wv >= 6)
+            __builtin_amdgcn_global_load_lds((gptr_t)(a.vec + u * kVec + 256 * (wv - 6) + 4 * lane),
+                                             (lptr_t)(vs2 + (hi & 1) * kVec + 256 * (wv - 6)), 16, 0, 0);
+    };
+    issue(0);
+    if constexpr (PL::MATS) {
+        constexpr int n = 2 * kMat * (int)sizeof(E) / 1024;   // K^T and Q^T, 1 KiB each
+        static_assert(n % 16 == 0, "whole rounds");
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-            const frag_t<E> kj = load_frag(kf + (j * NK + kb) * 512), kw = load_frag(kf + (w * NK + kb) * 512);
-            mma(kk[j], kj, kw);
-            if (j <= w) mma(qkT[j], kj, load_frag(qf + (w * NK + kb) * 512));   // rows s, columns t
-            if (j >= w) mma(qkN[j], load_frag(qf + (j * NK + kb) * 512), kw);   // rows t, columns s
+        for (int i = 0; i < n / 8; ++i) {
+            const int b = 8 * i + wv, e = b * 64 * V;
+            const E *src = e < kMat ? ktg + e : qtg + (e - kMat);
+            __builtin_amdgcn_global_load_lds((gptr_t)(src + V * lane), (lptr_t)(mats + e), 16, 0, 0);
         }
     }
-    // the wave's q and k rows in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
-    E qe[NB][4], ke[NB][4];
+    const E *ktf = (PL::MATS ? mats : ktg) + 8 * lane, *qtf = (PL::MATS ? mats + kMat : qtg) + 8 * lane;
+
+    // The pair matrices of the wave's 16 tokens: block i holds rows of block i against
+    // columns of block w, as (s, t) pairs where i <= w and as (t, s) pairs where i > w; the
+    // diagonal block is needed both ways (the D arrays: as (t, s)).
+    floatx4 qk[4], kk[4], qkD = floatx4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qk[i] = kk[i] = floatx4{0, 0, 0, 0};
+    if (half == 0)
+        for (int kb = 0; kb < NK; ++kb) {
+            const frag_t<E> kw = load_frag(kf + (w * NK + kb) * 512 + 8 * lane), qw = load_frag(qf + (w * NK + kb) * 512 + 8 * lane);
+            mma(qkD, qw, kw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const frag_t<E> ki = load_frag(kf + (i * NK + kb) * 512 + 8 * lane);
+                mma(kk[i], ki, kw);
+                if (i <= w) mma(qk[i], ki, qw);
+                else mma(qk[i], load_frag(qf + (i * NK + kb) * 512 + 8 * lane), kw);
+            }
+        }
+    // the wave's q and k in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
+    // (packed in pairs, for the registers)
+    constexpr int QW = sizeof(E) == 2 ? 2 : 4;
+    uint32_t qe[HB][QW], ke[HB][QW];
     const int64_t kq0 = (t0 * a.G + grp) * a.N;
     const uint32_t kqld = (uint32_t)(a.G * a.N) * sizeof(E);
     const __amdgpu_buffer_rsrc_t qrs = rows_rsrc((const E *)a.q + kq0, count, (int64_t)a.G * a.N, a.N);
     const __amdgpu_buffer_rsrc_t krs = rows_rsrc((const E *)a.k + kq0, count, (int64_t)a.G * a.N, a.N);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < HB; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * g + r, n = 16 * nb + l;
+            const int t = 16 * w + 4 * g + r, n = 16 * (half * HB + nb) + l;
             const uint32_t off = n < a.N ? t * kqld + n * sizeof(E) : kOffNone;
-            qe[nb][r] = bload_elem<E>(qrs, off);
-            ke[nb][r] = bload_elem<E>(krs, off);
+            if constexpr (sizeof(E) == 2) {
+                const uint32_t qv = __builtin_bit_cast(unsigned short, bload_elem<E>(qrs, off));
+                const uint32_t kv = __builtin_bit_cast(unsigned short, bload_elem<E>(krs, off));
+                qe[nb][r / 2] = r % 2 ? qe[nb][r / 2] | qv << 16 : qv;
+                ke[nb][r / 2] = r % 2 ? ke[nb][r / 2] | kv << 16 : kv;
+            } else {
+                qe[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(qrs, off));
+                ke[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(krs, off));
+            }
         }
-    floatx4 dq[NB], dk[NB];
+    floatx4 dq[HB], dk[HB];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
+    for (int nb = 0; nb < HB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
 
-    const int KP = a.Pp / 32;
-    const int64_t yld = (int64_t)a.H * a.P;
-    for (int h = h0; h < h1; ++h) {
-        const int64_t u = (int64_t)c * a.H + h;
+    floatx4 wm[4], zm[4], wD, zD, ab, bs;
+    float db = 0.f, sd = 0.f;
+    for (int j = 0; j < J; ++j) {
+        const int h = h0 + j / NPC, pc = j % NPC;
+        loads_done();
         __syncthreads();
-        for (int i = threadIdx.x; i < kVec; i += kThreads) vs[i] = a.vec[u * kVec + i];
-        __syncthreads();
-        const E *U = (const E *)a.ust + u * kC * a.Pp, *Hh = (const E *)a.hst + u * kC * a.Pp;
-        const E *S = (const E *)a.sst + u * NT * a.Pp, *D = (const E *)a.dst + u * NT * a.Pp;
-        const __amdgpu_buffer_rsrc_t dyrs = rows_rsrc((const E *)a.dy + (t0 * a.H + h) * a.P, count, yld, a.P);
-        auto dyf = [&](int tb, int kb) {   // rows past the count and columns past P are zero
-            frag_t<E> f;
-            const int t = 16 * tb + l, pp = 32 * kb + 8 * g;
-            bload_frag(dyrs, pp < a.P ? (t * (uint32_t)yld + pp) * (uint32_t)sizeof(E) : kOffNone, f);
-            return f;
-        };
-        auto rowf = [&](const E *base, int row0, int kb) {
-            return load_frag(base + ((int64_t)(row0 / 16 * KP + kb) * 64 + lane) * 8);
-        };
-        // the pair products, in both orientations
-        floatx4 wT[4], wN[4], zT[4], zN[4];
+        if (PL::TWICE && j + 1 < J) issue(j + 1);
+        const E *buf = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kBlocks * 512 + 8 * lane;
+        const E *Sb = buf, *Db = buf + NB * KPC * 512, *Ub = buf + 2 * NB * KPC * 512, *Hb = Ub + 4 * KPC * 512,
+                *Yb = Hb + 4 * KPC * 512;
+        const float *vs = vs2 + ((h - h0) & 1) * kVec;
+        if (pc == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wT[j] = wN[j] = zT[j] = zN[j] = floatx4{0, 0, 0, 0};
-        float db = 0.f;
-        for (int kb = 0; kb < KP; ++kb) {
-            const frag_t<E> uw = rowf(U, 16 * w, kb), hw = rowf(Hh, 16 * w, kb), yw = dyf(w, kb);
-            const floatx8 uf = to_f32(uw), hf = to_f32(hw);
+            for (int i = 0; i < 4; ++i) wm[i] = zm[i] = floatx4{0, 0, 0, 0};
+            wD = zD = ab = bs = floatx4{0, 0, 0, 0};
+            db = sd = 0.f;
+        }
+        frag_t<E> uw[KPC], hw[KPC], yw[KPC];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) db += uf[j] * hf[j];
+        for (int kb = 0; kb < KPC; ++kb)
+            {
+                uw[kb] = load_frag(Ub + (w * KPC + kb) * 512);
+                hw[kb] = load_frag(Hb + (w * KPC + kb) * 512);
+                yw[kb] = load_frag(Yb + (w * KPC + kb) * 512);
+                if (half) {
+                    const floatx8 uf = to_f32(uw[kb]), hf = to_f32(hw[kb]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j <= w) {
-                    const frag_t<E> uj = rowf(U, 16 * j, kb);
-                    mma(wT[j], uj, yw);   // rows s, columns t
-                    mma(zT[j], uj, hw);
+                    for (int i = 0; i < 8; ++i) db += uf[i] * hf[i];
                 }
-                if (j >= w) {
-                    mma(wN[j], dyf(j, kb), uw);   // rows t, columns s
-                    mma(zN[j], rowf(Hh, 16 * j, kb), uw);
+                mma(wD, yw[kb], uw[kb]);
+                mma(zD, hw[kb], uw[kb]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i <= w) {
+                        const frag_t<E> ui = load_frag(Ub + (i * KPC + kb) * 512);
+                        mma(wm[i], ui, yw[kb]);
+                        mma(zm[i], ui, hw[kb]);
+                    } else {
+                        mma(wm[i], load_frag(Yb + (i * KPC + kb) * 512), uw[kb]);
+                        mma(zm[i], load_frag(Hb + (i * KPC + kb) * 512), uw[kb]);
+                    }
                 }
+            }
+        // the state products
+        {
+            const floatx4 bt = vec4(vs + kBeta + 16 * w + 4 * g);
+            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), ch = vec4(vs + kSince + 16 * w + 4 * g) * bt,
+                          cd = vec4(vs + kTillBeta + 16 * w + 4 * g);
+#pragma unroll
+            for (int nb = 0; nb < HB; ++nb) {
+                floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
+#pragma unroll
+                for (int kb = 0; kb < KPC; ++kb)
+                    {
+                        const frag_t<E> sf = load_frag(Sb + ((half * HB + nb) * KPC + kb) * 512);
+                        const frag_t<E> df = load_frag(Db + ((half * HB + nb) * KPC + kb) * 512);
+                        mma(ys, yw[kb], sf);
+                        mma(hs, hw[kb], sf);
+                        mma(ud, uw[kb], df);
+                        if ((nb & 3) == w || HB < 4) {
+                            const floatx8 s8 = to_f32(sf), d8 = to_f32(df);
+                            float t = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) t += s8[i] * d8[i];
+                            sd += (nb & 3) == w ? t : 0.f;
+                        }
+                    }
+                ys *= cq;
+                hs *= ch;
+                ud *= cd;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    uint32_t qw = qe[nb][r * QW / 4], kw = ke[nb][r * QW / 4];
+                    asm volatile("" : "+v"(qw), "+v"(kw));
+                    if (QW == 2) {
+                        qw = r % 2 ? qw & 0xffff0000u : qw << 16;
+                        kw = r % 2 ? kw & 0xffff0000u : kw << 16;
+                    }
+                    const float qv = __uint_as_float(qw), kv = __uint_as_float(kw);
+                    ab[r] += qv * ys[r] - kv * (hs[r] + ud[r]);
+                    bs[r] += kv * ud[r];
+                }
+                dq[nb] += ys;
+                dk[nb] += ud - hs;
             }
         }
-        db += __shfl_xor(db, 16);
-        db += __shfl_xor(db, 32);
-        if (g == 0 && 16 * w + l < count)
-            ((E *)a.dbeta)[(t0 + 16 * w + l) * a.H + h] = from_float<E>(db);
-        float rowX = 0.f, colX = 0.f;   // of token 16 w + l, this lane's share
-        const int tl = 16 * w + l;
-        const float bl = vs[kBeta + tl];
+        if (!PL::TWICE && j + 1 < J) {
+            if (pc != NPC - 1) {   // (the last part of a head meets below)
+                __syncthreads();
+                issue(j + 1);
+            }
+        }
+        if (pc != NPC - 1) continue;
+        // the head's pair matrices; rows past the count held data of other rows
+        float dx = 0.f;
+        // (opaque, so that the comparisons below are made here and not kept in registers)
+        int tl = 16 * w + l, o0 = 4 * g;
+        asm volatile("" : "+v"(tl), "+v"(o0));
+        const float bl = vs[kBeta + tl], chi = vs[kCsHi + tl], clo = vs[kCsLo + tl];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int o = 16 * j + 4 * g + r;
+                const int o = 16 * i + o0 + r;
                 const float bo = vs[kBeta + o];
-                const float dh = vs[kCsHi + tl] - vs[kCsHi + o], dl = vs[kCsLo + tl] - vs[kCsLo + o];
-                if (j <= w) {   // t = tl, s = o
-                    const float gam = o <= tl ? exp2_((dh + dl) * kLog2e) * bo : 0.f;
-                    wT[j][r] = a.scale * gam * wT[j][r];
-                    zT[j][r] = o < tl ? gam * bl * zT[j][r] : 0.f;
-                    if (o > tl) wT[j][r] = 0.f;
-                    rowX += wT[j][r] * qkT[j][r] - zT[j][r] * kk[j][r];
-                }
-                if (j >= w) {   // t = o, s = tl
-                    const float gam = tl <= o ? exp2_(-(dh + dl) * kLog2e) * bl : 0.f;
-                    wN[j][r] = a.scale * gam * wN[j][r];
-                    zN[j][r] = tl < o ? gam * bo * zN[j][r] : 0.f;
-                    if (tl > o) wN[j][r] = 0.f;
-                    colX += wN[j][r] * qkN[j][r] - zN[j][r] * kk[j][r];
-                }
+                const float d = ((chi - vs[kCsHi + o]) + (clo - vs[kCsLo + o])) * kLog2e;
+                const bool row_is_s = i <= w;
+                const int tt = row_is_s ? tl : o, ss = row_is_s ? o : tl;
+                const float gam = exp2_(ss <= tt ? (row_is_s ? d : -d) : 0.f) * (row_is_s ? bo : bl);
+                wm[i][r] = ss <= tt && tt < count ? a.scale * gam * wm[i][r] : 0.f;
+                zm[i][r] = ss < tt ? gam * (row_is_s ? bl : bo) * zm[i][r] : 0.f;
+                const float xv = wm[i][r] * qk[i][r] - zm[i][r] * kk[i][r];
+                dx += row_is_s ? xv : -xv;
             }
-        float dx = rowX - colX;
-        dx += __shfl_xor(dx, 16);
-        dx += __shfl_xor(dx, 32);
-        // the state products
-        floatx4 since = vec4(vs + kSince + 16 * w + 4 * g), bt = vec4(vs + kBeta + 16 * w + 4 * g);
-        const floatx4 cq = a.scale * since, ch = since * bt, cd = vec4(vs + kTill + 16 * w + 4 * g) * bt;
-        floatx4 ab = floatx4{0, 0, 0, 0}, bs = ab;
-        float sd = 0.f;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
-            for (int kb = 0; kb < KP; ++kb) {
-                const frag_t<E> sf = rowf(S, 16 * nb, kb), df = rowf(D, 16 * nb, kb);
-                mma(ys, dyf(w, kb), sf);
-                mma(hs, rowf(Hh, 16 * w, kb), sf);
-                mma(ud, rowf(U, 16 * w, kb), df);
-                if ((nb & 3) == w) {
-                    const floatx8 s8 = to_f32(sf), d8 = to_f32(df);
+        for (int r = 0; r < 4; ++r) {   // the diagonal block as (t, s)
+            const int o = 16 * w + o0 + r;
+            const float bo = vs[kBeta + o];
+            const float d = ((vs[kCsHi + o] - chi) + (vs[kCsLo + o] - clo)) * kLog2e;
+            const float gam = exp2_(tl <= o ? d : 0.f) * bl;
+            wD[r] = tl <= o && o < count ? a.scale * gam * wD[r] : 0.f;
+            zD[r] = tl < o ? gam * bo * zD[r] : 0.f;
+            float kd = kk[0][r];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sd += s8[j] * d8[j];
-                }
-            }
-            ys *= cq;
-            hs *= ch;
-            ud *= cd;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float qv = to_float(qe[nb][r]), kv = to_float(ke[nb][r]);
-                ab[r] += qv * ys[r] - kv * hs[r];
-                bs[r] += kv * ud[r];
-            }
-            dq[nb] += ys;
-            dk[nb] += ud - hs;
+            for (int i = 1; i < 4; ++i) kd = i == w ? kk[i][r] : kd;
+            dx -= wD[r] * qkD[r] - zD[r] * kd;
         }
         // W K, W^T Q and (Z + Z^T) K
-        floatx4 zs[4];
+        {
+            const floatx4 none = floatx4{0, 0, 0, 0};
+            floatx4 zs[4], up[4], dn[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) zs[j] = j < w ? -zT[j] : j > w ? -zN[j] : -(zT[j] + zN[j]);
-        const frag_t<E> a0 = round_pair<E>(wT[0], wT[1]), a1 = round_pair<E>(wT[2], wT[3]);
-        const frag_t<E> b0 = round_pair<E>(wN[0], wN[1]), b1 = round_pair<E>(wN[2], wN[3]);
-        const frag_t<E> z0 = round_pair<E>(zs[0], zs[1]), z1 = round_pair<E>(zs[2], zs[3]);
+            for (int i = 0; i < 4; ++i) {
+                up[i] = i <= w ? wm[i] : none;
+                dn[i] = i < w ? none : i == w ? wD : wm[i];
+                zs[i] = i == w ? -(zm[i] + zD) : -zm[i];
+            }
+            const frag_t<E> a0 = round_pair<E>(up[0], up[1]), a1 = round_pair<E>(up[2], up[3]);
+            const frag_t<E> b0 = round_pair<E>(dn[0], dn[1]), b1 = round_pair<E>(dn[2], dn[3]);
+            const frag_t<E> z0 = round_pair<E>(zs[0], zs[1]), z1 = round_pair<E>(zs[2], zs[3]);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const frag_t<E> k0 = load_frag(ktf + 2 * nb * 512), k1 = load_frag(ktf + (2 * nb + 1) * 512);
-            const frag_t<E> q0 = load_frag(qtf + 2 * nb * 512), q1 = load_frag(qtf + (2 * nb + 1) * 512);
-            mma(dq[nb], a0, k0);
-            mma(dq[nb], a1, k1);
-            mma(dk[nb], b0, q0);
-            mma(dk[nb], b1, q1);
-            mma(dk[nb], z0, k0);
-            mma(dk[nb], z1, k1);
+            for (int nb = 0; nb < HB; ++nb) {
+                const E *kt = ktf + 2 * (half * HB + nb) * 512, *qt = qtf + 2 * (half * HB + nb) * 512;
+                const frag_t<E> k0 = load_frag(kt), k1 = load_frag(kt + 512);
+                mma(dq[nb], a0, k0);
+                mma(dk[nb], b0, load_frag(qt));
+                mma(dq[nb], a1, k1);
+                mma(dk[nb], z0, k0);
+                mma(dk[nb], b1, load_frag(qt + 512));
+                mma(dk[nb], z1, k1);
+            }
         }
-        // dg
-        ab -= bs;
-        float sb = bs[0] + bs[1] + bs[2] + bs[3];
+        // dg and dbeta
+        float sb = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool in = 16 * w + 4 * g + r < count;
+            ab[r] = in ? ab[r] : 0.f;
+            sb += bs[r];
+        }
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1)
 #pragma unroll
@@ -1221,33 +1346,46 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad(GradArgs a)
             sb += __shfl_xor(sb, d);
             sd += __shfl_xor(sd, d);
         }
-        if (g == 0) dcs[16 * w + l] = dx;
-        if (lane == 0) {
-            red[w] = sb;
-            red[4 + w] = sd;
+        if (half == 0) {
+            dx += __shfl_xor(dx, 16);
+            dx += __shfl_xor(dx, 32);
+            if (g == 0) dcs[2][tl] = dx;
+        } else {
+            db += __shfl_xor(db, 16);
+            db += __shfl_xor(db, 32);
+            if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
         }
-        __syncthreads();
         if (l == 0)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dcs[16 * w + 4 * g + r] += ab[r];
+            for (int r = 0; r < 4; ++r) dcs[half][16 * w + 4 * g + r] = ab[r];
+        if (lane == 0) {
+            red[wv] = sb;
+            red[8 + wv] = sd;
+        }
         __syncthreads();
-        if (w == 0) {
-            float s = dcs[63 - lane];
+        if (!PL::TWICE && j + 1 < J) issue(j + 1);
+        if (wv == 0) {
+            const int t = 63 - lane;
+            float s = dcs[0][t] + dcs[1][t] + dcs[2][t], sum_b = 0.f, sum_sd = 0.f;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const float o = __shfl_up(s, d);
                 if (lane >= d) s += o;
             }
-            s += red[0] + red[1] + red[2] + red[3] +
-                 vs[kSince + kC - 1] * (red[4] + red[5] + red[6] + red[7]);
-            if (63 - lane < count) ((E *)a.dg)[(t0 + 63 - lane) * a.H + h] = from_float<E>(s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum_b += red[i];
+                sum_sd += red[8 + i];
+            }
+            s += sum_b + vs[kSince + kC - 1] * sum_sd;
+            if (t < count) ((E *)a.dg)[(t0 + t) * a.H + h] = from_float<E>(s);
         }
     }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < HB; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * g + r, n = 16 * nb + l;
+            const int t = 16 * w + 4 * g + r, n = 16 * (half * HB + nb) + l;
             if (a.hsplit > 1) {
                 float *o = a.part + (((int64_t)c * a.G + grp) * a.hsplit + sp) * 2 * kMat + (int64_t)t * NT + n;
                 o[0] = dq[nb][r];
