@@ -17,6 +17,8 @@
 // partial sums; a second kernel adds those rows.  No atomics: the order is fixed.
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_device.hpp"
 
 namespace ssd {
@@ -43,6 +45,22 @@ template <int V, typename E> __device__ __forceinline__ void store_v(E *p, const
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = v[i];
         *reinterpret_cast<bf16x8 *>(p) = __builtin_convertvector(f, bf16x8);
+    }
+}
+// A vector as it is in memory (one or four words), and its floats.
+template <int V, typename E> struct Raw {
+    typedef typename std::conditional<V == 1, E, uint4>::type type;
+};
+template <int V, typename E> __device__ __forceinline__ void unpack(const typename Raw<V, E>::type &r, float (&o)[V])
+{
+    if constexpr (V == 1) o[0] = to_float(r);
+    else if constexpr (V == 4) {
+        o[0] = __uint_as_float(r.x); o[1] = __uint_as_float(r.y);
+        o[2] = __uint_as_float(r.z); o[3] = __uint_as_float(r.w);
+    } else {
+        const floatx8 f = __builtin_convertvector(__builtin_bit_cast(bf16x8, r), floatx8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = f[i];
     }
 }
 // V floats of an fp32 vector at any 4-byte-aligned place of a 16-byte-aligned run.
@@ -154,24 +172,40 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
     for (int i = 0; i < (PARTS ? IT : 1); ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
-    const int64_t r0 = (int64_t)blockIdx.x * strip;
+    const int64_t r0 = (int64_t)blockIdx.x * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
+    // the next row's vectors are on their way while this one is summed; vectors past the row
+    // and rows past the strip load its first ones instead of branching
+    using W = typename Raw<V, E>::type;
+    W xr[IT], gr[IT];
+    float mu_n, rs_n;
+    auto fetch = [&](int64_t row) {
+        const int64_t rr = row < r1 ? row : r0, at = rr * dim;
+        mu_n = mean[rr];
+        rs_n = rstd[rr];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = i * L + ln < nv ? i * L + ln : 0;
+            xr[i] = *reinterpret_cast<const W *>(x + at + c * V);
+            gr[i] = *reinterpret_cast<const W *>(dy + at + c * V);
+        }
+    };
+    fetch(r0 + rg);
     int flip = 0;
-    for (int64_t rb = r0; rb < r0 + strip && rb < rows; rb += R, flip ^= 1) {
+    for (int64_t rb = r0; rb < r1; rb += R, flip ^= 1) {
         const int64_t row = rb + rg;
-        const bool live = row < rows && row < r0 + strip;   // the whole row group agrees
-        const int64_t at = (live ? row : 0) * dim;
+        const bool live = row < r1;   // the whole row group agrees
+        const int64_t at = row * dim;
         float xv[IT][V], gv[IT][V];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int c = i * L + ln;
+            unpack<V, E>(xr[i], xv[i]);
+            unpack<V, E>(gr[i], gv[i]);
+            if (!live)
 #pragma unroll
-            for (int e = 0; e < V; ++e) xv[i][e] = gv[i][e] = 0.f;
-            if (live && c < nv) {
-                load_v<V>(x + at + c * V, xv[i]);
-                load_v<V>(dy + at + c * V, gv[i]);
-            }
+                for (int e = 0; e < V; ++e) xv[i][e] = gv[i][e] = 0.f;
         }
-        const float mu = live ? mean[row] : 0.f, rs = live ? rstd[row] : 0.f;
+        const float mu = mu_n, rs = rs_n;
+        if (rb + R < r1) fetch(row + R);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -185,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
             for (int e = 0; e < V; ++e) {
                 const float xh = (xv[i][e] - mu) * rs, gy = gv[i][e];
                 if (PARTS) {
-                    dw[i][e] += live ? gy * xh : 0.f;
+                    dw[i][e] += gy * xh;
                     db[i][e] += gy;
                 }
                 const float gw = gy * w[e];

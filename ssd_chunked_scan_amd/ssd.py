@@ -16,7 +16,9 @@ and the backward ``bwd`` (= ``ssd_bwd``); the gated delta rule ``gdr_fwd``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -177,8 +179,7 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_fwd_gated.argtypes = [P, vp, vp]
     lib.ssd_conv1d_silu.argtypes = [ctypes.POINTER(ConvArgs), vp]
     lib.ssd_fwd_noalloc.argtypes = [P, vp]
-    # the structures below are passed by address (ctypes.addressof): a call per token
-    # should not pay for the pointer objects
+    # the structures below are passed as packed bytes or by address
     lib.ssd_gdr_fwd_workspace_size.argtypes = [vp, vp]
     lib.ssd_gdr_bwd_workspace_size.argtypes = [vp, vp]
     lib.ssd_gdr_fwd.argtypes = [vp, vp]
@@ -599,6 +600,16 @@ def bwd(x, dt, A, B, C, chunk, y, dy, D=None, initial_states=None, dfinal_states
 # ---------------------------------------------------------------------------
 # the gated delta rule and layer norm
 # ---------------------------------------------------------------------------
+# A decode step is a few microseconds of GPU time, so these calls keep the host side
+# short: the argument structures are packed into bytes, workspace sizes are asked for
+# once per shape.
+
+_GDR = struct.Struct("6qif7Pq4P")           # ssd_gdr_args
+_GDR_BWD = struct.Struct("10P")             # ssd_gdr_bwd_args
+_GDR_STEP = struct.Struct("5qif7P")         # ssd_gdr_step_args
+_NORM = struct.Struct("2qif6P")             # ssd_norm_args
+_NORM_BWD = struct.Struct("2q2i10P")        # ssd_norm_bwd_args
+
 
 def _same(t, name, dtype, shape, dev):
     """``_check`` with the common case first: everything as it should be."""
@@ -608,78 +619,83 @@ def _same(t, name, dtype, shape, dev):
     _check(t, name, dtype, shape, dev)
 
 
-class _Launch:
-    """Device and stream of one call.  Within it the tensors' device is current and,
-    for a stream of the caller's, what is allocated belongs to that stream (memory of
-    the current stream could be handed out again while the other still uses it)."""
-
-    def __init__(self, dev, stream):
-        cur = torch.cuda.current_stream(dev).cuda_stream
-        self.stream = cur if stream is None else int(stream)
-        self.ctx = []
-        if self.stream != cur:
-            self.ctx.append(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=dev)))
-        elif torch.cuda.current_device() != dev.index:
-            self.ctx.append(torch.cuda.device(dev))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
-
-
-def _run(name, rc):
+def _launch(name, dev, stream, call):
+    """``call(stream handle)`` with the tensors' device current.  For a stream of the
+    caller's own, what ``call`` allocates belongs to that stream (memory of the current
+    stream could be handed out again while the other still uses it)."""
+    cur = torch.cuda.current_stream(dev).cuda_stream
+    if stream is not None and int(stream) != cur:
+        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
+            rc, out = call(int(stream))
+    elif torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            rc, out = call(cur)
+    else:
+        rc, out = call(cur)
     if rc != 0:
         raise SSDError(rc, name)
+    return out
 
 
-def _bytes_of(name, args):
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, packed):
     n = ctypes.c_size_t(0)
-    _run(name, getattr(load_library(), name)(ctypes.addressof(args), ctypes.addressof(n)))
+    rc = getattr(load_library(), name)(packed, ctypes.addressof(n))
+    if rc != 0:
+        raise SSDError(rc, name)
     return n.value
 
 
 def _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq):
-    """Validated ``GdrArgs`` (no outputs), and the shape of the states."""
+    """Checked inputs: (sizes and dtype, scale, input pointers, shape of the states)."""
     if not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("v must be [batch, seqlen, nheads, headdim]")
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [batch, seqlen, ngroups, dstate]")
-    b, T, H, P = v.shape
+    b, T, H, P = shape = v.shape
     G, N = q.shape[2:]
     dtype, dev = v.dtype, v.device
     if dtype not in _DTYPES:
         raise TypeError("v must be float32 or bfloat16")
-    _same(v, "v", dtype, v.shape, dev)
+    _same(v, "v", dtype, shape, dev)
     _same(q, "q", dtype, (b, T, G, N), dev)
     _same(k, "k", dtype, (b, T, G, N), dev)
     _same(g, "g", dtype, (b, T, H), dev)
     _same(beta, "beta", dtype, (b, T, H), dev)
+    n = 0
     if seq_idx is not None:
         _same(seq_idx, "seq_idx", torch.int32, (T,), dev)
         if nseq is None:
             raise ValueError("nseq is required with seq_idx (no device->host read)")
-    n = 0 if seq_idx is None else int(nseq)
+        n = int(nseq)
     states = (b if seq_idx is None else n, H, P, N)
     if initial_states is not None:
         _same(initial_states, "initial_states", torch.float32, states, dev)
-    a = GdrArgs(b, T, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale, q.data_ptr(), k.data_ptr(),
-                v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(initial_states), _ptr(seq_idx), n)
-    return a, states
+    head = (b, T, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale)
+    ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            0 if initial_states is None else initial_states.data_ptr(), 0 if seq_idx is None else seq_idx.data_ptr())
+    return head, ptrs, n, states
+
+
+def _gdr_pack(head, ptrs, n, y=0, final_states=0, workspace=0, nbytes=0):
+    return _GDR.pack(*head, *ptrs[:6], ptrs[6], n, y, final_states, workspace, nbytes)
+
+
+def _gdr_workspace(name, head, ptrs, n):
+    # only the sizes matter, and whether there is a seq_idx
+    return _workspace_bytes(name, _gdr_pack(head, (0,) * 6 + (16 if ptrs[6] else 0,), n))
 
 
 def gdr_fwd_workspace_bytes(q, k, v, g, beta, seq_idx=None, nseq=None) -> int:
     """Bytes of the ``workspace`` that ``gdr_fwd`` takes for these shapes."""
-    return _bytes_of("ssd_gdr_fwd_workspace_size", _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)[0])
+    head, ptrs, n, _ = _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)
+    return _gdr_workspace("ssd_gdr_fwd_workspace_size", head, ptrs, n)
 
 
 def gdr_bwd_workspace_bytes(q, k, v, g, beta, seq_idx=None, nseq=None) -> int:
     """Bytes of the ``workspace`` that ``gdr_bwd`` takes for these shapes."""
-    return _bytes_of("ssd_gdr_bwd_workspace_size", _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)[0])
+    head, ptrs, n, _ = _gdr_args(q, k, v, g, beta, None, None, seq_idx, nseq)
+    return _gdr_workspace("ssd_gdr_bwd_workspace_size", head, ptrs, n)
 
 
 def gdr_fwd(q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, nseq=None, y=None, final_states=None,
@@ -689,26 +705,28 @@ def gdr_fwd(q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, nse
     bf16; ``scale`` multiplies y (default 1).  States are [b,H,P,N] fp32, with
     ``seq_idx`` (packed streams, batch 1) [nseq,H,P,N], one per segment.  ``y``,
     ``final_states`` and ``workspace`` (uint8) may be passed pre-allocated."""
-    a, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
+    head, ptrs, n, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
     dev = v.device
-    with _Launch(dev, stream) as st:
-        if y is None:
-            y = torch.empty_like(v)
+
+    def call(st):
+        yy, fin, ws = y, final_states, workspace
+        if yy is None:
+            yy = torch.empty_like(v)
         else:
-            _same(y, "y", v.dtype, v.shape, dev)
-        if final_states is None:
+            _same(yy, "y", v.dtype, v.shape, dev)
+        if fin is None:
             if want_final:
-                final_states = torch.empty(states, dtype=torch.float32, device=dev)
+                fin = torch.empty(states, dtype=torch.float32, device=dev)
         else:
-            _same(final_states, "final_states", torch.float32, states, dev)
-        if workspace is None:
-            workspace = torch.empty(_bytes_of("ssd_gdr_fwd_workspace_size", a), dtype=torch.uint8, device=dev)
+            _same(fin, "final_states", torch.float32, states, dev)
+        if ws is None:
+            ws = torch.empty(_gdr_workspace("ssd_gdr_fwd_workspace_size", head, ptrs, n), dtype=torch.uint8, device=dev)
         else:
-            _check(workspace, "workspace", torch.uint8, None, dev)
-        a.y, a.final_states = y.data_ptr(), _ptr(final_states)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        _run("ssd_gdr_fwd", load_library().ssd_gdr_fwd(ctypes.addressof(a), st))
-    return y, final_states
+            _check(ws, "workspace", torch.uint8, None, dev)
+        a = _gdr_pack(head, ptrs, n, yy.data_ptr(), 0 if fin is None else fin.data_ptr(), ws.data_ptr(), ws.numel())
+        return load_library().ssd_gdr_fwd(a, st), (yy, fin)
+
+    return _launch("ssd_gdr_fwd", dev, stream, call)
 
 
 def gdr_bwd(q, k, v, g, beta, dy, scale=None, initial_states=None, dfinal_states=None, seq_idx=None, nseq=None,
@@ -716,13 +734,14 @@ def gdr_bwd(q, k, v, g, beta, dy, scale=None, initial_states=None, dfinal_states
     """Gradients of sum(y * dy) + sum(final_states * dfinal_states) (``ssd_gdr_bwd``):
     a dict with dq, dk, dv, dg, dbeta and dinitial_states (None unless
     ``want_dinit``); ``grads`` may pass those tensors pre-allocated."""
-    a, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
+    head, ptrs, n, states = _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq)
     dev, dtype = v.device, v.dtype
     _same(dy, "dy", dtype, v.shape, dev)
     if dfinal_states is not None:
         _same(dfinal_states, "dfinal_states", torch.float32, states, dev)
-    out = dict(grads or {})
-    with _Launch(dev, stream) as st:
+
+    def call(st):
+        out, ws = dict(grads or {}), workspace
         for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
             if out.get(name) is None:
                 out[name] = torch.empty_like(like)
@@ -732,15 +751,17 @@ def gdr_bwd(q, k, v, g, beta, dy, scale=None, initial_states=None, dfinal_states
             _same(out["dinitial_states"], "dinitial_states", torch.float32, states, dev)
         else:
             out["dinitial_states"] = torch.empty(states, dtype=torch.float32, device=dev) if want_dinit else None
-        if workspace is None:
-            workspace = torch.empty(_bytes_of("ssd_gdr_bwd_workspace_size", a), dtype=torch.uint8, device=dev)
+        if ws is None:
+            ws = torch.empty(_gdr_workspace("ssd_gdr_bwd_workspace_size", head, ptrs, n), dtype=torch.uint8, device=dev)
         else:
-            _check(workspace, "workspace", torch.uint8, None, dev)
-        ga = GdrBwdArgs(dy.data_ptr(), _ptr(dfinal_states), out["dq"].data_ptr(), out["dk"].data_ptr(),
-                        out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(),
-                        _ptr(out["dinitial_states"]), workspace.data_ptr(), workspace.numel())
-        _run("ssd_gdr_bwd", load_library().ssd_gdr_bwd(ctypes.addressof(a), ctypes.addressof(ga), st))
-    return out
+            _check(ws, "workspace", torch.uint8, None, dev)
+        dinit = out["dinitial_states"]
+        ga = _GDR_BWD.pack(dy.data_ptr(), 0 if dfinal_states is None else dfinal_states.data_ptr(), out["dq"].data_ptr(),
+                           out["dk"].data_ptr(), out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(),
+                           0 if dinit is None else dinit.data_ptr(), ws.data_ptr(), ws.numel())
+        return load_library().ssd_gdr_bwd(_gdr_pack(head, ptrs, n), ga, st), out
+
+    return _launch("ssd_gdr_bwd", dev, stream, call)
 
 
 def gdr_step(q, k, v, g, beta, state, scale=None, y=None, stream=None):
@@ -750,26 +771,29 @@ def gdr_step(q, k, v, g, beta, state, scale=None, y=None, stream=None):
         raise ValueError("v must be [batch, nheads, headdim]")
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [batch, ngroups, dstate]")
-    b, H, P = v.shape
+    b, H, P = shape = v.shape
     G, N = q.shape[1:]
     dtype, dev = v.dtype, v.device
     if dtype not in _DTYPES:
         raise TypeError("v must be float32 or bfloat16")
-    _same(v, "v", dtype, v.shape, dev)
+    _same(v, "v", dtype, shape, dev)
     _same(q, "q", dtype, (b, G, N), dev)
     _same(k, "k", dtype, (b, G, N), dev)
     _same(g, "g", dtype, (b, H), dev)
     _same(beta, "beta", dtype, (b, H), dev)
     _same(state, "state", torch.float32, (b, H, P, N), dev)
-    with _Launch(dev, stream) as st:
-        if y is None:
-            y = torch.empty_like(v)
+
+    def call(st):
+        yy = y
+        if yy is None:
+            yy = torch.empty_like(v)
         else:
-            _same(y, "y", dtype, v.shape, dev)
-        a = GdrStepArgs(b, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale, q.data_ptr(), k.data_ptr(),
-                        v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), y.data_ptr())
-        _run("ssd_gdr_step", load_library().ssd_gdr_step(ctypes.addressof(a), st))
-    return y
+            _same(yy, "y", dtype, shape, dev)
+        a = _GDR_STEP.pack(b, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale, q.data_ptr(), k.data_ptr(),
+                           v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), yy.data_ptr())
+        return load_library().ssd_gdr_step(a, st), yy
+
+    return _launch("ssd_gdr_step", dev, stream, call)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None, want_stats=True):
@@ -779,30 +803,39 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=
     ``want_stats``.  ``y`` may be ``x``."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be [..., dim]")
-    dtype, dev, lead, dim = x.dtype, x.device, x.shape[:-1], x.shape[-1]
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    lead, dim = shape[:-1], shape[-1]
     if dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16")
-    _same(x, "x", dtype, x.shape, dev)
+    _same(x, "x", dtype, shape, dev)
     if weight is not None:
         _same(weight, "weight", torch.float32, (dim,), dev)
     if bias is not None:
         _same(bias, "bias", torch.float32, (dim,), dev)
-    with _Launch(dev, stream) as st:
-        if y is None:
-            y = torch.empty_like(x)
+
+    def call(st):
+        yy, m, r = y, mean, rstd
+        if yy is None:
+            yy = torch.empty_like(x)
         else:
-            _same(y, "y", dtype, x.shape, dev)
-        if want_stats:
-            mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else mean
-            rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
-            _same(mean, "mean", torch.float32, lead, dev)
-            _same(rstd, "rstd", torch.float32, lead, dev)
+            _same(yy, "y", dtype, shape, dev)
+        if not want_stats:
+            m = r = None
         else:
-            mean = rstd = None
-        a = NormArgs(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], eps, x.data_ptr(), _ptr(weight), _ptr(bias),
-                     y.data_ptr(), _ptr(mean), _ptr(rstd))
-        _run("ssd_layer_norm_fwd", load_library().ssd_layer_norm_fwd(ctypes.addressof(a), st))
-    return y, mean, rstd
+            if m is None:
+                m = torch.empty(lead, dtype=torch.float32, device=dev)
+            else:
+                _same(m, "mean", torch.float32, lead, dev)
+            if r is None:
+                r = torch.empty(lead, dtype=torch.float32, device=dev)
+            else:
+                _same(r, "rstd", torch.float32, lead, dev)
+        a = _NORM.pack(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], eps, x.data_ptr(),
+                       0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(), yy.data_ptr(),
+                       0 if m is None else m.data_ptr(), 0 if r is None else r.data_ptr())
+        return load_library().ssd_layer_norm_fwd(a, st), (yy, m, r)
+
+    return _launch("ssd_layer_norm_fwd", dev, stream, call)
 
 
 def layer_norm_bwd(x, dy, mean, rstd, weight=None, grads=None, workspace=None, stream=None, want_params=None):
@@ -812,35 +845,40 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, grads=None, workspace=None, s
     ``dy``)."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be [..., dim]")
-    dtype, dev, lead, dim = x.dtype, x.device, x.shape[:-1], x.shape[-1]
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    lead, dim = shape[:-1], shape[-1]
     if dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16")
-    _same(x, "x", dtype, x.shape, dev)
-    _same(dy, "dy", dtype, x.shape, dev)
+    _same(x, "x", dtype, shape, dev)
+    _same(dy, "dy", dtype, shape, dev)
     _same(mean, "mean", torch.float32, lead, dev)
     _same(rstd, "rstd", torch.float32, lead, dev)
     if weight is not None:
         _same(weight, "weight", torch.float32, (dim,), dev)
     params = weight is not None if want_params is None else want_params
-    out = dict(grads or {})
-    with _Launch(dev, stream) as st:
+    rows = x.numel() // dim if dim else 0
+
+    def call(st):
+        out, ws = dict(grads or {}), workspace
         if out.get("dx") is None:
             out["dx"] = torch.empty_like(x)
         else:
-            _same(out["dx"], "dx", dtype, x.shape, dev)
+            _same(out["dx"], "dx", dtype, shape, dev)
         for name in ("dweight", "dbias"):
             if out.get(name) is not None:
                 _same(out[name], name, torch.float32, (dim,), dev)
             elif params:
                 out[name] = torch.empty(dim, dtype=torch.float32, device=dev)
         dw, db = out.get("dweight"), out.get("dbias")
-        a = NormBwdArgs(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], 0, x.data_ptr(), dy.data_ptr(),
-                        mean.data_ptr(), rstd.data_ptr(), _ptr(weight), out["dx"].data_ptr(), _ptr(dw), _ptr(db))
-        if workspace is not None:
-            _check(workspace, "workspace", torch.uint8, None, dev)
+        if ws is not None:
+            _check(ws, "workspace", torch.uint8, None, dev)
         elif dw is not None or db is not None:
-            workspace = torch.empty(_bytes_of("ssd_layer_norm_bwd_workspace_size", a), dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        _run("ssd_layer_norm_bwd", load_library().ssd_layer_norm_bwd(ctypes.addressof(a), st))
-    return out
+            size = _workspace_bytes("ssd_layer_norm_bwd_workspace_size", _NORM_BWD.pack(rows, dim, _DTYPES[dtype], 0, *(0,) * 10))
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        a = _NORM_BWD.pack(rows, dim, _DTYPES[dtype], 0, x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                           0 if weight is None else weight.data_ptr(), out["dx"].data_ptr(),
+                           0 if dw is None else dw.data_ptr(), 0 if db is None else db.data_ptr(),
+                           0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+        return load_library().ssd_layer_norm_bwd(a, st), out
+
+    return _launch("ssd_layer_norm_bwd", dev, stream, call)

@@ -189,3 +189,15 @@ def test_the_binding_refuses_host_tensors_types_and_shapes():
         ssd.layer_norm_fwd(z(4, 8).double())
     with pytest.raises(ValueError, match="GPU"):
         ssd.layer_norm_bwd(z(4, 8), z(4, 8), z(4), z(4))
+
+
+def test_packed_arguments_match_the_structures():
+    """The binding packs its arguments into bytes: same size, same place of every field."""
+    import struct
+    for packer, mirror in ((ssd._GDR, ssd.GdrArgs), (ssd._GDR_BWD, ssd.GdrBwdArgs), (ssd._GDR_STEP, ssd.GdrStepArgs),
+                           (ssd._NORM, ssd.NormArgs), (ssd._NORM_BWD, ssd.NormBwdArgs)):
+        assert packer.size == ctypes.sizeof(mirror)
+        n = len(mirror._fields_)
+        vals = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(mirror._fields_)]
+        a = mirror.from_buffer_copy(packer.pack(*vals))
+        assert [getattr(a, f) for f, _ in mirror._fields_] == vals and n == len(struct.unpack(packer.format, bytes(a)))
