@@ -115,7 +115,7 @@ int64_t head_split(const Shape &s)
     return k > hpg ? hpg : k < 1 ? 1 : k;
 }
 
-constexpr int64_t kTwiceUpTo = 256;   // workgroups: one per CU
+constexpr int64_t kNarrowUpTo = 256;   // wide workgroups: one per CU
 
 struct Workspace {
     size_t cmap, chain, range, kq, vec, tri, sst, ust, dst, hst, part, total;
@@ -154,14 +154,13 @@ template <typename F> ssd_status with_nt(int64_t NT, F &&f)
     return f(std::integral_constant<int, 256>{});
 }
 
-// How the chains' operands are staged: twice where a workgroup per CU is all there
-// is (its own loads then hide behind its own steps), once where several share a CU.
-template <typename E, int NT, typename F> void with_flow(int64_t workgroups, F &&f)
+// How the chains run: narrow (a step shared by a workgroup's waves) while wide workgroups
+// would not give every CU one, else wide with their operands in LDS where they fit.
+template <typename E, int NT, typename F, typename G> void with_flow(bool narrow, F &&wide, G &&slim)
 {
-    if constexpr (!kStaged<E, NT>) f(std::integral_constant<int, 0>{});
-    else if constexpr (!kTwice<E, NT>) f(std::integral_constant<int, 1>{});
-    else if (workgroups <= kTwiceUpTo) f(std::integral_constant<int, 2>{});
-    else f(std::integral_constant<int, 1>{});
+    if (narrow) slim();
+    else if constexpr (kStaged<E, NT>) wide(std::integral_constant<int, 1>{});
+    else wide(std::integral_constant<int, 0>{});
 }
 
 // What both directions form first: the chunk map, the operand copies, the triangles.
@@ -210,6 +209,16 @@ template <typename E> ChainArgs chain_args(const Shape &s, const ssd_gdr_args *a
     return c;
 }
 
+// Whether `directions` chains of these units run narrow; if so c is set for 16 columns per
+// workgroup.
+bool narrowed(ChainArgs &c, const Shape &s, int directions)
+{
+    if ((int64_t)c.units * directions > kNarrowUpTo) return false;
+    c.np = (int)(s.Pp / 16);
+    c.units = (int)(s.chains * s.H * c.np);
+    return true;
+}
+
 template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_gdr_args *a, hipStream_t st)
 {
     const Workspace w = layout(s, false);
@@ -222,10 +231,15 @@ template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_gdr_args *a
     c.s1 = a->final_states;
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        with_flow<E, NT>(c.units, [&](auto flow) {
-            hipLaunchKernelGGL((k_gdr_chain<E, NT / 16, decltype(flow)::value>), dim3((unsigned)c.units), dim3(kThreads), 0,
-                               st, c);
-        });
+        with_flow<E, NT>(
+            narrowed(c, s, 1),
+            [&](auto flow) {
+                hipLaunchKernelGGL((k_gdr_chain<E, NT / 16, decltype(flow)::value>), dim3((unsigned)c.units), dim3(kThreads),
+                                   0, st, c);
+            },
+            [&] {
+                hipLaunchKernelGGL((k_gdr_chain_narrow<E, NT / 16>), dim3((unsigned)c.units), dim3(64 * kNW<NT / 16>), 0, st, c);
+            });
         return launched();
     });
 }
@@ -272,10 +286,16 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
     ga.scale = a->scale;
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        with_flow<E, NT>(2 * (int64_t)c.units, [&](auto flow) {
-            hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, decltype(flow)::value>), dim3(2u * (unsigned)c.units),
-                               dim3(kThreads), 0, st, c);
-        });
+        with_flow<E, NT>(
+            narrowed(c, s, 2),
+            [&](auto flow) {
+                hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, decltype(flow)::value>), dim3(2u * (unsigned)c.units),
+                                   dim3(kThreads), 0, st, c);
+            },
+            [&] {
+                hipLaunchKernelGGL((k_gdr_chains_narrow<E, NT / 16>), dim3(2u * (unsigned)c.units), dim3(64 * kNW<NT / 16>),
+                                   0, st, c);
+            });
         hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kGradThreads), 0, st, ga);
         if (hs > 1)
             hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G)), dim3(kThreads), 0, st,

@@ -453,22 +453,22 @@ template <typename E, int NB> struct StateOps {
 };
 
 template <typename E, int NB>
-__device__ __forceinline__ void load_state(const float *src, floatx4 (&s)[NB], int p, int g, int P, int N)
+__device__ __forceinline__ void load_state(const float *src, floatx4 (&s)[NB], int p, int g, int P, int N, int n0 = 0)
 {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const int n = 16 * nb + 4 * g;
+        const int n = n0 + 16 * nb + 4 * g;
         s[nb] = floatx4{0, 0, 0, 0};
         if (src && p < P && n < N) s[nb] = *reinterpret_cast<const floatx4 *>(src + (int64_t)p * N + n);
     }
 }
 template <int NB>
-__device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], int p, int g, int P, int N)
+__device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], int p, int g, int P, int N, int n0 = 0)
 {
     if (!dst || p >= P) return;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const int n = 16 * nb + 4 * g;
+        const int n = n0 + 16 * nb + 4 * g;
         if (n < N) *reinterpret_cast<floatx4 *>(dst + (int64_t)p * N + n) = s[nb];
     }
 }
@@ -502,13 +502,14 @@ template <typename E> __device__ __forceinline__ int64_t piece(int b, int rows, 
     return ((int64_t)block * 64 + l + 16 * (((p0 & 31) >> 3) + (g >> 1))) * 8 + 4 * (g & 1);
 }
 template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *dst, const frag_t<E> (&f)[NF],
-                                                                           const Select<E> &sel, int p0, int lane)
+                                                                           const Select<E> &sel, int p0, int lane,
+                                                                           int rows = 2 * NF, int row0 = 0)
 {
 #pragma unroll
     for (int b = 0; b < 2 * NF; ++b) {
         floatx4 d = floatx4{0, 0, 0, 0};
         mma(d, f[b >> 1], sel.half[b & 1]);
-        store_round4(dst + piece<E>(b, 2 * NF, p0, lane >> 4, lane & 15), d);
+        store_round4(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
     }
 }
 
@@ -998,11 +999,463 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
     save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N);
 }
 
+// ---- narrow chains ----
+// With fewer chains than CUs a step's length is all that counts.  Here a workgroup owns 16
+// columns and its kNW waves share a step: the state's rows n are split over them (each
+// holds its part, and multiplies its part of K, Q and K^T), and so are the chunk's tokens
+// (16 or 32 each) for what is not a product with the state.  Three exchanges through LDS a
+// step: the partial products K S (and Q S), the right-hand sides X, and U.  Every first
+// operand is now used by one wave once, so it comes from memory into registers, requested
+// for the next step as soon as this step has used it.
+template <int NB> constexpr int kNW = NB / 2 < 4 ? NB / 2 : 4;
+template <typename E, int NB, int KIND> struct Narrow {
+    static constexpr int NW = kNW<NB>, NBW = NB / NW, TBW = 4 / NW, KBW = NBW / 2, NK = NB / 2;
+    static constexpr int kPart = NW * 4 * 64 * 4;                         // floats: [wave][tb][lane][4]
+    static constexpr int kFrag = 512 * kPlanes<E>;                        // elements of a split operand
+    static constexpr int kBytes = (KIND == 0 ? 2 : 1) * kPart * 4 + (2 * 2 * kFrag + (KIND == 0 ? 2 * 512 : 0)) * (int)sizeof(E);
+};
+// The half of a split second operand that the 16 tokens of row block tb are, and the operand.
+template <typename E> __device__ __forceinline__ void put_half(E *f, int tb, int lane, const floatx4 &v)
+{
+    store_split4(f + (tb >> 1) * 512 * kPlanes<E> + 8 * lane + 4 * (tb & 1), 512, v);
+}
+template <typename E> __device__ __forceinline__ void get_split(const E *f, int kb, int lane, frag_t<E> &hi, frag_t<E> &lo)
+{
+    hi = load_frag(f + kb * 512 * kPlanes<E> + 8 * lane);
+    if (kPlanes<E> == 2) lo = load_frag(f + kb * 512 * kPlanes<E> + 512 + 8 * lane);
+}
+// acc += T X for row block tb of a triangle T (blocks given by block(tb, kb), planes PL
+// apart) and split X; `from`, `to`: the range of kb.
+template <typename E> struct TriRow {
+    frag_t<E> hi[2], lo[2];
+    template <typename B> __device__ __forceinline__ void load(const E *t, int k0, int k1, B block)
+    {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb >= k0 && kb <= k1) {
+                hi[kb] = load_frag(t + block(kb) * 512);
+                if (kPlanes<E> == 2) lo[kb] = load_frag(t + 512 * kTri + block(kb) * 512);
+            }
+    }
+    __device__ __forceinline__ void product(floatx4 &d, int k0, int k1, const frag_t<E> (&xh)[2], const frag_t<E> (&xl)[2]) const
+    {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb >= k0 && kb <= k1) {
+                mma(d, hi[kb], xh[kb]);
+                if (kPlanes<E> == 2) {
+                    mma(d, hi[kb], xl[kb]);
+                    mma(d, lo[kb], xh[kb]);
+                }
+            }
+    }
+};
+// One 16 x 16 tile of a caller's rows, as Tile.
+template <typename E> __device__ __forceinline__ floatx4 tile_rows(const typename Tile<E>::vec &x, const Select<E> &sel)
+{
+    frag_t<E> f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = x[j];
+        f[4 + j] = from_float<E>(0.f);
+    }
+    floatx4 o = floatx4{0, 0, 0, 0};
+    mma(o, f, sel.half[0]);
+    return o;
+}
+template <typename E> __device__ __forceinline__ typename Tile<E>::vec tile_load(__amdgpu_buffer_rsrc_t rs, uint32_t off)
+{
+    if constexpr (sizeof(E) == 2) return __builtin_bit_cast(typename Tile<E>::vec, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
+    else return __builtin_bit_cast(typename Tile<E>::vec, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
+template <typename E> __device__ __forceinline__ floatx4 transposed(const floatx4 &v, const Select<E> &sel)
+{
+    floatx4 d = floatx4{0, 0, 0, 0};
+    mma(d, round_pair<E>(v, floatx4{0, 0, 0, 0}), sel.half[0]);
+    return d;
+}
+template <typename E> __device__ __forceinline__ void tile_store(__amdgpu_buffer_rsrc_t rs, uint32_t off, const floatx4 &v,
+                                                                 const Select<E> &sel)
+{
+    const floatx4 d = transposed<E>(v, sel);
+    if constexpr (sizeof(E) == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(
+            __builtin_bit_cast(__attribute__((__vector_size__(8))) unsigned int, uint2{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])}),
+            rs, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((__vector_size__(16))) unsigned int, d), rs, off, 0, 0);
+}
+
+template <typename E, int NB, bool KEEP>
+__device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *smem)
+{
+    constexpr int KIND = KEEP ? 1 : 0;
+    using C = Narrow<E, NB, KIND>;
+    constexpr int NT = 16 * NB, kMat = kC * NT, NW = C::NW, NBW = C::NBW, TBW = C::TBW, KBW = C::KBW, NK = C::NK;
+    constexpr int kTriE = 512 * kTri;
+    float *part = reinterpret_cast<float *>(smem), *partq = part + C::kPart;
+    E *xf = reinterpret_cast<E *>(part + (KEEP ? 1 : 2) * C::kPart), *uf = xf + 2 * C::kFrag, *wf = uf + 2 * C::kFrag;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = 16 * ptile;
+    int c0, n, len;
+    int64_t t0;
+    chain_at(a.m, ch, c0, n, t0, len);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N, ld = (int64_t)a.H * a.P;
+    floatx4 S[NBW];
+    load_state<E, NBW>(a.s0 ? a.s0 + so : nullptr, S, p0 + l, g, a.P, a.N, 16 * NBW * wv);
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), poff = p0 < a.P ? (p0 + 4 * g) * sizeof(E) : kOffNone;
+    const int grp = h / (a.H / a.G);
+    auto rows_of = [&](const void *base, int i) {
+        const int left = len - i * kC;
+        return rows_rsrc((const E *)base + ((t0 + i * kC) * a.H + h) * a.P, left < kC ? left : kC, ld, a.P);
+    };
+    Select<E> sel;
+    sel.init(lane);
+    frag_t<E> kf[4][KBW], qf[KEEP ? 1 : 4][KBW], ktf[NBW][2], pf[KEEP ? 1 : TBW][2];
+    TriRow<E> nf[TBW];
+    floatx4 since[TBW], bt[TBW], tillb[TBW], scaled[TBW];
+    typename Tile<E>::vec v[TBW];
+    float whole;
+    const E *kq, *tri;
+    const float *vec;
+    auto at = [&](int i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        kq = (const E *)a.kq + ((int64_t)(c0 + i) * a.G + grp) * (KEEP ? 4 : 3) * kMat + 8 * lane;
+        tri = (const E *)a.tri + u * tri_elems<E>(KEEP) + 8 * lane;
+        vec = a.vec + u * kVec + 4 * g;
+    };
+    auto load_kq = [&]() {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+            for (int kb = 0; kb < KBW; ++kb) {
+                kf[tb][kb] = load_frag(kq + (tb * NK + wv * KBW + kb) * 512);
+                if (!KEEP) qf[tb][kb] = load_frag(kq + 2 * kMat + (tb * NK + wv * KBW + kb) * 512);
+            }
+    };
+    auto load_v = [&](int i) {
+        const __amdgpu_buffer_rsrc_t rs = rows_of(a.v, i);
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            v[j] = tile_load<E>(rs, poff + (16 * tb + l) * ldb);
+            since[j] = vec4(vec + kSince + 16 * tb);
+            bt[j] = vec4(vec + kBeta + 16 * tb);
+        }
+    };
+    auto load_tri = [&]() {
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            nf[j].load(tri, 0, tb >> 1, [&](int kb) { return lower_block(tb, kb); });
+            if (!KEEP)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+                    if (kb <= tb >> 1) pf[j][kb] = load_frag(tri + kPlanes<E> * kTriE + lower_block(tb, kb) * 512);
+        }
+    };
+    auto load_rest = [&]() {
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            tillb[j] = vec4(vec + kTillBeta + 16 * tb);
+            if (!KEEP) scaled[j] = vec4(vec + kScaled + 16 * tb);
+        }
+        whole = vec[kSince + kC - 1 - 4 * g];
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) ktf[nb][kb] = load_frag(kq + kMat + (2 * (wv * NBW + nb) + kb) * 512);
+    };
+    if (n > 0) {
+        at(0);
+        load_kq();
+        load_v(0);
+        load_tri();
+        load_rest();
+    }
+    for (int i = 0; i < n; ++i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        const bool more = i + 1 < n;
+        StateOps<E, NBW> so_;
+        so_.of(S);
+        floatx4 ks[4], qs[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < KBW; ++kb)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                mma(ks[tb], kf[tb][kb], so_.hi[kb]);
+                if (kPlanes<E> == 2) mma(ks[tb], kf[tb][kb], so_.lo[kb]);
+                if (!KEEP) mma(qs[tb], qf[tb][kb], so_.hi[kb]);
+            }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            *reinterpret_cast<floatx4 *>(part + ((wv * 4 + tb) * 64 + lane) * 4) = ks[tb];
+            if (!KEEP) *reinterpret_cast<floatx4 *>(partq + ((wv * 4 + tb) * 64 + lane) * 4) = qs[tb];
+        }
+        if (more) {
+            at(i + 1);
+            load_kq();
+        }
+        __syncthreads();
+        floatx4 R[TBW], qsum[TBW];
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            floatx4 s = vec4(part + (tb * 64 + lane) * 4);
+#pragma unroll
+            for (int o = 1; o < NW; ++o) s += vec4(part + ((o * 4 + tb) * 64 + lane) * 4);
+            if (!KEEP) {
+                qsum[j] = vec4(partq + (tb * 64 + lane) * 4);
+#pragma unroll
+                for (int o = 1; o < NW; ++o) qsum[j] += vec4(partq + ((o * 4 + tb) * 64 + lane) * 4);
+            }
+            R[j] = tile_rows<E>(v[j], sel) - since[j] * s;
+            put_half<E>(xf, tb, lane, bt[j] * R[j]);
+        }
+        floatx4 b_now[TBW];
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) b_now[j] = bt[j];
+        if (more) load_v(i + 1);
+        __syncthreads();
+        frag_t<E> xh[2], xl[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) get_split<E>(xf, kb, lane, xh[kb], xl[kb]);
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            floatx4 d = floatx4{0, 0, 0, 0};
+            nf[j].product(d, 0, tb >> 1, xh, xl);
+            R[j] -= d;   // U
+            put_half<E>(uf, tb, lane, tillb[j] * R[j]);
+            if (!KEEP) store_round4(wf + (tb >> 1) * 512 + 8 * lane + 4 * (tb & 1), b_now[j] * R[j]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) get_split<E>(uf, kb, lane, xh[kb], xl[kb]);
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb) S[nb] *= whole;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int nb = 0; nb < NBW; ++nb) {
+                mma(S[nb], ktf[nb][kb], xh[kb]);
+                if (kPlanes<E> == 2) mma(S[nb], ktf[nb][kb], xl[kb]);
+            }
+        if (KEEP) {
+#pragma unroll
+            for (int j = 0; j < TBW; ++j)
+                store_round4((E *)a.ust + u * kC * a.Pp + piece<E>(wv * TBW + j, 4, p0, g, l), transposed<E>(R[j], sel));
+            store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane, NB, NBW * wv);
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = rows_of(a.y, i);
+            const frag_t<E> w0 = load_frag(wf + 8 * lane), w1 = load_frag(wf + 512 + 8 * lane);
+#pragma unroll
+            for (int j = 0; j < TBW; ++j) {
+                const int tb = wv * TBW + j;
+                floatx4 s = scaled[j] * qsum[j];
+                mma(s, pf[j][0], w0);
+                if (tb >= 2) mma(s, pf[j][1], w1);
+                tile_store<E>(rs, poff + (16 * tb + l) * ldb, s, sel);
+            }
+        }
+        if (more) {
+            load_tri();
+            load_rest();
+        }
+    }
+    save_state<NBW>(a.s1 ? a.s1 + so : nullptr, S, p0 + l, g, a.P, a.N, 16 * NBW * wv);
+}
+
+template <typename E, int NB>
+__device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *smem)
+{
+    using C = Narrow<E, NB, 2>;
+    constexpr int NT = 16 * NB, kMat = kC * NT, NW = C::NW, NBW = C::NBW, TBW = C::TBW, KBW = C::KBW, NK = C::NK;
+    constexpr int kTriE = 512 * kTri;
+    float *part = reinterpret_cast<float *>(smem);
+    E *xf = reinterpret_cast<E *>(part + C::kPart), *uf = xf + 2 * C::kFrag;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int p0 = 16 * ptile;
+    int c0, n, len;
+    int64_t t0;
+    chain_at(a.m, ch, c0, n, t0, len);
+    const int64_t so = ((int64_t)ch * a.H + h) * a.P * a.N, ld = (int64_t)a.H * a.P;
+    floatx4 D[NBW];
+    load_state<E, NBW>(a.d1 ? a.d1 + so : nullptr, D, p0 + l, g, a.P, a.N, 16 * NBW * wv);
+    const uint32_t ldb = (uint32_t)ld * sizeof(E), poff = p0 < a.P ? (p0 + 4 * g) * sizeof(E) : kOffNone;
+    const int grp = h / (a.H / a.G);
+    auto rows_of = [&](const void *base, int i) {
+        const int left = len - i * kC;
+        return rows_rsrc((const E *)base + ((t0 + i * kC) * a.H + h) * a.P, left < kC ? left : kC, ld, a.P);
+    };
+    Select<E> sel;
+    sel.init(lane);
+    frag_t<E> kf[4][KBW], ktf[NBW][2], qtf[NBW][2];
+    TriRow<E> nf[TBW], pf[TBW];
+    floatx4 till[TBW], bt[TBW], erase[TBW], scaled[4];
+    Tile<E> dy;
+    float whole;
+    const E *kq, *tri;
+    const float *vec;
+    auto at = [&](int i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        kq = (const E *)a.kq + ((int64_t)(c0 + i) * a.G + grp) * 4 * kMat + 8 * lane;
+        tri = (const E *)a.tri + u * tri_elems<E>(true) + 8 * lane;
+        vec = a.vec + u * kVec + 4 * g;
+    };
+    auto load_k = [&]() {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+            for (int kb = 0; kb < KBW; ++kb) kf[tb][kb] = load_frag(kq + (tb * NK + wv * KBW + kb) * 512);
+    };
+    auto load_dy = [&](int i) {
+        dy.load(rows_of(a.dy, i), ldb, poff, l);
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            till[j] = vec4(vec + kTill + 16 * tb);
+            pf[j].load(tri + 2 * kPlanes<E> * kTriE, tb >> 1, 1, [&](int kb) { return upper_block(tb, kb); });
+        }
+    };
+    auto load_tri = [&]() {
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            nf[j].load(tri + kPlanes<E> * kTriE, tb >> 1, 1, [&](int kb) { return upper_block(tb, kb); });
+            bt[j] = vec4(vec + kBeta + 16 * tb);
+            erase[j] = vec4(vec + kErase + 16 * tb);
+        }
+    };
+    auto load_rest = [&]() {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) scaled[tb] = vec4(vec + kScaled + 16 * tb);
+        whole = vec[kSince + kC - 1 - 4 * g];
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                ktf[nb][kb] = load_frag(kq + kMat + (2 * (wv * NBW + nb) + kb) * 512);
+                qtf[nb][kb] = load_frag(kq + 3 * kMat + (2 * (wv * NBW + nb) + kb) * 512);
+            }
+    };
+    if (n > 0) {
+        at(n - 1);
+        load_k();
+        load_dy(n - 1);
+        load_tri();
+        load_rest();
+    }
+    for (int i = n - 1; i >= 0; --i) {
+        const int64_t u = (int64_t)(c0 + i) * a.H + h;
+        const bool more = i > 0;
+        StateOps<E, NBW> dop;
+        dop.of(D);
+        floatx4 ks[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) ks[tb] = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < KBW; ++kb)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                mma(ks[tb], kf[tb][kb], dop.hi[kb]);
+                if (kPlanes<E> == 2) mma(ks[tb], kf[tb][kb], dop.lo[kb]);
+            }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) *reinterpret_cast<floatx4 *>(part + ((wv * 4 + tb) * 64 + lane) * 4) = ks[tb];
+        floatx4 yt[4];
+        dy.rows(yt, sel);
+        const frag_t<E> y01[2] = {round_pair<E>(yt[0], yt[1]), round_pair<E>(yt[2], yt[3])};   // exact
+        floatx4 W[TBW];
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            W[j] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb >= tb >> 1) {
+                    mma(W[j], pf[j].hi[kb], y01[kb]);
+                    if (kPlanes<E> == 2) mma(W[j], pf[j].lo[kb], y01[kb]);
+                }
+        }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) yt[tb] *= scaled[tb];
+        frag_t<E> yh[2], yl[2];
+        split_pair(yt[0], yt[1], yh[0], yl[0]);
+        split_pair(yt[2], yt[3], yh[1], yl[1]);
+        if (more) {
+            at(i - 1);
+            load_k();
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            floatx4 s = vec4(part + (tb * 64 + lane) * 4);
+#pragma unroll
+            for (int o = 1; o < NW; ++o) s += vec4(part + ((o * 4 + tb) * 64 + lane) * 4);
+            W[j] += till[j] * s;
+            put_half<E>(xf, tb, lane, bt[j] * W[j]);
+        }
+        if (more) load_dy(i - 1);
+        __syncthreads();
+        frag_t<E> xh[2], xl[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) get_split<E>(xf, kb, lane, xh[kb], xl[kb]);
+        floatx4 X[TBW];
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            floatx4 d = floatx4{0, 0, 0, 0};
+            nf[j].product(d, tb >> 1, 1, xh, xl);
+            W[j] -= d;              // H
+            X[j] = bt[j] * W[j];    // dv
+            put_half<E>(uf, tb, lane, erase[j] * W[j]);
+        }
+        if (more) load_tri();
+        __syncthreads();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) get_split<E>(uf, kb, lane, xh[kb], xl[kb]);
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb) D[nb] *= whole;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int nb = 0; nb < NBW; ++nb) {
+                mma(D[nb], qtf[nb][kb], yh[kb]);
+                if (kPlanes<E> == 2) mma(D[nb], qtf[nb][kb], yl[kb]);
+                mma(D[nb], ktf[nb][kb], xh[kb]);
+                if (kPlanes<E> == 2) mma(D[nb], ktf[nb][kb], xl[kb]);
+            }
+        if (more) load_rest();
+        const __amdgpu_buffer_rsrc_t rs = rows_of(a.dv, i);
+#pragma unroll
+        for (int j = 0; j < TBW; ++j) {
+            const int tb = wv * TBW + j;
+            tile_store<E>(rs, poff + (16 * tb + l) * ldb, X[j], sel);
+            store_round4((E *)a.hst + u * kC * a.Pp + piece<E>(tb, 4, p0, g, l), transposed<E>(W[j], sel));
+        }
+        store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, lane, NB, NBW * wv);
+    }
+    save_state<NBW>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N, 16 * NBW * wv);
+}
+
 template <typename E, int NB, int FLOW>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_chain(ChainArgs a)
 {
     __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0, FLOW>::kBytes];
     chain_fwd<E, NB, false, FLOW>(a, blockIdx.x, smem);
+}
+template <typename E, int NB>
+__global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chain_narrow(ChainArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char smem[Narrow<E, NB, 0>::kBytes];
+    narrow_fwd<E, NB, false>(a, blockIdx.x, smem);
 }
 
 // The backward's two chains in one launch: neither needs the other.
@@ -1012,6 +1465,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_chains(ChainArgs a)
     __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2, FLOW>::kBytes];   // the larger of both
     if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, FLOW>(a, blockIdx.x, smem);
     else chain_fwd<E, NB, true, FLOW>(a, blockIdx.x - a.units, smem);
+}
+template <typename E, int NB>
+__global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chains_narrow(ChainArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char smem[Narrow<E, NB, 2>::kBytes];   // as large as KIND 1's
+    if (blockIdx.x < (unsigned)a.units) narrow_bwd<E, NB>(a, blockIdx.x, smem);
+    else narrow_fwd<E, NB, true>(a, blockIdx.x - a.units, smem);
 }
 
 // ---------------------------------------------------------------------------

@@ -612,18 +612,26 @@ _NORM_BWD = struct.Struct("2q2i10P")        # ssd_norm_bwd_args
 
 
 def _same(t, name, dtype, shape, dev):
-    """``_check`` with the common case first: everything as it should be."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
-            and t.is_contiguous() and t.is_cuda):
-        return
+    """``_check`` with the common case first: everything as it should be (``dev``: a GPU)."""
+    try:
+        if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:   # not a tensor
+        pass
     _check(t, name, dtype, shape, dev)
+
+
+# The current stream's handle by device index, without the object around it where this
+# build of torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch(name, dev, stream, call):
     """``call(stream handle)`` with the tensors' device current.  For a stream of the
     caller's own, what ``call`` allocates belongs to that stream (memory of the current
     stream could be handed out again while the other still uses it)."""
-    cur = torch.cuda.current_stream(dev).cuda_stream
+    cur = _raw_stream(dev.index)
     if stream is not None and int(stream) != cur:
         with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
             rc, out = call(int(stream))
@@ -657,7 +665,7 @@ def _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq):
     dtype, dev = v.dtype, v.device
     if dtype not in _DTYPES:
         raise TypeError("v must be float32 or bfloat16")
-    _same(v, "v", dtype, shape, dev)
+    _check(v, "v")   # on the GPU, contiguous
     _same(q, "q", dtype, (b, T, G, N), dev)
     _same(k, "k", dtype, (b, T, G, N), dev)
     _same(g, "g", dtype, (b, T, H), dev)
@@ -776,7 +784,7 @@ def gdr_step(q, k, v, g, beta, state, scale=None, y=None, stream=None):
     dtype, dev = v.dtype, v.device
     if dtype not in _DTYPES:
         raise TypeError("v must be float32 or bfloat16")
-    _same(v, "v", dtype, shape, dev)
+    _check(v, "v")   # on the GPU, contiguous
     _same(q, "q", dtype, (b, G, N), dev)
     _same(k, "k", dtype, (b, G, N), dev)
     _same(g, "g", dtype, (b, H), dev)
@@ -807,7 +815,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=
     lead, dim = shape[:-1], shape[-1]
     if dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16")
-    _same(x, "x", dtype, shape, dev)
+    _check(x, "x")   # on the GPU, contiguous
     if weight is not None:
         _same(weight, "weight", torch.float32, (dim,), dev)
     if bias is not None:
@@ -849,7 +857,7 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, grads=None, workspace=None, s
     lead, dim = shape[:-1], shape[-1]
     if dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16")
-    _same(x, "x", dtype, shape, dev)
+    _check(x, "x")   # on the GPU, contiguous
     _same(dy, "dy", dtype, shape, dev)
     _same(mean, "mean", torch.float32, lead, dev)
     _same(rstd, "rstd", torch.float32, lead, dev)
