@@ -60,9 +60,14 @@ constexpr int kC = 64;            // tokens per chunk
 constexpr int kTri = 6;           // 16 x 32 operand blocks in a triangle of 64 x 64
 // Per-token scalars of a (chunk, head), 64 floats each: e^{cs}, beta, scale e^{cs},
 // beta e^{cs_last - cs}, e^{cs_last - cs}, -beta e^{cs}, and cs as a sum of two floats.
-constexpr int kVec = 8 * kC;
+// Then, for the gradients, Gam between different blocks of 16 tokens as a product: with
+// the reference r_b = cs before block b, for t in block b and s before it
+//   Gam_ts = e^{cs_t - r_b} e^{r_b - cs_s}   (both at most 1)
+// scale e^{cs_t - r_b}, beta_t e^{cs_t - r_b} (zero past the count), and beta_s e^{r_b -
+// cs_s} for b = 1, 2, 3.
+constexpr int kVec = 16 * kC, kVecChain = 8 * kC;
 constexpr int kSince = 0, kBeta = kC, kScaled = 2 * kC, kTillBeta = 3 * kC, kTill = 4 * kC, kErase = 5 * kC,
-              kCsHi = 6 * kC, kCsLo = 7 * kC;
+              kCsHi = 6 * kC, kCsLo = 7 * kC, kRowScale = 8 * kC, kRowBeta = 9 * kC, kColBeta = 10 * kC;
 constexpr double kLog2eD = 1.4426950408889634;
 constexpr float kMinLogDecay = -64.f;   // e^-64 = 1.6e-28: smaller decays act as this one
 
@@ -331,6 +336,18 @@ __global__ __launch_bounds__(kThreads) void k_gdr_prep(const E *__restrict__ kq,
         vo[kErase + lane] = -bv * since;
         vo[kCsHi + lane] = hi;
         vo[kCsLo + lane] = (float)(s - (double)hi);
+        if (BWD) {
+            const int blk = lane >> 4;
+            const double r = __shfl(s, blk ? 16 * blk - 1 : 0);
+            const float row = lane < count ? exp2_((float)((s - (blk ? r : 0.0)) * kLog2eD)) : 0.f;
+            vo[kRowScale + lane] = scale * row;
+            vo[kRowBeta + lane] = bv * row;
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                const double rk = __shfl(s, 16 * k - 1);
+                vo[kColBeta + (k - 1) * kC + lane] = lane < 16 * k ? bv * exp2_((float)((rk - s) * kLog2eD)) : 0.f;
+            }
+        }
     }
     __syncthreads();
     const E *kf = kq + ((int64_t)c * G + h / (H / G)) * (BWD ? 4 : 3) * kMat, *qf = kf + 2 * kMat;
@@ -610,7 +627,7 @@ template <typename E, int NB, int KIND, int FLOW> struct Regions {
     static constexpr int kOne = kMat + (KIND == 0 ? kMat : KIND == 2 ? kN : 0);
     // phase 2: N or N^T | the pair matrix (KIND 0) | K^T | Q^T (KIND 2)
     static constexpr int kTwo = kN + (KIND == 0 ? kTri : 0) + kMat + (KIND == 2 ? kMat : 0);
-    static constexpr int kBytes = FLOW ? FLOW * (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVec * 4 : 16;
+    static constexpr int kBytes = FLOW ? FLOW * (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVecChain * 4 : 16;
 };
 
 typedef __attribute__((address_space(1))) const void *gptr_t;
@@ -673,9 +690,9 @@ template <typename E, int NB, int KIND, int FLOW> struct Operands {
             stage<E, R::kMat>(kq, o, wv, lane);
             if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, o + kMatE, wv, lane);
             if (KIND == 2) stage<E, R::kN>(tri + kPt, o + kMatE, wv, lane);
-            if (wv >= 2)   // kVec floats: two loads
+            if (wv >= 2)   // kVecChain floats: two loads
                 __builtin_amdgcn_global_load_lds((gptr_t)(vec + 256 * (wv - 2) + 4 * lane),
-                                                 (lptr_t)(vecs + kVec * turn + 256 * (wv - 2)), 16, 0, 0);
+                                                 (lptr_t)(vecs + kVecChain * turn + 256 * (wv - 2)), 16, 0, 0);
         }
     }
     __device__ __forceinline__ void stage_two()
@@ -709,7 +726,7 @@ template <typename E, int NB, int KIND, int FLOW> struct Operands {
     {
         return (LDS ? two_at(t) + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane;
     }
-    __device__ __forceinline__ const float *scalars(int t) const { return LDS ? vecs + kVec * t : vec; }
+    __device__ __forceinline__ const float *scalars(int t) const { return LDS ? vecs + kVecChain * t : vec; }
 };
 
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
@@ -1557,22 +1574,46 @@ constexpr int kGradThreads = 512;
 template <typename E, int NB> struct GradPlan {
     static constexpr int KPC = kColBlocks<E>;                   // 32-column blocks per stage
     static constexpr int kBlocks = (2 * NB + 12) * KPC;         // S | D | U | H | dy
-    static constexpr int kStage = kBlocks * 512 * (int)sizeof(E);
+    static constexpr int kRoom = kBlocks < 24 ? 24 : kBlocks;   // (at least what is exchanged below)
+    static constexpr int kStage = kRoom * 512 * (int)sizeof(E);
     static constexpr int kMats = 2 * 2 * NB * 512 * (int)sizeof(E);   // K^T and Q^T
     static constexpr int kRest = 2 * kVec * 4 + 1024;
     static constexpr bool TWICE = 2 * kStage + kMats + kRest <= 160 * 1024;
     static constexpr bool MATS = kStage + kMats + kRest <= 160 * 1024;   // K^T and Q^T in LDS as well
 };
 
+// acc + the sum of eight products (bf16: two per instruction, in fp32).
+__device__ __forceinline__ float dot8(const bf16x8 &x, const bf16x8 &y, float acc)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        acc = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x[i], x[i + 1]}, bf16x2{y[i], y[i + 1]}, acc, false);
+    return acc;
+}
+__device__ __forceinline__ float dot8(const floatx8 &x, const floatx8 &y, float acc)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc += x[i] * y[i];
+    return acc;
+}
+// The sum over a row of 16 lanes, in all of them.
+__device__ __forceinline__ float row_sum16(float v)
+{
+    v += dpp_mov<kDppQuadXor1>(v);
+    v += dpp_mov<kDppQuadXor2>(v);
+    v += dpp_mov<kDppRowHalfMirror>(v);
+    return v + dpp_mov<kDppRowRor8>(v);
+}
+
 template <typename E, int NB>
 __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 {
     using PL = GradPlan<E, NB>;
     constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT, KPC = PL::KPC, HB = NB / 2, V = kVec16<E>;
-    __shared__ __attribute__((aligned(16))) E stage_m[(PL::TWICE ? 2 : 1) * PL::kBlocks * 512];
+    __shared__ __attribute__((aligned(16))) E stage_m[(PL::TWICE ? 2 : 1) * PL::kRoom * 512];
     __shared__ __attribute__((aligned(16))) E mats[PL::MATS ? 2 * kMat : 8];
     __shared__ __attribute__((aligned(16))) float vs2[2 * kVec];
-    __shared__ float dcs[3][kC], red[16];
+    __shared__ float dcs[4][kC], red[16];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     const int w = wv & 3, half = wv >> 2;
     int x = blockIdx.x;
@@ -1602,7 +1643,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     auto issue = [&](int j) {
         const int hi = j / NPC, pc = j - hi * NPC, h = h0 + hi;
         const int64_t u = (int64_t)c * a.H + h;
-        E *dst = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kBlocks * 512;
+        E *dst = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kRoom * 512;
         const int64_t so = u * NT * a.Pp + pc * (NB * KPC * 512), uo = u * kC * a.Pp + pc * (4 * KPC * 512);
         using BS = std::integral_constant<int, NB * KPC>;
         using BU = std::integral_constant<int, 4 * KPC>;
@@ -1621,11 +1662,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
             __builtin_amdgcn_global_load_lds((gptr_t)(dy + (int64_t)(t < count ? t : count - 1) * yld + (pp < a.P ? pp : 0)),
                                              (lptr_t)(dst + wv * 64 * V), 16, 0, 0);
         }
-        if (pc == 0 && wv >= 6)
-            __builtin_amdgcn_global_load_lds((gptr_t)(a.vec + u * kVec + 256 * (wv - 6) + 4 * lane),
-                                             (lptr_t)(vs2 + (hi & 1) * kVec + 256 * (wv - 6)), 16, 0, 0);
+        if (pc == 0 && wv >= 4)
+            __builtin_amdgcn_global_load_lds((gptr_t)(a.vec + u * kVec + 256 * (wv - 4) + 4 * lane),
+                                             (lptr_t)(vs2 + (hi & 1) * kVec + 256 * (wv - 4)), 16, 0, 0);
     };
-    issue(0);
+    if (PL::TWICE) issue(0);
     if constexpr (PL::MATS) {
         constexpr int n = 2 * kMat * (int)sizeof(E) / 1024;   // K^T and Q^T, 1 KiB each
         static_assert(n % 16 == 0, "whole rounds");
@@ -1638,24 +1679,24 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     }
     const E *ktf = (PL::MATS ? mats : ktg) + 8 * lane, *qtf = (PL::MATS ? mats + kMat : qtg) + 8 * lane;
 
-    // The pair matrices of the wave's 16 tokens: block i holds rows of block i against
-    // columns of block w, as (s, t) pairs where i <= w and as (t, s) pairs where i > w; the
-    // diagonal block is needed both ways (the D arrays: as (t, s)).
-    floatx4 qk[4], kk[4], qkD = floatx4{0, 0, 0, 0};
+    // The pair matrices of the wave's 16 tokens (half 0: W, half 1: Z): block i holds rows of
+    // block i against columns of block w, as (s, t) pairs where i <= w and as (t, s) pairs
+    // where i > w; the diagonal block is needed both ways (mD: as (t, s)).  kq: q.k or k.k
+    // of the same pairs.
+    floatx4 kq[4], kqD = floatx4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) qk[i] = kk[i] = floatx4{0, 0, 0, 0};
-    if (half == 0)
+    for (int i = 0; i < 4; ++i) kq[i] = floatx4{0, 0, 0, 0};
+    {
+        const E *xf = half ? kf : qf;   // what stands for t
         for (int kb = 0; kb < NK; ++kb) {
-            const frag_t<E> kw = load_frag(kf + (w * NK + kb) * 512 + 8 * lane), qw = load_frag(qf + (w * NK + kb) * 512 + 8 * lane);
-            mma(qkD, qw, kw);
+            const frag_t<E> kw = load_frag(kf + (w * NK + kb) * 512 + 8 * lane), xw = load_frag(xf + (w * NK + kb) * 512 + 8 * lane);
+            mma(kqD, xw, kw);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const frag_t<E> ki = load_frag(kf + (i * NK + kb) * 512 + 8 * lane);
-                mma(kk[i], ki, kw);
-                if (i <= w) mma(qk[i], ki, qw);
-                else mma(qk[i], load_frag(qf + (i * NK + kb) * 512 + 8 * lane), kw);
-            }
+            for (int i = 0; i < 4; ++i)
+                if (i <= w) mma(kq[i], load_frag(kf + (i * NK + kb) * 512 + 8 * lane), xw);
+                else mma(kq[i], load_frag(xf + (i * NK + kb) * 512 + 8 * lane), kw);
         }
+    }
     // the wave's q and k in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
     // (packed in pairs, for the registers)
     constexpr int QW = sizeof(E) == 2 ? 2 : 4;
@@ -1684,146 +1725,178 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 #pragma unroll
     for (int nb = 0; nb < HB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
 
-    floatx4 wm[4], zm[4], wD, zD, ab, bs;
+    floatx4 m[4], mD, aq, ak, bk;
     float db = 0.f, sd = 0.f;
+    const int tl0 = 16 * w + l;
     for (int j = 0; j < J; ++j) {
         const int h = h0 + j / NPC, pc = j % NPC;
+        if (!PL::TWICE) {
+            __syncthreads();
+            issue(j);
+        }
         loads_done();
         __syncthreads();
         if (PL::TWICE && j + 1 < J) issue(j + 1);
-        const E *buf = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kBlocks * 512 + 8 * lane;
+        E *room = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kRoom * 512;
+        const E *buf = room + 8 * lane;
         const E *Sb = buf, *Db = buf + NB * KPC * 512, *Ub = buf + 2 * NB * KPC * 512, *Hb = Ub + 4 * KPC * 512,
-                *Yb = Hb + 4 * KPC * 512;
+                *Yb = Hb + 4 * KPC * 512, *Xb = half ? Hb : Yb;
         const float *vs = vs2 + ((h - h0) & 1) * kVec;
         if (pc == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) wm[i] = zm[i] = floatx4{0, 0, 0, 0};
-            wD = zD = ab = bs = floatx4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) m[i] = floatx4{0, 0, 0, 0};
+            mD = aq = ak = bk = floatx4{0, 0, 0, 0};
             db = sd = 0.f;
         }
         frag_t<E> uw[KPC], hw[KPC], yw[KPC];
 #pragma unroll
-        for (int kb = 0; kb < KPC; ++kb)
-            {
-                uw[kb] = load_frag(Ub + (w * KPC + kb) * 512);
-                hw[kb] = load_frag(Hb + (w * KPC + kb) * 512);
-                yw[kb] = load_frag(Yb + (w * KPC + kb) * 512);
-                if (half) {
-                    const floatx8 uf = to_f32(uw[kb]), hf = to_f32(hw[kb]);
+        for (int kb = 0; kb < KPC; ++kb) {
+            uw[kb] = load_frag(Ub + (w * KPC + kb) * 512);
+            hw[kb] = load_frag(Hb + (w * KPC + kb) * 512);
+            yw[kb] = load_frag(Yb + (w * KPC + kb) * 512);
+            if (half) db = dot8(uw[kb], hw[kb], db);
+            const frag_t<E> xw = load_frag(Xb + (w * KPC + kb) * 512);
+            mma(mD, xw, uw[kb]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) db += uf[i] * hf[i];
-                }
-                mma(wD, yw[kb], uw[kb]);
-                mma(zD, hw[kb], uw[kb]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i <= w) {
-                        const frag_t<E> ui = load_frag(Ub + (i * KPC + kb) * 512);
-                        mma(wm[i], ui, yw[kb]);
-                        mma(zm[i], ui, hw[kb]);
-                    } else {
-                        mma(wm[i], load_frag(Yb + (i * KPC + kb) * 512), uw[kb]);
-                        mma(zm[i], load_frag(Hb + (i * KPC + kb) * 512), uw[kb]);
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (i <= w) mma(m[i], load_frag(Ub + (i * KPC + kb) * 512), xw);
+                else mma(m[i], load_frag(Xb + (i * KPC + kb) * 512), uw[kb]);
+        }
         // the state products
         {
-            const floatx4 bt = vec4(vs + kBeta + 16 * w + 4 * g);
-            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), ch = vec4(vs + kSince + 16 * w + 4 * g) * bt,
-                          cd = vec4(vs + kTillBeta + 16 * w + 4 * g);
+            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
+                          ch = vec4(vs + kErase + 16 * w + 4 * g);
 #pragma unroll
             for (int nb = 0; nb < HB; ++nb) {
                 floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
 #pragma unroll
-                for (int kb = 0; kb < KPC; ++kb)
-                    {
-                        const frag_t<E> sf = load_frag(Sb + ((half * HB + nb) * KPC + kb) * 512);
-                        const frag_t<E> df = load_frag(Db + ((half * HB + nb) * KPC + kb) * 512);
-                        mma(ys, yw[kb], sf);
-                        mma(hs, hw[kb], sf);
-                        mma(ud, uw[kb], df);
-                        if ((nb & 3) == w || HB < 4) {
-                            const floatx8 s8 = to_f32(sf), d8 = to_f32(df);
-                            float t = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) t += s8[i] * d8[i];
-                            sd += (nb & 3) == w ? t : 0.f;
-                        }
-                    }
-                ys *= cq;
-                hs *= ch;
-                ud *= cd;
+                for (int kb = 0; kb < KPC; ++kb) {
+                    const frag_t<E> sf = load_frag(Sb + ((half * HB + nb) * KPC + kb) * 512);
+                    const frag_t<E> df = load_frag(Db + ((half * HB + nb) * KPC + kb) * 512);
+                    mma(ys, yw[kb], sf);
+                    mma(hs, hw[kb], sf);
+                    mma(ud, uw[kb], df);
+                    if ((nb & 3) == w) sd = dot8(sf, df, sd);
+                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     uint32_t qw = qe[nb][r * QW / 4], kw = ke[nb][r * QW / 4];
-                    asm volatile("" : "+v"(qw), "+v"(kw));
+                    asm volatile("" : "+v"(qw), "+v"(kw));   // (unpacked here, not kept unpacked)
                     if (QW == 2) {
                         qw = r % 2 ? qw & 0xffff0000u : qw << 16;
                         kw = r % 2 ? kw & 0xffff0000u : kw << 16;
                     }
-                    const float qv = __uint_as_float(qw), kv = __uint_as_float(kw);
-                    ab[r] += qv * ys[r] - kv * (hs[r] + ud[r]);
-                    bs[r] += kv * ud[r];
+                    aq[r] += __uint_as_float(qw) * ys[r];
+                    ak[r] += __uint_as_float(kw) * hs[r];
+                    bk[r] += __uint_as_float(kw) * ud[r];
+                    dq[nb][r] += cq[r] * ys[r];
+                    dk[nb][r] += cd[r] * ud[r];
+                    dk[nb][r] += ch[r] * hs[r];
                 }
-                dq[nb] += ys;
-                dk[nb] += ud - hs;
-            }
-        }
-        if (!PL::TWICE && j + 1 < J) {
-            if (pc != NPC - 1) {   // (the last part of a head meets below)
-                __syncthreads();
-                issue(j + 1);
             }
         }
         if (pc != NPC - 1) continue;
-        // the head's pair matrices; rows past the count held data of other rows
-        float dx = 0.f;
+        // the head's pair matrix and its part of dg.  Rows past the count hold data of the last
+        // row; their factors are zero.
+        // (sums over s and over t apart, so that what cancels does so exactly)
+        float dx = 0.f, dx_s = 0.f;
         // (opaque, so that the comparisons below are made here and not kept in registers)
-        int tl = 16 * w + l, o0 = 4 * g;
+        int tl = tl0, o0 = 4 * g;
         asm volatile("" : "+v"(tl), "+v"(o0));
-        const float bl = vs[kBeta + tl], chi = vs[kCsHi + tl], clo = vs[kCsLo + tl];
+        const float *row = vs + (half ? kRowBeta : kRowScale);
+        const float row_l = row[tl];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+            if (i < w) {   // t = tl, s = o
+                m[i] *= row_l * vec4(vs + kColBeta + (w - 1) * kC + 16 * i + o0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int o = 16 * i + o0 + r;
-                const float bo = vs[kBeta + o];
-                const float d = ((chi - vs[kCsHi + o]) + (clo - vs[kCsLo + o])) * kLog2e;
-                const bool row_is_s = i <= w;
-                const int tt = row_is_s ? tl : o, ss = row_is_s ? o : tl;
-                const float gam = exp2_(ss <= tt ? (row_is_s ? d : -d) : 0.f) * (row_is_s ? bo : bl);
-                wm[i][r] = ss <= tt && tt < count ? a.scale * gam * wm[i][r] : 0.f;
-                zm[i][r] = ss < tt ? gam * (row_is_s ? bl : bo) * zm[i][r] : 0.f;
-                const float xv = wm[i][r] * qk[i][r] - zm[i][r] * kk[i][r];
-                dx += row_is_s ? xv : -xv;
+                for (int r = 0; r < 4; ++r) dx += m[i][r] * kq[i][r];
+            } else if (i > w) {   // t = o, s = tl
+                m[i] *= vs[kColBeta + (i - 1) * kC + tl] * vec4(row + 16 * i + o0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dx_s += m[i][r] * kq[i][r];
+            } else {
+                const float chi = vs[kCsHi + tl], clo = vs[kCsLo + tl], bl = vs[kBeta + tl];
+                const floatx4 oh = vec4(vs + kCsHi + 16 * i + o0), ol = vec4(vs + kCsLo + 16 * i + o0),
+                              bo = vec4(vs + kBeta + 16 * i + o0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int o = 16 * i + o0 + r;
+                    const float d = ((chi - oh[r]) + (clo - ol[r])) * kLog2e;
+                    const bool down = half ? o < tl : o <= tl, up = half ? tl < o : tl <= o;
+                    const float f = exp2_(down ? d : 0.f) * bo[r] * (half ? bl : a.scale);
+                    m[i][r] = down && tl < count ? f * m[i][r] : 0.f;
+                    const float fD = exp2_(up ? -d : 0.f) * bl * (half ? bo[r] : a.scale);
+                    mD[r] = up && o < count ? fD * mD[r] : 0.f;
+                    dx += m[i][r] * kq[i][r];
+                    dx_s += mD[r] * kqD[r];
+                }
             }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {   // the diagonal block as (t, s)
-            const int o = 16 * w + o0 + r;
-            const float bo = vs[kBeta + o];
-            const float d = ((vs[kCsHi + o] - chi) + (vs[kCsLo + o] - clo)) * kLog2e;
-            const float gam = exp2_(tl <= o ? d : 0.f) * bl;
-            wD[r] = tl <= o && o < count ? a.scale * gam * wD[r] : 0.f;
-            zD[r] = tl < o ? gam * bo * zD[r] : 0.f;
-            float kd = kk[0][r];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) kd = i == w ? kk[i][r] : kd;
-            dx -= wD[r] * qkD[r] - zD[r] * kd;
-        }
-        // W K, W^T Q and (Z + Z^T) K
+        dx -= dx_s;
+        // its operands change hands through what this stage no longer needs
+        __syncthreads();
         {
             const floatx4 none = floatx4{0, 0, 0, 0};
-            floatx4 zs[4], up[4], dn[4];
+            E *mine = room + w * 6 * 512 + 8 * lane;
+            if (half == 0) {
+                floatx4 up[4], dn[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                up[i] = i <= w ? wm[i] : none;
-                dn[i] = i < w ? none : i == w ? wD : wm[i];
-                zs[i] = i == w ? -(zm[i] + zD) : -zm[i];
+                for (int i = 0; i < 4; ++i) {
+                    up[i] = i <= w ? m[i] : none;
+                    dn[i] = i < w ? none : i == w ? mD : m[i];
+                }
+                store_frag(mine, round_pair<E>(up[0], up[1]));
+                store_frag(mine + 512, round_pair<E>(up[2], up[3]));
+                store_frag(mine + 1024, round_pair<E>(dn[0], dn[1]));
+                store_frag(mine + 1536, round_pair<E>(dn[2], dn[3]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = i == w ? -m[i] - mD : -m[i];
+                store_frag(mine + 2048, round_pair<E>(m[0], m[1]));
+                store_frag(mine + 2560, round_pair<E>(m[2], m[3]));
+                dx = -dx;
             }
-            const frag_t<E> a0 = round_pair<E>(up[0], up[1]), a1 = round_pair<E>(up[2], up[3]);
-            const frag_t<E> b0 = round_pair<E>(dn[0], dn[1]), b1 = round_pair<E>(dn[2], dn[3]);
-            const frag_t<E> z0 = round_pair<E>(zs[0], zs[1]), z1 = round_pair<E>(zs[2], zs[3]);
+        }
+        // dg and dbeta
+        floatx4 ab;
+        float sb = 0.f;
+        {
+            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
+                          ch = vec4(vs + kErase + 16 * w + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = 16 * w + 4 * g + r < count;
+                const float b = cd[r] * bk[r];
+                sb += b;
+                ab[r] = in ? row_sum16(cq[r] * aq[r] + ch[r] * ak[r] - b) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            sb += __shfl_xor(sb, d);
+            sd += __shfl_xor(sd, d);
+        }
+        dx += __shfl_xor(dx, 16);
+        dx += __shfl_xor(dx, 32);
+        if (half) {
+            db += __shfl_xor(db, 16);
+            db += __shfl_xor(db, 32);
+            if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
+        }
+        if (g == 0) dcs[2 + half][tl] = dx;
+        if (l == 0)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dcs[half][16 * w + 4 * g + r] = ab[r];
+        if (lane == 0) {
+            red[wv] = sb;
+            red[8 + wv] = sd;
+        }
+        __syncthreads();
+        // W K, W^T Q and (Z + Z^T) K
+        {
+            const E *theirs = room + w * 6 * 512 + 8 * lane;
+            const frag_t<E> a0 = load_frag(theirs), a1 = load_frag(theirs + 512), b0 = load_frag(theirs + 1024),
+                            b1 = load_frag(theirs + 1536), z0 = load_frag(theirs + 2048), z1 = load_frag(theirs + 2560);
 #pragma unroll
             for (int nb = 0; nb < HB; ++nb) {
                 const E *kt = ktf + 2 * (half * HB + nb) * 512, *qt = qtf + 2 * (half * HB + nb) * 512;
@@ -1836,44 +1909,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
                 mma(dk[nb], z1, k1);
             }
         }
-        // dg and dbeta
-        float sb = 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool in = 16 * w + 4 * g + r < count;
-            ab[r] = in ? ab[r] : 0.f;
-            sb += bs[r];
-        }
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) ab[r] += __shfl_xor(ab[r], d);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            sb += __shfl_xor(sb, d);
-            sd += __shfl_xor(sd, d);
-        }
-        if (half == 0) {
-            dx += __shfl_xor(dx, 16);
-            dx += __shfl_xor(dx, 32);
-            if (g == 0) dcs[2][tl] = dx;
-        } else {
-            db += __shfl_xor(db, 16);
-            db += __shfl_xor(db, 32);
-            if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
-        }
-        if (l == 0)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dcs[half][16 * w + 4 * g + r] = ab[r];
-        if (lane == 0) {
-            red[wv] = sb;
-            red[8 + wv] = sd;
-        }
-        __syncthreads();
-        if (!PL::TWICE && j + 1 < J) issue(j + 1);
-        if (wv == 0) {
+        if (wv == (j & 7)) {
             const int t = 63 - lane;
-            float s = dcs[0][t] + dcs[1][t] + dcs[2][t], sum_b = 0.f, sum_sd = 0.f;
+            float s = dcs[0][t] + dcs[1][t] + dcs[2][t] + dcs[3][t], sum_b = 0.f, sum_sd = 0.f;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const float o = __shfl_up(s, d);
