@@ -1605,6 +1605,33 @@ __device__ __forceinline__ float row_sum16(float v)
     return v + dpp_mov<kDppRowRor8>(v);
 }
 
+// The sum over lanes l, l + 16, l + 32, l + 48, in all of them (row swaps: no LDS).
+__device__ __forceinline__ float cross_sum4(float v)
+{
+    const int x = __float_as_int(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    const float s = __int_as_float(a[0]) + __int_as_float(a[1]);
+    const int y = __float_as_int(s);
+    const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return __int_as_float(b[0]) + __int_as_float(b[1]);
+}
+// Inclusive prefix sum over the wave: shifts by 1, 2, 4, 8 inside each row of 16, then the
+// last lane of row 0 (2) to row 1 (3), and of row 1 to rows 2 and 3.
+__device__ __forceinline__ float prefix_sum64(float v)
+{
+    auto add = [&](auto ctrl, auto rows) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    return v;
+}
+
 template <typename E, int NB>
 __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 {
@@ -1871,16 +1898,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
                 ab[r] = in ? row_sum16(cq[r] * aq[r] + ch[r] * ak[r] - b) : 0.f;
             }
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            sb += __shfl_xor(sb, d);
-            sd += __shfl_xor(sd, d);
-        }
-        dx += __shfl_xor(dx, 16);
-        dx += __shfl_xor(dx, 32);
+        sb = cross_sum4(row_sum16(sb));
+        sd = cross_sum4(row_sum16(sd));
+        dx = cross_sum4(dx);
         if (half) {
-            db += __shfl_xor(db, 16);
-            db += __shfl_xor(db, 32);
+            db = cross_sum4(db);
             if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
         }
         if (g == 0) dcs[2 + half][tl] = dx;
@@ -1911,12 +1933,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
         }
         if (wv == (j & 7)) {
             const int t = 63 - lane;
-            float s = dcs[0][t] + dcs[1][t] + dcs[2][t] + dcs[3][t], sum_b = 0.f, sum_sd = 0.f;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const float o = __shfl_up(s, d);
-                if (lane >= d) s += o;
-            }
+            float s = prefix_sum64(dcs[0][t] + dcs[1][t] + dcs[2][t] + dcs[3][t]), sum_b = 0.f, sum_sd = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sum_b += red[i];
