@@ -118,7 +118,7 @@ int64_t head_split(const Shape &s)
 constexpr int64_t kNarrowUpTo = 256;   // wide workgroups: one per CU
 
 struct Workspace {
-    size_t cmap, chain, range, kq, vec, tri, sst, ust, dst, hst, part, total;
+    size_t cmap, chain, range, order, kq, vec, tri, sst, ust, dst, hst, part, total;
 };
 Workspace layout(const Shape &s, bool bwd)
 {
@@ -129,6 +129,7 @@ Workspace layout(const Shape &s, bool bwd)
         w.cmap = take((size_t)s.nct * 8);
         w.chain = take((size_t)s.nseq * 16);
         w.range = take((size_t)s.nseq * 8);
+        w.order = take((size_t)s.nseq * 4);
     }
     const size_t u = (size_t)(s.nct * s.H);
     const int tri = s.dtype == SSD_DTYPE_BF16 ? tri_elems<bf16>(bwd) : tri_elems<float>(bwd);
@@ -167,14 +168,16 @@ template <typename E, int NT, typename F, typename G> void with_flow(bool narrow
 template <typename E, bool BWD>
 ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Workspace &w, Chunks *m, hipStream_t st)
 {
-    *m = Chunks{nullptr, nullptr, (int)s.T, (int)s.nc};
+    *m = Chunks{nullptr, nullptr, nullptr, (int)s.T, (int)s.nc};
     if (s.packed) {
         int2 *cmap = reinterpret_cast<int2 *>(ws + w.cmap);
         int4 *chain = reinterpret_cast<int4 *>(ws + w.chain);
         hipLaunchKernelGGL(k_gdr_map, dim3(1), dim3(kMapThreads), 0, st, a->seq_idx,
-                           reinterpret_cast<int2 *>(ws + w.range), chain, cmap, (int)s.T, (int)s.nseq, (int)s.nct);
+                           reinterpret_cast<int2 *>(ws + w.range), chain, cmap,
+                           reinterpret_cast<int *>(ws + w.order), (int)s.T, (int)s.nseq, (int)s.nct);
         m->cmap = cmap;
         m->chain = chain;
+        m->order = reinterpret_cast<const int *>(ws + w.order);
         if (launched() != SSD_OK) return SSD_ERR_HIP;
     }
     return with_nt(s.NT, [&](auto nt) {
@@ -298,7 +301,7 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
             });
         hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kGradThreads), 0, st, ga);
         if (hs > 1)
-            hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G)), dim3(kThreads), 0, st,
+            hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G), NT / 16), dim3(kThreads), 0, st,
                                (const float *)ga.part, (E *)g->dq, (E *)g->dk, m, (int)s.G, (int)s.N, (int)hs);
         return launched();
     });

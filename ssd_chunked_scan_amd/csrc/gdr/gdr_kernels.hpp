@@ -85,6 +85,7 @@ template <typename E> constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
 struct Chunks {
     const int2 *cmap;
     const int4 *chain;
+    const int *order;   // packed: the chains by falling length, or null
     int T, nc;   // tokens and chunks per batch row (not packed)
 };
 
@@ -101,9 +102,10 @@ __device__ __forceinline__ void chunk_at(const Chunks &m, int c, int64_t &t0, in
     }
 }
 
-__device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n, int64_t &t0, int &len)
+__device__ __forceinline__ void chain_at(const Chunks &m, int &i, int &c0, int &n, int64_t &t0, int &len)
 {
     if (m.chain) {
+        i = __builtin_amdgcn_readfirstlane(m.order[i]);   // the i-th longest
         const int4 v = m.chain[i];
         c0 = __builtin_amdgcn_readfirstlane(v.x);
         n = __builtin_amdgcn_readfirstlane(v.y);
@@ -122,22 +124,41 @@ __device__ __forceinline__ void chain_at(const Chunks &m, int i, int &c0, int &n
 // an invalid stream gives wrong chunks but no access out of bounds.
 constexpr int kMapThreads = 1024;
 __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restrict__ seq_idx, int2 *__restrict__ range,
-                                                         int4 *__restrict__ chain, int2 *__restrict__ cmap, int T,
-                                                         int nseq, int ncmax)
+                                                         int4 *__restrict__ chain, int2 *__restrict__ cmap,
+                                                         int *__restrict__ order, int T, int nseq, int ncmax)
 {
-    __shared__ int wsum[kMapThreads / 64], base;
+    __shared__ int wsum[kMapThreads / 64], base, chunks[kMapThreads];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     for (int i = tid; i < nseq; i += kMapThreads) range[i] = int2{0, 0};
     if (tid == 0) base = 0;
     __syncthreads();
-    // range[id] = {start, end}: the words of one id are written by the threads of
-    // its first and its last token
+    // range[id] = {start, end}: the words of one id are written by the threads of its
+    // first and its last token.  Four tokens per thread, four such groups in flight.
     int *words = reinterpret_cast<int *>(range);
-    for (int t = tid; t < T; t += kMapThreads) {
-        const int id = seq_idx[t];
-        if (id < 0 || id >= nseq) continue;
-        if (t == 0 || seq_idx[t - 1] != id) words[2 * id] = t;
-        if (t == T - 1 || seq_idx[t + 1] != id) words[2 * id + 1] = t + 1;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc_n(seq_idx, T * 4);   // past the end: 0, not used
+    constexpr int U = 4;
+    for (int tb = 0; tb < T; tb += U * 4 * kMapThreads) {
+        int id[U][6];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = tb + (u * kMapThreads + tid) * 4;
+            const uint4 v = bload16(rs, 4u * t);
+            id[u][0] = t > 0 ? __builtin_amdgcn_raw_buffer_load_b32(rs, 4u * t - 4, 0, 0) : -1;
+            id[u][1] = v.x;
+            id[u][2] = v.y;
+            id[u][3] = v.z;
+            id[u][4] = v.w;
+            id[u][5] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4u * t + 16, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = tb + (u * kMapThreads + tid) * 4 + e, me = id[u][e + 1];
+                if (t >= T || me < 0 || me >= nseq) continue;
+                if (t == 0 || id[u][e] != me) words[2 * me] = t;
+                if (t == T - 1 || id[u][e + 2] != me) words[2 * me + 1] = t + 1;
+            }
     }
     __syncthreads();
     for (int i0 = 0; i0 < nseq; i0 += kMapThreads) {
@@ -151,6 +172,7 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
             if (lane >= d) s += o;
         }
         if (lane == 63) wsum[wv] = s;
+        chunks[tid] = n;
         __syncthreads();
         int before = base;
         for (int w = 0; w < wv; ++w) before += wsum[w];
@@ -158,6 +180,14 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
         if (i < nseq) {
             const int lo = c0 < ncmax ? c0 : ncmax;
             chain[i] = int4{lo, c0 + n <= ncmax ? n : ncmax - lo, r.x, len};
+            // long chains first (up to kMapThreads of them, each with its rank): a long one
+            // started last would run alone at the end
+            int rank = i;
+            if (nseq <= kMapThreads) {
+                rank = 0;
+                for (int o = 0; o < nseq; ++o) rank += chunks[o] > n || (chunks[o] == n && o < i) ? 1 : 0;
+            }
+            order[rank] = i;
         }
         __syncthreads();
         if (tid == kMapThreads - 1) base = before + s;
@@ -736,7 +766,8 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -878,7 +909,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -1134,7 +1166,8 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem), *partq = part + C::kPart;
     E *xf = reinterpret_cast<E *>(part + (KEEP ? 1 : 2) * C::kPart), *uf = xf + 2 * C::kFrag, *wf = uf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
@@ -1336,7 +1369,8 @@ __device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem);
     E *xf = reinterpret_cast<E *>(part + C::kPart), *uf = xf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H, ch = unit / (a.np * a.H);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
@@ -1971,7 +2005,7 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad_sum(const float *__restri
     int count;
     chunk_at(m, c, t0, count);
     const float *p = part + ((int64_t)c * G + grp) * hsplit * 2 * kMat;
-    for (int i = threadIdx.x; i < 2 * kMat / 4; i += kThreads) {
+    for (int i = blockIdx.y * kThreads + threadIdx.x; i < 2 * kMat / 4; i += gridDim.y * kThreads) {
         const int which = i / (kMat / 4), e = 4 * (i % (kMat / 4)), t = e / NT, n = e % NT;
         if (t >= count || n >= N) continue;
         floatx4 s = floatx4{0, 0, 0, 0};
