@@ -80,6 +80,7 @@ ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
     const int64_t cols = a->dtype == SSD_DTYPE_BF16 ? 32 * kColBlocks<bf16> : 32 * kColBlocks<float>;
     s->Pp = (s->P + cols - 1) / cols * cols;
     s->np = (s->Pp + kC - 1) / kC;
+    if (s->packed && s->T > ((int64_t)1 << 28)) return SSD_ERR_BAD_SHAPE;   // ids are read with 31-bit byte offsets
     // a chunk's rows of all heads or groups are addressed with 31-bit byte offsets
     if (s->H * s->P > (1 << 22) || s->G * s->N > (1 << 22)) return SSD_ERR_BAD_SHAPE;
     // grids and int32 indices
@@ -115,6 +116,7 @@ int64_t head_split(const Shape &s)
     return k > hpg ? hpg : k < 1 ? 1 : k;
 }
 
+constexpr int64_t kPrepWaves = 4096;   // four per SIMD
 constexpr int64_t kNarrowUpTo = 256;   // wide workgroups: one per CU
 
 struct Workspace {
@@ -185,9 +187,14 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
         E *kq = reinterpret_cast<E *>(ws + w.kq);
         hipLaunchKernelGGL((k_gdr_frags<E, NT>), dim3((unsigned)(s.nct * s.G), 2), dim3(kThreads), 0, st,
                            (const E *)a->k, (const E *)a->q, kq, *m, (int)s.G, (int)s.N, BWD ? 4 : 3);
-        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)(s.nct * s.H)), dim3(kThreads), 0, st,
+        // heads per wave: what K K^T costs is shared by them, but every SIMD wants waves first
+        const int64_t hpg = s.H / s.G;
+        int64_t hpw = s.nct * s.H / kPrepWaves;
+        hpw = hpw > hpg ? hpg : hpw < 1 ? 1 : hpw;
+        const int64_t units = s.nct * s.G * ((hpg + hpw - 1) / hpw);
+        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)((units + 3) / 4)), dim3(kThreads), 0, st,
                            (const E *)kq, (const E *)a->g, (const E *)a->beta, reinterpret_cast<float *>(ws + w.vec),
-                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, a->scale);
+                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, a->scale, (int)hpw, (int)units);
         return launched();
     });
 }

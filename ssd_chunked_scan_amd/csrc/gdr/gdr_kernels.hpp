@@ -255,6 +255,23 @@ __device__ __forceinline__ void store_round4(bf16 *p, const floatx4 &v)
 }
 __device__ __forceinline__ void store_round4(float *p, const floatx4 &v) { *reinterpret_cast<floatx4 *>(p) = v; }
 
+__device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
+// Rows of the identity as a second operand: slot row (g, j) of a 32-row block against
+// column 16 HALF + l.  An operand read as a first operand is its transpose; a product
+// with these moves it to accumulators, exactly, with rows and columns exchanged.  That
+// is how tiles enter and leave a chain with four consecutive elements per lane instead
+// of one (4 accesses of 8 bytes instead of 16 of 2).
+template <typename E> struct Select {
+    frag_t<E> half[2];
+    __device__ __forceinline__ void init(int lane)
+    {
+        const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) half[h][j] = from_float<E>(slot_row(g, j) == 16 * h + l ? 1.f : 0.f);
+    }
+};
 // K and Q of one chunk and group as operand blocks in slot order: rows (64 tokens,
 // slots over N: 4 x NT/32 blocks) and transposed (NT rows n, slots over tokens:
 // NT/16 x 2 blocks).  Tokens past the chunk's count and columns past N are zero.
@@ -315,160 +332,222 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
     return 512 * kTri * (bwd ? 3 * kPlanes<E> : kPlanes<E> + 1);
 }
 
-// Everything of one chunk and head that no state enters.  One wave per block of
-// 16 tokens.  cs is summed in 64 bits, since Gam takes differences of it; A in
-// fp32 in LDS.  The inverse goes by blocks of 16: the diagonal blocks' inverses
-// Tm = (I + Db A)^-1 by substitution (a wave each, a column per lane), then block
-// row i of N from right to left,
+// Everything of one chunk and head that no state enters, by one wave: no barrier, and the
+// four waves of a workgroup keep a CU's SIMDs busy with four of them.  A wave takes `hpw`
+// heads of a group one after another, so that K K^T and Q K^T, which they share, are
+// formed once.  cs is summed in 64 bits, since Gam takes differences of it.
+//
+// Blocks of 16 x 16 (i, j <= i), as accumulators with rows s of block j and columns t of
+// block i: four consecutive slots of an operand block with rows t.  Between different
+// blocks Gam is a product of two prepared factors (kVec), on the diagonal an exponential.
+// The inverse goes by blocks too: the diagonal blocks' inverses Tm = (I + Db A)^-1 by
+// substitution, the four of them side by side (lane group g: block g, a column per lane),
+// then block row i of N from right to left,
 //   N_ij = (A_ij - sum_{j < k <= i} N_ik (Db A)_kj) Tm_jj,
-// transposed, so that the accumulators are the next product's second operand and
-// hold four consecutive slots of N's operand blocks.  fp32 matrix instructions.
-template <typename E, int NT, bool BWD>
-__global__ __launch_bounds__(kThreads) void k_gdr_prep(const E *__restrict__ kq, const E *__restrict__ gate,
-                                                       const E *__restrict__ beta, float *__restrict__ vec,
-                                                       E *__restrict__ tri, Chunks m, int H, int G, float scale)
+// transposed, so that an accumulator is the next product's second operand.  fp32 matrix
+// instructions; A's blocks lie in LDS for the first operands.
+constexpr int kPrepRow = 20, kPrepBlock = 16 * kPrepRow + 4;   // floats: 16-byte rows, blocks on other banks
+constexpr int kPrepTables = 7 * kC;                            // row factor, 3 column factors, cs hi, lo, beta
+constexpr int kPrepWave = 10 * kPrepBlock + 4 * 16 * 17 + kPrepTables;
+__device__ __forceinline__ constexpr int tri_block(int i, int j) { return i * (i + 1) / 2 + j; }
+
+// What this wave's lanes wrote to LDS is there for all of them (LDS serves a wave in order;
+// the compiler has to keep that order too).
+__device__ __forceinline__ void wave_sync()
 {
-    constexpr int LD = kC + 4, NK = NT / 32, kMat = kC * NT;
-    __shared__ __attribute__((aligned(16))) float A[kC * LD];
-    __shared__ __attribute__((aligned(16))) float Tm[4][16][17];
-    __shared__ double csd[kC];
-    __shared__ float bt[kC];
-    const int c = blockIdx.x / H, h = blockIdx.x % H;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <typename E, int NT, bool BWD>
+__global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ kq, const E *__restrict__ gate,
+                                                          const E *__restrict__ beta, float *__restrict__ vec,
+                                                          E *__restrict__ tri, Chunks m, int H, int G, float scale,
+                                                          int hpw, int units)
+{
+    constexpr int NK = NT / 32, kMat = kC * NT, PL = 512 * kTri;
+    __shared__ __attribute__((aligned(16))) float lds[4 * kPrepWave];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+    float *A = lds + wv * kPrepWave, *Tm = A + 10 * kPrepBlock, *row = Tm + 4 * 16 * 17, *col = row + kC, *chi = row + 4 * kC,
+          *clo = chi + kC, *bt = clo + kC;
+    const int unit = blockIdx.x * 4 + wv;   // (chunk, group, part of its heads)
+    if (unit >= units) return;
+    const int hpg = H / G, parts = (hpg + hpw - 1) / hpw;
+    const int part = unit % parts, grp = unit / parts % G, c = unit / (parts * G);
     int64_t t0;
     int count;
     chunk_at(m, c, t0, count);
     if (count <= 0) return;
-    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
-    const int64_t unit = (int64_t)c * H + h;
-    if (i == 0) {
-        float gv = 0.f, bv = 0.f;
-        if (lane < count) {
-            gv = to_float(gate[(t0 + lane) * H + h]);
-            bv = to_float(beta[(t0 + lane) * H + h]);
-        }
-        double s = gv < kMinLogDecay ? kMinLogDecay : gv;
+    const E *kf = kq + ((int64_t)c * G + grp) * (BWD ? 4 : 3) * kMat + 8 * lane, *qf = kf + 2 * kMat;
+    floatx4 kk[10], qk[10];
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_up(s, d);
-            if (lane >= d) s += o;
+    for (int b = 0; b < 10; ++b) kk[b] = qk[b] = floatx4{0, 0, 0, 0};
+    for (int kb = 0; kb < NK; ++kb) {
+        frag_t<E> k[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k[i] = load_frag(kf + (i * NK + kb) * 512);
+            q[i] = load_frag(qf + (i * NK + kb) * 512);
         }
-        csd[lane] = s;
-        bt[lane] = bv;
-        const double last = __shfl(s, 63);
-        float *vo = vec + unit * kVec;
-        const float hi = (float)s;
-        const float since = exp2_((float)(s * kLog2eD)), till = exp2_((float)((last - s) * kLog2eD));
-        vo[kSince + lane] = since;
-        vo[kBeta + lane] = bv;
-        vo[kScaled + lane] = scale * since;
-        vo[kTillBeta + lane] = till * bv;
-        vo[kTill + lane] = till;
-        vo[kErase + lane] = -bv * since;
-        vo[kCsHi + lane] = hi;
-        vo[kCsLo + lane] = (float)(s - (double)hi);
-        if (BWD) {
-            const int blk = lane >> 4;
-            const double r = __shfl(s, blk ? 16 * blk - 1 : 0);
-            const float row = lane < count ? exp2_((float)((s - (blk ? r : 0.0)) * kLog2eD)) : 0.f;
-            vo[kRowScale + lane] = scale * row;
-            vo[kRowBeta + lane] = bv * row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                mma(kk[tri_block(i, j)], k[j], k[i]);
+                mma(qk[tri_block(i, j)], k[j], q[i]);
+            }
+    }
+    Select<E> sel;
+    sel.init(lane);
+    const int h0 = grp * hpg + part * hpw, h1 = h0 + hpw < (grp + 1) * hpg ? h0 + hpw : (grp + 1) * hpg;
+    for (int h = h0; h < h1; ++h) {
+        const int64_t u = (int64_t)c * H + h;
+        {
+            float gv = 0.f, bv = 0.f;
+            if (lane < count) {
+                gv = to_float(gate[(t0 + lane) * H + h]);
+                bv = to_float(beta[(t0 + lane) * H + h]);
+            }
+            double s = gv < kMinLogDecay ? kMinLogDecay : gv;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double o = __shfl_up(s, d);
+                if (lane >= d) s += o;
+            }
+            const double last = __shfl(s, 63);
+            float *vo = vec + u * kVec;
+            const float hi = (float)s, lo = (float)(s - (double)hi);
+            const float since = exp2_((float)(s * kLog2eD)), till = exp2_((float)((last - s) * kLog2eD));
+            const double ref[4] = {0.0, __shfl(s, 15), __shfl(s, 31), __shfl(s, 47)};
+            const double r = g == 0 ? ref[0] : g == 1 ? ref[1] : g == 2 ? ref[2] : ref[3];
+            const float rf = exp2_((float)((s - r) * kLog2eD));
+            vo[kSince + lane] = since;
+            vo[kBeta + lane] = bv;
+            vo[kScaled + lane] = scale * since;
+            vo[kTillBeta + lane] = till * bv;
+            vo[kTill + lane] = till;
+            vo[kErase + lane] = -bv * since;
+            vo[kCsHi + lane] = hi;
+            vo[kCsLo + lane] = lo;
+            row[lane] = rf;
+            chi[lane] = hi;
+            clo[lane] = lo;
+            bt[lane] = bv;
+            if (BWD) {
+                vo[kRowScale + lane] = lane < count ? scale * rf : 0.f;
+                vo[kRowBeta + lane] = lane < count ? bv * rf : 0.f;
+            }
 #pragma unroll
             for (int k = 1; k < 4; ++k) {
-                const double rk = __shfl(s, 16 * k - 1);
-                vo[kColBeta + (k - 1) * kC + lane] = lane < 16 * k ? bv * exp2_((float)((rk - s) * kLog2eD)) : 0.f;
+                const float cf = lane < 16 * k ? exp2_((float)((ref[k] - s) * kLog2eD)) : 0.f;
+                col[(k - 1) * kC + lane] = cf;
+                if (BWD) vo[kColBeta + (k - 1) * kC + lane] = bv * cf;
             }
         }
-    }
-    __syncthreads();
-    const E *kf = kq + ((int64_t)c * G + h / (H / G)) * (BWD ? 4 : 3) * kMat, *qf = kf + 2 * kMat;
-    E *tri_o = tri + unit * tri_elems<E>(BWD);
-    constexpr int64_t PL = 512 * kTri;
-    E *n_o = tri_o, *p_o = tri_o + kPlanes<E> * PL;
-    E *nt_o = tri_o + kPlanes<E> * PL, *pt_o = nt_o + kPlanes<E> * PL;   // backward
-
-    // blocks (i, j) of K K^T and Q K^T, j <= i, with rows s and columns t
-    frag_t<E> ki[NK], qi[NK];
+        wave_sync();
+        E *n_o = tri + u * tri_elems<E>(BWD), *p_o = n_o + kPlanes<E> * PL, *nt_o = p_o, *pt_o = nt_o + kPlanes<E> * PL;
+        floatx4 a[10], p[10];
 #pragma unroll
-    for (int kb = 0; kb < NK; ++kb) {
-        ki[kb] = load_frag(kf + (i * NK + kb) * 512 + 8 * lane);
-        qi[kb] = load_frag(qf + (i * NK + kb) * 512 + 8 * lane);
-    }
-    const int t = 16 * i + l;
-    for (int j = 0; j <= (i | 1); ++j) {
-        floatx4 a = floatx4{0, 0, 0, 0}, p = a, pt = a;
-        if (j <= i) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb) {
-                const frag_t<E> kj = load_frag(kf + (j * NK + kb) * 512 + 8 * lane);
-                mma(a, kj, ki[kb]);
-                if (BWD) mma(pt, qi[kb], kj);
-                else mma(p, kj, qi[kb]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int s = 16 * j + 4 * g + r;
-                const float gam = exp2_((float)((csd[t] - csd[s]) * kLog2eD));
-                a[r] = s < t ? gam * a[r] : 0.f;
-                if (!BWD) p[r] = s <= t ? scale * gam * p[r] : 0.f;
-                else {   // rows t, columns s
-                    const int tt = 16 * i + 4 * g + r, ss = 16 * j + l;
-                    pt[r] = ss <= tt ? scale * exp2_((float)((csd[tt] - csd[ss]) * kLog2eD)) * pt[r] : 0.f;
-                }
-            }
-            *reinterpret_cast<floatx4 *>(&A[t * LD + 16 * j + 4 * g]) = a;
-        }
-        if (!BWD) store_round4(p_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), p);
-        else store_split4(pt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, pt);
-    }
-    __syncthreads();
-    {
-        // column l of Tm_ii (the four lane groups do the same work)
-        float x[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < r; ++e) s += A[(16 * i + r) * LD + 16 * i + e] * x[e];
-            x[r] = (r == l ? 1.f : 0.f) - bt[16 * i + r] * s;
-        }
-        if (g == 0)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) Tm[i][r][l] = x[r];
-    }
-    __syncthreads();
-    floatx4 nt[4];   // N^T_ji: rows s of block j, columns t of block i
-#pragma unroll
-    for (int j = 3; j >= 0; --j) {
-        floatx4 x = floatx4{0, 0, 0, 0}, n = x;
-        if (j <= i) {
-            x = *reinterpret_cast<const floatx4 *>(&A[t * LD + 16 * j + 4 * g]);
-#pragma unroll
-            for (int k = j + 1; k < 4; ++k)
-                if (k <= i)
+            for (int j = 0; j <= i; ++j) {
+                const int b = tri_block(i, j), t = 16 * i + l;
+                floatx4 gam;
+                if (j < i) {
+                    gam = row[t] * vec4(col + (i - 1) * kC + 16 * j + 4 * g);
+                    a[b] = gam * kk[b];
+                    p[b] = (scale * gam) * qk[b];
+                } else {
+                    const floatx4 oh = vec4(chi + 16 * j + 4 * g), ol = vec4(clo + 16 * j + 4 * g);
+                    const float th = chi[t], tl = clo[t];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int kt = 16 * k + 4 * g + r;
-                        x = __builtin_amdgcn_mfma_f32_16x16x4f32(-bt[kt] * A[kt * LD + 16 * j + l], nt[k][r], x, 0, 0, 0);
+                        const int s = 4 * g + r;
+                        gam[r] = exp2_(s <= l ? ((th - oh[r]) + (tl - ol[r])) * kLog2e : 0.f);
+                        a[b][r] = s < l ? gam[r] * kk[b][r] : 0.f;
+                        p[b][r] = s <= l ? scale * gam[r] * qk[b][r] : 0.f;
                     }
+                }
+                *reinterpret_cast<floatx4 *>(A + b * kPrepBlock + l * kPrepRow + 4 * g) = a[b];
+            }
+        wave_sync();
+        {
+            // column l of Tm of diagonal block g
+            const float *D = A + tri_block(0, 0) * kPrepBlock;
+            D = A + (g == 0 ? tri_block(0, 0) : g == 1 ? tri_block(1, 1) : g == 2 ? tri_block(2, 2) : tri_block(3, 3)) * kPrepBlock;
+            float x[16];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                n = __builtin_amdgcn_mfma_f32_16x16x4f32(Tm[j][4 * g + r][l], x[r], n, 0, 0, 0);
+            for (int r = 0; r < 16; ++r) {
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < r; ++e) s += D[r * kPrepRow + e] * x[e];
+                x[r] = (r == l ? 1.f : 0.f) - bt[16 * g + r] * s;
+                Tm[(16 * g + r) * 17 + l] = x[r];
+            }
         }
-        nt[j] = n;
-        if (j <= (i | 1)) store_split4(n_o + lower_block(i, j >> 1) * 512 + 8 * lane + 4 * (j & 1), PL, n);
-    }
-    if (!BWD) return;
-    __syncthreads();
+        wave_sync();
+        // first operands: -(Db A)_kj (rows: tokens of block j) and Tm_jj^T
+        float op[6][4], tm[4][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j <= i) *reinterpret_cast<floatx4 *>(&A[t * LD + 16 * j + 4 * g]) = nt[j];
-    __syncthreads();
-    for (int j = 0; j <= (i | 1); ++j) {
-        floatx4 v = floatx4{0, 0, 0, 0};
-        if (j <= i)
+        for (int k = 1; k < 4; ++k)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = A[(16 * i + 4 * g + r) * LD + 16 * j + l];
-        store_split4(nt_o + upper_block(j, i >> 1) * 512 + 8 * lane + 4 * (i & 1), PL, v);
+            for (int j = 0; j < k; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    op[k * (k - 1) / 2 + j][r] = -bt[16 * k + 4 * g + r] * A[tri_block(k, j) * kPrepBlock + (4 * g + r) * kPrepRow + l];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) tm[j][r] = Tm[(16 * j + 4 * g + r) * 17 + l];
+        // N^T, all block rows i at once (they are independent), j falling
+#pragma unroll
+        for (int dj = 0; dj < 4; ++dj)
+#pragma unroll
+            for (int i = dj; i < 4; ++i) {
+                const int j = i - dj;
+                floatx4 x = a[tri_block(i, j)], n = floatx4{0, 0, 0, 0};
+#pragma unroll
+                for (int k = j + 1; k <= i; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x = __builtin_amdgcn_mfma_f32_16x16x4f32(op[k * (k - 1) / 2 + j][r], a[tri_block(i, k)][r], x, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) n = __builtin_amdgcn_mfma_f32_16x16x4f32(tm[j][r], x[r], n, 0, 0, 0);
+                a[tri_block(i, j)] = n;   // A_ij is not needed again
+            }
+        // N with rows t; Gam Q K^T with rows t (forward); both with rows s (backward), through
+        // products with the identity, plane by plane
+        const floatx4 none = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int kb = 0; kb <= i / 2; ++kb) {
+                const int j = 2 * kb;
+                const bool two = j + 1 <= i;
+                frag_t<E> f[2 * 2];   // hi, lo of N; hi, lo of the pair matrix
+                split_pair(a[tri_block(i, j)], two ? a[tri_block(i, two ? j + 1 : j)] : none, f[0], f[1]);
+                store_frag(n_o + lower_block(i, kb) * 512 + 8 * lane, f[0]);
+                if (kPlanes<E> == 2) store_frag(n_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[1]);
+                if (!BWD) {
+                    store_frag(p_o + lower_block(i, kb) * 512 + 8 * lane,
+                               round_pair<E>(p[tri_block(i, j)], two ? p[tri_block(i, two ? j + 1 : j)] : none));
+                    continue;
+                }
+                split_pair(p[tri_block(i, j)], two ? p[tri_block(i, two ? j + 1 : j)] : none, f[2], f[3]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    E *o = (x ? pt_o : nt_o) + 8 * lane + 4 * (i & 1);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int pl = 0; pl < kPlanes<E>; ++pl) {
+                            floatx4 d = none;
+                            mma(d, f[2 * x + pl], sel.half[half]);
+                            store_round4(o + pl * PL + upper_block(j + half, i >> 1) * 512, d);
+                        }
+                }
+            }
+        wave_sync();
     }
 }
 
@@ -520,22 +599,6 @@ __device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], i
     }
 }
 
-// Rows of the identity as a second operand: slot row (g, j) of a 32-row block against
-// column 16 HALF + l.  An operand read as a first operand is its transpose; a product
-// with these moves it to accumulators, exactly, with rows and columns exchanged.  That
-// is how tiles enter and leave a chain with four consecutive elements per lane instead
-// of one (4 accesses of 8 bytes instead of 16 of 2).
-template <typename E> struct Select {
-    frag_t<E> half[2];
-    __device__ __forceinline__ void init(int lane)
-    {
-        const int g = lane >> 4, l = lane & 15;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) half[h][j] = from_float<E>(slot_row(g, j) == 16 * h + l ? 1.f : 0.f);
-    }
-};
 // S, U, D and H of a chunk and head are kept as operand blocks with their columns p as
 // slots (in order, 8 per lane), kColBlocks blocks of 32 columns for each row block, the
 // columns after these after all rows: what the gradient kernel takes at a time is
@@ -633,7 +696,6 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t l
     }
 }
 
-__device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
 
 // ---- operands of a chain's step, staged through LDS ----
 // The waves of a workgroup own different columns and read the same first operands, 44
