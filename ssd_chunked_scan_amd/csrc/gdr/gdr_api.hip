@@ -106,18 +106,25 @@ Sizes sizes_of(const Shape &s)
     return z;
 }
 
-// The heads of a group go to `hsplit` workgroups of the gradient kernel when the
-// chunks and groups alone would leave the GPU short of them (about 1024 wanted);
-// every split adds fp32 sums of dq and dk to write and read back.
+// The heads of a group go to `hsplit` workgroups of the gradient kernel.  One workgroup is
+// what a CU holds, so a run takes rounds of 256; a workgroup takes its heads and about two
+// heads' time to start and to end; every split adds fp32 sums of dq and dk to write and
+// read back, about one.
 int64_t head_split(const Shape &s)
 {
     const int64_t tiles = s.nct * s.G, hpg = s.H / s.G;
-    int64_t k = tiles ? (1024 + tiles - 1) / tiles : 1;
-    return k > hpg ? hpg : k < 1 ? 1 : k;
+    int64_t best = 1, cost = INT64_MAX;
+    for (int64_t k = 1; k <= hpg && k <= 32; ++k) {
+        const int64_t c = (tiles * k + 255) / 256 * ((hpg + k - 1) / k + 2) + (k > 1 ? 1 : 0);
+        if (c < cost) {
+            cost = c;
+            best = k;
+        }
+    }
+    return best;
 }
 
-constexpr int64_t kPrepWaves = 4096;   // four per SIMD
-constexpr int64_t kNarrowUpTo = 256;   // wide workgroups: one per CU
+constexpr int64_t kNarrowUpTo = 256;    // wide workgroups: one per CU
 
 struct Workspace {
     size_t cmap, chain, range, order, kq, vec, tri, sst, ust, dst, hst, part, total;
@@ -184,17 +191,24 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
     }
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        E *kq = reinterpret_cast<E *>(ws + w.kq);
-        hipLaunchKernelGGL((k_gdr_frags<E, NT>), dim3((unsigned)(s.nct * s.G), 2), dim3(kThreads), 0, st,
-                           (const E *)a->k, (const E *)a->q, kq, *m, (int)s.G, (int)s.N, BWD ? 4 : 3);
-        // heads per wave: what K K^T costs is shared by them, but every SIMD wants waves first
+        // heads per wave: 2048 waves (two per SIMD) run at a time, and a wave pays for K K^T and
+        // Q K^T once, about NT / 256 of a head's time
         const int64_t hpg = s.H / s.G;
-        int64_t hpw = s.nct * s.H / kPrepWaves;
-        hpw = hpw > hpg ? hpg : hpw < 1 ? 1 : hpw;
+        int64_t hpw = 1;
+        double cost = 1e300;
+        for (int64_t k = 1; k <= hpg && k <= 32; ++k) {
+            const int64_t waves = s.nct * s.G * ((hpg + k - 1) / k);
+            const double t = (double)((waves + 2047) / 2048) * ((double)k + (double)NT / 256);
+            if (t < cost) {
+                cost = t;
+                hpw = k;
+            }
+        }
         const int64_t units = s.nct * s.G * ((hpg + hpw - 1) / hpw);
-        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)((units + 3) / 4)), dim3(kThreads), 0, st,
-                           (const E *)kq, (const E *)a->g, (const E *)a->beta, reinterpret_cast<float *>(ws + w.vec),
-                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, a->scale, (int)hpw, (int)units);
+        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)((units + 2 * s.nct * s.G + 3) / 4)),
+                           dim3(kThreads), 0, st, (const E *)a->k, (const E *)a->q, (const E *)a->g, (const E *)a->beta,
+                           reinterpret_cast<E *>(ws + w.kq), reinterpret_cast<float *>(ws + w.vec),
+                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, (int)s.N, a->scale, (int)hpw, (int)units);
         return launched();
     });
 }

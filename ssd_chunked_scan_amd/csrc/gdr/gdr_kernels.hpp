@@ -272,58 +272,31 @@ template <typename E> struct Select {
             for (int j = 0; j < 8; ++j) half[h][j] = from_float<E>(slot_row(g, j) == 16 * h + l ? 1.f : 0.f);
     }
 };
-// K and Q of one chunk and group as operand blocks in slot order: rows (64 tokens,
-// slots over N: 4 x NT/32 blocks) and transposed (NT rows n, slots over tokens:
-// NT/16 x 2 blocks).  Tokens past the chunk's count and columns past N are zero.
-// `out` [which] : 0 = K rows, 1 = K^T, 2 = Q rows, 3 = Q^T (backward only).
-template <typename E, int NT>
-__global__ __launch_bounds__(kThreads) void k_gdr_frags(const E *__restrict__ k, const E *__restrict__ q,
-                                                        E *__restrict__ out, Chunks m, int G, int N, int nmat)
+// One element through a buffer resource: out of range reads are zero and writes are
+// dropped, so ragged tiles need no branches (a branch around each of 16 loads makes
+// each wait for its own).
+template <typename E> __device__ __forceinline__ E bload_elem(__amdgpu_buffer_rsrc_t r, uint32_t off)
 {
-    constexpr int LD = NT + 16 / (int)sizeof(E);   // LDS row stride: 16 bytes of padding
-    __shared__ __attribute__((aligned(16))) E tile[kC * LD];
-    const int c = blockIdx.x / G, grp = blockIdx.x % G, src = blockIdx.y;   // src: 0 = k, 1 = q
-    int64_t t0;
-    int count;
-    chunk_at(m, c, t0, count);
-    if (count <= 0) return;
-    constexpr int V = kVec16<E>;
-    const uint32_t ld = (uint32_t)(G * N) * sizeof(E);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc((src ? q : k) + (t0 * G + grp) * N, ((int64_t)(count - 1) * G + 1) * N * (int64_t)sizeof(E));
-    constexpr int IT = kC * NT / V / kThreads;
-    uint4 v[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int e = i * kThreads + threadIdx.x, t = e / (NT / V), n = (e % (NT / V)) * V;
-        v[i] = bload16(rs, n < N ? t * ld + n * sizeof(E) : kOffNone);
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int e = i * kThreads + threadIdx.x, t = e / (NT / V), n = (e % (NT / V)) * V;
-        *reinterpret_cast<uint4 *>(&tile[t * LD + n]) = v[i];
-    }
-    __syncthreads();
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
-    E *o = out + ((int64_t)c * G + grp) * nmat * kC * NT + (int64_t)(2 * src) * kC * NT;
-    for (int b = wv; b < 4 * (NT / 32); b += kThreads / 64) {
-        const E *row = &tile[(16 * (b / (NT / 32)) + l) * LD + 32 * (b % (NT / 32)) + 4 * g];
-        frag_t<E> f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = row[j];
-            f[4 + j] = row[16 + j];
-        }
-        store_frag(o + b * 512 + 8 * lane, f);
-    }
-    if (2 * src + 1 >= nmat) return;
-    o += kC * NT;
-    for (int b = wv; b < 2 * (NT / 16); b += kThreads / 64) {
-        frag_t<E> f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = tile[(32 * (b & 1) + slot_row(g, j)) * LD + 16 * (b >> 1) + l];
-        store_frag(o + b * 512 + 8 * lane, f);
-    }
+    if constexpr (sizeof(E) == 2)
+        return __builtin_bit_cast(E, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    else return __builtin_bit_cast(E, (unsigned int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
+template <typename E> __device__ __forceinline__ void bstore_elem(__amdgpu_buffer_rsrc_t r, uint32_t off, E v)
+{
+    if constexpr (sizeof(E) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), r, off, 0, 0);
+}
+// The buffer of one head's rows of a chunk: `count` rows of P elements, `ld` apart
+// (the host keeps 64 ld elements below 2^31 bytes).
+template <typename E> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const E *base, int count, int64_t ld, int P)
+{
+    return make_rsrc(base, ((count - 1) * ld + P) * (int64_t)sizeof(E));
+}
+// K and Q of one chunk and group are kept as operand blocks in slot order: rows (64
+// tokens, slots over N: 4 x NT/32 blocks) and transposed (NT rows n, slots over tokens:
+// NT/16 x 2 blocks), in the order K, K^T, Q, Q^T (the last for the backward only).  Tokens
+// past the chunk's count and columns past N are zero.
 
 // Elements of one (chunk, head) of the prepared triangles: N (its planes) and Gam o
 // Q K^T rounded; for the backward N, N^T and (Gam o Q K^T)^T (their planes).
@@ -335,7 +308,7 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 // Everything of one chunk and head that no state enters, by one wave: no barrier, and the
 // four waves of a workgroup keep a CU's SIMDs busy with four of them.  A wave takes `hpw`
 // heads of a group one after another, so that K K^T and Q K^T, which they share, are
-// formed once.  cs is summed in 64 bits, since Gam takes differences of it.
+// formed once.  Further waves write the operand blocks of K and Q.  cs is summed in 64 bits, since Gam takes differences of it.
 //
 // Blocks of 16 x 16 (i, j <= i), as accumulators with rows s of block j and columns t of
 // block i: four consecutive slots of an operand block with rows t.  Between different
@@ -360,9 +333,10 @@ __device__ __forceinline__ void wave_sync()
 }
 
 template <typename E, int NT, bool BWD>
-__global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ kq, const E *__restrict__ gate,
-                                                          const E *__restrict__ beta, float *__restrict__ vec,
-                                                          E *__restrict__ tri, Chunks m, int H, int G, float scale,
+__global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ kin, const E *__restrict__ qin,
+                                                          const E *__restrict__ gate, const E *__restrict__ beta,
+                                                          E *__restrict__ kq, float *__restrict__ vec,
+                                                          E *__restrict__ tri, Chunks m, int H, int G, int N, float scale,
                                                           int hpw, int units)
 {
     constexpr int NK = NT / 32, kMat = kC * NT, PL = 512 * kTri;
@@ -370,24 +344,85 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     float *A = lds + wv * kPrepWave, *Tm = A + 10 * kPrepBlock, *row = Tm + 4 * 16 * 17, *col = row + kC, *chi = row + 4 * kC,
           *clo = chi + kC, *bt = clo + kC;
-    const int unit = blockIdx.x * 4 + wv;   // (chunk, group, part of its heads)
-    if (unit >= units) return;
-    const int hpg = H / G, parts = (hpg + hpw - 1) / hpw;
-    const int part = unit % parts, grp = unit / parts % G, c = unit / (parts * G);
+    // units: (chunk, group, part of its heads), and after them (chunk, group, K or Q) to copy
+    const int job = blockIdx.x * 4 + wv, hpg = H / G, parts = (hpg + hpw - 1) / hpw;
+    const bool copies = job >= units;
+    const int unit = copies ? job - units : job, per = copies ? 2 : parts;
+    const int part = unit % per, grp = unit / per % G, c = unit / (per * G);
+    if (copies && unit >= 2 * (units / parts)) return;
     int64_t t0;
     int count;
     chunk_at(m, c, t0, count);
     if (count <= 0) return;
-    const E *kf = kq + ((int64_t)c * G + grp) * (BWD ? 4 : 3) * kMat + 8 * lane, *qf = kf + 2 * kMat;
+    E *copy = kq + ((int64_t)c * G + grp) * (BWD ? 4 : 3) * kMat + 8 * lane;
+    const __amdgpu_buffer_rsrc_t krs = rows_rsrc(kin + (t0 * G + grp) * N, count, (int64_t)G * N, N);
+    const __amdgpu_buffer_rsrc_t qrs = rows_rsrc(qin + (t0 * G + grp) * N, count, (int64_t)G * N, N);
+    Select<E> sel;
+    sel.init(lane);
     floatx4 kk[10], qk[10];
 #pragma unroll
     for (int b = 0; b < 10; ++b) kk[b] = qk[b] = floatx4{0, 0, 0, 0};
+    // 32 columns at a time, straight from the rows: slots 0..3 are columns 4 g .., 4..7 are 16 + 4 g ..
+    auto fetch = [&](__amdgpu_buffer_rsrc_t rs, int i, int kb) {
+        const int n = 32 * kb + 4 * g;
+        const uint32_t o = (uint32_t)((16 * i + l) * (G * N) + n) * (uint32_t)sizeof(E);
+        const uint32_t o0 = n < N ? o : kOffNone, o1 = n + 16 < N ? o + 16 * (uint32_t)sizeof(E) : kOffNone;
+        frag_t<E> f;
+        if constexpr (sizeof(E) == 2) {
+            const uint2 x = bload8s(rs, o0, 0), y = bload8s(rs, o1, 0);
+            f = __builtin_bit_cast(bf16x8, uint4{x.x, x.y, y.x, y.y});
+        } else {
+            const floatx4 x = __builtin_bit_cast(floatx4, bload16(rs, o0)), y = __builtin_bit_cast(floatx4, bload16(rs, o1));
+            f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        return f;
+    };
+    if (copies) {
+        const __amdgpu_buffer_rsrc_t rs = part ? qrs : krs;
+        E *o = copy + 2 * part * kMat;
+        const bool both = BWD || part == 0;
+#pragma unroll 2
+        for (int kb = 0; kb < NK; ++kb) {
+            frag_t<E> f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = fetch(rs, i, kb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_frag(o + (i * NK + kb) * 512, f[i]);
+            if (!both) continue;
+            // the columns' blocks of the transpose, through products with the identity
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    floatx4 a = floatx4{0, 0, 0, 0}, b = a;
+                    mma(a, f[2 * tb], sel.half[half]);
+                    mma(b, f[2 * tb + 1], sel.half[half]);
+                    store_frag(o + kMat + (2 * (2 * kb + half) + tb) * 512, round_pair<E>(a, b));
+                }
+        }
+        return;
+    }
+    // (for the pairs any order of the slots will do: eight consecutive columns, one load)
+    auto fetch8 = [&](__amdgpu_buffer_rsrc_t rs, int i, int kb) {
+        const int n = 32 * kb + 8 * g;
+        frag_t<E> f;
+        bload_frag(rs, n < N ? (uint32_t)((16 * i + l) * (G * N) + n) * (uint32_t)sizeof(E) : kOffNone, f);
+        return f;
+    };
+    frag_t<E> kn[4], qn[4];   // the next 32 columns, on their way
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        kn[i] = fetch8(krs, i, 0);
+        qn[i] = fetch8(qrs, i, 0);
+    }
     for (int kb = 0; kb < NK; ++kb) {
         frag_t<E> k[4], q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            k[i] = load_frag(kf + (i * NK + kb) * 512);
-            q[i] = load_frag(qf + (i * NK + kb) * 512);
+            k[i] = kn[i];
+            q[i] = qn[i];
+            kn[i] = fetch8(krs, i, kb + 1);   // (past the end: zero)
+            qn[i] = fetch8(qrs, i, kb + 1);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -397,8 +432,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                 mma(qk[tri_block(i, j)], k[j], q[i]);
             }
     }
-    Select<E> sel;
-    sel.init(lane);
     const int h0 = grp * hpg + part * hpw, h1 = h0 + hpw < (grp + 1) * hpg ? h0 + hpw : (grp + 1) * hpg;
     for (int h = h0; h < h1; ++h) {
         const int64_t u = (int64_t)c * H + h;
@@ -623,27 +656,6 @@ template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *ds
     }
 }
 
-// One element through a buffer resource: out of range reads are zero and writes are
-// dropped, so ragged tiles need no branches (a branch around each of 16 loads makes
-// each wait for its own).
-template <typename E> __device__ __forceinline__ E bload_elem(__amdgpu_buffer_rsrc_t r, uint32_t off)
-{
-    if constexpr (sizeof(E) == 2)
-        return __builtin_bit_cast(E, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
-    else return __builtin_bit_cast(E, (unsigned int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
-template <typename E> __device__ __forceinline__ void bstore_elem(__amdgpu_buffer_rsrc_t r, uint32_t off, E v)
-{
-    if constexpr (sizeof(E) == 2)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), r, off, 0, 0);
-}
-// The buffer of one head's rows of a chunk: `count` rows of P elements, `ld` apart
-// (the host keeps 64 ld elements below 2^31 bytes).
-template <typename E> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const E *base, int count, int64_t ld, int P)
-{
-    return make_rsrc(base, ((count - 1) * ld + P) * (int64_t)sizeof(E));
-}
 // A [64 tokens][16 columns] tile of a caller's tensor: lane (g, l) moves columns
 // 4 g .. 4 g + 3 of token 16 tb + l (`off`: byte offset of column p0 + 4 g, kOffNone past P).
 template <typename E> struct Tile {
