@@ -164,15 +164,6 @@ template <typename F> ssd_status with_nt(int64_t NT, F &&f)
     return f(std::integral_constant<int, 256>{});
 }
 
-// How the chains run: narrow (a step shared by a workgroup's waves) while wide workgroups
-// would not give every CU one, else wide with their operands in LDS where they fit.
-template <typename E, int NT, typename F, typename G> void with_flow(bool narrow, F &&wide, G &&slim)
-{
-    if (narrow) slim();
-    else if constexpr (kStaged<E, NT>) wide(std::integral_constant<int, 1>{});
-    else wide(std::integral_constant<int, 0>{});
-}
-
 // What both directions form first: the chunk map, the operand copies, the triangles.
 template <typename E, bool BWD>
 ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Workspace &w, Chunks *m, hipStream_t st)
@@ -255,15 +246,10 @@ template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_gdr_args *a
     c.s1 = a->final_states;
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        with_flow<E, NT>(
-            narrowed(c, s, 1),
-            [&](auto flow) {
-                hipLaunchKernelGGL((k_gdr_chain<E, NT / 16, decltype(flow)::value>), dim3((unsigned)c.units), dim3(kThreads),
-                                   0, st, c);
-            },
-            [&] {
-                hipLaunchKernelGGL((k_gdr_chain_narrow<E, NT / 16>), dim3((unsigned)c.units), dim3(64 * kNW<NT / 16>), 0, st, c);
-            });
+        if (narrowed(c, s, 1))
+            hipLaunchKernelGGL((k_gdr_chain_narrow<E, NT / 16>), dim3((unsigned)c.units), dim3(64 * kNW<NT / 16>), 0, st, c);
+        else
+            hipLaunchKernelGGL((k_gdr_chain<E, NT / 16, kStaged<E, NT>>), dim3((unsigned)c.units), dim3(kThreads), 0, st, c);
         return launched();
     });
 }
@@ -310,16 +296,12 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
     ga.scale = a->scale;
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        with_flow<E, NT>(
-            narrowed(c, s, 2),
-            [&](auto flow) {
-                hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, decltype(flow)::value>), dim3(2u * (unsigned)c.units),
-                                   dim3(kThreads), 0, st, c);
-            },
-            [&] {
-                hipLaunchKernelGGL((k_gdr_chains_narrow<E, NT / 16>), dim3(2u * (unsigned)c.units), dim3(64 * kNW<NT / 16>),
-                                   0, st, c);
-            });
+        if (narrowed(c, s, 2))
+            hipLaunchKernelGGL((k_gdr_chains_narrow<E, NT / 16>), dim3(2u * (unsigned)c.units), dim3(64 * kNW<NT / 16>), 0,
+                               st, c);
+        else
+            hipLaunchKernelGGL((k_gdr_chains<E, NT / 16, kStaged<E, NT>>), dim3(2u * (unsigned)c.units), dim3(kThreads), 0,
+                               st, c);
         hipLaunchKernelGGL((k_gdr_grad<E, NT / 16>), dim3((unsigned)(s.nct * s.G * hs)), dim3(kGradThreads), 0, st, ga);
         if (hs > 1)
             hipLaunchKernelGGL((k_gdr_grad_sum<E, NT>), dim3((unsigned)(s.nct * s.G), NT / 16), dim3(kThreads), 0, st,

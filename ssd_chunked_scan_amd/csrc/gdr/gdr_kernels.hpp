@@ -254,6 +254,16 @@ __device__ __forceinline__ void store_round4(bf16 *p, const floatx4 &v)
     *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
 }
 __device__ __forceinline__ void store_round4(float *p, const floatx4 &v) { *reinterpret_cast<floatx4 *>(p) = v; }
+// the same, past the caches
+__device__ __forceinline__ void store_round4_once(bf16 *p, const floatx4 &v)
+{
+    typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, reinterpret_cast<uint2v *>(p));
+}
+__device__ __forceinline__ void store_round4_once(float *p, const floatx4 &v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p));
+}
 
 __device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
 // Rows of the identity as a second operand: slot row (g, j) of a 32-row block against
@@ -280,12 +290,6 @@ template <typename E> __device__ __forceinline__ E bload_elem(__amdgpu_buffer_rs
     if constexpr (sizeof(E) == 2)
         return __builtin_bit_cast(E, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
     else return __builtin_bit_cast(E, (unsigned int)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
-template <typename E> __device__ __forceinline__ void bstore_elem(__amdgpu_buffer_rsrc_t r, uint32_t off, E v)
-{
-    if constexpr (sizeof(E) == 2)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), r, off, 0, 0);
 }
 // The buffer of one head's rows of a chunk: `count` rows of P elements, `ld` apart
 // (the host keeps 64 ld elements below 2^31 bytes).
@@ -652,7 +656,7 @@ template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *ds
     for (int b = 0; b < 2 * NF; ++b) {
         floatx4 d = floatx4{0, 0, 0, 0};
         mma(d, f[b >> 1], sel.half[b & 1]);
-        store_round4(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
+        store_round4_once(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
     }
 }
 
@@ -713,32 +717,34 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t l
 // The waves of a workgroup own different columns and read the same first operands, 44
 // to 72 KB a step at N = 128.  They come straight from memory into LDS (16 bytes per
 // lane, no registers), in two regions: phase 1 of a step reads what meets the entering
-// state (K, and Q or the pair matrix), phase 2 the rest.
-//   FLOW 1: while a phase computes from one region, the other one's next contents are
-//   in flight; one barrier before each phase says both that its operands are there and
-//   that the other region is free.
-//   FLOW 2: both regions twice (where 160 KB hold them); a whole step's operands are in
-//   flight while the step before it computes, with one barrier a step.
-//   FLOW 0: larger sets (fp32 at N = 256) are read from global memory by every wave.
+// state (K, and Q or the pair matrix), phase 2 the rest.  While a phase computes from one
+// region, the other one's next contents are in flight; one barrier before each phase says
+// both that its operands are there and that the other region is free.  Sets too large for
+// LDS (fp32 at N = 256) are read from global memory by every wave (STAGED false).
 template <typename E, int NT> constexpr bool kStaged = sizeof(E) * NT <= 512;
-template <typename E, int NT> constexpr bool kTwice = sizeof(E) * NT <= 256;
 
 // KIND 0: the forward (y), 1: the forward for the backward (S and U), 2: the backward
-template <typename E, int NB, int KIND, int FLOW> struct Regions {
+template <typename E, int NB, int KIND, bool STAGED> struct Regions {
     static constexpr int kMat = 4 * NB / 2;   // blocks of K, K^T, Q or Q^T (64 x NT)
     static constexpr int kN = kTri * kPlanes<E>;
     // phase 1: K | Q (KIND 0) or the transposed pair matrix (KIND 2)
     static constexpr int kOne = kMat + (KIND == 0 ? kMat : KIND == 2 ? kN : 0);
     // phase 2: N or N^T | the pair matrix (KIND 0) | K^T | Q^T (KIND 2)
     static constexpr int kTwo = kN + (KIND == 0 ? kTri : 0) + kMat + (KIND == 2 ? kMat : 0);
-    static constexpr int kBytes = FLOW ? FLOW * (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVecChain * 4 : 16;
+    static constexpr int kBytes = STAGED ? (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVecChain * 4 : 16;
 };
 
 typedef __attribute__((address_space(1))) const void *gptr_t;
 typedef __attribute__((address_space(3))) void *lptr_t;
 
+// What is read by one workgroup only is loaded, and what another kernel reads much later
+// is stored, past the caches (non-temporal), which keeps them for K and Q, whose blocks a
+// group's heads share: 8 x 2048 tokens of 80 heads, chains 666 -> 639 us, gradients 592 ->
+// 558 us; packed prompts' chains 245 -> 238 us.
+constexpr int kOnce = 2;
+
 // `n` operand blocks from memory to LDS, a wave every fourth block.
-template <typename E, int n> __device__ __forceinline__ void stage(const E *src, E *dst, int wv, int lane)
+template <typename E, int n, int HOW = 0> __device__ __forceinline__ void stage(const E *src, E *dst, int wv, int lane)
 {
     constexpr int V = kVec16<E>;
 #pragma unroll
@@ -748,7 +754,7 @@ template <typename E, int n> __device__ __forceinline__ void stage(const E *src,
 #pragma unroll
             for (int j = 0; j < 512; j += 64 * V)
                 __builtin_amdgcn_global_load_lds((gptr_t)(src + b * 512 + j + V * lane), (lptr_t)(dst + b * 512 + j), 16,
-                                                 0, 0);
+                                                 0, HOW);
     }
 }
 // This wave's loads have arrived.  Called before a step's stores are issued, so that
@@ -756,21 +762,20 @@ template <typename E, int n> __device__ __forceinline__ void stage(const E *src,
 __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
 
 // A step's operand pointers: in LDS, or in memory.
-template <typename E, int NB, int KIND, int FLOW> struct Operands {
-    using R = Regions<E, NB, KIND, FLOW>;
+template <typename E, int NB, int KIND, bool STAGED> struct Operands {
+    using R = Regions<E, NB, KIND, STAGED>;
     static constexpr int kMatE = kC * 16 * NB;
-    static constexpr bool LDS = FLOW != 0;
     E *one, *two;
     float *vecs;
     const E *kq, *tri;
     const float *vec;
-    int wv, lane, turn;   // turn: which copy of what is kept twice is being staged
+    int wv, lane, turn;   // turn: which of the two copies of the scalars is being staged
 
     __device__ __forceinline__ void init(char *smem, int wv_, int lane_)
     {
         one = reinterpret_cast<E *>(smem);
-        two = one + (FLOW == 2 ? 2 : 1) * R::kOne * 512;
-        vecs = reinterpret_cast<float *>(two + (FLOW == 2 ? 2 : 1) * R::kTwo * 512);
+        two = one + R::kOne * 512;
+        vecs = reinterpret_cast<float *>(two + R::kTwo * 512);
         wv = wv_;
         lane = lane_;
         turn = 0;
@@ -785,15 +790,12 @@ template <typename E, int NB, int KIND, int FLOW> struct Operands {
     }
     // in `tri`: N | Gam QK^T, or N | N^T | (Gam QK^T)^T; in `kq`: K | K^T | Q | Q^T
     static constexpr int kPL = 512 * kTri, kNt = kPlanes<E> * kPL, kPt = 2 * kPlanes<E> * kPL;
-    __device__ __forceinline__ E *one_at(int t) const { return one + (FLOW == 2 ? t * R::kOne * 512 : 0); }
-    __device__ __forceinline__ E *two_at(int t) const { return two + (FLOW == 2 ? t * R::kTwo * 512 : 0); }
     __device__ __forceinline__ void stage_one()
     {
-        if constexpr (LDS) {
-            E *o = one_at(turn);
-            stage<E, R::kMat>(kq, o, wv, lane);
-            if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, o + kMatE, wv, lane);
-            if (KIND == 2) stage<E, R::kN>(tri + kPt, o + kMatE, wv, lane);
+        if constexpr (STAGED) {
+            stage<E, R::kMat>(kq, one, wv, lane);
+            if (KIND == 0) stage<E, R::kMat>(kq + 2 * kMatE, one + kMatE, wv, lane);
+            if (KIND == 2) stage<E, R::kN, kOnce>(tri + kPt, one + kMatE, wv, lane);
             if (wv >= 2)   // kVecChain floats: two loads
                 __builtin_amdgcn_global_load_lds((gptr_t)(vec + 256 * (wv - 2) + 4 * lane),
                                                  (lptr_t)(vecs + kVecChain * turn + 256 * (wv - 2)), 16, 0, 0);
@@ -801,41 +803,35 @@ template <typename E, int NB, int KIND, int FLOW> struct Operands {
     }
     __device__ __forceinline__ void stage_two()
     {
-        if constexpr (LDS) {
-            E *o = two_at(turn);
-            stage<E, R::kN>(tri + (KIND == 2 ? kNt : 0), o, wv, lane);
+        if constexpr (STAGED) {
+            E *o = two;
+            stage<E, R::kN, kOnce>(tri + (KIND == 2 ? kNt : 0), o, wv, lane);
             o += R::kN * 512;
             if (KIND == 0) {
-                stage<E, kTri>(tri + kPlanes<E> * kPL, o, wv, lane);
+                stage<E, kTri, kOnce>(tri + kPlanes<E> * kPL, o, wv, lane);
                 o += kTri * 512;
             }
             stage<E, R::kMat>(kq + kMatE, o, wv, lane);
             if (KIND == 2) stage<E, R::kMat>(kq + 3 * kMatE, o + kMatE, wv, lane);
         }
     }
-    // the operands of the step whose turn is t
-    __device__ __forceinline__ const E *k(int t) const { return (LDS ? one_at(t) : kq) + 8 * lane; }
-    __device__ __forceinline__ const E *q(int t) const { return (LDS ? one_at(t) + kMatE : kq + 2 * kMatE) + 8 * lane; }
-    __device__ __forceinline__ const E *pt(int t) const { return (LDS ? one_at(t) + kMatE : tri + kPt) + 8 * lane; }
-    __device__ __forceinline__ const E *n(int t) const { return (LDS ? two_at(t) : tri + (KIND == 2 ? kNt : 0)) + 8 * lane; }
-    __device__ __forceinline__ const E *p(int t) const
+    __device__ __forceinline__ const E *k() const { return (STAGED ? one : kq) + 8 * lane; }
+    __device__ __forceinline__ const E *q() const { return (STAGED ? one + kMatE : kq + 2 * kMatE) + 8 * lane; }
+    __device__ __forceinline__ const E *pt() const { return (STAGED ? one + kMatE : tri + kPt) + 8 * lane; }
+    __device__ __forceinline__ const E *n() const { return (STAGED ? two : tri + (KIND == 2 ? kNt : 0)) + 8 * lane; }
+    __device__ __forceinline__ const E *p() const { return (STAGED ? two + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane; }
+    __device__ __forceinline__ const E *kt() const
     {
-        return (LDS ? two_at(t) + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane;
+        return (STAGED ? two + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
     }
-    __device__ __forceinline__ const E *kt(int t) const
-    {
-        return (LDS ? two_at(t) + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
-    }
-    __device__ __forceinline__ const E *qt(int t) const
-    {
-        return (LDS ? two_at(t) + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane;
-    }
-    __device__ __forceinline__ const float *scalars(int t) const { return LDS ? vecs + kVecChain * t : vec; }
+    __device__ __forceinline__ const E *qt() const { return (STAGED ? two + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane; }
+    // the scalars of the step whose turn is t
+    __device__ __forceinline__ const float *scalars(int t) const { return STAGED ? vecs + kVecChain * t : vec; }
 };
 
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
 // and not y.
-template <typename E, int NB, bool KEEP, int FLOW>
+template <typename E, int NB, bool KEEP, bool STAGED>
 __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *smem)
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
@@ -858,37 +854,28 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
     };
     Select<E> sel;
     sel.init(lane);
-    Operands<E, NB, KEEP ? 1 : 0, FLOW> op;
+    Operands<E, NB, KEEP ? 1 : 0, STAGED> op;
     op.init(smem, wv, lane);
     Tile<E> v;
     if (n > 0) {
         op.at(a, c0, h, grp);
         op.stage_one();
-        if (FLOW == 2) op.stage_two();
         v.load(rows_of(a.v, 0), ldb, poff, l);
     }
     for (int i = 0; i < n; ++i) {
         const int64_t u = (int64_t)(c0 + i) * a.H + h;
-        const int turn = op.turn;
-        if (FLOW) {
+        if (STAGED) {
             if (i == 0) loads_done();
             __syncthreads();
         }
-        if (FLOW == 1) op.stage_two();
+        op.stage_two();
         floatx4 R[4], X[4];
         v.rows(R, sel);
-        if (FLOW == 2 && i + 1 < n) {
-            op.at(a, c0 + i + 1, h, grp);
-            op.turn ^= 1;
-            op.stage_one();
-            op.stage_two();
-            v.load(rows_of(a.v, i + 1), ldb, poff, l);
-        }
-        const float *vec = op.scalars(turn);
+        const float *vec = op.scalars(op.turn);
         StateOps<E, NB> so_;
         so_.of(S);
         floatx4 ks[4], qs[4];
-        const E *kf = op.k(turn), *qf = op.q(turn);
+        const E *kf = op.k(), *qf = op.q();
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) ks[tb] = qs[tb] = floatx4{0, 0, 0, 0};
 #pragma unroll
@@ -910,12 +897,12 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
-        if (FLOW == 1) {
+        if (STAGED) {
             loads_done();
             __syncthreads();
         }
-        const E *nf = op.n(turn), *pf = op.p(turn), *ktf = op.kt(turn);
-        if (FLOW != 2 && i + 1 < n) {
+        const E *nf = op.n(), *pf = op.p(), *ktf = op.kt();
+        if (i + 1 < n) {
             op.at(a, c0 + i + 1, h, grp);
             op.turn ^= 1;
             op.stage_one();
@@ -956,7 +943,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 if (kPlanes<E> == 2) mma(S[nb], f, xl[kb]);
             }
         if (KEEP) {
-            if (FLOW) loads_done();
+            if (STAGED) loads_done();
             if (keep) {
                 store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane);
                 store_pieces<E>((E *)a.ust + u * kC * a.Pp, w, sel, p0, lane);
@@ -969,7 +956,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w[0]);
                 if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w[1]);
             }
-            if (FLOW) loads_done();
+            if (STAGED) loads_done();
             store_tile<E>(rows_of(a.y, i), ldb, poff, y, sel, l);
         }
     }
@@ -978,7 +965,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
 
 // One backward chain: D of every chunk (the gradient of the state that leaves it),
 // H, and dv.
-template <typename E, int NB, int FLOW>
+template <typename E, int NB, bool STAGED>
 __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *smem)
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
@@ -1001,37 +988,28 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
     };
     Select<E> sel;
     sel.init(lane);
-    Operands<E, NB, 2, FLOW> op;
+    Operands<E, NB, 2, STAGED> op;
     op.init(smem, wv, lane);
     Tile<E> dy;
     if (n > 0) {
         op.at(a, c0 + n - 1, h, grp);
         op.stage_one();
-        if (FLOW == 2) op.stage_two();
         dy.load(rows_of(a.dy, n - 1), ldb, poff, l);
     }
     for (int i = n - 1; i >= 0; --i) {
         const int64_t u = (int64_t)(c0 + i) * a.H + h;
-        const int turn = op.turn;
-        if (FLOW) {
+        if (STAGED) {
             if (i == n - 1) loads_done();
             __syncthreads();
         }
-        if (FLOW == 1) op.stage_two();
+        op.stage_two();
         floatx4 yt[4];
         dy.rows(yt, sel);
-        if (FLOW == 2 && i > 0) {
-            op.at(a, c0 + i - 1, h, grp);
-            op.turn ^= 1;
-            op.stage_one();
-            op.stage_two();
-            dy.load(rows_of(a.dy, i - 1), ldb, poff, l);
-        }
-        const float *vec = op.scalars(turn);
+        const float *vec = op.scalars(op.turn);
         StateOps<E, NB> dop;
         dop.of(D);
         const frag_t<E> y0 = round_pair<E>(yt[0], yt[1]), y1 = round_pair<E>(yt[2], yt[3]);   // exact
-        const E *kf = op.k(turn), *ptf = op.pt(turn);
+        const E *kf = op.k(), *ptf = op.pt();
         floatx4 W[4], X[4], bt[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) W[tb] = floatx4{0, 0, 0, 0};
@@ -1057,12 +1035,12 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
         frag_t<E> xh[2], xl[2];
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
-        if (FLOW == 1) {
+        if (STAGED) {
             loads_done();
             __syncthreads();
         }
-        const E *nt = op.n(turn), *ktf = op.kt(turn), *qtf = op.qt(turn);
-        if (FLOW != 2 && i > 0) {
+        const E *nt = op.n(), *ktf = op.kt(), *qtf = op.qt();
+        if (i > 0) {
             op.at(a, c0 + i - 1, h, grp);
             op.turn ^= 1;
             op.stage_one();
@@ -1112,7 +1090,7 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
                 mma(D[nb], f, xh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], f, xl[kb]);
             }
-        if (FLOW) loads_done();
+        if (STAGED) loads_done();
         store_tile<E>(rows_of(a.dv, i), ldb, poff, X, sel, l);
         if (keep) {
             store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, lane);
@@ -1615,11 +1593,11 @@ __device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *s
     save_state<NBW>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N, 16 * NBW * wv);
 }
 
-template <typename E, int NB, int FLOW>
+template <typename E, int NB, bool STAGED>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_chain(ChainArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0, FLOW>::kBytes];
-    chain_fwd<E, NB, false, FLOW>(a, blockIdx.x, smem);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0, STAGED>::kBytes];
+    chain_fwd<E, NB, false, STAGED>(a, blockIdx.x, smem);
 }
 template <typename E, int NB>
 __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chain_narrow(ChainArgs a)
@@ -1631,12 +1609,12 @@ __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chain_narrow(ChainArgs 
 }
 
 // The backward's two chains in one launch: neither needs the other.
-template <typename E, int NB, int FLOW>
+template <typename E, int NB, bool STAGED>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_chains(ChainArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2, FLOW>::kBytes];   // the larger of both
-    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, FLOW>(a, blockIdx.x, smem);
-    else chain_fwd<E, NB, true, FLOW>(a, blockIdx.x - a.units, smem);
+    __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2, STAGED>::kBytes];   // the larger of both
+    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, STAGED>(a, blockIdx.x, smem);
+    else chain_fwd<E, NB, true, STAGED>(a, blockIdx.x - a.units, smem);
 }
 template <typename E, int NB>
 __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chains_narrow(ChainArgs a)
@@ -1773,7 +1751,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 #pragma unroll
         for (int i = 0; i < kParts; i += 8)
             if (kParts % 8 == 0 || i + wv < kParts)
-                __builtin_amdgcn_global_load_lds((gptr_t)(src + mine + i * 64 * V), (lptr_t)(dst + (i + wv) * 64 * V), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((gptr_t)(src + mine + i * 64 * V), (lptr_t)(dst + (i + wv) * 64 * V), 16, 0, kOnce);
     };
     auto issue = [&](int j) {
         const int hi = j / NPC, pc = j - hi * NPC, h = h0 + hi;
