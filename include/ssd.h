@@ -381,7 +381,10 @@ ssd_status ssd_conv1d_silu(const ssd_conv_args *args, void *stream);
  *
  * ssd_gdr_fwd computes y and the final states in chunks of 64 tokens; ssd_gdr_bwd
  * every gradient; ssd_gdr_step one token per batch row.  Supported: batch >= 1,
- * seqlen >= 0, H % G == 0, P % 16 == 0, N % 16 == 0, N <= 256, P <= 4096.
+ * seqlen >= 0, H % G == 0, P % 16 == 0, N % 16 == 0, N <= 256, P <= 4096, H*P
+ * and G*N <= 2^22 (ssd_gdr_fwd and ssd_gdr_bwd: a chunk's rows are addressed in 31
+ * bits), seqlen <= 2^28 with seq_idx; batch, seqlen and nheads that need more chunks
+ * or chains than a grid or 31 bits count are SSD_ERR_BAD_SHAPE.
  * Results do not change from call to call: every sum has a fixed order.  g, beta
  * and their gradients need only the alignment of their elements (a token's gates
  * of a few heads may start anywhere).
@@ -469,7 +472,8 @@ ssd_status ssd_gdr_step(const ssd_gdr_step_args *args, void *stream);
  * parameters, and may each be NULL (1 and 0).  mean and rstd [rows] fp32 are
  * outputs that the backward reads; NULL if no backward follows.
  * Supported: rows >= 0, 1 <= dim <= 65536, rows * dim <= 2^40, any dim (odd ones
- * take narrower accesses).  mean and rstd need 4-byte alignment.  y may be x itself, not overlap it otherwise.
+ * take narrower accesses).  mean and rstd need 4-byte alignment.  y may be x itself,
+ * not overlap it otherwise.
  */
 typedef struct {
     int64_t rows, dim;

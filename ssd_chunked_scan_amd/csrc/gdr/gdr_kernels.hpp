@@ -127,7 +127,10 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
                                                          int4 *__restrict__ chain, int2 *__restrict__ cmap,
                                                          int *__restrict__ order, int T, int nseq, int ncmax)
 {
-    __shared__ int wsum[kMapThreads / 64], base, chunks[kMapThreads];
+    // chunks before a segment: 64 bits, since the overlapping ranges of an invalid stream may
+    // add up to more than 2^31
+    __shared__ int64_t wsum[kMapThreads / 64], base;
+    __shared__ int chunks[kMapThreads];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     for (int i = tid; i < nseq; i += kMapThreads) range[i] = int2{0, 0};
     if (tid == 0) base = 0;
@@ -165,20 +168,20 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
         const int i = i0 + tid;
         const int2 r = i < nseq ? range[i] : int2{0, 0};
         const int len = r.y > r.x ? r.y - r.x : 0, n = (len + kC - 1) / kC;
-        int s = n;
+        int64_t s = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(s, d);
+            const int64_t o = __shfl_up((long long)s, d);
             if (lane >= d) s += o;
         }
         if (lane == 63) wsum[wv] = s;
         chunks[tid] = n;
         __syncthreads();
-        int before = base;
+        int64_t before = base;
         for (int w = 0; w < wv; ++w) before += wsum[w];
-        const int c0 = before + s - n;
+        const int64_t c0 = before + s - n;
         if (i < nseq) {
-            const int lo = c0 < ncmax ? c0 : ncmax;
+            const int lo = c0 < ncmax ? (int)c0 : ncmax;
             chain[i] = int4{lo, c0 + n <= ncmax ? n : ncmax - lo, r.x, len};
             // long chains first (up to kMapThreads of them, each with its rank): a long one
             // started last would run alone at the end
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(kMapThreads) void k_gdr_map(const int32_t *__restri
             cmap[ch.x + j] = int2{r.x + j * kC, left < kC ? left : kC};
         }
     }
-    for (int c = base + tid; c < ncmax; c += kMapThreads) cmap[c] = int2{0, 0};
+    for (int64_t c = base + tid; c < ncmax; c += kMapThreads) cmap[c] = int2{0, 0};
 }
 
 // ---------------------------------------------------------------------------
