@@ -124,7 +124,17 @@ int64_t head_split(const Shape &s)
     return best;
 }
 
-constexpr int64_t kNarrowUpTo = 256;    // wide workgroups: one per CU
+// Narrow chains share a step among a workgroup's waves, wide ones have fewer bytes to load
+// per column.  Narrow where wide workgroups (of both directions together) would not come
+// near one per CU.  2048 tokens, heads of 64, whole passes in us, wide against narrow:
+//   forward   N = 64    128 heads 104, 99    192 heads 113, 122    256 heads 136, 181
+//             N = 128              147, 112              157, 147              163, 207
+//             N = 256              216, 150              226, 217              237, 275
+//   backward  N = 64    64 heads  195, 165   128 heads 264, 320
+//             N = 128             248, 196             321, 395
+//             N = 256             412, 342             582, 681
+constexpr int64_t kNarrowUpTo = 192;
+constexpr size_t kCacheBytes = (size_t)256 << 20;
 
 struct Workspace {
     size_t cmap, chain, range, order, kq, vec, tri, sst, ust, dst, hst, part, total;
@@ -196,10 +206,20 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
             }
         }
         const int64_t units = s.nct * s.G * ((hpg + hpw - 1) / hpw);
-        hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD>), dim3((unsigned)((units + 2 * s.nct * s.G + 3) / 4)),
-                           dim3(kThreads), 0, st, (const E *)a->k, (const E *)a->q, (const E *)a->g, (const E *)a->beta,
-                           reinterpret_cast<E *>(ws + w.kq), reinterpret_cast<float *>(ws + w.vec),
-                           reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H, (int)s.G, (int)s.N, a->scale, (int)hpw, (int)units);
+        // triangles that the last level of cache cannot hold are written past it: 370 MB of
+        // packed prompts, forming them and the chains 380 -> 366 us; 720 MB of a backward over
+        // 8 x 2048 tokens of 80 heads, all kernels 1433 -> 1404 us; but 100 MB of 2 x 2048 tokens
+        // of 24 heads 141 -> 160 us
+        const bool once = (size_t)(s.nct * s.H) * tri_elems<E>(BWD) * sizeof(E) > kCacheBytes;
+        auto launch = [&](auto past) {
+            hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD, decltype(past)::value>),
+                               dim3((unsigned)((units + 2 * s.nct * s.G + 3) / 4)), dim3(kThreads), 0, st, (const E *)a->k,
+                               (const E *)a->q, (const E *)a->g, (const E *)a->beta, reinterpret_cast<E *>(ws + w.kq),
+                               reinterpret_cast<float *>(ws + w.vec), reinterpret_cast<E *>(ws + w.tri), *m, (int)s.H,
+                               (int)s.G, (int)s.N, a->scale, (int)hpw, (int)units);
+        };
+        if (once) launch(std::true_type{});
+        else launch(std::false_type{});
         return launched();
     });
 }

@@ -257,15 +257,27 @@ __device__ __forceinline__ void store_round4(bf16 *p, const floatx4 &v)
     *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
 }
 __device__ __forceinline__ void store_round4(float *p, const floatx4 &v) { *reinterpret_cast<floatx4 *>(p) = v; }
-// the same, past the caches
-__device__ __forceinline__ void store_round4_once(bf16 *p, const floatx4 &v)
+// The same, past the caches where ONCE (non-temporal).
+typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
+typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
+template <bool ONCE> __device__ __forceinline__ void store_round4(bf16 *p, const floatx4 &v)
 {
-    typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
-    __builtin_nontemporal_store(uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, reinterpret_cast<uint2v *>(p));
+    if (ONCE) __builtin_nontemporal_store(uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, reinterpret_cast<uint2v *>(p));
+    else store_round4(p, v);
 }
-__device__ __forceinline__ void store_round4_once(float *p, const floatx4 &v)
+template <bool ONCE> __device__ __forceinline__ void store_round4(float *p, const floatx4 &v)
 {
-    __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p));
+    if (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p));
+    else store_round4(p, v);
+}
+template <bool ONCE, typename E> __device__ __forceinline__ void store_block(E *p, const frag_t<E> &f)
+{
+    if constexpr (!ONCE) store_frag(p, f);
+    else if constexpr (sizeof(E) == 2) __builtin_nontemporal_store(__builtin_bit_cast(uint4v, f), reinterpret_cast<uint4v *>(p));
+    else {
+        store_round4<true>(p, __builtin_shufflevector(f, f, 0, 1, 2, 3));
+        store_round4<true>(p + 4, __builtin_shufflevector(f, f, 4, 5, 6, 7));
+    }
 }
 
 __device__ __forceinline__ floatx4 vec4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
@@ -339,7 +351,7 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-template <typename E, int NT, bool BWD>
+template <typename E, int NT, bool BWD, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ kin, const E *__restrict__ qin,
                                                           const E *__restrict__ gate, const E *__restrict__ beta,
                                                           E *__restrict__ kq, float *__restrict__ vec,
@@ -440,14 +452,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
             }
     }
     const int h0 = grp * hpg + part * hpw, h1 = h0 + hpw < (grp + 1) * hpg ? h0 + hpw : (grp + 1) * hpg;
+    // a head's gates are requested while the head before it is worked on, ahead of that
+    // one's stores (a load waits for the stores issued before it): 238 -> 230 us of 8 x 2048
+    // tokens' 80 heads
+    const int64_t gat = (t0 + (lane < count ? lane : count - 1)) * H;
+    E g_next = gate[gat + h0], b_next = beta[gat + h0];
     for (int h = h0; h < h1; ++h) {
         const int64_t u = (int64_t)c * H + h;
         {
-            float gv = 0.f, bv = 0.f;
-            if (lane < count) {
-                gv = to_float(gate[(t0 + lane) * H + h]);
-                bv = to_float(beta[(t0 + lane) * H + h]);
-            }
+            const float gv = lane < count ? to_float(g_next) : 0.f, bv = lane < count ? to_float(b_next) : 0.f;
+            const int hn = h + 1 < h1 ? h + 1 : h;
+            g_next = gate[gat + hn];
+            b_next = beta[gat + hn];
             double s = gv < kMinLogDecay ? kMinLogDecay : gv;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
@@ -566,10 +582,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                 const bool two = j + 1 <= i;
                 frag_t<E> f[2 * 2];   // hi, lo of N; hi, lo of the pair matrix
                 split_pair(a[tri_block(i, j)], two ? a[tri_block(i, two ? j + 1 : j)] : none, f[0], f[1]);
-                store_frag(n_o + lower_block(i, kb) * 512 + 8 * lane, f[0]);
-                if (kPlanes<E> == 2) store_frag(n_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[1]);
+                store_block<ONCE>(n_o + lower_block(i, kb) * 512 + 8 * lane, f[0]);
+                if (kPlanes<E> == 2) store_block<ONCE>(n_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[1]);
                 if (!BWD) {
-                    store_frag(p_o + lower_block(i, kb) * 512 + 8 * lane,
+                    store_block<ONCE>(p_o + lower_block(i, kb) * 512 + 8 * lane,
                                round_pair<E>(p[tri_block(i, j)], two ? p[tri_block(i, two ? j + 1 : j)] : none));
                     continue;
                 }
@@ -583,7 +599,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                         for (int pl = 0; pl < kPlanes<E>; ++pl) {
                             floatx4 d = none;
                             mma(d, f[2 * x + pl], sel.half[half]);
-                            store_round4(o + pl * PL + upper_block(j + half, i >> 1) * 512, d);
+                            store_round4<ONCE>(o + pl * PL + upper_block(j + half, i >> 1) * 512, d);
                         }
                 }
             }
@@ -659,7 +675,7 @@ template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *ds
     for (int b = 0; b < 2 * NF; ++b) {
         floatx4 d = floatx4{0, 0, 0, 0};
         mma(d, f[b >> 1], sel.half[b & 1]);
-        store_round4_once(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
+        store_round4<true>(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
     }
 }
 
