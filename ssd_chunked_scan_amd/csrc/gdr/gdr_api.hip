@@ -107,15 +107,16 @@ Sizes sizes_of(const Shape &s)
 }
 
 // The heads of a group go to `hsplit` workgroups of the gradient kernel.  One workgroup is
-// what a CU holds, so a run takes rounds of 256; a workgroup takes its heads and about two
-// heads' time to start and to end; every split adds fp32 sums of dq and dk to write and
-// read back, about one.
+// what a CU holds, so a run takes rounds of 256.  In half heads' time: a workgroup takes its
+// heads and 4 to start and to end, and every split adds fp32 sums of dq and dk to write and
+// read back, about 2; fp32's matrix instructions make a head itself twice as long.
 int64_t head_split(const Shape &s)
 {
     const int64_t tiles = s.nct * s.G, hpg = s.H / s.G;
+    const int64_t ends = s.dtype == SSD_DTYPE_BF16 ? 4 : 2, sums = s.dtype == SSD_DTYPE_BF16 ? 2 : 1;
     int64_t best = 1, cost = INT64_MAX;
     for (int64_t k = 1; k <= hpg && k <= 32; ++k) {
-        const int64_t c = (tiles * k + 255) / 256 * ((hpg + k - 1) / k + 2) + (k > 1 ? 1 : 0);
+        const int64_t c = (tiles * k + 255) / 256 * (2 * ((hpg + k - 1) / k) + ends) + (k > 1 ? sums : 0);
         if (c < cost) {
             cost = c;
             best = k;
