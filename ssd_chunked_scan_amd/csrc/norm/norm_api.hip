@@ -40,16 +40,6 @@ ssd_status check_dims(int64_t rows, int64_t dim, int dtype)
     return SSD_OK;
 }
 
-// Workgroups of the backward, each a strip of consecutive rows: enough to keep
-// every CU loading, few enough that the rows of partial sums stay a small part of
-// the traffic.
-constexpr int64_t kStrips = 512;
-int64_t strip_of(int64_t rows, int row_groups)
-{
-    const int64_t s = (rows + kStrips - 1) / kStrips;
-    return (s + row_groups - 1) / row_groups * row_groups;
-}
-
 // How a row of `dim` is held: vector width, lanes per row and vectors per lane (0:
 // longer than the registers).
 struct Plan {
@@ -75,6 +65,19 @@ Plan plan_of(int64_t dim, int dtype)
     p.L = 0;
     p.IT = 0;
     return p;
+}
+
+// Rows per workgroup of the backward: as many workgroups (strips) as keep every CU loading,
+// few enough that the rows of partial sums stay a small part of the traffic.  512 for rows of
+// 2 KB and more and for fp32; bf16 rows that are shorter, or read by single elements, keep
+// few bytes in flight per workgroup and take 1024.  2^26 elements in us, 512 against 1024:
+// bf16 dim 64 135, 109; 320 115, 97; 1531 137, 109; 1024 88, 95; 5120 91, 99; fp32 320 164, 175.
+int64_t strip_of(const Plan &p, int64_t rows, int64_t dim, int dtype)
+{
+    const bool few = dtype == SSD_DTYPE_BF16 && p.L != 0 && (p.V == 1 || dim < 1024);
+    const int64_t strips = few ? 1024 : 512, groups = p.L ? kThreads / p.L : 1;
+    const int64_t s = (rows + strips - 1) / strips;
+    return (s + groups - 1) / groups * groups;
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
@@ -134,7 +137,7 @@ template <typename E> ssd_status run_bwd(const ssd_norm_bwd_args *a, hipStream_t
     const bool sums = a->dweight || a->dbias;
     float *parts = static_cast<float *>(a->workspace);
     const Plan p = plan_of(a->dim, a->dtype);
-    const int64_t strip = strip_of(a->rows, p.L ? kThreads / p.L : 1);
+    const int64_t strip = strip_of(p, a->rows, a->dim, a->dtype);
     const int64_t blocks = (a->rows + strip - 1) / strip;
     if (p.L == 0) {
         if (sums)   // before dx, which may be dy
@@ -197,7 +200,7 @@ ssd_status ssd_layer_norm_bwd_workspace_size(const ssd_norm_bwd_args *a, size_t 
     if (r != SSD_OK) return r;
     if (!bytes) return SSD_ERR_NULL_POINTER;
     const Plan p = plan_of(a->dim, a->dtype);
-    const int64_t strip = strip_of(a->rows, p.L ? kThreads / p.L : 1);
+    const int64_t strip = strip_of(p, a->rows, a->dim, a->dtype);
     *bytes = a->rows ? (size_t)((a->rows + strip - 1) / strip) * 2 * (size_t)a->dim * 4 : 0;
     return SSD_OK;
 }

@@ -189,6 +189,16 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
             gr[i] = *reinterpret_cast<const W *>(dy + at + c * V);
         }
     };
+    // this lane's part of the weight, once for all rows (read again for every row it came
+    // from L1 beside them: 16384 rows of 5120 bf16 121 -> 102 us, 2^20 of 64 210 -> 136 us)
+    float wt[IT][V];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int c = i * L + ln < nv ? i * L + ln : 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) wt[i][e] = 1.f;
+        if (weight) load_p<V>(weight + c * V, wt[i]);
+    }
     fetch(r0 + rg);
     int flip = 0;
     for (int64_t rb = r0; rb < r1; rb += R, flip ^= 1) {
@@ -211,10 +221,6 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
         for (int i = 0; i < IT; ++i) {
             const int c = i * L + ln;
             if (c >= nv) continue;
-            float w[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = 1.f;
-            if (weight) load_p<V>(weight + c * V, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float xh = (xv[i][e] - mu) * rs, gy = gv[i][e];
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
                     dw[i][e] += gy * xh;
                     db[i][e] += gy;
                 }
-                const float gw = gy * w[e];
+                const float gw = gy * wt[i][e];
                 xv[i][e] = xh;
                 gv[i][e] = gw;
                 s1 += gw;
