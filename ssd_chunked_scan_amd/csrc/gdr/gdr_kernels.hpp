@@ -848,6 +848,21 @@ template <typename E, int NB, int KIND, bool STAGED> struct Operands {
     __device__ __forceinline__ const float *scalars(int t) const { return STAGED ? vecs + kVecChain * t : vec; }
 };
 
+// Unit (workgroup) -> column tile, head, chain.  Workgroups go round the 8 XCDs; where a
+// chain's units divide by 8, an XCD takes consecutive ones, so that the heads of a group find
+// its K and Q in one L2 (packed prompts, 8 groups of 8 heads: chains 235 -> 209 us; ragged
+// fp32, 3 groups of 2: 38 -> 34 us).  Not with all heads in one group, whose K and Q every L2
+// holds anyway (16K tokens 565 -> 585 us).
+__device__ __forceinline__ void unit_at(const ChainArgs &a, int unit, int &ptile, int &h, int &ch)
+{
+    const int per = a.np * a.H;
+    int i = unit % per;
+    ch = unit / per;
+    if (a.G > 1 && per % 8 == 0) i = (i & 7) * (per >> 3) + (i >> 3);
+    ptile = i % a.np;
+    h = i / a.np;
+}
+
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
 // and not y.
 template <typename E, int NB, bool KEEP, bool STAGED>
@@ -855,8 +870,8 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
-    int ch = unit / (a.np * a.H);
+    int ptile, h, ch;
+    unit_at(a, unit, ptile, h, ch);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -989,8 +1004,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
-    int ch = unit / (a.np * a.H);
+    int ptile, h, ch;
+    unit_at(a, unit, ptile, h, ch);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -1237,8 +1252,8 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem), *partq = part + C::kPart;
     E *xf = reinterpret_cast<E *>(part + (KEEP ? 1 : 2) * C::kPart), *uf = xf + 2 * C::kFrag, *wf = uf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
-    int ch = unit / (a.np * a.H);
+    int ptile, h, ch;
+    unit_at(a, unit, ptile, h, ch);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
@@ -1440,8 +1455,8 @@ __device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem);
     E *xf = reinterpret_cast<E *>(part + C::kPart), *uf = xf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
-    int ch = unit / (a.np * a.H);
+    int ptile, h, ch;
+    unit_at(a, unit, ptile, h, ch);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
