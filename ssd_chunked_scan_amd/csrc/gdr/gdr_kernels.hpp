@@ -327,7 +327,14 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 // Everything of one chunk and head that no state enters, by one wave: no barrier, and the
 // four waves of a workgroup keep a CU's SIMDs busy with four of them.  A wave takes `hpw`
 // heads of a group one after another, so that K K^T and Q K^T, which they share, are
-// formed once.  Further waves write the operand blocks of K and Q.  cs is summed in 64 bits, since Gam takes differences of it.
+// formed once.  Further waves write the operand blocks of K and Q.  cs is summed in 64 bits,
+// since Gam takes differences of it.
+//
+// Bound, for the backward, by the bytes it writes (36 KB of triangles and 4 KB of scalars per
+// chunk and head): 8 x 2048 tokens of 80 heads 235 us, 1.15 GB moved at 4.9 TB/s.  The forward
+// writes half and is bound by latency at two waves a SIMD (247 registers): packed prompts of
+// 64 heads 134 us, matrix pipes 20 % and vector pipes 25 % busy.  Workgroups of four waves
+// that shared one head, with barriers between the blocks, took 177 us there.
 //
 // Blocks of 16 x 16 (i, j <= i), as accumulators with rows s of block j and columns t of
 // block i: four consecutive slots of an operand block with rows t.  Between different
@@ -740,6 +747,11 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t l
 // region, the other one's next contents are in flight; one barrier before each phase says
 // both that its operands are there and that the other region is free.  Sets too large for
 // LDS (fp32 at N = 256) are read from global memory by every wave (STAGED false).
+//
+// 8 x 2048 tokens of 80 heads of 64, N = 128, both directions: 620 us for 2.5 GB, 4.0 TB/s of
+// the 5.1 that a copy reaches; without its operand loads or without its stores (timing
+// variants) 480 and 440 us, without both 305 us, the arithmetic's own time at two workgroups
+// a CU.  Packed prompts of 64 heads, forward: 209 us.
 template <typename E, int NT> constexpr bool kStaged = sizeof(E) * NT <= 512;
 
 // KIND 0: the forward (y), 1: the forward for the backward (S and U), 2: the backward
@@ -1142,6 +1154,12 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
 // step: the partial products K S (and Q S), the right-hand sides X, and U.  Every first
 // operand is now used by one wave once, so it comes from memory into registers, requested
 // for the next step as soon as this step has used it.
+//
+// 16K tokens of 32 heads, N = 256: 545 us (wide: 1.36 ms), 2.1 us a step, of which 1.4 are
+// the chain of products and exchanges and the rest 112 KB of operands at a CU's 64 bytes a
+// cycle.  2 x 2048 tokens of 24 heads, N = 64, both directions: 74 us.  Requests issued
+// earlier, between the products, made no difference (570 us), nor did touching the operands
+// of two steps ahead for L2 (570 us).
 template <int NB> constexpr int kNW = NB / 2 < 4 ? NB / 2 : 4;
 template <typename E, int NB, int KIND> struct Narrow {
     static constexpr int NW = kNW<NB>, NBW = NB / NW, TBW = 4 / NW, KBW = NBW / 2, NK = NB / 2;
@@ -1690,6 +1708,11 @@ struct GradArgs {
 // What a head brings (S, D, U, H and dy, 64 columns p at a time) comes into LDS as
 // operand blocks without passing through registers, for the next head while this one
 // computes where LDS holds it twice (TWICE).
+//
+// 8 x 2048 tokens of 80 heads, N = 128: 555 us (900 us before half the waves formed W and the
+// others Z).  It has 1.25 GB to read, 250 us of a copy's rate; what holds it is the chain
+// inside a head at two waves a SIMD: waves wait half of the time, vector pipes are busy 43 %,
+// matrix pipes 14 %, and LDS (54 KB read per wave and head) a quarter.
 constexpr int kGradThreads = 512;
 template <typename E, int NB> struct GradPlan {
     static constexpr int KPC = kColBlocks<E>;                   // 32-column blocks per stage
@@ -2080,7 +2103,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
         }
 }
 
-// dq and dk of one chunk and group from their parts, added in order of the split.
+// dq and dk of one chunk and group from their parts, added in order of the split.  Many
+// small workgroups, each a strip of the block: 13 us where one per block took 34.
 template <typename E, int NT>
 __global__ __launch_bounds__(kThreads) void k_gdr_grad_sum(const float *__restrict__ part, E *__restrict__ dq,
                                                            E *__restrict__ dk, Chunks m, int G, int N, int hsplit)
@@ -2107,7 +2131,9 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad_sum(const float *__restri
 // fp32, read and written once.  NL lanes share a row of the state (four
 // consecutive n each, 16-byte accesses); the two sums over n (with k before the
 // update, with q after it) are reduced inside those lanes.  Bound by the state's
-// bytes, like any step of a recurrence.
+// bytes, like any step of a recurrence: 64 sequences of 80 heads of 64 x 128, 337 MB in
+// 55 us, 6.1 TB/s (part of the state is still in the last cache level from the step before;
+// a copy of memory runs at 5.1).
 constexpr int kStepRows = 4;   // rows in flight per thread
 template <typename E, int NL>
 __global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, const E *__restrict__ k,
