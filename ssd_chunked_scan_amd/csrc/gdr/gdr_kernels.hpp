@@ -2131,10 +2131,12 @@ __global__ __launch_bounds__(kThreads) void k_gdr_grad_sum(const float *__restri
 // fp32, read and written once.  NL lanes share a row of the state (four
 // consecutive n each, 16-byte accesses); the two sums over n (with k before the
 // update, with q after it) are reduced inside those lanes.  Bound by the state's
-// bytes, like any step of a recurrence: 64 sequences of 80 heads of 64 x 128, 337 MB in
-// 55 us, 6.1 TB/s (part of the state is still in the last cache level from the step before;
-// a copy of memory runs at 5.1).
-constexpr int kStepRows = 4;   // rows in flight per thread
+// bytes, like any step of a recurrence.  The state goes past the caches (non-temporal): it
+// comes back only after all the other layers' states.  64 sequences of 80 heads of 64 x 128,
+// 337 MB, of which a copy's rate makes 66 us: 65 us between events with other data in the
+// caches (with ordinary accesses 81, with 4 rows a thread 67), 58 us with its own in the last
+// level (55).
+constexpr int kStepRows = 2;   // rows in flight per thread
 template <typename E, int NL>
 __global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, const E *__restrict__ k,
                                                        const E *__restrict__ v, const E *__restrict__ gate,
@@ -2154,7 +2156,7 @@ __global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, 
     for (int i = 0; i < kStepRows; ++i) {
         const int p = p0 + i * RPB;
         s[i] = floatx4{0, 0, 0, 0};
-        if (in && p < P) s[i] = *reinterpret_cast<const floatx4 *>(st + (int64_t)p * N + n);
+        if (in && p < P) s[i] = __builtin_nontemporal_load(reinterpret_cast<const floatx4 *>(st + (int64_t)p * N + n));
     }
     if (in) {
         load4_f32(k + kq, kv);
@@ -2180,7 +2182,7 @@ __global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, 
 #pragma unroll
         for (int x = 1; x < NL; x <<= 1) o += __shfl_xor(o, x);
         if (p < P) {
-            if (in) *reinterpret_cast<floatx4 *>(st + (int64_t)p * N + n) = s[i];
+            if (in) __builtin_nontemporal_store(s[i], reinterpret_cast<floatx4 *>(st + (int64_t)p * N + n));
             if (ln == 0) y[(int64_t)bh * P + p] = from_float<E>(scale * o);
         }
     }

@@ -31,15 +31,12 @@ namespace norm {
 
 constexpr int kLongThreads = 1024;
 
-template <int V, typename E> __device__ __forceinline__ void load_v(const E *p, float (&o)[V])
+// 16 bytes that are read once: past the caches, whose other contents they would push out and,
+// where dirty, have written back first.
+__device__ __forceinline__ uint4 load16_once(const void *p)
 {
-    if constexpr (V == 1) o[0] = to_float(*p);
-    else if constexpr (V == 4) load4_f32(p, o);
-    else {
-        const floatx8 f = __builtin_convertvector(*reinterpret_cast<const bf16x8 *>(p), floatx8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = f[i];
-    }
+    typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const uint4v *>(p)));
 }
 template <int V, typename E> __device__ __forceinline__ void store_v(E *p, const float (&v)[V])
 {
@@ -117,7 +114,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(const E *x, const float *
         const int c = i * L + ln;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[i][e] = 0.f;
-        if (c < nv) load_v<V>(xr + c * V, v[i]);
+        if (c >= nv) continue;
+        if constexpr (V == 1) v[i][0] = to_float(xr[c]);
+        else unpack<V, E>(load16_once(xr + c * V), v[i]);
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i)
@@ -180,8 +179,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
     const int64_t r0 = (int64_t)blockIdx.x * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
     // the next row's vectors are on their way while this one is summed; vectors past the row
     // and rows past the strip load its first ones instead of branching
-    using W = typename Raw<V, E>::type;
-    W xr[IT], gr[IT];
+    typename Raw<V, E>::type xr[IT], gr[IT];
     float mu_n, rs_n;
     auto fetch = [&](int64_t row) {
         const int64_t rr = row < r1 ? row : r0, at = rr * dim;
@@ -190,8 +188,13 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = i * L + ln < nv ? i * L + ln : 0;
-            xr[i] = *reinterpret_cast<const W *>(x + at + c * V);
-            gr[i] = *reinterpret_cast<const W *>(dy + at + c * V);
+            if constexpr (V == 1) {
+                xr[i] = x[at + c];
+                gr[i] = dy[at + c];
+            } else {
+                xr[i] = load16_once(x + at + c * V);
+                gr[i] = load16_once(dy + at + c * V);
+            }
         }
     };
     // this lane's part of the weight, once for all rows (read again for every row it came
