@@ -71,7 +71,7 @@ Plan plan_of(int64_t dim, int dtype)
 // few enough that the rows of partial sums stay a small part of the traffic.  512 for rows of
 // 2 KB and more and for fp32; bf16 rows that are shorter, or read by single elements, keep
 // few bytes in flight per workgroup and take 1024.  2^26 elements in us, 512 against 1024:
-// bf16 dim 64 135, 109; 320 115, 97; 1531 137, 109; 1024 88, 95; 5120 91, 99; fp32 320 164, 175.
+// bf16 dim 64 131, 106; 320 114, 95; 1531 142, 109; 1024 77, 82; 5120 78, 86; fp32 320 149, 151.
 int64_t strip_of(const Plan &p, int64_t rows, int64_t dim, int dtype)
 {
     const bool few = dtype == SSD_DTYPE_BF16 && p.L != 0 && (p.V == 1 || dim < 1024);

@@ -16,10 +16,11 @@
 // strip of rows, joins its row groups through LDS and writes one fp32 row of
 // partial sums; a second kernel adds those rows.  No atomics: the order is fixed.
 //
-// 16384 rows of bf16, against 5.1 TB/s of a copy: forward, dim 2560, 168 MB in 31 us (5.4
-// TB/s, partly from the last cache level); backward, dim 5120, 503 MB in 102 us (4.9 TB/s)
-// and 7 us for the sums.  2^26 elements of fp32, backward, dims 64 to 8192: 4.6 to 5.0 TB/s.
-// Rows of odd length move at 3.7 (bf16) and 4.9 TB/s (fp32), the long kernels at 2.3.
+// 16384 rows of bf16, against 5.1 TB/s of a copy: forward, dim 2560, 168 MB in 37 us (41 with
+// ordinary loads); backward, dim 5120, 503 MB in 111 us with other data in the caches and 95
+// with its own (147 and 112 with ordinary loads), 7 of them for the sums.  2^26 elements,
+// backward, dims 1024 to 5120: 4.8 to 5.2 TB/s in bf16, 5.4 to 6.0 in fp32; rows of odd length
+// 3.7 and 4.9, the long kernels, which read twice, 2.3.
 #pragma once
 
 #include <type_traits>
@@ -198,7 +199,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const E *__restrict__ x, 
         }
     };
     // this lane's part of the weight, once for all rows (read again for every row it came
-    // from L1 beside them: 16384 rows of 5120 bf16 121 -> 102 us, 2^20 of 64 210 -> 136 us)
+    // from L1 beside them: 16384 rows of 5120 bf16 121 -> 102 us, 2^20 of 64 210 -> 136 us,
+    // both before the loads went past the caches)
     float wt[IT][V];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
