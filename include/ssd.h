@@ -383,8 +383,11 @@ ssd_status ssd_conv1d_silu(const ssd_conv_args *args, void *stream);
  * every gradient; ssd_gdr_step one token per batch row.  Supported: batch >= 1,
  * seqlen >= 0, H % G == 0, P % 16 == 0, N % 16 == 0, N <= 256, P <= 4096, H*P
  * and G*N <= 2^22 (ssd_gdr_fwd and ssd_gdr_bwd: a chunk's rows are addressed in 31
- * bits), seqlen <= 2^28 with seq_idx; batch, seqlen and nheads that need more chunks
- * or chains than a grid or 31 bits count are SSD_ERR_BAD_SHAPE.
+ * bits), seqlen <= 2^28 with seq_idx.  A launch has fewer than 2^32 threads:
+ * sizes with 2^23 chains (batch rows or segments, times heads and 64-column
+ * tiles) or more, 2^24 rows times heads in ssd_gdr_step, or chunks times
+ * (nheads + 2 ngroups) of 2^26, are SSD_ERR_BAD_SHAPE (ssd_gdr_bwd: chunks times
+ * ngroups of 2^23 too, or fewer where a group's heads are shared out).
  * Results do not change from call to call: every sum has a fixed order.  g, beta
  * and their gradients need only the alignment of their elements (a token's gates
  * of a few heads may start anywhere).

@@ -16,6 +16,7 @@ using namespace ssd::gdr;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in a launch
 
 struct Shape {
     int64_t b, T, H, P, N, G, nseq;
@@ -83,8 +84,9 @@ ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
     if (s->packed && s->T > ((int64_t)1 << 28)) return SSD_ERR_BAD_SHAPE;   // ids are read with 31-bit byte offsets
     // a chunk's rows of all heads or groups are addressed with 31-bit byte offsets
     if (s->H * s->P > (1 << 22) || s->G * s->N > (1 << 22)) return SSD_ERR_BAD_SHAPE;
-    // grids and int32 indices
-    if (s->chains > INT32_MAX / s->H / s->np / 2 || s->nct > INT32_MAX / s->H / 2 || s->nct * kC > INT32_MAX)
+    // int32 indices, and grids: a launch has fewer than 2^32 threads (the chains of both
+    // directions, 4 preparing waves to a workgroup, 512 threads of the gradient kernel)
+    if (s->chains > kMaxGroups / 2 / s->H / s->np || s->nct > kMaxGroups * 4 / (s->H + 2 * s->G) || s->nct * kC > INT32_MAX)
         return SSD_ERR_BAD_SHAPE;
     // byte counts stay far below 2^63
     if (s->nct * s->H > ((int64_t)1 << 40) / (s->P * s->NT) * 64 || s->chains * s->H > ((int64_t)1 << 44) / (s->P * s->N))
@@ -123,6 +125,13 @@ int64_t head_split(const Shape &s)
         }
     }
     return best;
+}
+
+ssd_status parse_bwd(const ssd_gdr_args *a, Shape *s)
+{
+    const ssd_status r = parse_shape(a, s);
+    if (r != SSD_OK) return r;
+    return s->nct * s->G * head_split(*s) > kMaxGroups / 2 ? SSD_ERR_BAD_SHAPE : SSD_OK;
 }
 
 // Narrow chains share a step among a workgroup's waves, wide ones have fewer bytes to load
@@ -333,9 +342,9 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
 
 void copy_states(float *dst, const float *src, const Shape &s, hipStream_t st)
 {
-    const int64_t n = s.chains * s.H * s.P * s.N;
-    if (dst)
-        hipLaunchKernelGGL(k_gdr_copy, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, dst, src, n);
+    if (!dst) return;
+    const int64_t n = s.chains * s.H * s.P * s.N, blocks = (n / 4 + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(k_gdr_copy, dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(kThreads), 0, st, dst, src, n);
 }
 
 // Inputs of the chunked calls: present, aligned.
@@ -397,7 +406,7 @@ ssd_status ssd_gdr_fwd_workspace_size(const ssd_gdr_args *args, size_t *bytes)
 ssd_status ssd_gdr_bwd_workspace_size(const ssd_gdr_args *args, size_t *bytes)
 {
     Shape s;
-    const ssd_status r = parse_shape(args, &s);
+    const ssd_status r = parse_bwd(args, &s);
     if (r != SSD_OK) return r;
     if (!bytes) return SSD_ERR_NULL_POINTER;
     *bytes = layout(s, true).total;
@@ -431,7 +440,7 @@ ssd_status ssd_gdr_fwd(const ssd_gdr_args *a, void *stream)
 ssd_status ssd_gdr_bwd(const ssd_gdr_args *a, const ssd_gdr_bwd_args *g, void *stream)
 {
     Shape s;
-    ssd_status r = parse_shape(a, &s);
+    ssd_status r = parse_bwd(a, &s);
     if (r != SSD_OK) return r;
     if (!g) return SSD_ERR_NULL_POINTER;
     if ((r = check_inputs(a, s)) != SSD_OK) return r;
@@ -463,6 +472,7 @@ ssd_status ssd_gdr_step(const ssd_gdr_step_args *a, void *stream)
     if (!a) return SSD_ERR_NULL_POINTER;
     const ssd_status r = check_dims(a->batch, a->nheads, a->headdim, a->dstate, a->ngroups, a->dtype);
     if (r != SSD_OK) return r;
+    if (a->batch * a->nheads > kMaxGroups) return SSD_ERR_BAD_SHAPE;
     if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->state || !a->y) return SSD_ERR_NULL_POINTER;
     const void *ptrs[] = {a->q, a->k, a->v, a->state, a->y};
     for (const void *p : ptrs)

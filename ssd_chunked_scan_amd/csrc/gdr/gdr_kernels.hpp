@@ -2191,8 +2191,8 @@ __global__ __launch_bounds__(kThreads) void k_gdr_step(const E *__restrict__ q, 
 // final_states = initial_states (or zero): no tokens.
 __global__ __launch_bounds__(kThreads) void k_gdr_copy(float *__restrict__ dst, const float *__restrict__ src, int64_t n)
 {
-    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-    if (i < n) *reinterpret_cast<floatx4 *>(dst + i) = src ? vec4(src + i) : floatx4{0, 0, 0, 0};
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * kThreads * 4)
+        *reinterpret_cast<floatx4 *>(dst + i) = src ? vec4(src + i) : floatx4{0, 0, 0, 0};
 }
 
 }  // namespace gdr

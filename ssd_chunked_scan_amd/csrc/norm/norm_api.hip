@@ -34,11 +34,14 @@ constexpr int64_t kMaxNormDim = 65536;
 ssd_status check_dims(int64_t rows, int64_t dim, int dtype)
 {
     if (dtype != SSD_DTYPE_F32 && dtype != SSD_DTYPE_BF16) return SSD_ERR_BAD_DTYPE;
-    // one workgroup per row must fit a grid
+    // rows are counted in 31 bits
     if (rows < 0 || dim < 1 || dim > kMaxNormDim || rows > INT32_MAX || rows > ((int64_t)1 << 40) / dim)
         return SSD_ERR_BAD_SHAPE;
     return SSD_OK;
 }
+
+// Rows of one launch: at up to 1024 threads each, fewer than 2^32 threads.
+constexpr int64_t kLaunchRows = (int64_t)1 << 21;
 
 // How a row of `dim` is held: vector width, lanes per row and vectors per lane (0:
 // longer than the registers).
@@ -114,20 +117,26 @@ template <typename E> ssd_status run_fwd(const ssd_norm_args *a, hipStream_t st)
 {
     const int dim = (int)a->dim;
     const Plan p = plan_of(a->dim, a->dtype);
-    if (p.L == 0) {
-        hipLaunchKernelGGL(k_norm_fwd_long<E>, dim3((unsigned)a->rows), dim3(kLongThreads), 0, st, (const E *)a->x,
-                           a->weight, a->bias, (E *)a->y, a->mean, a->rstd, dim, a->eps);
-        return launched();
+    for (int64_t r0 = 0; r0 < a->rows; r0 += kLaunchRows) {
+        const int64_t rows = a->rows - r0 < kLaunchRows ? a->rows - r0 : kLaunchRows;
+        const E *x = (const E *)a->x + r0 * dim;
+        E *y = (E *)a->y + r0 * dim;
+        float *mean = a->mean ? a->mean + r0 : nullptr, *rstd = a->rstd ? a->rstd + r0 : nullptr;
+        if (p.L == 0) {
+            hipLaunchKernelGGL(k_norm_fwd_long<E>, dim3((unsigned)rows), dim3(kLongThreads), 0, st, x, a->weight, a->bias, y,
+                               mean, rstd, dim, a->eps);
+            continue;
+        }
+        with_plan<E>(p, [&](auto v, auto l, auto it) {
+            constexpr int L = decltype(l)::value;
+            // few rows: a wave per workgroup, so they spread over the CUs
+            const int threads = L == 256 ? 256 : rows * L <= 64 * 1024 ? 64 : kThreads;
+            const int64_t per = threads / L;
+            hipLaunchKernelGGL((k_norm_fwd<E, decltype(v)::value, L, decltype(it)::value>),
+                               dim3((unsigned)((rows + per - 1) / per)), dim3(threads), 0, st, x, a->weight, a->bias, y, mean,
+                               rstd, rows, dim, a->eps);
+        });
     }
-    with_plan<E>(p, [&](auto v, auto l, auto it) {
-        constexpr int L = decltype(l)::value;
-        // few rows: a wave per workgroup, so they spread over the CUs
-        const int threads = L == 256 ? 256 : a->rows * L <= 64 * 1024 ? 64 : kThreads;
-        const int64_t per = threads / L;
-        hipLaunchKernelGGL((k_norm_fwd<E, decltype(v)::value, L, decltype(it)::value>),
-                           dim3((unsigned)((a->rows + per - 1) / per)), dim3(threads), 0, st, (const E *)a->x,
-                           a->weight, a->bias, (E *)a->y, a->mean, a->rstd, a->rows, dim, a->eps);
-    });
     return launched();
 }
 
@@ -144,8 +153,11 @@ template <typename E> ssd_status run_bwd(const ssd_norm_bwd_args *a, hipStream_t
             hipLaunchKernelGGL(k_norm_cols_long<E>, dim3((unsigned)blocks, (unsigned)((dim + kThreads - 1) / kThreads)),
                                dim3(kThreads), 0, st, (const E *)a->x, (const E *)a->dy, a->mean, a->rstd, parts, a->rows,
                                dim, (int)strip);
-        hipLaunchKernelGGL(k_norm_dx_long<E>, dim3((unsigned)a->rows), dim3(kLongThreads), 0, st, (const E *)a->x,
-                           (const E *)a->dy, a->mean, a->rstd, a->weight, (E *)a->dx, dim);
+        for (int64_t r0 = 0; r0 < a->rows; r0 += kLaunchRows) {
+            const int64_t rows = a->rows - r0 < kLaunchRows ? a->rows - r0 : kLaunchRows;
+            hipLaunchKernelGGL(k_norm_dx_long<E>, dim3((unsigned)rows), dim3(kLongThreads), 0, st, (const E *)a->x + r0 * dim,
+                               (const E *)a->dy + r0 * dim, a->mean + r0, a->rstd + r0, a->weight, (E *)a->dx + r0 * dim, dim);
+        }
     } else {
         with_plan<E>(p, [&](auto v, auto l, auto it) {
             auto launch = [&](auto kern) {
