@@ -860,19 +860,15 @@ template <typename E, int NB, int KIND, bool STAGED> struct Operands {
     __device__ __forceinline__ const float *scalars(int t) const { return STAGED ? vecs + kVecChain * t : vec; }
 };
 
-// Unit (workgroup) -> column tile, head, chain.  Workgroups go round the 8 XCDs; where a
+// Workgroup -> unit (chain, head, column tile).  Workgroups go round the 8 XCDs; where a
 // chain's units divide by 8, an XCD takes consecutive ones, so that the heads of a group find
 // its K and Q in one L2 (packed prompts, 8 groups of 8 heads: chains 235 -> 209 us; ragged
 // fp32, 3 groups of 2: 38 -> 34 us).  Not with all heads in one group, whose K and Q every L2
-// holds anyway (16K tokens 565 -> 585 us).
-__device__ __forceinline__ void unit_at(const ChainArgs &a, int unit, int &ptile, int &h, int &ch)
+// holds anyway.
+__device__ __forceinline__ int by_group(const ChainArgs &a, int unit)
 {
-    const int per = a.np * a.H;
-    int i = unit % per;
-    ch = unit / per;
-    if (a.G > 1 && per % 8 == 0) i = (i & 7) * (per >> 3) + (i >> 3);
-    ptile = i % a.np;
-    h = i / a.np;
+    const int per = a.np * a.H, i = unit % per;
+    return a.G > 1 && per % 8 == 0 ? unit - i + (i & 7) * (per >> 3) + (i >> 3) : unit;
 }
 
 // One forward chain.  KEEP: for the backward, which wants S and U of every chunk
@@ -882,8 +878,8 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    int ptile, h, ch;
-    unit_at(a, unit, ptile, h, ch);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -1016,8 +1012,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
 {
     constexpr int NT = 16 * NB, NK = NT / 32, PL = 512 * kTri;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    int ptile, h, ch;
-    unit_at(a, unit, ptile, h, ch);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = ptile * kC + 16 * wv;
     const bool keep = p0 < a.Pp;
     int c0, n, len;
@@ -1270,8 +1266,8 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem), *partq = part + C::kPart;
     E *xf = reinterpret_cast<E *>(part + (KEEP ? 1 : 2) * C::kPart), *uf = xf + 2 * C::kFrag, *wf = uf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    int ptile, h, ch;
-    unit_at(a, unit, ptile, h, ch);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
@@ -1473,8 +1469,8 @@ __device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *s
     float *part = reinterpret_cast<float *>(smem);
     E *xf = reinterpret_cast<E *>(part + C::kPart), *uf = xf + 2 * C::kFrag;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
-    int ptile, h, ch;
-    unit_at(a, unit, ptile, h, ch);
+    const int ptile = unit % a.np, h = (unit / a.np) % a.H;
+    int ch = unit / (a.np * a.H);
     const int p0 = 16 * ptile;
     int c0, n, len;
     int64_t t0;
@@ -1649,7 +1645,7 @@ template <typename E, int NB, bool STAGED>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_chain(ChainArgs a)
 {
     __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 0, STAGED>::kBytes];
-    chain_fwd<E, NB, false, STAGED>(a, blockIdx.x, smem);
+    chain_fwd<E, NB, false, STAGED>(a, by_group(a, blockIdx.x), smem);
 }
 template <typename E, int NB>
 __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chain_narrow(ChainArgs a)
@@ -1665,15 +1661,15 @@ template <typename E, int NB, bool STAGED>
 __global__ __launch_bounds__(kThreads, 2) void k_gdr_chains(ChainArgs a)
 {
     __shared__ __attribute__((aligned(16))) char smem[Regions<E, NB, 2, STAGED>::kBytes];   // the larger of both
-    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, STAGED>(a, blockIdx.x, smem);
-    else chain_fwd<E, NB, true, STAGED>(a, blockIdx.x - a.units, smem);
+    if (blockIdx.x < (unsigned)a.units) chain_bwd<E, NB, STAGED>(a, by_group(a, blockIdx.x), smem);
+    else chain_fwd<E, NB, true, STAGED>(a, by_group(a, blockIdx.x - a.units), smem);
 }
 template <typename E, int NB>
 __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chains_narrow(ChainArgs a)
 {
     __shared__ __attribute__((aligned(16))) char smem[Narrow<E, NB, 2>::kBytes];   // as large as KIND 1's
-    if (blockIdx.x < (unsigned)a.units) narrow_bwd<E, NB>(a, blockIdx.x, smem);
-    else narrow_fwd<E, NB, true>(a, blockIdx.x - a.units, smem);
+    if (blockIdx.x < (unsigned)a.units) narrow_bwd<E, NB>(a, by_group(a, blockIdx.x), smem);
+    else narrow_fwd<E, NB, true>(a, by_group(a, blockIdx.x - a.units), smem);
 }
 
 // ---------------------------------------------------------------------------
