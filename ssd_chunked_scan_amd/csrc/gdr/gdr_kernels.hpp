@@ -1705,11 +1705,13 @@ struct GradArgs {
 // operand blocks without passing through registers, for the next head while this one
 // computes where LDS holds it twice (TWICE).
 //
-// 8 x 2048 tokens of 80 heads, N = 128: 555 us (900 us before half the waves formed W and the
-// others Z).  It has 1.25 GB to read, 250 us of a copy's rate; what holds it is the chain
-// inside a head at two waves a SIMD: waves wait half of the time, vector pipes are busy 43 %,
-// matrix pipes 14 %, and LDS (54 KB read per wave and head) a quarter.
+// 8 x 2048 tokens of 80 heads, N = 128: 495 us (900 us before half the waves formed W and the
+// others Z; 555 with a head's dg finished by one wave at its end and the next stage requested
+// first).  It has 1.25 GB to read, 250 us of a copy's rate; what holds it is the chain inside
+// a head at two waves a SIMD: without the stages' loads (a timing variant) 440 us.  Waves
+// wait half of the time; LDS (54 KB read per wave and head) is busy a quarter.
 constexpr int kGradThreads = 512;
+constexpr int kDgHeads = 4;   // heads whose dg is finished at a time
 template <typename E, int NB> struct GradPlan {
     static constexpr int KPC = kColBlocks<E>;                   // 32-column blocks per stage
     static constexpr int kBlocks = (2 * NB + 12) * KPC;         // S | D | U | H | dy
@@ -1779,7 +1781,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     __shared__ __attribute__((aligned(16))) E stage_m[(PL::TWICE ? 2 : 1) * PL::kRoom * 512];
     __shared__ __attribute__((aligned(16))) E mats[PL::MATS ? 2 * kMat : 8];
     __shared__ __attribute__((aligned(16))) float vs2[2 * kVec];
-    __shared__ float dcs[4][kC], red[16];
+    __shared__ float dcs[kDgHeads][4][kC], red[kDgHeads][17];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     const int w = wv & 3, half = wv >> 2;
     int x = blockIdx.x;
@@ -1902,7 +1904,6 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
         }
         loads_done();
         __syncthreads();
-        if (PL::TWICE && j + 1 < J) issue(j + 1);
         E *room = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kRoom * 512;
         const E *buf = room + 8 * lane;
         const E *Sb = buf, *Db = buf + NB * KPC * 512, *Ub = buf + 2 * NB * KPC * 512, *Hb = Ub + 4 * KPC * 512,
@@ -1928,6 +1929,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
                 if (i <= w) mma(m[i], load_frag(Ub + (i * KPC + kb) * 512), xw);
                 else mma(m[i], load_frag(Xb + (i * KPC + kb) * 512), uw[kb]);
         }
+        // (requested here and not at the head of the stage, where the compiler has the first LDS
+        // read wait for it; the exchange below waits for it in any case)
+        if (PL::TWICE && j + 1 < J) issue(j + 1);
         // the state products
         {
             const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
@@ -2044,13 +2048,15 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
             db = cross_sum4(db);
             if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
         }
-        if (g == 0) dcs[2 + half][tl] = dx;
+        const int slot = (h - h0) % kDgHeads;
+        if (g == 0) dcs[slot][2 + half][tl] = dx;
         if (l == 0)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dcs[half][16 * w + 4 * g + r] = ab[r];
+            for (int r = 0; r < 4; ++r) dcs[slot][half][16 * w + 4 * g + r] = ab[r];
         if (lane == 0) {
-            red[wv] = sb;
-            red[8 + wv] = sd;
+            red[slot][wv] = sb;
+            red[slot][8 + wv] = sd;
+            if (wv == 0) red[slot][16] = vs[kSince + kC - 1];
         }
         __syncthreads();
         // W K, W^T Q and (Z + Z^T) K
@@ -2070,16 +2076,20 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
                 mma(dk[nb], z1, k1);
             }
         }
-        if (wv == (j & 7)) {
+        // dg of several heads at a time, a wave each: once per head it would hold the other
+        // waves up
+        if ((slot == kDgHeads - 1 || h == h1 - 1) && wv <= slot) {
             const int t = 63 - lane;
-            float s = prefix_sum64(dcs[0][t] + dcs[1][t] + dcs[2][t] + dcs[3][t]), sum_b = 0.f, sum_sd = 0.f;
+            const float(&d)[4][kC] = dcs[wv];
+            const float *rd = red[wv];
+            float s = prefix_sum64(d[0][t] + d[1][t] + d[2][t] + d[3][t]), sum_b = 0.f, sum_sd = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum_b += red[i];
-                sum_sd += red[8 + i];
+                sum_b += rd[i];
+                sum_sd += rd[8 + i];
             }
-            s += sum_b + vs[kSince + kC - 1] * sum_sd;
-            if (t < count) ((E *)a.dg)[(t0 + t) * a.H + h] = from_float<E>(s);
+            s += sum_b + rd[16] * sum_sd;
+            if (t < count) ((E *)a.dg)[(t0 + t) * a.H + h - slot + wv] = from_float<E>(s);
         }
     }
 #pragma unroll
