@@ -1856,13 +1856,18 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     for (int i = 0; i < 4; ++i) kq[i] = floatx4{0, 0, 0, 0};
     {
         const E *xf = half ? kf : qf;   // what stands for t
+        // (where from is selected, not branched on, so that the loads go out together)
+#pragma unroll 2
         for (int kb = 0; kb < NK; ++kb) {
             const frag_t<E> kw = load_frag(kf + (w * NK + kb) * 512 + 8 * lane), xw = load_frag(xf + (w * NK + kb) * 512 + 8 * lane);
+            frag_t<E> f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = load_frag((i <= w ? kf : xf) + (i * NK + kb) * 512 + 8 * lane);
             mma(kqD, xw, kw);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i <= w) mma(kq[i], load_frag(kf + (i * NK + kb) * 512 + 8 * lane), xw);
-                else mma(kq[i], load_frag(xf + (i * NK + kb) * 512 + 8 * lane), kw);
+                if (i <= w) mma(kq[i], f[i], xw);
+                else mma(kq[i], f[i], kw);
         }
     }
     // the wave's q and k in accumulator layout: token 16 w + 4 g + r, column 16 nb + l
@@ -1921,13 +1926,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
             uw[kb] = load_frag(Ub + (w * KPC + kb) * 512);
             hw[kb] = load_frag(Hb + (w * KPC + kb) * 512);
             yw[kb] = load_frag(Yb + (w * KPC + kb) * 512);
-            if (half) db = dot8(uw[kb], hw[kb], db);
             const frag_t<E> xw = load_frag(Xb + (w * KPC + kb) * 512);
+            frag_t<E> f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = load_frag((i <= w ? Ub : Xb) + (i * KPC + kb) * 512);
+            if (half) db = dot8(uw[kb], hw[kb], db);
             mma(mD, xw, uw[kb]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i <= w) mma(m[i], load_frag(Ub + (i * KPC + kb) * 512), xw);
-                else mma(m[i], load_frag(Xb + (i * KPC + kb) * 512), uw[kb]);
+                if (i <= w) mma(m[i], f[i], xw);
+                else mma(m[i], f[i], uw[kb]);
         }
         // (requested here and not at the head of the stage, where the compiler has the first LDS
         // read wait for it; the exchange below waits for it in any case)
