@@ -1982,21 +1982,27 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
         int tl = tl0, o0 = 4 * g;
         asm volatile("" : "+v"(tl), "+v"(o0));
         const float *row = vs + (half ? kRowBeta : kRowScale);
-        const float row_l = row[tl];
+        // the factors of every block first, then the branches, so that the reads go out together
+        floatx4 fo[4];   // of o: before t (i < w), or t itself
+        float fl[4];     // of tl: t itself, or before t
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fo[i] = vec4((i < w ? vs + kColBeta + (w - 1) * kC : row) + 16 * i + o0);
+            fl[i] = (i < w ? row : vs + kColBeta + (i - 1) * kC)[tl];
+        }
+        const float chi = vs[kCsHi + tl], clo = vs[kCsLo + tl], bl = vs[kBeta + tl];
+        const floatx4 oh = vec4(vs + kCsHi + 16 * w + o0), ol = vec4(vs + kCsLo + 16 * w + o0),
+                      bo = vec4(vs + kBeta + 16 * w + o0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < w) {   // t = tl, s = o
-                m[i] *= row_l * vec4(vs + kColBeta + (w - 1) * kC + 16 * i + o0);
+            if (i != w) {   // t = tl, s = o (i < w); t = o, s = tl
+                m[i] *= fl[i] * fo[i];
+                float d = 0.f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dx += m[i][r] * kq[i][r];
-            } else if (i > w) {   // t = o, s = tl
-                m[i] *= vs[kColBeta + (i - 1) * kC + tl] * vec4(row + 16 * i + o0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dx_s += m[i][r] * kq[i][r];
+                for (int r = 0; r < 4; ++r) d += m[i][r] * kq[i][r];
+                dx += i < w ? d : 0.f;
+                dx_s += i < w ? 0.f : d;
             } else {
-                const float chi = vs[kCsHi + tl], clo = vs[kCsLo + tl], bl = vs[kBeta + tl];
-                const floatx4 oh = vec4(vs + kCsHi + 16 * i + o0), ol = vec4(vs + kCsLo + 16 * i + o0),
-                              bo = vec4(vs + kBeta + 16 * i + o0);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int o = 16 * i + o0 + r;
