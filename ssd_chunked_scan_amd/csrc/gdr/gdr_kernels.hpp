@@ -464,6 +464,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
     // tokens' 80 heads
     const int64_t gat = (t0 + (lane < count ? lane : count - 1)) * H;
     E g_next = gate[gat + h0], b_next = beta[gat + h0];
+    {   // (the first ones have arrived: the loop's wait for the next ones then leaves the stores
+        // behind them in flight)
+        float gw = to_float(g_next), bw = to_float(b_next);
+        asm volatile("" : "+v"(gw), "+v"(bw));
+    }
     for (int h = h0; h < h1; ++h) {
         const int64_t u = (int64_t)c * H + h;
         {
@@ -509,7 +514,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
         }
         wave_sync();
         E *n_o = tri + u * tri_elems<E>(BWD), *p_o = n_o + kPlanes<E> * PL, *nt_o = p_o, *pt_o = nt_o + kPlanes<E> * PL;
-        floatx4 a[10], p[10];
+        floatx4 a[10], gd[4];   // gd: Gam of the diagonal blocks
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -519,7 +524,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                 if (j < i) {
                     gam = row[t] * vec4(col + (i - 1) * kC + 16 * j + 4 * g);
                     a[b] = gam * kk[b];
-                    p[b] = (scale * gam) * qk[b];
                 } else {
                     const floatx4 oh = vec4(chi + 16 * j + 4 * g), ol = vec4(clo + 16 * j + 4 * g);
                     const float th = chi[t], tl = clo[t];
@@ -528,8 +532,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                         const int s = 4 * g + r;
                         gam[r] = exp2_(s <= l ? ((th - oh[r]) + (tl - ol[r])) * kLog2e : 0.f);
                         a[b][r] = s < l ? gam[r] * kk[b][r] : 0.f;
-                        p[b][r] = s <= l ? scale * gam[r] * qk[b][r] : 0.f;
                     }
+                    gd[i] = gam;
                 }
                 *reinterpret_cast<floatx4 *>(A + b * kPrepBlock + l * kPrepRow + 4 * g) = a[b];
             }
@@ -581,6 +585,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
         // N with rows t; Gam Q K^T with rows t (forward); both with rows s (backward), through
         // products with the identity, plane by plane
         const floatx4 none = floatx4{0, 0, 0, 0};
+        auto pair = [&](int i, int j) {   // block (i, j) of scale Gam o Q K^T
+            const int b = tri_block(i, j), t = 16 * i + l;
+            if (j < i) return (scale * (row[t] * vec4(col + (i - 1) * kC + 16 * j + 4 * g))) * qk[b];
+            floatx4 d;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[r] = 4 * g + r <= l ? scale * gd[i][r] * qk[b][r] : 0.f;
+            return d;
+        };
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -593,10 +605,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                 if (kPlanes<E> == 2) store_block<ONCE>(n_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[1]);
                 if (!BWD) {
                     store_block<ONCE>(p_o + lower_block(i, kb) * 512 + 8 * lane,
-                               round_pair<E>(p[tri_block(i, j)], two ? p[tri_block(i, two ? j + 1 : j)] : none));
+                               round_pair<E>(pair(i, j), two ? pair(i, two ? j + 1 : j) : none));
                     continue;
                 }
-                split_pair(p[tri_block(i, j)], two ? p[tri_block(i, two ? j + 1 : j)] : none, f[2], f[3]);
+                split_pair(pair(i, j), two ? pair(i, two ? j + 1 : j) : none, f[2], f[3]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     E *o = (x ? pt_o : nt_o) + 8 * lane + 4 * (i & 1);
