@@ -202,14 +202,16 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
     }
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        // heads per wave: 2048 waves (two per SIMD) run at a time, and a wave pays for K K^T and
-        // Q K^T once, about NT / 256 of a head's time
+        // heads per wave: 2048 waves (two per SIMD) run at a time, and a wave pays for its start,
+        // K K^T and Q K^T once, about 1 + NT / 256 heads' time (packed prompts of 8 heads a group,
+        // N = 128, with 1, 2, 4 and 8 heads a wave: 166, 134, 120, 136 us; 16K tokens of 32 heads
+        // in one group, N = 256, with 2, 4 and 8: 75, 58, 61 us)
         const int64_t hpg = s.H / s.G;
         int64_t hpw = 1;
         double cost = 1e300;
         for (int64_t k = 1; k <= hpg && k <= 32; ++k) {
             const int64_t waves = s.nct * s.G * ((hpg + k - 1) / k);
-            const double t = (double)((waves + 2047) / 2048) * ((double)k + (double)NT / 256);
+            const double t = (double)((waves + 2047) / 2048) * ((double)k + 1 + (double)NT / 256);
             if (t < cost) {
                 cost = t;
                 hpw = k;

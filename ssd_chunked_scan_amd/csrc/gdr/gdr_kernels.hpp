@@ -330,11 +330,13 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 // formed once.  Further waves write the operand blocks of K and Q.  cs is summed in 64 bits,
 // since Gam takes differences of it.
 //
-// Bound, for the backward, by the bytes it writes (36 KB of triangles and 4 KB of scalars per
-// chunk and head): 8 x 2048 tokens of 80 heads 235 us, 1.15 GB moved at 4.9 TB/s.  The forward
-// writes half and is bound by latency at two waves a SIMD (247 registers): packed prompts of
-// 64 heads 134 us, matrix pipes 20 % and vector pipes 25 % busy.  Workgroups of four waves
-// that shared one head, with barriers between the blocks, took 177 us there.
+// 8 x 2048 tokens of 80 heads, backward: 168 us, 1.15 GB (36 KB of triangles and 4 KB of
+// scalars to write per chunk and head) at 6.8 TB/s, part of it still on its way through the
+// last cache level.  (235 us while Gam o Q K^T was formed before the inverse, whose spilled
+// registers came back from memory behind the stores.)  The forward writes half and is bound by
+// latency at two waves a SIMD (232 registers): packed prompts of 64 heads 120 us, matrix and
+// vector pipes about a quarter busy.  Workgroups of four waves that shared one head, with
+// barriers between the blocks, took 177 us there.
 //
 // Blocks of 16 x 16 (i, j <= i), as accumulators with rows s of block j and columns t of
 // block i: four consecutive slots of an operand block with rows t.  Between different
@@ -460,8 +462,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
     }
     const int h0 = grp * hpg + part * hpw, h1 = h0 + hpw < (grp + 1) * hpg ? h0 + hpw : (grp + 1) * hpg;
     // a head's gates are requested while the head before it is worked on, ahead of that
-    // one's stores (a load waits for the stores issued before it): 238 -> 230 us of 8 x 2048
-    // tokens' 80 heads
+    // one's stores (a load waits for the stores issued before it)
     const int64_t gat = (t0 + (lane < count ? lane : count - 1)) * H;
     E g_next = gate[gat + h0], b_next = beta[gat + h0];
     {   // (the first ones have arrived: the loop's wait for the next ones then leaves the stores
@@ -1717,11 +1718,11 @@ struct GradArgs {
 // operand blocks without passing through registers, for the next head while this one
 // computes where LDS holds it twice (TWICE).
 //
-// 8 x 2048 tokens of 80 heads, N = 128: 495 us (900 us before half the waves formed W and the
+// 8 x 2048 tokens of 80 heads, N = 128: 485 us (900 us before half the waves formed W and the
 // others Z; 555 with a head's dg finished by one wave at its end and the next stage requested
 // first).  It has 1.25 GB to read, 250 us of a copy's rate; what holds it is the chain inside
-// a head at two waves a SIMD: without the stages' loads (a timing variant) 440 us.  Waves
-// wait half of the time; LDS (54 KB read per wave and head) is busy a quarter.
+// a head at two waves a SIMD.  Waves wait half of the time; LDS (54 KB read per wave and
+// head) is busy a quarter.
 constexpr int kGradThreads = 512;
 constexpr int kDgHeads = 4;   // heads whose dg is finished at a time
 template <typename E, int NB> struct GradPlan {
