@@ -403,7 +403,8 @@ ssd_status ssd_conv1d_silu(const ssd_conv_args *args, void *stream);
  * the buffers is touched).  Unlike ssd_fwd every segment has an initial state of
  * its own: initial_states is [nseq,H,P,N], so a stream of prompts can continue
  * nseq carried states.  A segment without tokens has its initial state as its
- * final state.
+ * final state (a stream without any, seqlen 0, is a packed one if seq_idx is not
+ * NULL; no id is read).
  */
 typedef struct {
     int64_t batch, seqlen, nheads, headdim, dstate, ngroups; /* b, T, H, P, N, G */

@@ -609,6 +609,7 @@ _GDR_BWD = struct.Struct("10P")             # ssd_gdr_bwd_args
 _GDR_STEP = struct.Struct("5qif7P")         # ssd_gdr_step_args
 _NORM = struct.Struct("2qif6P")             # ssd_norm_args
 _NORM_BWD = struct.Struct("2q2i10P")        # ssd_norm_bwd_args
+_NO_IDS = 16                                # a seq_idx that is there and not read
 
 
 def _same(t, name, dtype, shape, dev):
@@ -680,8 +681,11 @@ def _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq):
     if initial_states is not None:
         _same(initial_states, "initial_states", torch.float32, states, dev)
     head = (b, T, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale)
+    # a stream without tokens has no ids to point to, and is a packed stream all the same (the
+    # library reads none of them)
+    ids = 0 if seq_idx is None else seq_idx.data_ptr() or _NO_IDS
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            0 if initial_states is None else initial_states.data_ptr(), 0 if seq_idx is None else seq_idx.data_ptr())
+            0 if initial_states is None else initial_states.data_ptr(), ids)
     return head, ptrs, n, states
 
 
@@ -691,7 +695,7 @@ def _gdr_pack(head, ptrs, n, y=0, final_states=0, workspace=0, nbytes=0):
 
 def _gdr_workspace(name, head, ptrs, n):
     # only the sizes matter, and whether there is a seq_idx
-    return _workspace_bytes(name, _gdr_pack(head, (0,) * 6 + (16 if ptrs[6] else 0,), n))
+    return _workspace_bytes(name, _gdr_pack(head, (0,) * 6 + (_NO_IDS if ptrs[6] else 0,), n))
 
 
 def gdr_fwd_workspace_bytes(q, k, v, g, beta, seq_idx=None, nseq=None) -> int:
