@@ -394,8 +394,9 @@ ssd_status ssd_conv1d_silu(const ssd_conv_args *args, void *stream);
  *
  * bf16 problems hold the states (S and its gradient) in fp32 throughout and feed
  * them to the matrix cores as sums of two bf16 numbers, so that final_states and
- * dinitial_states are as exact as fp32 storage asks for; y and the other
- * gradients are rounded to bf16 once, from products with operands of 8 bits.
+ * dinitial_states are as exact as fp32 storage asks for; so are the operands of y,
+ * which is rounded to bf16 once.  The other gradients are rounded once, from
+ * products with operands of 8 bits.
  *
  * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0,
  * nseq), not checked here: see ssd_check_seq_idx; an invalid stream gives wrong

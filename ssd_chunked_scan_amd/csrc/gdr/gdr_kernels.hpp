@@ -43,9 +43,13 @@
 // Numerics.  Inputs are exact in their type.  For bf16 problems the chain carries
 // S, U and D in fp32 and hands them to the matrix cores as a sum of two bf16
 // numbers (16 bits of significand; the error of a product is about 2^-18 of its
-// size), so states and dV are as good as fp32 storage of them needs; the
-// products that end in bf16 outputs without feeding the chain (Q S, (Gam o Q
-// K^T) U, and those of dq and dk) take one bf16 number for S, U, D and H.
+// size), so states and dV are as good as fp32 storage of them needs, and y takes
+// its operands (S, beta U, Gam o Q K^T) the same way: with similar keys, beta near
+// 1 and weak decay the terms of y are several times y itself, and single bf16
+// numbers left y off by 1.6e-2 of its norm (keys at cosines of 0.9) where its own
+// rounding is 1.7e-3.  It costs the 16K-token chains 592 -> 695 us and packed
+// prompts 326 -> 367.  The products of dq and dk take one bf16 number for S, U, D
+// and H.
 // fp32 problems use the fp32 matrix instructions throughout.
 #pragma once
 
@@ -317,11 +321,11 @@ template <typename E> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsr
 // NT/16 x 2 blocks), in the order K, K^T, Q, Q^T (the last for the backward only).  Tokens
 // past the chunk's count and columns past N are zero.
 
-// Elements of one (chunk, head) of the prepared triangles: N (its planes) and Gam o
-// Q K^T rounded; for the backward N, N^T and (Gam o Q K^T)^T (their planes).
+// Elements of one (chunk, head) of the prepared triangles, all in their planes: N and Gam
+// o Q K^T; for the backward N, N^T and (Gam o Q K^T)^T.
 template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 {
-    return 512 * kTri * (bwd ? 3 * kPlanes<E> : kPlanes<E> + 1);
+    return 512 * kTri * kPlanes<E> * (bwd ? 3 : 2);
 }
 
 // Everything of one chunk and head that no state enters, by one wave: no barrier, and the
@@ -604,12 +608,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_gdr_prep(const E *__restrict__ 
                 split_pair(a[tri_block(i, j)], two ? a[tri_block(i, two ? j + 1 : j)] : none, f[0], f[1]);
                 store_block<ONCE>(n_o + lower_block(i, kb) * 512 + 8 * lane, f[0]);
                 if (kPlanes<E> == 2) store_block<ONCE>(n_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[1]);
+                split_pair(pair(i, j), two ? pair(i, two ? j + 1 : j) : none, f[2], f[3]);
                 if (!BWD) {
-                    store_block<ONCE>(p_o + lower_block(i, kb) * 512 + 8 * lane,
-                               round_pair<E>(pair(i, j), two ? pair(i, two ? j + 1 : j) : none));
+                    store_block<ONCE>(p_o + lower_block(i, kb) * 512 + 8 * lane, f[2]);
+                    if (kPlanes<E> == 2) store_block<ONCE>(p_o + PL + lower_block(i, kb) * 512 + 8 * lane, f[3]);
                     continue;
                 }
-                split_pair(pair(i, j), two ? pair(i, two ? j + 1 : j) : none, f[2], f[3]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     E *o = (x ? pt_o : nt_o) + 8 * lane + 4 * (i & 1);
@@ -774,7 +778,7 @@ template <typename E, int NB, int KIND, bool STAGED> struct Regions {
     // phase 1: K | Q (KIND 0) or the transposed pair matrix (KIND 2)
     static constexpr int kOne = kMat + (KIND == 0 ? kMat : KIND == 2 ? kN : 0);
     // phase 2: N or N^T | the pair matrix (KIND 0) | K^T | Q^T (KIND 2)
-    static constexpr int kTwo = kN + (KIND == 0 ? kTri : 0) + kMat + (KIND == 2 ? kMat : 0);
+    static constexpr int kTwo = kN + (KIND == 0 ? kN : 0) + kMat + (KIND == 2 ? kMat : 0);
     static constexpr int kBytes = STAGED ? (kOne + kTwo) * 512 * (int)sizeof(E) + 2 * kVecChain * 4 : 16;
 };
 
@@ -852,8 +856,8 @@ template <typename E, int NB, int KIND, bool STAGED> struct Operands {
             stage<E, R::kN, kOnce>(tri + (KIND == 2 ? kNt : 0), o, wv, lane);
             o += R::kN * 512;
             if (KIND == 0) {
-                stage<E, kTri, kOnce>(tri + kPlanes<E> * kPL, o, wv, lane);
-                o += kTri * 512;
+                stage<E, R::kN, kOnce>(tri + kPlanes<E> * kPL, o, wv, lane);
+                o += R::kN * 512;
             }
             stage<E, R::kMat>(kq + kMatE, o, wv, lane);
             if (KIND == 2) stage<E, R::kMat>(kq + 3 * kMatE, o + kMatE, wv, lane);
@@ -866,7 +870,7 @@ template <typename E, int NB, int KIND, bool STAGED> struct Operands {
     __device__ __forceinline__ const E *p() const { return (STAGED ? two + R::kN * 512 : tri + kPlanes<E> * kPL) + 8 * lane; }
     __device__ __forceinline__ const E *kt() const
     {
-        return (STAGED ? two + (R::kN + (KIND == 0 ? kTri : 0)) * 512 : kq + kMatE) + 8 * lane;
+        return (STAGED ? two + (R::kN + (KIND == 0 ? R::kN : 0)) * 512 : kq + kMatE) + 8 * lane;
     }
     __device__ __forceinline__ const E *qt() const { return (STAGED ? two + R::kN * 512 + kMatE : kq + 3 * kMatE) + 8 * lane; }
     // the scalars of the step whose turn is t
@@ -940,7 +944,11 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
                 const frag_t<E> f = load_frag(kf + (tb * NK + kb) * 512);
                 mma(ks[tb], f, so_.hi[kb]);
                 if (kPlanes<E> == 2) mma(ks[tb], f, so_.lo[kb]);
-                if (!KEEP) mma(qs[tb], load_frag(qf + (tb * NK + kb) * 512), so_.hi[kb]);
+                if (!KEEP) {
+                    const frag_t<E> fq = load_frag(qf + (tb * NK + kb) * 512);
+                    mma(qs[tb], fq, so_.hi[kb]);
+                    if (kPlanes<E> == 2) mma(qs[tb], fq, so_.lo[kb]);
+                }
             }
         floatx4 bt[4];
 #pragma unroll
@@ -979,11 +987,12 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
             X[tb] = vec4(vec + kTillBeta + 16 * tb + 4 * g) * R[tb];
         }
         // beta U for y, or U itself for the backward
-        frag_t<E> w[2];
+        frag_t<E> w[2], wl[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            w[j] = KEEP ? round_pair<E>(R[2 * j], R[2 * j + 1])
-                        : round_pair<E>(bt[2 * j] * R[2 * j], bt[2 * j + 1] * R[2 * j + 1]);
+        for (int j = 0; j < 2; ++j) {
+            if (KEEP) w[j] = round_pair<E>(R[2 * j], R[2 * j + 1]);
+            else split_pair(bt[2 * j] * R[2 * j], bt[2 * j + 1] * R[2 * j + 1], w[j], wl[j]);
+        }
         split_pair(X[0], X[1], xh[0], xl[0]);
         split_pair(X[2], X[3], xh[1], xl[1]);
         const float whole = vec[kSince + kC - 1];
@@ -1008,8 +1017,15 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
                 y[tb] = vec4(vec + kScaled + 16 * tb + 4 * g) * qs[tb];
-                mma(y[tb], load_frag(pf + lower_block(tb, 0) * 512), w[0]);
-                if (tb >= 2) mma(y[tb], load_frag(pf + lower_block(tb, 1) * 512), w[1]);
+#pragma unroll
+                for (int kb = 0; kb <= tb / 2; ++kb) {
+                    const frag_t<E> f = load_frag(pf + lower_block(tb, kb) * 512);
+                    mma(y[tb], f, w[kb]);
+                    if (kPlanes<E> == 2) {
+                        mma(y[tb], f, wl[kb]);
+                        mma(y[tb], load_frag(pf + PL + lower_block(tb, kb) * 512), w[kb]);
+                    }
+                }
             }
             if (STAGED) loads_done();
             store_tile<E>(rows_of(a.y, i), ldb, poff, y, sel, l);
@@ -1174,7 +1190,7 @@ template <typename E, int NB, int KIND> struct Narrow {
     static constexpr int NW = kNW<NB>, NBW = NB / NW, TBW = 4 / NW, KBW = NBW / 2, NK = NB / 2;
     static constexpr int kPart = NW * 4 * 64 * 4;                         // floats: [wave][tb][lane][4]
     static constexpr int kFrag = 512 * kPlanes<E>;                        // elements of a split operand
-    static constexpr int kBytes = (KIND == 0 ? 2 : 1) * kPart * 4 + (2 * 2 * kFrag + (KIND == 0 ? 2 * 512 : 0)) * (int)sizeof(E);
+    static constexpr int kBytes = (KIND == 0 ? 2 : 1) * kPart * 4 + (KIND == 0 ? 3 : 2) * 2 * kFrag * (int)sizeof(E);
 };
 // The half of a split second operand that the 16 tokens of row block tb are, and the operand.
 template <typename E> __device__ __forceinline__ void put_half(E *f, int tb, int lane, const floatx4 &v)
@@ -1296,8 +1312,8 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
     };
     Select<E> sel;
     sel.init(lane);
-    frag_t<E> kf[4][KBW], qf[KEEP ? 1 : 4][KBW], ktf[NBW][2], pf[KEEP ? 1 : TBW][2];
-    TriRow<E> nf[TBW];
+    frag_t<E> kf[4][KBW], qf[KEEP ? 1 : 4][KBW], ktf[NBW][2];
+    TriRow<E> nf[TBW], pf[KEEP ? 1 : TBW];
     floatx4 since[TBW], bt[TBW], tillb[TBW], scaled[TBW];
     typename Tile<E>::vec v[TBW];
     float whole;
@@ -1341,10 +1357,7 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
         for (int j = 0; j < TBW; ++j) {
             const int tb = wv * TBW + j;
             nf[j].load(tri, 0, 0, tb >> 1, [&](int kb) { return lower_block(tb, kb); });
-            if (!KEEP)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-                    pf[j][kb] = tri.get(kPlanes<E> * kTriE + lower_block(tb, kb <= tb >> 1 ? kb : 0) * 512);
+            if (!KEEP) pf[j].load(tri, kPlanes<E> * kTriE, 0, tb >> 1, [&](int kb) { return lower_block(tb, kb); });
         }
     };
     auto load_rest = [&]() {
@@ -1401,7 +1414,10 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb)
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) mma(qs[tb], qf[tb][kb], so_.hi[kb]);
+                for (int tb = 0; tb < 4; ++tb) {
+                    mma(qs[tb], qf[tb][kb], so_.hi[kb]);
+                    if (kPlanes<E> == 2) mma(qs[tb], qf[tb][kb], so_.lo[kb]);
+                }
         }
 #pragma unroll
         for (int j = 0; j < TBW; ++j) {
@@ -1432,7 +1448,7 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
             nf[j].product(d, 0, tb >> 1, xh, xl);
             R[j] -= d;   // U
             put_half<E>(uf, tb, lane, tillb[j] * R[j]);
-            if (!KEEP) store_round4(wf + (tb >> 1) * 512 + 8 * lane + 4 * (tb & 1), b_now[j] * R[j]);
+            if (!KEEP) put_half<E>(wf, tb, lane, b_now[j] * R[j]);
         }
         __syncthreads();
 #pragma unroll
@@ -1453,7 +1469,9 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
             store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane, NB, NBW * wv);
         } else {
             const __amdgpu_buffer_rsrc_t rs = rows_of(a.y, i);
-            const frag_t<E> w0 = load_frag(wf + 8 * lane), w1 = load_frag(wf + 512 + 8 * lane);
+            frag_t<E> w[2], wl[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) get_split<E>(wf, kb, lane, w[kb], wl[kb]);
 #pragma unroll
             for (int j = 0; j < TBW; ++j) {
                 const int tb = wv * TBW + j;
@@ -1461,8 +1479,7 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
 #pragma unroll
                 for (int o = 1; o < NW; ++o) s += vec4(partq + ((o * 4 + tb) * 64 + lane) * 4);
                 s *= scaled[j];
-                mma(s, pf[j][0], w0);
-                if (tb >= 2) mma(s, pf[j][1], w1);
+                pf[j].product(s, 0, tb >> 1, w, wl);
                 tile_store<E>(rs, poff + (16 * tb + l) * ldb, s, sel);
             }
         }
