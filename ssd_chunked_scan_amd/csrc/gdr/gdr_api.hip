@@ -78,8 +78,7 @@ ssd_status parse_shape(const ssd_gdr_args *a, Shape *s)
     s->nct = s->packed ? s->T / kC + (s->nseq < s->T ? s->nseq : s->T) : s->b * s->nc;
     s->chains = s->packed ? s->nseq : s->b;
     s->NT = s->N <= 64 ? 64 : s->N <= 128 ? 128 : 256;
-    const int64_t cols = a->dtype == SSD_DTYPE_BF16 ? 32 * kColBlocks<bf16> : 32 * kColBlocks<float>;
-    s->Pp = (s->P + cols - 1) / cols * cols;
+    s->Pp = (s->P + 31) / 32 * 32;
     s->np = (s->Pp + kC - 1) / kC;
     if (s->packed && s->T > ((int64_t)1 << 28)) return SSD_ERR_BAD_SHAPE;   // ids are read with 31-bit byte offsets
     // a chunk's rows of all heads or groups are addressed with 31-bit byte offsets
@@ -110,12 +109,13 @@ Sizes sizes_of(const Shape &s)
 
 // The heads of a group go to `hsplit` workgroups of the gradient kernel.  One workgroup is
 // what a CU holds, so a run takes rounds of 256.  In half heads' time: a workgroup takes its
-// heads and 4 to start and to end, and every split adds fp32 sums of dq and dk to write and
-// read back, about 2; fp32's matrix instructions make a head itself twice as long.
+// heads and 2 to start and to end, and every split adds fp32 sums of dq and dk to write and
+// read back, about 1 (with 4 and 2, or 6 and 3, nine backwards of 55 to 1530 us took the same
+// or up to 2 us more).
 int64_t head_split(const Shape &s)
 {
     const int64_t tiles = s.nct * s.G, hpg = s.H / s.G;
-    const int64_t ends = s.dtype == SSD_DTYPE_BF16 ? 4 : 2, sums = s.dtype == SSD_DTYPE_BF16 ? 2 : 1;
+    const int64_t ends = 2, sums = 1;
     int64_t best = 1, cost = INT64_MAX;
     for (int64_t k = 1; k <= hpg && k <= 32; ++k) {
         const int64_t c = (tiles * k + 255) / 256 * (2 * ((hpg + k - 1) / k) + ends) + (k > 1 ? sums : 0);
@@ -166,10 +166,11 @@ Workspace layout(const Shape &s, bool bwd)
     w.vec = take(u * kVec * 4);
     w.tri = take(u * (size_t)tri * s.esz);
     if (bwd) {
-        w.sst = take(u * (size_t)(s.NT * s.Pp) * s.esz);
-        w.ust = take(u * kC * (size_t)s.Pp * s.esz);
-        w.dst = take(u * (size_t)(s.NT * s.Pp) * s.esz);
-        w.hst = take(u * kC * (size_t)s.Pp * s.esz);
+        const size_t col = (size_t)s.Pp * (s.dtype == SSD_DTYPE_BF16 ? kPlanes<bf16> : kPlanes<float>) * s.esz;
+        w.sst = take(u * (size_t)s.NT * col);
+        w.ust = take(u * kC * col);
+        w.dst = take(u * (size_t)s.NT * col);
+        w.hst = take(u * kC * col);
         const int64_t hs = head_split(s);
         w.part = take(hs > 1 ? (size_t)(s.nct * s.G * hs) * 2 * kC * (size_t)s.NT * 4 : 0);
     }
@@ -312,7 +313,7 @@ template <typename E> ssd_status bwd_typed(const Shape &s, const ssd_gdr_args *a
     ga.ust = c.ust;
     ga.dst = c.dst;
     ga.hst = c.hst;
-    ga.vec = c.vec;
+    ga.vec = reinterpret_cast<float *>(ws + w.vec);
     ga.dq = g->dq;
     ga.dk = g->dk;
     ga.dg = g->dg;

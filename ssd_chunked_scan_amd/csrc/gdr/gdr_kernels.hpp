@@ -40,16 +40,17 @@
 // only the first operands (K, K^T, Q, N, Gam o Q K^T) come from memory, laid out
 // once per chunk in that slot order ("slot order" below).
 //
-// Numerics.  Inputs are exact in their type.  For bf16 problems the chain carries
-// S, U and D in fp32 and hands them to the matrix cores as a sum of two bf16
-// numbers (16 bits of significand; the error of a product is about 2^-18 of its
-// size), so states and dV are as good as fp32 storage of them needs, and y takes
-// its operands (S, beta U, Gam o Q K^T) the same way: with similar keys, beta near
-// 1 and weak decay the terms of y are several times y itself, and single bf16
-// numbers left y off by 1.6e-2 of its norm (keys at cosines of 0.9) where its own
-// rounding is 1.7e-3.  It costs the 16K-token chains 592 -> 695 us and packed
-// prompts 326 -> 367.  The products of dq and dk take one bf16 number for S, U, D
-// and H.
+// Numerics.  Inputs are exact in their type.  For bf16 problems S, U, D and every
+// sum are fp32, and whatever is not an input goes to the matrix cores as a sum of
+// two bf16 numbers (16 bits of significand; a product drops that of the two small
+// parts, about 2^-18 of its size).  So y and the gradients are off by the one
+// rounding of their type (1.7e-3 in norm), states by 3e-6 to 4e-5.  With single bf16
+// numbers for the operands of the outputs that do not feed the chain (S, beta U and
+// Gam o Q K^T of y; S, U, D, H and the pair matrices of the gradients) random keys
+// gave 2.9e-3; but with similar keys, beta near 1 and weak decay the terms are
+// several times the sum, and keys at cosines of 0.9 gave 1.6e-2 for y and up to
+// 6e-2 for dg.  The second numbers cost 592 -> 694 us for 16K tokens forward,
+// 326 -> 367 for packed prompts and 1112 -> 1494 for the 2.7B-scale backward.
 // fp32 problems use the fp32 matrix instructions throughout.
 #pragma once
 
@@ -68,10 +69,10 @@ constexpr int kTri = 6;           // 16 x 32 operand blocks in a triangle of 64 
 // the reference r_b = cs before block b, for t in block b and s before it
 //   Gam_ts = e^{cs_t - r_b} e^{r_b - cs_s}   (both at most 1)
 // scale e^{cs_t - r_b}, beta_t e^{cs_t - r_b} (zero past the count), and beta_s e^{r_b -
-// cs_s} for b = 1, 2, 3.
+// cs_s} for b = 1, 2, 3; and room for one vector (dg of the first pass).
 constexpr int kVec = 16 * kC, kVecChain = 8 * kC;
 constexpr int kSince = 0, kBeta = kC, kScaled = 2 * kC, kTillBeta = 3 * kC, kTill = 4 * kC, kErase = 5 * kC,
-              kCsHi = 6 * kC, kCsLo = 7 * kC, kRowScale = 8 * kC, kRowBeta = 9 * kC, kColBeta = 10 * kC;
+              kCsHi = 6 * kC, kCsLo = 7 * kC, kRowScale = 8 * kC, kRowBeta = 9 * kC, kColBeta = 10 * kC, kDgPass = 13 * kC;
 constexpr double kLog2eD = 1.4426950408889634;
 constexpr float kMinLogDecay = -64.f;   // e^-64 = 1.6e-28: smaller decays act as this one
 
@@ -336,9 +337,10 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 //
 // 8 x 2048 tokens of 80 heads, backward: 168 us, 1.15 GB (36 KB of triangles and 4 KB of
 // scalars to write per chunk and head) at 6.8 TB/s, part of it still on its way through the
-// last cache level.  (235 us while Gam o Q K^T was formed before the inverse, whose spilled
-// registers came back from memory behind the stores.)  The forward writes half and is bound by
-// latency at two waves a SIMD (232 registers): packed prompts of 64 heads 120 us, matrix and
+// last cache level.  (235 us while Gam o Q K^T was formed before the inverse, with more spilled
+// registers, which came back from memory behind the stores; the bf16 backward that stores past
+// the caches spills 9.)  The forward writes two thirds and is bound by
+// latency at two waves a SIMD (247 registers): packed prompts of 64 heads 130 us, matrix and
 // vector pipes about a quarter busy.  Workgroups of four waves that shared one head, with
 // barriers between the blocks, took 177 us there.
 //
@@ -643,7 +645,7 @@ struct ChainArgs {
     float *s1, *d0;              // final state, gradient of the initial state, or null
     void *sst, *ust, *dst, *hst; // backward only: S, U, D, H of every (chunk, head)
     Chunks m;
-    int H, G, P, N, Pp, np;      // Pp: P rounded up to 32 kColBlocks; np: workgroups per head
+    int H, G, P, N, Pp, np;      // Pp: P rounded up to 32; np: workgroups per head
     int units;                   // chains * H * np
     float scale;
 };
@@ -680,26 +682,39 @@ __device__ __forceinline__ void save_state(float *dst, const floatx4 (&s)[NB], i
 }
 
 // S, U, D and H of a chunk and head are kept as operand blocks with their columns p as
-// slots (in order, 8 per lane), kColBlocks blocks of 32 columns for each row block, the
-// columns after these after all rows: what the gradient kernel takes at a time is
-// contiguous.  Where lane (g, l) puts columns p0 + 4 g .. + 3 of row l of row block b (a
-// wave's 16 x 16 piece is 512 contiguous bytes of bf16):
-template <typename E> constexpr int kColBlocks = sizeof(E) == 2 ? 2 : 1;
-template <typename E> __device__ __forceinline__ int64_t piece(int b, int rows, int p0, int g, int l)
+// slots (in order, 8 per lane): for every 32 columns the row blocks of each plane, so that
+// what the gradient kernel takes at a time is contiguous.  Where lane (g, l) puts columns
+// p0 + 4 g .. + 3 of row l of row block b (a wave's 16 x 16 piece is 512 contiguous bytes of
+// bf16):
+template <typename E> __device__ __forceinline__ int64_t piece(int b, int rows, int p0, int g, int l, int plane)
 {
-    constexpr int KB = kColBlocks<E>;
-    const int block = (p0 / (32 * KB) * rows + b) * KB + (p0 >> 5) % KB;
+    const int block = ((p0 >> 5) * kPlanes<E> + plane) * rows + b;
     return ((int64_t)block * 64 + l + 16 * (((p0 & 31) >> 3) + (g >> 1))) * 8 + 4 * (g & 1);
 }
-template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *dst, const frag_t<E> (&f)[NF],
-                                                                           const Select<E> &sel, int p0, int lane,
-                                                                           int rows = 2 * NF, int row0 = 0)
+template <typename E, int NF> __device__ __forceinline__ void store_pieces(E *dst, const frag_t<E> (&hi)[NF],
+                                                                           const frag_t<E> (&lo)[NF], const Select<E> &sel,
+                                                                           int p0, int lane, int rows = 2 * NF, int row0 = 0)
 {
 #pragma unroll
-    for (int b = 0; b < 2 * NF; ++b) {
+    for (int b = 0; b < 2 * NF; ++b)
+#pragma unroll
+        for (int pl = 0; pl < kPlanes<E>; ++pl) {
+            floatx4 d = floatx4{0, 0, 0, 0};
+            mma(d, pl ? lo[b >> 1] : hi[b >> 1], sel.half[b & 1]);
+            store_round4<true>(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15, pl), d);
+        }
+}
+// One 16 x 16 accumulator of such a matrix of 64 rows.
+template <typename E> __device__ __forceinline__ void store_piece(E *dst, const floatx4 &v, const Select<E> &sel, int b,
+                                                                  int p0, int lane)
+{
+    frag_t<E> hi, lo;
+    split_pair(v, floatx4{0, 0, 0, 0}, hi, lo);
+#pragma unroll
+    for (int pl = 0; pl < kPlanes<E>; ++pl) {
         floatx4 d = floatx4{0, 0, 0, 0};
-        mma(d, f[b >> 1], sel.half[b & 1]);
-        store_round4<true>(dst + piece<E>(row0 + b, rows, p0, lane >> 4, lane & 15), d);
+        mma(d, pl ? lo : hi, sel.half[0]);
+        store_round4(dst + piece<E>(b, 4, p0, lane >> 4, lane & 15, pl), d);
     }
 }
 
@@ -765,10 +780,11 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t l
 // both that its operands are there and that the other region is free.  Sets too large for
 // LDS (fp32 at N = 256) are read from global memory by every wave (STAGED false).
 //
-// 8 x 2048 tokens of 80 heads of 64, N = 128, both directions: 620 us for 2.5 GB, 4.0 TB/s of
-// the 5.1 that a copy reaches; without its operand loads or without its stores (timing
-// variants) 480 and 440 us, without both 305 us, the arithmetic's own time at two workgroups
-// a CU.  Packed prompts of 64 heads, forward: 209 us.
+// 8 x 2048 tokens of 80 heads of 64, N = 128, both directions: 720 us for 3.5 GB, 4.8 TB/s of
+// the 5.1 that a copy reaches.  (While S, U, D and H were kept as single bf16 numbers, 2.5 GB
+// took 620 us; without the operand loads or without the stores 480 and 440 us, without both
+// 305 us, the arithmetic's own time at two workgroups a CU.)  Packed prompts of 64 heads,
+// forward: 229 us.
 template <typename E, int NT> constexpr bool kStaged = sizeof(E) * NT <= 512;
 
 // KIND 0: the forward (y), 1: the forward for the backward (S and U), 2: the backward
@@ -990,7 +1006,7 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
         frag_t<E> w[2], wl[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            if (KEEP) w[j] = round_pair<E>(R[2 * j], R[2 * j + 1]);
+            if (KEEP) split_pair(R[2 * j], R[2 * j + 1], w[j], wl[j]);
             else split_pair(bt[2 * j] * R[2 * j], bt[2 * j + 1] * R[2 * j + 1], w[j], wl[j]);
         }
         split_pair(X[0], X[1], xh[0], xl[0]);
@@ -1009,8 +1025,8 @@ __device__ __forceinline__ void chain_fwd(const ChainArgs &a, int unit, char *sm
         if (KEEP) {
             if (STAGED) loads_done();
             if (keep) {
-                store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane);
-                store_pieces<E>((E *)a.ust + u * kC * a.Pp, w, sel, p0, lane);
+                store_pieces<E>((E *)a.sst + u * kPlanes<E> * NT * a.Pp, so_.hi, so_.lo, sel, p0, lane);
+                store_pieces<E>((E *)a.ust + u * kPlanes<E> * kC * a.Pp, w, wl, sel, p0, lane);
             }
         } else {
             floatx4 y[4];
@@ -1148,7 +1164,9 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
                 mma(D[nb], fq, yh[kb]);
                 if (kPlanes<E> == 2) mma(D[nb], fq, yl[kb]);
             }
-        const frag_t<E> hf[2] = {round_pair<E>(W[0], W[1]), round_pair<E>(W[2], W[3])};
+        frag_t<E> hf[2], hl[2];
+        split_pair(W[0], W[1], hf[0], hl[0]);
+        split_pair(W[2], W[3], hf[1], hl[1]);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) W[tb] *= vec4(vec + kErase + 16 * tb + 4 * g);
         split_pair(W[0], W[1], xh[0], xl[0]);
@@ -1164,8 +1182,8 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
         if (STAGED) loads_done();
         store_tile<E>(rows_of(a.dv, i), ldb, poff, X, sel, l);
         if (keep) {
-            store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, lane);
-            store_pieces<E>((E *)a.hst + u * kC * a.Pp, hf, sel, p0, lane);
+            store_pieces<E>((E *)a.dst + u * kPlanes<E> * NT * a.Pp, dop.hi, dop.lo, sel, p0, lane);
+            store_pieces<E>((E *)a.hst + u * kPlanes<E> * kC * a.Pp, hf, hl, sel, p0, lane);
         }
     }
     save_state<NB>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N);
@@ -1180,11 +1198,12 @@ __device__ __forceinline__ void chain_bwd(const ChainArgs &a, int unit, char *sm
 // operand is now used by one wave once, so it comes from memory into registers, requested
 // for the next step as soon as this step has used it.
 //
-// 16K tokens of 32 heads, N = 256: 545 us (wide: 1.36 ms), 2.1 us a step, of which 1.4 are
-// the chain of products and exchanges and the rest 112 KB of operands at a CU's 64 bytes a
-// cycle.  2 x 2048 tokens of 24 heads, N = 64, both directions: 74 us.  Requests issued
-// earlier, between the products, made no difference (570 us), nor did touching the operands
-// of two steps ahead for L2 (570 us).
+// 16K tokens of 32 heads, N = 256: 645 us, 2.5 us a step; 545 us (wide: 1.36 ms), 2.1 us a
+// step, before y took two bf16 numbers for its operands: 1.4 us for the chain of products and
+// exchanges and the rest for 112 KB of operands at a CU's 64 bytes a cycle.  2 x 2048 tokens
+// of 24 heads, N = 64, both directions: 82 us.  Requests issued earlier, between the products,
+// made no difference then (570 us), nor did touching the operands of two steps ahead for L2
+// (570 us).
 template <int NB> constexpr int kNW = NB / 2 < 4 ? NB / 2 : 4;
 template <typename E, int NB, int KIND> struct Narrow {
     static constexpr int NW = kNW<NB>, NBW = NB / NW, TBW = 4 / NW, KBW = NBW / 2, NK = NB / 2;
@@ -1465,8 +1484,8 @@ __device__ __forceinline__ void narrow_fwd(const ChainArgs &a, int unit, char *s
         if (KEEP) {
 #pragma unroll
             for (int j = 0; j < TBW; ++j)
-                store_round4((E *)a.ust + u * kC * a.Pp + piece<E>(wv * TBW + j, 4, p0, g, l), transposed<E>(R[j], sel));
-            store_pieces<E>((E *)a.sst + u * NT * a.Pp, so_.hi, sel, p0, lane, NB, NBW * wv);
+                store_piece<E>((E *)a.ust + u * kPlanes<E> * kC * a.Pp, R[j], sel, wv * TBW + j, p0, lane);
+            store_pieces<E>((E *)a.sst + u * kPlanes<E> * NT * a.Pp, so_.hi, so_.lo, sel, p0, lane, NB, NBW * wv);
         } else {
             const __amdgpu_buffer_rsrc_t rs = rows_of(a.y, i);
             frag_t<E> w[2], wl[2];
@@ -1664,9 +1683,9 @@ __device__ __forceinline__ void narrow_bwd(const ChainArgs &a, int unit, char *s
         for (int j = 0; j < TBW; ++j) {
             const int tb = wv * TBW + j;
             tile_store<E>(rs, poff + (16 * tb + l) * ldb, X[j], sel);
-            store_round4((E *)a.hst + u * kC * a.Pp + piece<E>(tb, 4, p0, g, l), transposed<E>(W[j], sel));
+            store_piece<E>((E *)a.hst + u * kPlanes<E> * kC * a.Pp, W[j], sel, tb, p0, lane);
         }
-        store_pieces<E>((E *)a.dst + u * NT * a.Pp, dop.hi, sel, p0, lane, NB, NBW * wv);
+        store_pieces<E>((E *)a.dst + u * kPlanes<E> * NT * a.Pp, dop.hi, dop.lo, sel, p0, lane, NB, NBW * wv);
     }
     save_state<NBW>(a.d0 ? a.d0 + so : nullptr, D, p0 + l, g, a.P, a.N, 16 * NBW * wv);
 }
@@ -1721,7 +1740,7 @@ __global__ __launch_bounds__(64 * kNW<NB>, 1) void k_gdr_chains_narrow(ChainArgs
 // the same sum, would need dq and dv far beyond bf16: 9e-3 against 2e-3 of dg.)
 struct GradArgs {
     const void *kq, *k, *q, *dy, *sst, *ust, *dst, *hst;
-    const float *vec;
+    float *vec;                  // (written: kDgPass)
     void *dq, *dk, *dg, *dbeta;
     float *part;                 // hsplit > 1: fp32 sums of dq and dk per split
     Chunks m;
@@ -1731,26 +1750,33 @@ struct GradArgs {
 
 // One workgroup per (chunk, group, part of the group's heads), 8 waves: wave (tb, half)
 // owns 16 tokens and half of the columns n of dq and dk, in registers over all heads.
-// What a head brings (S, D, U, H and dy, 64 columns p at a time) comes into LDS as
-// operand blocks without passing through registers, for the next head while this one
-// computes where LDS holds it twice (TWICE).
+// What a head brings (S, D, U, H and dy, 32 columns p at a time) comes into LDS as
+// operand blocks without passing through registers, for the next stage while this one
+// computes where LDS holds it twice (TWICE).  At N = 256 registers and LDS hold half of the
+// columns n: a workgroup goes over its heads twice, forms the pair matrices again and adds
+// up dg, whose terms are sums over n (in one pass it spilled 141 registers in bf16 and 196 in
+// fp32: 16K tokens of 32 heads 2380 against 1535 us for the whole backward, fp32 of 2048
+// tokens of 128 heads 2680 against 2240; 32 and 44 are left).
 //
-// 8 x 2048 tokens of 80 heads, N = 128: 485 us (900 us before half the waves formed W and the
-// others Z; 555 with a head's dg finished by one wave at its end and the next stage requested
-// first).  It has 1.25 GB to read, 250 us of a copy's rate; what holds it is the chain inside
-// a head at two waves a SIMD.  Waves wait half of the time; LDS (54 KB read per wave and
-// head) is busy a quarter.
+// 8 x 2048 tokens of 80 heads, N = 128: 690 us, 2.24 GB read at 3.3 TB/s.  What holds it is
+// the chain inside a stage at two waves a SIMD (247 registers): waves wait a third of the
+// time, the matrix pipe is busy 27 %.  (410 us, half the bytes, with single bf16 numbers; 900
+// before half the waves formed W and the others Z; 70 more with a head's dg finished by one
+// wave at its end and the next stage requested first.)
 constexpr int kGradThreads = 512;
 constexpr int kDgHeads = 4;   // heads whose dg is finished at a time
 template <typename E, int NB> struct GradPlan {
-    static constexpr int KPC = kColBlocks<E>;                   // 32-column blocks per stage
-    static constexpr int kBlocks = (2 * NB + 12) * KPC;         // S | D | U | H | dy
-    static constexpr int kRoom = kBlocks < 24 ? 24 : kBlocks;   // (at least what is exchanged below)
+    static constexpr int PL = kPlanes<E>;
+    static constexpr int kPasses = NB == 16 ? 2 : 1, kRows = NB / kPasses;   // row blocks n of a pass
+    static constexpr int kBlocks = (2 * kRows + 8) * PL + 4;              // of 32 columns: S | D | U | H | dy
+    static constexpr int kRoom = kBlocks < 24 * PL ? 24 * PL : kBlocks;   // (at least what is exchanged below)
     static constexpr int kStage = kRoom * 512 * (int)sizeof(E);
-    static constexpr int kMats = 2 * 2 * NB * 512 * (int)sizeof(E);   // K^T and Q^T
-    static constexpr int kRest = 2 * kVec * 4 + 1024;
-    static constexpr bool TWICE = 2 * kStage + kMats + kRest <= 160 * 1024;
-    static constexpr bool MATS = kStage + kMats + kRest <= 160 * 1024;   // K^T and Q^T in LDS as well
+    static constexpr int kMats = 2 * 2 * kRows * 512 * (int)sizeof(E);    // K^T and Q^T
+    static constexpr int kDg = kDgHeads * (4 * kC + 17) * 4;              // dcs and red
+    static constexpr int kLds = 160 * 1024;
+    static constexpr bool TWICE = 2 * kStage + kMats + 2 * kVec * 4 + kDg <= kLds;
+    static constexpr int kVecs = (TWICE ? 2 : 1) * kVec;
+    static_assert((TWICE ? 2 : 1) * kStage + kMats + kVecs * 4 + kDg <= kLds, "a workgroup's LDS");
 };
 
 // acc + the sum of eight products (bf16: two per instruction, in fp32).
@@ -1806,11 +1832,12 @@ __device__ __forceinline__ float prefix_sum64(float v)
 template <typename E, int NB>
 __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
 {
-    using PL = GradPlan<E, NB>;
-    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT, KPC = PL::KPC, HB = NB / 2, V = kVec16<E>;
-    __shared__ __attribute__((aligned(16))) E stage_m[(PL::TWICE ? 2 : 1) * PL::kRoom * 512];
-    __shared__ __attribute__((aligned(16))) E mats[PL::MATS ? 2 * kMat : 8];
-    __shared__ __attribute__((aligned(16))) float vs2[2 * kVec];
+    using Plan = GradPlan<E, NB>;
+    constexpr int NT = 16 * NB, NK = NT / 32, kMat = kC * NT, PL = Plan::PL, NBP = Plan::kRows, HB = NBP / 2, V = kVec16<E>;
+    constexpr int kHalf = kMat / Plan::kPasses;   // of K^T and Q^T, what a pass takes
+    __shared__ __attribute__((aligned(16))) E stage_m[(Plan::TWICE ? 2 : 1) * Plan::kRoom * 512];
+    __shared__ __attribute__((aligned(16))) E mats[2 * kHalf];
+    __shared__ __attribute__((aligned(16))) float vs2[Plan::kVecs];
     __shared__ float dcs[kDgHeads][4][kC], red[kDgHeads][17];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
     const int w = wv & 3, half = wv >> 2;
@@ -1824,12 +1851,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     if (count <= 0) return;
     const int hpg = a.H / a.G;
     const int h0 = grp * hpg + (int)((int64_t)hpg * sp / a.hsplit), h1 = grp * hpg + (int)((int64_t)hpg * (sp + 1) / a.hsplit);
-    const int NPC = a.Pp / (32 * KPC), J = (h1 - h0) * NPC;
+    const int NPC = a.Pp / 32, J = (h1 - h0) * NPC;
     const E *kf = (const E *)a.kq + ((int64_t)c * a.G + grp) * 4 * kMat;
     const E *ktg = kf + kMat, *qf = kf + 2 * kMat, *qtg = kf + 3 * kMat;
     const int64_t yld = (int64_t)a.H * a.P;
 
-    // stage j: head h0 + j / NPC, columns 32 KPC (j % NPC) ...
+    // stage j: head h0 + j / NPC, columns 32 (j % NPC) ...
+    int pass = 0;
     const int mine = wv * 64 * V + V * lane;
     auto run = [&](const E *src, E *dst, auto n) {   // n blocks, 1 KiB at a time from wave to wave
         constexpr int kParts = decltype(n)::value * 512 / (64 * V);
@@ -1841,41 +1869,44 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     auto issue = [&](int j) {
         const int hi = j / NPC, pc = j - hi * NPC, h = h0 + hi;
         const int64_t u = (int64_t)c * a.H + h;
-        E *dst = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kRoom * 512;
-        const int64_t so = u * NT * a.Pp + pc * (NB * KPC * 512), uo = u * kC * a.Pp + pc * (4 * KPC * 512);
-        using BS = std::integral_constant<int, NB * KPC>;
-        using BU = std::integral_constant<int, 4 * KPC>;
-        run((const E *)a.sst + so, dst, BS{});
-        run((const E *)a.dst + so, dst + NB * KPC * 512, BS{});
-        dst += 2 * NB * KPC * 512;
+        E *dst = stage_m + (Plan::TWICE ? (j & 1) : 0) * Plan::kRoom * 512;
+        const int64_t so = (u * a.Pp + 32 * pc) * (PL * NT), uo = (u * a.Pp + 32 * pc) * (PL * kC);
+        using BS = std::integral_constant<int, NBP * (Plan::kPasses == 1 ? PL : 1)>;
+        using BU = std::integral_constant<int, 4 * PL>;
+        for (int pl = 0; pl < (Plan::kPasses == 1 ? 1 : PL); ++pl) {   // (one pass: the planes lie one behind the other)
+            const int from = (pl * NB + pass * NBP) * 512, to = pl * NBP * 512;
+            run((const E *)a.sst + so + from, dst + to, BS{});
+            run((const E *)a.dst + so + from, dst + NBP * PL * 512 + to, BS{});
+        }
+        dst += 2 * NBP * PL * 512;
         run((const E *)a.ust + uo, dst, BU{});
-        run((const E *)a.hst + uo, dst + 4 * KPC * 512, BU{});
-        dst += 8 * KPC * 512;
-        // dy, 8 KiB, a KiB per wave.  Rows past the count and columns past P: any element of
-        // the row's own data (masked below; columns past P meet zeros of S, U and H)
-        {
-            const int r = mine / (512 * KPC), kk = mine / 512 % KPC, e = mine % 512;
-            const int t = 16 * r + (e >> 3) % 16, pp = 32 * (pc * KPC + kk) + 8 * (e >> 7) + (e & 7);
+        run((const E *)a.hst + uo, dst + 4 * PL * 512, BU{});
+        dst += 8 * PL * 512;
+        // dy, a KiB per wave.  Rows past the count and columns past P: any element of the row's
+        // own data (masked below; columns past P meet zeros of S, U and H)
+        if (mine < 4 * 512) {
+            const int e = mine % 512, t = 16 * (mine / 512) + (e >> 3) % 16, pp = 32 * pc + 8 * (e >> 7) + (e & 7);
             const E *dy = (const E *)a.dy + (t0 * a.H + h) * a.P;
             __builtin_amdgcn_global_load_lds((gptr_t)(dy + (int64_t)(t < count ? t : count - 1) * yld + (pp < a.P ? pp : 0)),
                                              (lptr_t)(dst + wv * 64 * V), 16, 0, 0);
         }
         if (pc == 0 && wv >= 4)
             __builtin_amdgcn_global_load_lds((gptr_t)(a.vec + u * kVec + 256 * (wv - 4) + 4 * lane),
-                                             (lptr_t)(vs2 + (hi & 1) * kVec + 256 * (wv - 4)), 16, 0, 0);
+                                             (lptr_t)(vs2 + (Plan::TWICE ? hi & 1 : 0) * kVec + 256 * (wv - 4)), 16, 0, 0);
     };
-    if (PL::TWICE) issue(0);
-    if constexpr (PL::MATS) {
-        constexpr int n = 2 * kMat * (int)sizeof(E) / 1024;   // K^T and Q^T, 1 KiB each
+    auto issue_mats = [&]() {
+        constexpr int n = 2 * kHalf * (int)sizeof(E) / 1024;   // K^T and Q^T, 1 KiB each
         static_assert(n % 16 == 0, "whole rounds");
 #pragma unroll
         for (int i = 0; i < n / 8; ++i) {
             const int b = 8 * i + wv, e = b * 64 * V;
-            const E *src = e < kMat ? ktg + e : qtg + (e - kMat);
+            const E *src = (e < kHalf ? ktg + e : qtg + (e - kHalf)) + pass * kHalf;
             __builtin_amdgcn_global_load_lds((gptr_t)(src + V * lane), (lptr_t)(mats + e), 16, 0, 0);
         }
-    }
-    const E *ktf = (PL::MATS ? mats : ktg) + 8 * lane, *qtf = (PL::MATS ? mats + kMat : qtg) + 8 * lane;
+    };
+    if (Plan::TWICE) issue(0);
+    issue_mats();
+    const E *ktf = mats + 8 * lane, *qtf = mats + kHalf + 8 * lane;
 
     // The pair matrices of the wave's 16 tokens (half 0: W, half 1: Z): block i holds rows of
     // block i against columns of block w, as (s, t) pairs where i <= w and as (t, s) pairs
@@ -1908,249 +1939,308 @@ __global__ __launch_bounds__(kGradThreads, 2) void k_gdr_grad(GradArgs a)
     const uint32_t kqld = (uint32_t)(a.G * a.N) * sizeof(E);
     const __amdgpu_buffer_rsrc_t qrs = rows_rsrc((const E *)a.q + kq0, count, (int64_t)a.G * a.N, a.N);
     const __amdgpu_buffer_rsrc_t krs = rows_rsrc((const E *)a.k + kq0, count, (int64_t)a.G * a.N, a.N);
-#pragma unroll
-    for (int nb = 0; nb < HB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * g + r, n = 16 * (half * HB + nb) + l;
-            const uint32_t off = n < a.N ? t * kqld + n * sizeof(E) : kOffNone;
-            if constexpr (sizeof(E) == 2) {
-                const uint32_t qv = __builtin_bit_cast(unsigned short, bload_elem<E>(qrs, off));
-                const uint32_t kv = __builtin_bit_cast(unsigned short, bload_elem<E>(krs, off));
-                qe[nb][r / 2] = r % 2 ? qe[nb][r / 2] | qv << 16 : qv;
-                ke[nb][r / 2] = r % 2 ? ke[nb][r / 2] | kv << 16 : kv;
-            } else {
-                qe[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(qrs, off));
-                ke[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(krs, off));
-            }
-        }
     floatx4 dq[HB], dk[HB];
-#pragma unroll
-    for (int nb = 0; nb < HB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
-
     floatx4 m[4], mD, aq, ak, bk;
     float db = 0.f, sd = 0.f;
     const int tl0 = 16 * w + l;
-    for (int j = 0; j < J; ++j) {
-        const int h = h0 + j / NPC, pc = j % NPC;
-        if (!PL::TWICE) {
-            __syncthreads();
-            issue(j);
+    // N = 256: one pass over the heads for each half of the columns n (their registers and LDS
+    // are those of N = 128; the pair matrices are formed twice)
+    for (; pass < Plan::kPasses; ++pass) {
+        if (pass) {
+            __syncthreads();   // the last pass has read its operands
+            if (Plan::TWICE) issue(0);
+            issue_mats();
         }
-        loads_done();
-        __syncthreads();
-        E *room = stage_m + (PL::TWICE ? (j & 1) : 0) * PL::kRoom * 512;
-        const E *buf = room + 8 * lane;
-        const E *Sb = buf, *Db = buf + NB * KPC * 512, *Ub = buf + 2 * NB * KPC * 512, *Hb = Ub + 4 * KPC * 512,
-                *Yb = Hb + 4 * KPC * 512, *Xb = half ? Hb : Yb;
-        const float *vs = vs2 + ((h - h0) & 1) * kVec;
-        if (pc == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = floatx4{0, 0, 0, 0};
-            mD = aq = ak = bk = floatx4{0, 0, 0, 0};
-            db = sd = 0.f;
-        }
-        frag_t<E> uw[KPC], hw[KPC], yw[KPC];
-#pragma unroll
-        for (int kb = 0; kb < KPC; ++kb) {
-            uw[kb] = load_frag(Ub + (w * KPC + kb) * 512);
-            hw[kb] = load_frag(Hb + (w * KPC + kb) * 512);
-            yw[kb] = load_frag(Yb + (w * KPC + kb) * 512);
-            const frag_t<E> xw = load_frag(Xb + (w * KPC + kb) * 512);
-            frag_t<E> f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = load_frag((i <= w ? Ub : Xb) + (i * KPC + kb) * 512);
-            if (half) db = dot8(uw[kb], hw[kb], db);
-            mma(mD, xw, uw[kb]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i <= w) mma(m[i], f[i], xw);
-                else mma(m[i], f[i], uw[kb]);
-        }
-        // (requested here and not at the head of the stage, where the compiler has the first LDS
-        // read wait for it; the exchange below waits for it in any case)
-        if (PL::TWICE && j + 1 < J) issue(j + 1);
-        // the state products
-        {
-            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
-                          ch = vec4(vs + kErase + 16 * w + 4 * g);
-#pragma unroll
-            for (int nb = 0; nb < HB; ++nb) {
-                floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
-#pragma unroll
-                for (int kb = 0; kb < KPC; ++kb) {
-                    const frag_t<E> sf = load_frag(Sb + ((half * HB + nb) * KPC + kb) * 512);
-                    const frag_t<E> df = load_frag(Db + ((half * HB + nb) * KPC + kb) * 512);
-                    mma(ys, yw[kb], sf);
-                    mma(hs, hw[kb], sf);
-                    mma(ud, uw[kb], df);
-                    if ((nb & 3) == w) sd = dot8(sf, df, sd);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    uint32_t qw = qe[nb][r * QW / 4], kw = ke[nb][r * QW / 4];
-                    asm volatile("" : "+v"(qw), "+v"(kw));   // (unpacked here, not kept unpacked)
-                    if (QW == 2) {
-                        qw = r % 2 ? qw & 0xffff0000u : qw << 16;
-                        kw = r % 2 ? kw & 0xffff0000u : kw << 16;
-                    }
-                    aq[r] += __uint_as_float(qw) * ys[r];
-                    ak[r] += __uint_as_float(kw) * hs[r];
-                    bk[r] += __uint_as_float(kw) * ud[r];
-                    dq[nb][r] += cq[r] * ys[r];
-                    dk[nb][r] += cd[r] * ud[r];
-                    dk[nb][r] += ch[r] * hs[r];
-                }
-            }
-        }
-        if (pc != NPC - 1) continue;
-        // the head's pair matrix and its part of dg.  Rows past the count hold data of the last
-        // row; their factors are zero.
-        // (sums over s and over t apart, so that what cancels does so exactly)
-        float dx = 0.f, dx_s = 0.f;
-        // (opaque, so that the comparisons below are made here and not kept in registers)
-        int tl = tl0, o0 = 4 * g;
-        asm volatile("" : "+v"(tl), "+v"(o0));
-        const float *row = vs + (half ? kRowBeta : kRowScale);
-        // the factors of every block first, then the branches, so that the reads go out together
-        floatx4 fo[4];   // of o: before t (i < w), or t itself
-        float fl[4];     // of tl: t itself, or before t
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fo[i] = vec4((i < w ? vs + kColBeta + (w - 1) * kC : row) + 16 * i + o0);
-            fl[i] = (i < w ? row : vs + kColBeta + (i - 1) * kC)[tl];
-        }
-        const float chi = vs[kCsHi + tl], clo = vs[kCsLo + tl], bl = vs[kBeta + tl];
-        const floatx4 oh = vec4(vs + kCsHi + 16 * w + o0), ol = vec4(vs + kCsLo + 16 * w + o0),
-                      bo = vec4(vs + kBeta + 16 * w + o0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i != w) {   // t = tl, s = o (i < w); t = o, s = tl
-                m[i] *= fl[i] * fo[i];
-                float d = 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) d += m[i][r] * kq[i][r];
-                dx += i < w ? d : 0.f;
-                dx_s += i < w ? 0.f : d;
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int o = 16 * i + o0 + r;
-                    const float d = ((chi - oh[r]) + (clo - ol[r])) * kLog2e;
-                    const bool down = half ? o < tl : o <= tl, up = half ? tl < o : tl <= o;
-                    const float f = exp2_(down ? d : 0.f) * bo[r] * (half ? bl : a.scale);
-                    m[i][r] = down && tl < count ? f * m[i][r] : 0.f;
-                    const float fD = exp2_(up ? -d : 0.f) * bl * (half ? bo[r] : a.scale);
-                    mD[r] = up && o < count ? fD * mD[r] : 0.f;
-                    dx += m[i][r] * kq[i][r];
-                    dx_s += mD[r] * kqD[r];
-                }
-            }
-        dx -= dx_s;
-        // its operands change hands through what this stage no longer needs
-        __syncthreads();
-        {
-            const floatx4 none = floatx4{0, 0, 0, 0};
-            E *mine = room + w * 6 * 512 + 8 * lane;
-            if (half == 0) {
-                floatx4 up[4], dn[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    up[i] = i <= w ? m[i] : none;
-                    dn[i] = i < w ? none : i == w ? mD : m[i];
-                }
-                store_frag(mine, round_pair<E>(up[0], up[1]));
-                store_frag(mine + 512, round_pair<E>(up[2], up[3]));
-                store_frag(mine + 1024, round_pair<E>(dn[0], dn[1]));
-                store_frag(mine + 1536, round_pair<E>(dn[2], dn[3]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m[i] = i == w ? -m[i] - mD : -m[i];
-                store_frag(mine + 2048, round_pair<E>(m[0], m[1]));
-                store_frag(mine + 2560, round_pair<E>(m[2], m[3]));
-                dx = -dx;
-            }
-        }
-        // dg and dbeta
-        floatx4 ab;
-        float sb = 0.f;
-        {
-            const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
-                          ch = vec4(vs + kErase + 16 * w + 4 * g);
+        for (int nb = 0; nb < HB; ++nb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool in = 16 * w + 4 * g + r < count;
-                const float b = cd[r] * bk[r];
-                sb += b;
-                ab[r] = in ? row_sum16(cq[r] * aq[r] + ch[r] * ak[r] - b) : 0.f;
+                const int t = 16 * w + 4 * g + r, n = 16 * (pass * NBP + half * HB + nb) + l;
+                const uint32_t off = n < a.N ? t * kqld + n * sizeof(E) : kOffNone;
+                if constexpr (sizeof(E) == 2) {
+                    const uint32_t qv = __builtin_bit_cast(unsigned short, bload_elem<E>(qrs, off));
+                    const uint32_t kv = __builtin_bit_cast(unsigned short, bload_elem<E>(krs, off));
+                    qe[nb][r / 2] = r % 2 ? qe[nb][r / 2] | qv << 16 : qv;
+                    ke[nb][r / 2] = r % 2 ? ke[nb][r / 2] | kv << 16 : kv;
+                } else {
+                    qe[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(qrs, off));
+                    ke[nb][r] = __builtin_bit_cast(uint32_t, bload_elem<E>(krs, off));
+                }
+            }
+#pragma unroll
+        for (int nb = 0; nb < HB; ++nb) dq[nb] = dk[nb] = floatx4{0, 0, 0, 0};
+
+        for (int j = 0; j < J; ++j) {
+            const int h = h0 + j / NPC, pc = j % NPC;
+            if (!Plan::TWICE) {
+                __syncthreads();
+                issue(j);
+            }
+            loads_done();
+            __syncthreads();
+            E *room = stage_m + (Plan::TWICE ? (j & 1) : 0) * Plan::kRoom * 512;
+            const E *buf = room + 8 * lane;
+            const E *Sb = buf, *Db = buf + NBP * PL * 512, *Ub = buf + 2 * NBP * PL * 512, *Hb = Ub + 4 * PL * 512,
+                    *Yb = Hb + 4 * PL * 512, *Xb = half ? Hb : Yb;
+            const float *vs = vs2 + (Plan::TWICE ? (h - h0) & 1 : 0) * kVec;
+            if (pc == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = floatx4{0, 0, 0, 0};
+                mD = aq = ak = bk = floatx4{0, 0, 0, 0};
+                db = sd = 0.f;
+            }
+            // (a second plane's products are those that hi and lo of both factors give, without lo
+            // lo; dy is exact in one)
+            frag_t<E> uw[PL], hw[PL];
+            const frag_t<E> yw = load_frag(Yb + w * 512), xw = load_frag(Xb + w * 512);
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) {
+                uw[pl] = load_frag(Ub + (4 * pl + w) * 512);
+                hw[pl] = load_frag(Hb + (4 * pl + w) * 512);
+            }
+            {
+                frag_t<E> f[4], fl[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = load_frag((i <= w ? Ub : Xb) + i * 512);
+                if (PL == 2)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fl[i] = load_frag((i <= w ? Ub : Hb) + (4 + i) * 512);
+                if (half) db = dot8(uw[0], hw[0], db);
+                mma(mD, xw, uw[0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i <= w) mma(m[i], f[i], xw);
+                    else mma(m[i], f[i], uw[0]);
+                if (PL == 2) {
+                    mma(mD, xw, uw[PL - 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i <= w) mma(m[i], fl[i], xw);
+                        else mma(m[i], f[i], uw[PL - 1]);
+                    if (half) {
+                        db = dot8(uw[0], hw[PL - 1], dot8(uw[PL - 1], hw[0], db));
+                        mma(mD, hw[PL - 1], uw[0]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i <= w) mma(m[i], f[i], hw[PL - 1]);
+                            else mma(m[i], fl[i], uw[0]);
+                    }
+                }
+            }
+            // (requested here and not at the head of the stage, where the compiler has the first LDS
+            // read wait for it; the exchange below waits for it in any case)
+            if (Plan::TWICE && j + 1 < J) issue(j + 1);
+            // the state products
+            {
+                const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
+                              ch = vec4(vs + kErase + 16 * w + 4 * g);
+#pragma unroll
+                for (int nb = 0; nb < HB; ++nb) {
+                    floatx4 ys = floatx4{0, 0, 0, 0}, hs = ys, ud = ys;
+                    frag_t<E> sf[PL], df[PL];
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) {
+                        sf[pl] = load_frag(Sb + (pl * NBP + half * HB + nb) * 512);
+                        df[pl] = load_frag(Db + (pl * NBP + half * HB + nb) * 512);
+                    }
+                    mma(ys, yw, sf[0]);
+                    mma(hs, hw[0], sf[0]);
+                    mma(ud, uw[0], df[0]);
+                    if (PL == 2) {
+                        mma(ys, yw, sf[PL - 1]);
+                        mma(hs, hw[0], sf[PL - 1]);
+                        mma(ud, uw[0], df[PL - 1]);
+                        mma(hs, hw[PL - 1], sf[0]);
+                        mma(ud, uw[PL - 1], df[0]);
+                    }
+                    if ((nb & 3) == w) {
+                        sd = dot8(sf[0], df[0], sd);
+                        if (PL == 2) sd = dot8(sf[0], df[PL - 1], dot8(sf[PL - 1], df[0], sd));
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        uint32_t qw = qe[nb][r * QW / 4], kw = ke[nb][r * QW / 4];
+                        asm volatile("" : "+v"(qw), "+v"(kw));   // (unpacked here, not kept unpacked)
+                        if (QW == 2) {
+                            qw = r % 2 ? qw & 0xffff0000u : qw << 16;
+                            kw = r % 2 ? kw & 0xffff0000u : kw << 16;
+                        }
+                        aq[r] += __uint_as_float(qw) * ys[r];
+                        ak[r] += __uint_as_float(kw) * hs[r];
+                        bk[r] += __uint_as_float(kw) * ud[r];
+                        dq[nb][r] += cq[r] * ys[r];
+                        dk[nb][r] += cd[r] * ud[r];
+                        dk[nb][r] += ch[r] * hs[r];
+                    }
+                }
+            }
+            if (pc != NPC - 1) continue;
+            // the head's pair matrix and its part of dg.  Rows past the count hold data of the last
+            // row; their factors are zero.
+            // (sums over s and over t apart, so that what cancels does so exactly)
+            float dx = 0.f, dx_s = 0.f;
+            // (opaque, so that the comparisons below are made here and not kept in registers)
+            int tl = tl0, o0 = 4 * g;
+            asm volatile("" : "+v"(tl), "+v"(o0));
+            const float *row = vs + (half ? kRowBeta : kRowScale);
+            // the factors of every block first, then the branches, so that the reads go out together
+            floatx4 fo[4];   // of o: before t (i < w), or t itself
+            float fl[4];     // of tl: t itself, or before t
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                fo[i] = vec4((i < w ? vs + kColBeta + (w - 1) * kC : row) + 16 * i + o0);
+                fl[i] = (i < w ? row : vs + kColBeta + (i - 1) * kC)[tl];
+            }
+            const float chi = vs[kCsHi + tl], clo = vs[kCsLo + tl], bl = vs[kBeta + tl];
+            const floatx4 oh = vec4(vs + kCsHi + 16 * w + o0), ol = vec4(vs + kCsLo + 16 * w + o0),
+                          bo = vec4(vs + kBeta + 16 * w + o0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i != w) {   // t = tl, s = o (i < w); t = o, s = tl
+                    m[i] *= fl[i] * fo[i];
+                    float d = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d += m[i][r] * kq[i][r];
+                    dx += i < w ? d : 0.f;
+                    dx_s += i < w ? 0.f : d;
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int o = 16 * i + o0 + r;
+                        const float d = ((chi - oh[r]) + (clo - ol[r])) * kLog2e;
+                        const bool down = half ? o < tl : o <= tl, up = half ? tl < o : tl <= o;
+                        const float f = exp2_(down ? d : 0.f) * bo[r] * (half ? bl : a.scale);
+                        m[i][r] = down && tl < count ? f * m[i][r] : 0.f;
+                        const float fD = exp2_(up ? -d : 0.f) * bl * (half ? bo[r] : a.scale);
+                        mD[r] = up && o < count ? fD * mD[r] : 0.f;
+                        dx += m[i][r] * kq[i][r];
+                        dx_s += mD[r] * kqD[r];
+                    }
+                }
+            dx = pass ? 0.f : dx - dx_s;   // (no columns n in it: counted once)
+            // its operands change hands through what this stage no longer needs
+            __syncthreads();
+            {
+                const floatx4 none = floatx4{0, 0, 0, 0};
+                E *mine = room + w * 6 * PL * 512 + 8 * lane;   // W up | W down | Z, two blocks each, in their planes
+                auto give = [&](int k, const floatx4 &x, const floatx4 &y) {
+                    frag_t<E> hi, lo;
+                    split_pair(x, y, hi, lo);
+                    store_frag(mine + k * PL * 512, hi);
+                    if (PL == 2) store_frag(mine + (k * PL + 1) * 512, lo);
+                };
+                if (half == 0) {
+                    floatx4 up[4], dn[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        up[i] = i <= w ? m[i] : none;
+                        dn[i] = i < w ? none : i == w ? mD : m[i];
+                    }
+                    give(0, up[0], up[1]);
+                    give(1, up[2], up[3]);
+                    give(2, dn[0], dn[1]);
+                    give(3, dn[2], dn[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[i] = i == w ? -m[i] - mD : -m[i];
+                    give(4, m[0], m[1]);
+                    give(5, m[2], m[3]);
+                    dx = -dx;
+                }
+            }
+            // dg and dbeta
+            floatx4 ab;
+            float sb = 0.f;
+            {
+                const floatx4 cq = vec4(vs + kScaled + 16 * w + 4 * g), cd = vec4(vs + kTillBeta + 16 * w + 4 * g),
+                              ch = vec4(vs + kErase + 16 * w + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = 16 * w + 4 * g + r < count;
+                    const float b = cd[r] * bk[r];
+                    sb += b;
+                    ab[r] = in ? row_sum16(cq[r] * aq[r] + ch[r] * ak[r] - b) : 0.f;
+                }
+            }
+            sb = cross_sum4(row_sum16(sb));
+            sd = cross_sum4(row_sum16(sd));
+            dx = cross_sum4(dx);
+            if (half) {
+                db = cross_sum4(db);
+                if (g == 0 && tl < count && pass == 0) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
+            }
+            const int slot = (h - h0) % kDgHeads;
+            if (g == 0) dcs[slot][2 + half][tl] = dx;
+            if (l == 0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dcs[slot][half][16 * w + 4 * g + r] = ab[r];
+            if (lane == 0) {
+                red[slot][wv] = sb;
+                red[slot][8 + wv] = sd;
+                if (wv == 0) red[slot][16] = vs[kSince + kC - 1];
+            }
+            __syncthreads();
+            // W K, W^T Q and (Z + Z^T) K
+            {
+                const E *theirs = room + w * 6 * PL * 512 + 8 * lane;
+                frag_t<E> x[6][PL];
+#pragma unroll
+                for (int k = 0; k < 6; ++k)
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) x[k][pl] = load_frag(theirs + (k * PL + pl) * 512);
+#pragma unroll
+                for (int nb = 0; nb < HB; ++nb) {
+                    const E *kt = ktf + 2 * (half * HB + nb) * 512, *qt = qtf + 2 * (half * HB + nb) * 512;
+                    const frag_t<E> k0 = load_frag(kt), k1 = load_frag(kt + 512), q0 = load_frag(qt), q1 = load_frag(qt + 512);
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) {
+                        mma(dq[nb], x[0][pl], k0);
+                        mma(dk[nb], x[2][pl], q0);
+                        mma(dq[nb], x[1][pl], k1);
+                        mma(dk[nb], x[4][pl], k0);
+                        mma(dk[nb], x[3][pl], q1);
+                        mma(dk[nb], x[5][pl], k1);
+                    }
+                }
+            }
+            // dg of several heads at a time, a wave each: once per head it would hold the other
+            // waves up
+            if ((slot == kDgHeads - 1 || h == h1 - 1) && wv <= slot) {
+                const int t = 63 - lane;
+                const float(&d)[4][kC] = dcs[wv];
+                const float *rd = red[wv];
+                float s = prefix_sum64(d[0][t] + d[1][t] + d[2][t] + d[3][t]), sum_b = 0.f, sum_sd = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sum_b += rd[i];
+                    sum_sd += rd[8 + i];
+                }
+                s += sum_b + rd[16] * sum_sd;
+                const int hw = h - slot + wv;
+                if (t < count) {   // (the same lane in every pass)
+                    float *before = a.vec + ((int64_t)c * a.H + hw) * kVec + kDgPass + t;
+                    if (pass) s += *before;
+                    if (pass + 1 < Plan::kPasses) *before = s;
+                    else ((E *)a.dg)[(t0 + t) * a.H + hw] = from_float<E>(s);
+                }
             }
         }
-        sb = cross_sum4(row_sum16(sb));
-        sd = cross_sum4(row_sum16(sd));
-        dx = cross_sum4(dx);
-        if (half) {
-            db = cross_sum4(db);
-            if (g == 0 && tl < count) ((E *)a.dbeta)[(t0 + tl) * a.H + h] = from_float<E>(db);
-        }
-        const int slot = (h - h0) % kDgHeads;
-        if (g == 0) dcs[slot][2 + half][tl] = dx;
-        if (l == 0)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dcs[slot][half][16 * w + 4 * g + r] = ab[r];
-        if (lane == 0) {
-            red[slot][wv] = sb;
-            red[slot][8 + wv] = sd;
-            if (wv == 0) red[slot][16] = vs[kSince + kC - 1];
-        }
-        __syncthreads();
-        // W K, W^T Q and (Z + Z^T) K
-        {
-            const E *theirs = room + w * 6 * 512 + 8 * lane;
-            const frag_t<E> a0 = load_frag(theirs), a1 = load_frag(theirs + 512), b0 = load_frag(theirs + 1024),
-                            b1 = load_frag(theirs + 1536), z0 = load_frag(theirs + 2048), z1 = load_frag(theirs + 2560);
+        for (int nb = 0; nb < HB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < HB; ++nb) {
-                const E *kt = ktf + 2 * (half * HB + nb) * 512, *qt = qtf + 2 * (half * HB + nb) * 512;
-                const frag_t<E> k0 = load_frag(kt), k1 = load_frag(kt + 512);
-                mma(dq[nb], a0, k0);
-                mma(dk[nb], b0, load_frag(qt));
-                mma(dq[nb], a1, k1);
-                mma(dk[nb], z0, k0);
-                mma(dk[nb], b1, load_frag(qt + 512));
-                mma(dk[nb], z1, k1);
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * w + 4 * g + r, n = 16 * (pass * NBP + half * HB + nb) + l;
+                if (a.hsplit > 1) {
+                    float *o = a.part + (((int64_t)c * a.G + grp) * a.hsplit + sp) * 2 * kMat + (int64_t)t * NT + n;
+                    o[0] = dq[nb][r];
+                    o[kMat] = dk[nb][r];
+                } else if (t < count && n < a.N) {
+                    const int64_t at = ((t0 + t) * a.G + grp) * a.N + n;
+                    ((E *)a.dq)[at] = from_float<E>(dq[nb][r]);
+                    ((E *)a.dk)[at] = from_float<E>(dk[nb][r]);
+                }
             }
-        }
-        // dg of several heads at a time, a wave each: once per head it would hold the other
-        // waves up
-        if ((slot == kDgHeads - 1 || h == h1 - 1) && wv <= slot) {
-            const int t = 63 - lane;
-            const float(&d)[4][kC] = dcs[wv];
-            const float *rd = red[wv];
-            float s = prefix_sum64(d[0][t] + d[1][t] + d[2][t] + d[3][t]), sum_b = 0.f, sum_sd = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sum_b += rd[i];
-                sum_sd += rd[8 + i];
-            }
-            s += sum_b + rd[16] * sum_sd;
-            if (t < count) ((E *)a.dg)[(t0 + t) * a.H + h - slot + wv] = from_float<E>(s);
-        }
     }
-#pragma unroll
-    for (int nb = 0; nb < HB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * g + r, n = 16 * (half * HB + nb) + l;
-            if (a.hsplit > 1) {
-                float *o = a.part + (((int64_t)c * a.G + grp) * a.hsplit + sp) * 2 * kMat + (int64_t)t * NT + n;
-                o[0] = dq[nb][r];
-                o[kMat] = dk[nb][r];
-            } else if (t < count && n < a.N) {
-                const int64_t at = ((t0 + t) * a.G + grp) * a.N + n;
-                ((E *)a.dq)[at] = from_float<E>(dq[nb][r]);
-                ((E *)a.dk)[at] = from_float<E>(dk[nb][r]);
-            }
-        }
 }
 
 // dq and dk of one chunk and group from their parts, added in order of the split.  Many

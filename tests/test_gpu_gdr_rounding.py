@@ -80,3 +80,25 @@ def test_y_is_off_by_one_rounding(shape, keys):
     e = worst(f64(y), delta.gdr_forward(**x)[0], x)
     print(f"[gdr rounding] y {keys} {shape} {e:.3f}", flush=True)
     assert e <= 1
+
+
+GRADS = ("dq", "dk", "dv", "dbeta", "dg")
+
+
+def worst_gradients(got, ref, x):
+    e = {n: worst(f64(got[n]), ref[n], x) for n in GRADS}
+    e["dinitial_states"] = max(np.linalg.norm(a - b) / max(np.linalg.norm(b), 1e-30)
+                               for a, b in zip(f64(got["dinitial_states"]), ref["dinitial_states"])) / 1e-4
+    return e
+
+
+@pytest.mark.parametrize("keys", KEYS)
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients_are_off_by_one_rounding(shape, keys):
+    """(dinitial_states, fp32: the bar of test_gpu_gdr.py.)"""
+    x, dy, dfin = alike(sum(shape) + 1, *shape, **KEYS[keys])
+    got = ssd.gdr_bwd(**gpu(x), dy=dy.cuda(), dfinal_states=None if dfin is None else dfin.cuda())
+    torch.cuda.synchronize()
+    e = worst_gradients(got, delta.gdr_backward(**x, dy=dy, dfinal_states=dfin), x)
+    print(f"[gdr rounding] {keys} {shape} " + " ".join(f"{n}={v:.3f}" for n, v in e.items()), flush=True)
+    assert max(e.values()) <= 1, e
