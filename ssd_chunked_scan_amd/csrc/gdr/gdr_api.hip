@@ -136,14 +136,24 @@ ssd_status parse_bwd(const ssd_gdr_args *a, Shape *s)
 
 // Narrow chains share a step among a workgroup's waves, wide ones have fewer bytes to load
 // per column.  Narrow where wide workgroups (of both directions together) would not come
-// near one per CU.  2048 tokens, heads of 64, whole passes in us, wide against narrow:
-//   forward   N = 64    128 heads 104, 99    192 heads 113, 122    256 heads 136, 181
-//             N = 128              147, 112              157, 147              163, 207
-//             N = 256              216, 150              226, 217              237, 275
-//   backward  N = 64    64 heads  195, 165   128 heads 264, 320
-//             N = 128             248, 196             321, 395
-//             N = 256             412, 342             582, 681
-constexpr int64_t kNarrowUpTo = 192;
+// near one per CU: up to 144 in bf16, 192 for its forward with N = 256 and for fp32.  2048
+// tokens, heads of 64, whole passes in us, wide against narrow:
+//   bf16, forward   N = 64   128 heads 119, 113   160 heads 127, 138   192 heads 136, 152   256 heads 157, 217
+//                   N = 128            140, 118             146, 154             155, 167             167, 241
+//                   N = 256            241, 155             243, 213             260, 228             272, 310
+//   bf16, backward  N = 64   64 heads  198, 182   80 heads  219, 232   96 heads  229, 273   128 heads 271, 356
+//                   N = 128            256, 210             275, 282             292, 330             347, 445
+//                   N = 256            412, 354             445, 451             480, 533             574, 707
+//   fp32, forward   N = 64   128 heads 268, 180   192 heads 287, 331   256 heads 291, 371
+//                   N = 128            383, 232             403, 343             413, 438
+//                   N = 256           1457, 430            1526, 629            1804, 838
+//   fp32, backward  N = 64   64 heads  402, 302   96 heads  459, 460   128 heads 522, 554
+//                   N = 128            611, 419             697, 647             797, 818
+//                   N = 256           1820, 797            1992, 1171           2264, 1518
+int64_t narrow_up_to(const Shape &s, int directions)
+{
+    return s.dtype == SSD_DTYPE_F32 || (s.N > 128 && directions == 1) ? 192 : 144;
+}
 constexpr size_t kCacheBytes = (size_t)256 << 20;
 
 struct Workspace {
@@ -204,9 +214,9 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
     return with_nt(s.NT, [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
         // heads per wave: 2048 waves (two per SIMD) run at a time, and a wave pays for its start,
-        // K K^T and Q K^T once, about 1 + NT / 256 heads' time (packed prompts of 8 heads a group,
-        // N = 128, with 1, 2, 4 and 8 heads a wave: 166, 134, 120, 136 us; 16K tokens of 32 heads
-        // in one group, N = 256, with 2, 4 and 8: 75, 58, 61 us)
+        // K K^T and Q K^T once, about 1 + NT / 256 heads' time.  Whole forwards with 1, 2, 4 and 8
+        // heads a wave: 16640 tokens of 64 heads, 8 a group, N = 128: 700, 672, 664, 686 us; 16384
+        // of 32 heads in one group, N = 256: 745, 710, 694, 690 us
         const int64_t hpg = s.H / s.G;
         int64_t hpw = 1;
         double cost = 1e300;
@@ -219,10 +229,10 @@ ssd_status prepare(const Shape &s, const ssd_gdr_args *a, char *ws, const Worksp
             }
         }
         const int64_t units = s.nct * s.G * ((hpg + hpw - 1) / hpw);
-        // triangles that the last level of cache cannot hold are written past it: 370 MB of
-        // packed prompts, forming them and the chains 380 -> 366 us; 720 MB of a backward over
-        // 8 x 2048 tokens of 80 heads, all kernels 1433 -> 1404 us; but 100 MB of 2 x 2048 tokens
-        // of 24 heads 141 -> 160 us
+        // triangles that the last level of cache cannot hold are written past it: 410 MB of a
+        // forward over 16640 tokens of 64 heads, all kernels 683 -> 664 us; 750 MB of a backward
+        // over 8 x 2048 tokens of 80 heads 1595 -> 1570 us; but 57 MB of 2 x 2048 tokens of 24 heads
+        // 151 -> 170 us
         const bool once = (size_t)(s.nct * s.H) * tri_elems<E>(BWD) * sizeof(E) > kCacheBytes;
         auto launch = [&](auto past) {
             hipLaunchKernelGGL((k_gdr_prep<E, NT, BWD, decltype(past)::value>),
@@ -261,7 +271,7 @@ template <typename E> ChainArgs chain_args(const Shape &s, const ssd_gdr_args *a
 // workgroup.
 bool narrowed(ChainArgs &c, const Shape &s, int directions)
 {
-    if ((int64_t)c.units * directions > kNarrowUpTo) return false;
+    if ((int64_t)c.units * directions > narrow_up_to(s, directions)) return false;
     c.np = (int)(s.Pp / 16);
     c.units = (int)(s.chains * s.H * c.np);
     return true;

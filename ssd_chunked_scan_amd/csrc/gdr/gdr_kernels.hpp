@@ -804,7 +804,7 @@ typedef __attribute__((address_space(3))) void *lptr_t;
 // What is read by one workgroup only is loaded, and what another kernel reads much later
 // is stored, past the caches (non-temporal), which keeps them for K and Q, whose blocks a
 // group's heads share: 8 x 2048 tokens of 80 heads, chains 666 -> 639 us, gradients 592 ->
-// 558 us; packed prompts' chains 245 -> 238 us.
+// 558 us; packed prompts' chains 245 -> 238 us (all while the outputs took single bf16 numbers).
 constexpr int kOnce = 2;
 
 // `n` operand blocks from memory to LDS, a wave every fourth block.
@@ -895,8 +895,8 @@ template <typename E, int NB, int KIND, bool STAGED> struct Operands {
 
 // Workgroup -> unit (chain, head, column tile).  Workgroups go round the 8 XCDs; where a
 // chain's units divide by 8, an XCD takes consecutive ones, so that the heads of a group find
-// its K and Q in one L2 (packed prompts, 8 groups of 8 heads: chains 235 -> 209 us; ragged
-// fp32, 3 groups of 2: 38 -> 34 us).  Not with all heads in one group, whose K and Q every L2
+// its K and Q in one L2 (packed prompts, 8 groups of 8 heads: chains 235 -> 209 us, before y
+// took two bf16 numbers for its operands; ragged fp32, 3 groups of 2: 38 -> 34 us).  Not with all heads in one group, whose K and Q every L2
 // holds anyway.
 __device__ __forceinline__ int by_group(const ChainArgs &a, int unit)
 {
