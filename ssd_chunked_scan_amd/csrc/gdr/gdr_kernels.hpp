@@ -335,14 +335,13 @@ template <typename E> __host__ __device__ constexpr int tri_elems(bool bwd)
 // formed once.  Further waves write the operand blocks of K and Q.  cs is summed in 64 bits,
 // since Gam takes differences of it.
 //
-// 8 x 2048 tokens of 80 heads, backward: 168 us, 1.15 GB (36 KB of triangles and 4 KB of
-// scalars to write per chunk and head) at 6.8 TB/s, part of it still on its way through the
-// last cache level.  (235 us while Gam o Q K^T was formed before the inverse, with more spilled
-// registers, which came back from memory behind the stores; the bf16 backward that stores past
-// the caches spills 9.)  The forward writes two thirds and is bound by
-// latency at two waves a SIMD (247 registers): packed prompts of 64 heads 130 us, matrix and
-// vector pipes about a quarter busy.  Workgroups of four waves that shared one head, with
-// barriers between the blocks, took 177 us there.
+// 8 x 2048 tokens of 80 heads, backward: 168 us, 0.9 GB (36 KB of triangles and 4 KB of
+// scalars to write per chunk and head) at 5.4 TB/s.  (235 us while Gam o Q K^T was formed
+// before the inverse, with more spilled registers, which came back from memory behind the
+// stores; the bf16 backward that stores past the caches still spills 9.)  The forward writes
+// two thirds and is bound by latency at two waves a SIMD (247 registers): packed prompts of 64
+// heads 131 us, matrix and vector pipes about a quarter busy.  Workgroups of four waves that
+// shared one head, with barriers between the blocks, took 177 us there while they wrote less.
 //
 // Blocks of 16 x 16 (i, j <= i), as accumulators with rows s of block j and columns t of
 // block i: four consecutive slots of an operand block with rows t.  Between different
@@ -780,7 +779,7 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t rs, uint32_t l
 // both that its operands are there and that the other region is free.  Sets too large for
 // LDS (fp32 at N = 256) are read from global memory by every wave (STAGED false).
 //
-// 8 x 2048 tokens of 80 heads of 64, N = 128, both directions: 720 us for 3.5 GB, 4.8 TB/s of
+// 8 x 2048 tokens of 80 heads of 64, N = 128, both directions: 720 us for 3.6 GB, 5.0 TB/s of
 // the 5.1 that a copy reaches.  (While S, U, D and H were kept as single bf16 numbers, 2.5 GB
 // took 620 us; without the operand loads or without the stores 480 and 440 us, without both
 // 305 us, the arithmetic's own time at two workgroups a CU.)  Packed prompts of 64 heads,
@@ -1758,7 +1757,7 @@ struct GradArgs {
 // fp32: 16K tokens of 32 heads 2380 against 1535 us for the whole backward, fp32 of 2048
 // tokens of 128 heads 2680 against 2240; 32 and 44 are left).
 //
-// 8 x 2048 tokens of 80 heads, N = 128: 690 us, 2.24 GB read at 3.3 TB/s.  What holds it is
+// 8 x 2048 tokens of 80 heads, N = 128: 690 us, 2.3 GB read at 3.4 TB/s.  What holds it is
 // the chain inside a stage at two waves a SIMD (247 registers): waves wait a third of the
 // time, the matrix pipe is busy 27 %.  (410 us, half the bytes, with single bf16 numbers; 900
 // before half the waves formed W and the others Z; 70 more with a head's dg finished by one
