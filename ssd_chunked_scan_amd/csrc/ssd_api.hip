@@ -447,6 +447,7 @@ int64_t bwd_m_hsplit(const Shape &s)
 {
     const int64_t qt = s.Q / 64, tiles = qt * (qt + 1) / 2 * s.nc * s.G * s.b;
     const int64_t hpg = s.H / s.G;
+    if (tiles == 0) return 1;   // no tokens
     int64_t k = (1024 + tiles - 1) / tiles;
     if (k > hpg) k = hpg;
     return k < 1 ? 1 : k;
