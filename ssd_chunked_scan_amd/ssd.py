@@ -202,6 +202,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+_NO_IDS = 16   # a seq_idx that is there and not read
+
+
+def _ids(seq_idx: Optional[torch.Tensor]):
+    """The address of a packed stream's ids.  A stream without tokens has none, and is a
+    packed stream all the same (the library reads none of its ids)."""
+    return None if seq_idx is None else seq_idx.data_ptr() or _NO_IDS
+
+
 def _check(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=None):
     if t is None:
         return
@@ -256,7 +265,7 @@ class Problem:
         self.device = dev
         self.args = FwdArgs(b, T, H, P, N, G, self.Q, _DTYPES[x.dtype], int(bool(dt_softplus)),
                             _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                            _ptr(initial_states), _ptr(seq_idx), self.nseq,
+                            _ptr(initial_states), _ids(seq_idx), self.nseq,
                             None, None, None, 0)
 
     # shapes of the outputs and intermediates
@@ -609,7 +618,6 @@ _GDR_BWD = struct.Struct("10P")             # ssd_gdr_bwd_args
 _GDR_STEP = struct.Struct("5qif7P")         # ssd_gdr_step_args
 _NORM = struct.Struct("2qif6P")             # ssd_norm_args
 _NORM_BWD = struct.Struct("2q2i10P")        # ssd_norm_bwd_args
-_NO_IDS = 16                                # a seq_idx that is there and not read
 
 
 def _same(t, name, dtype, shape, dev):
@@ -681,11 +689,8 @@ def _gdr_args(q, k, v, g, beta, scale, initial_states, seq_idx, nseq):
     if initial_states is not None:
         _same(initial_states, "initial_states", torch.float32, states, dev)
     head = (b, T, H, P, N, G, _DTYPES[dtype], 1.0 if scale is None else scale)
-    # a stream without tokens has no ids to point to, and is a packed stream all the same (the
-    # library reads none of them)
-    ids = 0 if seq_idx is None else seq_idx.data_ptr() or _NO_IDS
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            0 if initial_states is None else initial_states.data_ptr(), ids)
+            0 if initial_states is None else initial_states.data_ptr(), _ids(seq_idx) or 0)
     return head, ptrs, n, states
 
 

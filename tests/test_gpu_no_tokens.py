@@ -27,3 +27,20 @@ def test_gradients_of_rows_without_tokens(dtype):
     torch.cuda.synchronize()
     assert bool((gr["dinitial_states"] == dfin).all())
     assert bool((gr["dA"] == 0).all()) and bool((gr["dD"] == 0).all()) and gr["dx"].numel() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_an_empty_packed_stream(dtype):
+    """Every segment's final state is zero (none of its tokens received the initial state), and
+    so is the gradient of the initial state."""
+    nseq, H, P, N, G = 3, 2, 32, 48, 1
+    z = lambda *s, dt=dtype: torch.zeros(s, dtype=dt, device="cuda")
+    args = (z(1, 0, H, P), z(1, 0, H), -torch.ones(H, device="cuda"), z(1, 0, G, N), z(1, 0, G, N), 64)
+    kw = dict(initial_states=torch.randn(1, H, P, N, device="cuda"), seq_idx=z(0, dt=torch.int32), nseq=nseq)
+    fin = torch.full((nseq, H, P, N), 7.0, device="cuda")
+    y, f = ssd.fwd(*args, **kw, final_states=fin)
+    gr = ssd.bwd(*args, y, y.clone(), **kw, dfinal_states=torch.randn(nseq, H, P, N, device="cuda"))
+    torch.cuda.synchronize()
+    assert f is fin and y.numel() == 0
+    assert bool((fin == 0).all())
+    assert bool((gr["dinitial_states"] == 0).all())
