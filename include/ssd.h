@@ -521,6 +521,271 @@ typedef struct {
 ssd_status ssd_layer_norm_bwd_workspace_size(const ssd_norm_bwd_args *args, size_t *bytes);
 ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args *args, void *stream);
 
+/*
+ * The selective scan: the state space layer whose decay has a rate of its own for
+ * every channel and state (the SSD above is its form with one decay per head).
+ * Per batch row, channel d (group j = floor(d*G/D)) and token t, with the state
+ * h [N] of every channel:
+ *
+ *     Delta = softplus(dt_t,d + dt_bias_d)        (or dt_t,d + dt_bias_d)
+ *     h_t   = exp(Delta A_d) h_{t-1} + Delta x_t,d B_t        (elementwise over N)
+ *     y_t,d = (C_t . h_t + D_d x_t,d) * SiLU(z_t,d)
+ *
+ * A <= 0 is the supported domain.  ssd_selective_scan_fwd computes y and the final states,
+ * ssd_selective_scan_bwd every gradient, ssd_selective_scan_step one token per batch row.  Everything
+ * is computed in fp32 whatever the dtype; outputs are rounded once.
+ *
+ * x, dt, z, B and C may be columns of a wider row (a projection's output): their
+ * `*_stride` is the number of elements from one token to the next (batch rows
+ * follow each other, so token t of row b is token b*T + t), 0 for rows without
+ * gaps; the elements of a token are contiguous.  Outputs and dy have no gaps.
+ * Every pointer needs the alignment of its elements only.
+ *
+ * Supported: batch >= 1, seqlen >= 0, 1 <= N <= 64, any D with D % G == 0, D <= 2^20,
+ * G*N <= 2^20, batch * seqlen < 2^31 - 64, strides below 2^31; a launch has fewer
+ * than 2^32 threads (chunks of 64 tokens times tiles of 64 channels below 2^24 or so),
+ * larger sizes are SSD_ERR_BAD_SHAPE.  Results do not change from call to call: every
+ * sum has a fixed order.
+ *
+ * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0, nseq),
+ * not checked here: see ssd_check_seq_idx; an invalid stream gives wrong results and
+ * may leave tokens unwritten, but nothing outside the buffers is touched).  Every
+ * segment has an initial state of its own, initial_states is [nseq,D,N]; a segment
+ * without tokens has its initial state as its final state (a stream without any,
+ * seqlen 0, is a packed one if seq_idx is not NULL; no id is read).
+ */
+typedef struct {
+    int64_t batch, seqlen, dim, dstate, ngroups; /* b, T, D, N, G */
+    int32_t dtype;                /* ssd_dtype of x, dt, B, C, z, y and their gradients */
+    int32_t dt_softplus;          /* 1: Delta = softplus(dt + dt_bias); 0: Delta = dt + dt_bias */
+    const void *x;                /* [b,T,D] dtype */
+    const void *dt;               /* [b,T,D] dtype */
+    const float *A;               /* [D,N] fp32 */
+    const void *B;                /* [b,T,G,N] dtype */
+    const void *C;                /* [b,T,G,N] dtype */
+    const float *D;               /* [D] fp32, or NULL for no skip term */
+    const float *dt_bias;         /* [D] fp32, or NULL */
+    const void *z;                /* [b,T,D] dtype, or NULL for no gate */
+    int64_t x_stride, dt_stride, B_stride, C_stride, z_stride; /* elements per token, 0: no gaps */
+    const float *initial_states;  /* [b,D,N] (with seq_idx [nseq,D,N]) fp32, or NULL for zeros */
+    const int32_t *seq_idx;       /* [T] int32 segment ids, or NULL */
+    int64_t nseq;                 /* number of segment ids when seq_idx != NULL */
+    void *y;                      /* [b,T,D] dtype, out (ssd_selective_scan_fwd; not read or written by ssd_selective_scan_bwd) */
+    float *final_states;          /* shape of initial_states, fp32, out, or NULL (ssd_selective_scan_fwd) */
+    void *workspace;              /* device scratch, >= ssd_selective_scan_fwd_workspace_size, 16-byte aligned (ssd_selective_scan_fwd) */
+    size_t workspace_bytes;
+} ssd_selective_scan_args;
+
+/* Workspace bytes of ssd_selective_scan_fwd and of ssd_selective_scan_bwd for these shapes (only the
+ * shape and dtype fields, seq_idx != NULL and nseq are read). */
+ssd_status ssd_selective_scan_fwd_workspace_size(const ssd_selective_scan_args *args, size_t *bytes);
+ssd_status ssd_selective_scan_bwd_workspace_size(const ssd_selective_scan_args *args, size_t *bytes);
+
+/* y and final_states. */
+ssd_status ssd_selective_scan_fwd(const ssd_selective_scan_args *args, void *stream);
+
+/* The gradients of L = sum(y * dy) + sum(final_states * dfinal_states) with
+ * respect to every input.  `args` describes the forward's inputs; what the forward
+ * computed is formed again from them.  ddt is the gradient with respect to dt as
+ * passed.  All outputs are overwritten. */
+typedef struct {
+    const void *dy;               /* [b,T,D] dtype */
+    const float *dfinal_states;   /* shape of the final states, fp32, or NULL for zero */
+    void *dx;                     /* [b,T,D] dtype, out */
+    void *ddt;                    /* [b,T,D] dtype, out */
+    float *dA;                    /* [D,N] fp32, out */
+    void *dB;                     /* [b,T,G,N] dtype, out */
+    void *dC;                     /* [b,T,G,N] dtype, out */
+    float *dD;                    /* [D] fp32, out, or NULL */
+    float *ddt_bias;              /* [D] fp32, out, or NULL */
+    void *dz;                     /* [b,T,D] dtype, out; required with z, ignored without */
+    float *dinitial_states;       /* shape of the initial states, fp32, out, or NULL */
+    void *workspace;              /* device scratch, >= ssd_selective_scan_bwd_workspace_size, 16-byte aligned */
+    size_t workspace_bytes;
+} ssd_selective_scan_bwd_args;
+
+ssd_status ssd_selective_scan_bwd(const ssd_selective_scan_args *args, const ssd_selective_scan_bwd_args *grads, void *stream);
+
+/* One token of every batch row: x, dt, z, y [b,D], B, C [b,G,N] dtype, the state
+ * [b,D,N] fp32 read and overwritten; strides as above, from one batch row to the
+ * next.  Steps over tokens 0..T-1 from the initial states give ssd_selective_scan_fwd's y and
+ * final states. */
+typedef struct {
+    int64_t batch, dim, dstate, ngroups;
+    int32_t dtype, dt_softplus;
+    const void *x, *dt;
+    const float *A;
+    const void *B, *C;
+    const float *D, *dt_bias;
+    const void *z;
+    int64_t x_stride, dt_stride, B_stride, C_stride, z_stride;
+    float *state;
+    void *y;
+} ssd_selective_scan_step_args;
+
+ssd_status ssd_selective_scan_step(const ssd_selective_scan_step_args *args, void *stream);
+
+/*
+ * The causal convolution in front of the selective scan: every channel with its own
+ * `width` taps, with the inputs of the past carried in a window,
+ *
+ *     v[t,c] = bias[c] + sum_{k<width} weight[c][k] * x[t-(width-1)+k, c]
+ *     y[t,c] = SiLU(v[t,c])  (or v[t,c])
+ *
+ * where x before the first token of a sequence is its initial_window [width-1, dim]
+ * (zeros without one), the sequence being a batch row or, with seq_idx, a segment;
+ * final_window holds the last width-1 inputs of the sequence, those of its initial
+ * window among them where it is shorter.  ssd_causal_conv_fwd computes y and final_window,
+ * ssd_causal_conv_bwd the gradients, ssd_causal_conv_step one token per batch row.  x may be columns
+ * of a wider row, x_stride elements from token to token (0: no gaps); the rest has
+ * no gaps.  Sums are in fp32; outputs are rounded once.  Every pointer needs the alignment
+ * of its elements only; 16-byte aligned tensors with a dim and stride that are multiples
+ * of 8 are moved in wider accesses.
+ * Supported: batch >= 1, seqlen >= 0, any dim up to 2^22, width 1..4, batch * seqlen <
+ * 2^31 - 64.  Packed streams as for ssd_selective_scan_fwd.
+ */
+typedef struct {
+    int64_t batch, seqlen, dim, width;
+    int32_t dtype;                /* ssd_dtype of x, y, the windows and their gradients */
+    int32_t silu;                 /* 1: y = SiLU(v); 0: y = v */
+    const void *x;                /* [b,T,dim] dtype */
+    int64_t x_stride;             /* elements per token, 0: no gaps */
+    const float *weight;          /* [dim,width] fp32 */
+    const float *bias;            /* [dim] fp32, or NULL */
+    const void *initial_window;   /* [b,width-1,dim] (with seq_idx [nseq,width-1,dim]) dtype, or NULL */
+    const int32_t *seq_idx;       /* [T] int32 segment ids, or NULL */
+    int64_t nseq;
+    void *y;                      /* [b,T,dim] dtype, out (ssd_causal_conv_fwd) */
+    void *final_window;           /* shape of initial_window, dtype, out, or NULL (ssd_causal_conv_fwd) */
+} ssd_causal_conv_args;
+
+ssd_status ssd_causal_conv_fwd(const ssd_causal_conv_args *args, void *stream);
+
+/* The gradients of L = sum(y * dy) + sum(final_window * dfinal_window).  The sums over
+ * tokens are formed in fp32 in a fixed order through the workspace. */
+typedef struct {
+    const void *dy;               /* [b,T,dim] dtype */
+    const void *dfinal_window;    /* shape of the windows, dtype, or NULL for zero */
+    void *dx;                     /* [b,T,dim] dtype, out */
+    float *dweight;               /* [dim,width] fp32, out */
+    float *dbias;                 /* [dim] fp32, out, or NULL */
+    void *dinitial_window;        /* shape of the windows, dtype, out, or NULL */
+    void *workspace;              /* >= ssd_causal_conv_bwd_workspace_size, 16-byte aligned */
+    size_t workspace_bytes;
+} ssd_causal_conv_bwd_args;
+
+ssd_status ssd_causal_conv_bwd_workspace_size(const ssd_causal_conv_args *args, size_t *bytes);
+ssd_status ssd_causal_conv_bwd(const ssd_causal_conv_args *args, const ssd_causal_conv_bwd_args *grads, void *stream);
+
+/* One token of every batch row: x, y [b,dim], the window [b,width-1,dim] read and moved
+ * on by this token in place.  x_stride: elements from one batch row to the next. */
+typedef struct {
+    int64_t batch, dim, width;
+    int32_t dtype, silu;
+    const void *x;
+    int64_t x_stride;
+    const float *weight, *bias;
+    void *window;
+    void *y;
+} ssd_causal_conv_step_args;
+
+ssd_status ssd_causal_conv_step(const ssd_causal_conv_step_args *args, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, over the last axis of x
+ * [rows, dim]:
+ *
+ *     r = x + residual, rounded to the residual's type       (r = x without one)
+ *     y = r * rstd * weight,   rstd = 1 / sqrt(mean(r^2) + eps)
+ *
+ * What is normed is r as the stream holds it, so the backward needs r alone.  The
+ * output is y in the dtype, or in 8 bits (e4m3: a sign, 4 bits of exponent, 3 of
+ * mantissa, largest value 448), or both: block i of a row is its values 128 i to
+ * 128 i + 127,
+ *
+ *     scales[row][i] = max(max|y| / 448, 2^-126),   q = y / scales, to nearest even.
+ *
+ * A value that is not finite makes its row (of y and q) and the scales of its row
+ * undefined; other rows are not touched.  Sums are in fp32.
+ * Supported: rows >= 0, 1 <= dim <= 65536, rows * dim <= 2^40, any dim (one that is not
+ * a multiple of 8 takes narrower accesses).  Tensors [rows,dim] need 16-byte alignment;
+ * rstd and scales 4-byte.  residual_out may be residual (or x, of the same type)
+ * itself, y may be x; no other overlap.
+ */
+typedef struct {
+    int64_t rows, dim;
+    int32_t dtype;                /* ssd_dtype of x and y */
+    int32_t residual_dtype;       /* ssd_dtype of residual and residual_out */
+    float eps;
+    int32_t reserved;
+    const void *x;                /* [rows,dim] dtype */
+    const void *residual;         /* [rows,dim] residual_dtype, or NULL */
+    const float *weight;          /* [dim] fp32, or NULL */
+    void *residual_out;           /* [rows,dim] residual_dtype, out; required with residual, NULL without */
+    void *y;                      /* [rows,dim] dtype, out, or NULL if q is given */
+    void *q;                      /* [rows,dim] e4m3, out, or NULL */
+    float *scales;                /* [rows, ceil(dim/128)] fp32, out, with q */
+    float *rstd;                  /* [rows] fp32, out, or NULL */
+} ssd_rms_norm_args;
+
+ssd_status ssd_rms_norm_fwd(const ssd_rms_norm_args *args, void *stream);
+
+/* With hat = r rstd and w = dy * weight, the gradient of the norm's input r and of x
+ * and the residual, which is the same but for its type:
+ *
+ *     dr = rstd (w - hat avg(w hat)) + dresidual_out,   dweight = sum over rows of dy * hat
+ *
+ * dx may be dy, dresidual may be dresidual_out. */
+typedef struct {
+    int64_t rows, dim;
+    int32_t dtype;                /* ssd_dtype of dy and dx */
+    int32_t residual_dtype;       /* ssd_dtype of r, dresidual_out and dresidual */
+    const void *r;                /* [rows,dim] residual_dtype: residual_out as the forward left it, or x */
+    const void *dy;               /* [rows,dim] dtype */
+    const void *dresidual_out;    /* [rows,dim] residual_dtype, or NULL for zero */
+    const float *rstd;            /* [rows] fp32, as the forward left it */
+    const float *weight;          /* [dim] fp32, or NULL */
+    void *dx;                     /* [rows,dim] dtype, out */
+    void *dresidual;              /* [rows,dim] residual_dtype, out, or NULL */
+    float *dweight;               /* [dim] fp32, out, or NULL */
+    void *workspace;              /* >= ssd_rms_norm_bwd_workspace_size; unused without dweight */
+    size_t workspace_bytes;
+} ssd_rms_norm_bwd_args;
+
+ssd_status ssd_rms_norm_bwd_workspace_size(const ssd_rms_norm_bwd_args *args, size_t *bytes);
+ssd_status ssd_rms_norm_bwd(const ssd_rms_norm_bwd_args *args, void *stream);
+
+/*
+ * The block's projections in 8 bits: a matrix product of e4m3 numbers with a scale for
+ * each block of 128 along the inner axis, in rows of a (as ssd_rms_norm_fwd leaves
+ * them) and in 128 x 128 blocks of the weights,
+ *
+ *     out[m][n] = bias[n] + sum_i a_scales[m][i] w_scales[n/128][i]
+ *                           sum_{k in block i} a[m][k] w[n][k]
+ *
+ * Products and sums inside a block go through the matrix cores, their scaling and the
+ * sum over blocks are in fp32.  Supported: m, n >= 0, any n, k >= 1 a multiple of 16,
+ * k <= 2^22, each of m * k, n * k and m * n up to 2^40, m and n < 2^31 - 512.  a, w, out and the
+ * workspace need 16-byte alignment, the scales and bias 4-byte.
+ * Few rows are shared out along k; the parts are added in a fixed order.
+ */
+typedef struct {
+    int64_t m, n, k;
+    int32_t dtype;                /* ssd_dtype of out */
+    int32_t reserved;
+    const void *a;                /* [m,k] e4m3 */
+    const float *a_scales;        /* [m, ceil(k/128)] fp32 */
+    const void *w;                /* [n,k] e4m3 */
+    const float *w_scales;        /* [ceil(n/128), ceil(k/128)] fp32 */
+    const float *bias;            /* [n] fp32, or NULL */
+    void *out;                    /* [m,n] dtype, out */
+    void *workspace;              /* >= ssd_matmul_fp8_workspace_size (0 for most sizes) */
+    size_t workspace_bytes;
+} ssd_matmul_fp8_args;
+
+ssd_status ssd_matmul_fp8_workspace_size(const ssd_matmul_fp8_args *args, size_t *bytes);
+ssd_status ssd_matmul_fp8(const ssd_matmul_fp8_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,10 +12,14 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssd.so")
 SOURCES = [os.path.join(CSRC, "ssd_api.hip"), os.path.join(CSRC, "gdr", "gdr_api.hip"),
-           os.path.join(CSRC, "norm", "norm_api.hip")]
+           os.path.join(CSRC, "norm", "norm_api.hip"), os.path.join(CSRC, "norm", "rms_api.hip"),
+           os.path.join(CSRC, "scan", "scan_api.hip"), os.path.join(CSRC, "conv", "conv_api.hip"),
+           os.path.join(CSRC, "mm", "mm_api.hip")]
 HEADERS = [os.path.join(ROOT, "include", "ssd.h"), os.path.join(CSRC, "ssd_device.hpp"),
            os.path.join(CSRC, "ssd_kernels.hpp"), os.path.join(CSRC, "gdr", "gdr_kernels.hpp"),
-           os.path.join(CSRC, "norm", "norm_kernels.hpp")]
+           os.path.join(CSRC, "norm", "norm_kernels.hpp"), os.path.join(CSRC, "norm", "rms_kernels.hpp"),
+           os.path.join(CSRC, "scan", "scan_kernels.hpp"), os.path.join(CSRC, "conv", "conv_kernels.hpp"),
+           os.path.join(CSRC, "mm", "mm_kernels.hpp"), os.path.join(CSRC, "api_checks.hpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

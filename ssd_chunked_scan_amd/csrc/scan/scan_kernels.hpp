@@ -1,0 +1,694 @@
+// scan_kernels.hpp -- the selective scan (a decay rate for every channel and state),
+// forward, backward and one token, for gfx950.
+//
+//   Delta = softplus(dt + bias),  h_t = e^{Delta A} h_{t-1} + Delta x_t B_t,
+//   y_t = (C_t . h_t + D x_t) SiLU(z_t)
+//
+// The decays differ in every channel d and state n, so no product of matrices forms the
+// scan: it is an exponential and a few multiply-adds for each (t, d, n), and these bound
+// it, not the bytes (N = 16: 16 exponentials for 8 bytes of x, dt, z and y).
+//
+// Layout.  LN neighbouring lanes share a channel, each holding 4 of its states (LN = N / 4
+// rounded up to a power of two), so a wave has 64 / LN channels.  The LN lanes also share
+// the work that a channel has once per token: lane j loads x, dt and z of token j of LN
+// tokens, forms Delta and Delta x there, and the others read them by DPP.  B and C of a tile of
+// tokens are in LDS as fp32.
+//
+// Chunks.  A row (a batch row, or a segment of a packed stream) is one after another in
+// time; where the rows and channels are too few to fill the card, rows are cut into chunks:
+// first every chunk's end state from a zero start, then the states from chunk to chunk,
+// then every chunk from its own entering state.
+#pragma once
+
+#include <type_traits>
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+namespace sscan {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kGradQ = 64;    // tokens of a chunk of the backward
+
+struct ScanArgs {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D_, *bias;    // D_: the skip term
+    int64_t xs, dts, Bs, Cs, zs;   // elements from token to token
+    const float *s0;               // initial states
+    float *s1;                     // final states
+    void *y;
+    const int32_t *plan;           // packed streams: first token of every segment and of none, log2 of the chunk
+    float *S, *sum;                // chunk states [slots][D][N], sums of Delta [slots][D]
+    const void *dy;
+    const float *d1;               // gradient of the final states
+    float *d0;                     // gradient of the initial states
+    void *dx, *ddt, *dz;
+    float *R;                      // gradients of the chunk states [slots][D][N]
+    float *part;                   // dB, dC of every tile of channels [tokens][nblk][2][4 LN]
+    float *pD, *pbias;             // dD, ddt_bias of every chunk [slots][D]
+    int T, D, N, G, per, bpg, nblk, rows, lq, nch, softplus;
+};
+
+// The LN lanes of a channel, lane I's value in all of them.
+template <int LN, int I> __device__ __forceinline__ float from_lane(float v)
+{
+    if constexpr (LN == 1) return v;
+    else if constexpr (LN == 2) return dpp_mov<I | I << 2 | (2 + I) << 4 | (2 + I) << 6>(v);
+    else if constexpr (LN == 4) return dpp_mov<I * 0x55>(v);
+    else {   // 0x150 + i: lane i of each row of 16
+        const int s = __float_as_int(v), lo = __builtin_amdgcn_update_dpp(0, s, 0x150 + I, 0xf, 0xf, true);
+        if constexpr (LN == 16) return __int_as_float(lo);
+        else return __int_as_float(__builtin_amdgcn_update_dpp(lo, s, 0x150 + 8 + I, 0xf, 0xc, false));
+    }
+}
+// The sum over the LN lanes of a channel, in all of them.
+constexpr int kDppRowMirror = 0x140;
+template <int LN> __device__ __forceinline__ float lane_sum(float v)
+{
+    if constexpr (LN >= 2) v += dpp_mov<kDppQuadXor1>(v);
+    if constexpr (LN >= 4) v += dpp_mov<kDppQuadXor2>(v);
+    if constexpr (LN >= 8) v += dpp_mov<kDppRowHalfMirror>(v);
+    if constexpr (LN >= 16) v += dpp_mov<kDppRowMirror>(v);
+    return v;
+}
+template <int N, typename F> __device__ __forceinline__ void unrolled(F &&f)
+{
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
+// One element of a row's buffer, zero past its end.
+template <typename E> __device__ __forceinline__ float bload_el(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    if constexpr (sizeof(E) == 2)
+        return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0) << 16);
+    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+// `tokens` tokens of a tensor from token t0 on, `width` elements each.
+template <typename E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t token_rsrc(const void *p, int64_t t0, int64_t stride, int tokens, int width)
+{
+    return make_rsrc(static_cast<const E *>(p) + t0 * stride, tokens > 0 ? ((tokens - 1) * stride + width) * (int64_t)sizeof(E) : 0);
+}
+
+// ---------------------------------------------------------------------------
+// rows and chunks
+// ---------------------------------------------------------------------------
+// Chunk slot c.  Segment i of a packed stream that starts at token s_i has the slots from
+// s_i / Q + i on: as many as its chunks, whatever the lengths (floor(a) + ceil(b) <=
+// floor(a + b) + 1), so no list of chunks is needed, and T / Q + segments slots hold them
+// all.  Slots without tokens have count <= 0.
+struct Slot {
+    int row, j, count;   // the chunk's row, its number there, its tokens
+    int64_t t0;          // its first token
+    int len;             // tokens of the row
+    bool last;
+};
+__device__ __forceinline__ Slot slot_at(const ScanArgs &a, int c)
+{
+    Slot s;
+    int lq = a.lq, start = 0;
+    if (a.plan) {
+        lq = a.plan[a.rows + 1];
+        int lo = 0, hi = a.rows - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)(a.plan[mid] >> lq) + mid <= c) lo = mid;
+            else hi = mid - 1;
+        }
+        s.row = lo;
+        start = a.plan[lo];
+        s.len = a.plan[lo + 1] - start;
+        s.j = c - ((start >> lq) + lo);
+        s.t0 = start;
+    } else {
+        s.row = c / a.nch;
+        s.j = c - s.row * a.nch;
+        s.len = a.T;
+        s.t0 = (int64_t)s.row * a.T;
+    }
+    const int64_t at = (int64_t)s.j << lq, left = s.len - at, q = (int64_t)1 << lq;
+    s.t0 += at;
+    s.count = s.j < 0 || left <= 0 ? 0 : (int)(left < q ? left : q);
+    s.last = left <= q;
+    return s;
+}
+
+// start[i]: the first token of segment i, start[nseq] = T, for non-decreasing ids; the chunk
+// length.  Any stream leaves start in [0, T] (and what it cannot mean out).  One workgroup, 16
+// tokens a thread in flight.
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void k_scan_plan(const int32_t *__restrict__ seq_idx, int32_t *__restrict__ start,
+                                                            int T, int nseq, int lq_long, int limit)
+{
+    __shared__ int most;
+    const int tid = threadIdx.x;
+    if (tid == 0) most = 0;
+    // ids above the last one start at T; the others are written over below
+    for (int i = tid; i <= nseq; i += kPlanThreads) start[i] = T;
+    __syncthreads();
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc_n(seq_idx, T * 4);   // past the end: 0, not used
+    constexpr int U = 4;
+    for (int tb = 0; tb < T; tb += U * 4 * kPlanThreads) {
+        int id[U][5];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = tb + (u * kPlanThreads + tid) * 4;
+            id[u][0] = t > 0 && t < T ? (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * t - 4, 0, 0) : -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) id[u][e + 1] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * (t + e), 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = tb + (u * kPlanThreads + tid) * 4 + e;
+                if (t >= T) continue;
+                const int lo = id[u][e] < -1 ? -1 : id[u][e], hi = id[u][e + 1] < nseq ? id[u][e + 1] : nseq - 1;
+                for (int i = lo + 1; i <= hi; ++i) start[i] = t;   // this id's, and those of ids left out
+            }
+    }
+    __syncthreads();
+    int m = 0;
+    for (int i = tid; i < nseq; i += kPlanThreads) m = max(m, start[i + 1] - start[i]);
+    atomicMax(&most, m);
+    __syncthreads();
+    // rows that are short beside the whole need no cutting
+    if (tid == 0) start[nseq + 1] = most <= limit ? 30 : lq_long;
+}
+
+// ---------------------------------------------------------------------------
+// one tile of channels
+// ---------------------------------------------------------------------------
+template <int LN> struct Lanes {
+    static constexpr int CB = kThreads / LN;          // channels of a workgroup
+    static constexpr int NP = 4 * LN;                 // states, padded
+    static constexpr int TT = LN <= 2 ? 16 : LN == 4 ? 32 : 64;   // tokens of a tile
+    static constexpr int NG = TT / LN;                // groups of LN tokens
+    static constexpr int NL = (TT * NP + kThreads - 1) / kThreads;   // B (and C) values of a tile a thread loads
+};
+struct Place {
+    int g, d, j;     // group, channel, lane of the channel
+    bool live;       // whether the lane has a channel of its own
+};
+template <int LN> __device__ __forceinline__ Place place_of(const ScanArgs &a, int blk)
+{
+    Place p;
+    p.g = blk / a.bpg;
+    const int c = (blk - p.g * a.bpg) * Lanes<LN>::CB + threadIdx.x / LN;
+    p.live = c < a.per;
+    p.d = p.g * a.per + (p.live ? c : a.per - 1);
+    p.j = threadIdx.x % LN;
+    return p;
+}
+__device__ __forceinline__ void load_state(const float *p, int n0, int N, float (&h)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = n0 + k < N ? p[n0 + k] : 0.f;
+}
+__device__ __forceinline__ void store_state(float *p, int n0, int N, const float (&h)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (n0 + k < N) p[n0 + k] = h[k];
+}
+
+// B or C of `tokens` tokens from t0 on for LDS: element e of a tile is token e / NP, state e % NP.
+template <typename E, int LN, int NL>
+__device__ __forceinline__ void fetch_keys(const void *p, int64_t t0, int64_t stride, int g, int N, int tokens, float (&v)[NL])
+{
+    constexpr int NP = Lanes<LN>::NP;
+    const __amdgpu_buffer_rsrc_t r = token_rsrc<E>(static_cast<const E *>(p) + (int64_t)g * N, t0, stride, tokens, N);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = i * kThreads + threadIdx.x, t = e / NP, n = e % NP;
+        v[i] = bload_el<E>(r, n < N && t < tokens ? (uint32_t)((t * stride + n) * sizeof(E)) : kOffNone);
+    }
+}
+template <int LN, int NL> __device__ __forceinline__ void put_keys(float *dst, const float (&v)[NL], int elems)
+{
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = i * kThreads + threadIdx.x;
+        if (e < elems) dst[e] = v[i];
+    }
+}
+
+__device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplus_f(raw) : raw; }
+
+// Forward over a chunk.  MODE 0: y and the final states, from the state that enters the chunk.
+// MODE 1: the chunk's end state from a zero start into S, and the sum of its Delta.  MODE 2:
+// that, and what the chunk's dy add to the gradient of the state that enters it, R = sum over
+// t of (product of the decays up to t's) C_t dy_t SiLU(z_t).
+template <typename E, int LN, bool GATE, int MODE>
+__global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
+{
+    using L = Lanes<LN>;
+    constexpr int TT = L::TT, NP = L::NP, NG = L::NG, NL = L::NL;
+    constexpr bool HASX = true, HASC = MODE != 1, HASZ = GATE && MODE != 1, HASG = MODE == 2;
+    __shared__ float keys[2][HASC ? 2 : 1][TT * NP];
+    const int c = blockIdx.x / a.nblk, blk = blockIdx.x - c * a.nblk;
+    const Slot s = slot_at(a, c);
+    const Place p = place_of<LN>(a, blk);
+    const int n0 = 4 * p.j;
+    const int64_t dn = (int64_t)p.d * a.N, DN = (int64_t)a.D * a.N;
+    if (MODE == 0 ? s.count <= 0 && !(s.len <= 0 && s.j == 0) : s.count <= 0 || (s.last && (MODE == 1 || s.j == 0))) return;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {0.f, 0.f, 0.f, 0.f}, cum[4] = {1.f, 1.f, 1.f, 1.f};
+    if (MODE == 0) {
+        if (s.j > 0) load_state(a.S + c * DN + dn, n0, a.N, h);
+        else if (a.s0) load_state(a.s0 + s.row * DN + dn, n0, a.N, h);
+    }
+    float A2[4];
+    load_state(a.A + dn, n0, a.N, A2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
+    const float bias = a.bias ? a.bias[p.d] : 0.f, skip = a.D_ ? a.D_[p.d] : 0.f;
+    float total = 0.f;
+
+    // the next tile's values are on their way while this one is computed
+    float xr[NG], dr[NG], zr[HASZ ? NG : 1], gr[HASG ? NG : 1], kb[NL], kc[HASC ? NL : 1];
+    auto fetch = [&](int t1) {
+        const int64_t t = s.t0 + t1;
+        const int left = s.count - t1 < TT ? s.count - t1 : TT;
+        const __amdgpu_buffer_rsrc_t rx = token_rsrc<E>(a.x, t, a.xs, left, a.D), rd = token_rsrc<E>(a.dt, t, a.dts, left, a.D);
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const int at = q * LN + p.j;
+            xr[q] = bload_el<E>(rx, (uint32_t)((at * (int)a.xs + p.d) * (int)sizeof(E)));
+            dr[q] = bload_el<E>(rd, (uint32_t)((at * (int)a.dts + p.d) * (int)sizeof(E)));
+        }
+        if constexpr (HASZ) {
+            const __amdgpu_buffer_rsrc_t rz = token_rsrc<E>(a.z, t, a.zs, left, a.D);
+#pragma unroll
+            for (int q = 0; q < NG; ++q) zr[q] = bload_el<E>(rz, (uint32_t)(((q * LN + p.j) * (int)a.zs + p.d) * (int)sizeof(E)));
+        }
+        if constexpr (HASG) {
+            const __amdgpu_buffer_rsrc_t rg = token_rsrc<E>(a.dy, t, a.D, left, a.D);
+#pragma unroll
+            for (int q = 0; q < NG; ++q) gr[q] = bload_el<E>(rg, (uint32_t)(((q * LN + p.j) * a.D + p.d) * (int)sizeof(E)));
+        }
+        fetch_keys<E, LN, NL>(a.B, t, a.Bs, p.g, a.N, left, kb);
+        if constexpr (HASC) fetch_keys<E, LN, NL>(a.C, t, a.Cs, p.g, a.N, left, kc);
+    };
+    if (s.count > 0) fetch(0);
+    E *yp = static_cast<E *>(a.y);
+    for (int t1 = 0, b = 0; t1 < s.count; t1 += TT, b ^= 1) {
+        put_keys<LN, NL>(keys[b][0], kb, TT * NP);
+        if constexpr (HASC) put_keys<LN, NL>(keys[b][HASC ? 1 : 0], kc, TT * NP);
+        float xv[NG], dl[NG], zv[HASZ ? NG : 1], gv[HASG ? NG : 1];
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            // tokens past the chunk: no step, so that the state stays
+            const bool in = t1 + q * LN + p.j < s.count;
+            xv[q] = xr[q];
+            dl[q] = in ? step_size(dr[q] + bias, a.softplus) : 0.f;
+            if constexpr (HASZ) zv[q] = zr[q];
+            if constexpr (HASG) gv[q] = HASZ ? gr[q] * silu(zv[q]) : gr[q];
+        }
+        if (t1 + TT < s.count) fetch(t1 + TT);
+        __syncthreads();   // the tile's keys are there, and the tile before last is done with
+        const float *kB = keys[b][0] + n0, *kC = keys[b][HASC ? 1 : 0] + n0;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const float dx = dl[q] * xv[q];
+            float y = 0.f;
+            unrolled<LN>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dx);
+                const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (q * LN + i) * NP);
+                floatx4 C;
+                if constexpr (HASC) C = *reinterpret_cast<const floatx4 *>(kC + (q * LN + i) * NP);
+                float dyi = 0.f, acc = 0.f;
+                if constexpr (HASG) dyi = from_lane<LN, i>(gv[q]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float e = exp2_(di * A2[k]);
+                    h[k] = e * h[k] + dxi * B[k];
+                    if constexpr (MODE == 0) acc += h[k] * C[k];
+                    if constexpr (MODE == 2) {
+                        cum[k] *= e;
+                        R[k] += cum[k] * (C[k] * dyi);
+                    }
+                }
+                if constexpr (MODE == 0) {
+                    acc = lane_sum<LN>(acc);
+                    y = p.j == i ? acc : y;
+                }
+            });
+            if constexpr (MODE == 0) {
+                const int t = t1 + q * LN + p.j;
+                y += skip * xv[q];
+                if constexpr (HASZ) y *= silu(zv[q]);
+                if (t < s.count && p.live) yp[(s.t0 + t) * a.D + p.d] = from_float<E>(y);
+            } else total += dl[q];
+        }
+    }
+    if (!p.live) return;
+    if constexpr (MODE == 0) {
+        if (a.s1 && s.last) store_state(a.s1 + s.row * DN + dn, n0, a.N, h);
+    } else {
+        store_state(a.S + c * DN + dn, n0, a.N, h);
+        total = lane_sum<LN>(total);
+        if (p.j == 0) a.sum[(int64_t)c * a.D + p.d] = total;
+        if constexpr (MODE == 2) store_state(a.R + c * DN + dn, n0, a.N, R);
+    }
+}
+
+// From chunk to chunk, a state a thread: S becomes the state that enters the chunk, R (BWD) the
+// gradient of the state that leaves it.  The first chunk's S and the last one's R stay: those
+// come from the initial states and the final states' gradient.
+template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(ScanArgs a, int blocks)
+{
+    constexpr int U = 8;   // chunks in flight
+    const int row = blockIdx.x / blocks;
+    const int64_t DN = (int64_t)a.D * a.N, e = (int64_t)(blockIdx.x - row * blocks) * kThreads + threadIdx.x;
+    int lq = a.lq, len = a.T, c0 = row * a.nch;
+    if (a.plan) {
+        lq = a.plan[a.rows + 1];
+        const int start = a.plan[row];
+        len = a.plan[row + 1] - start;
+        c0 = (start >> lq) + row;
+    }
+    const int n = len <= 0 ? 0 : (int)(((int64_t)len + ((int64_t)1 << lq) - 1) >> lq);
+    if (n < 2 || e >= DN) return;
+    const int d = (int)(e / a.N);
+    const float A2 = a.A[e] * kLog2e;
+    float h = a.s0 ? a.s0[row * DN + e] : 0.f;
+    for (int j = 0; j < n - 1; j += U) {
+        float s[U], t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + (j + u < n - 1 ? j + u : n - 2);
+            s[u] = a.S[c * DN + e];
+            t[u] = a.sum[c * a.D + d];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u < n - 1) {
+                if (j + u > 0) a.S[(c0 + j + u) * DN + e] = h;
+                h = exp2_(A2 * t[u]) * h + s[u];
+            }
+    }
+    a.S[(c0 + n - 1) * DN + e] = h;
+    if constexpr (BWD) {
+        float g = a.d1 ? a.d1[row * DN + e] : 0.f;
+        for (int j = n - 1; j > 0; j -= U) {
+            float s[U], t[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + (j - u > 0 ? j - u : 1);
+                s[u] = a.R[c * DN + e];
+                t[u] = a.sum[c * a.D + d];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j - u > 0) {
+                    if (j - u < n - 1) a.R[(c0 + j - u) * DN + e] = g;
+                    g = exp2_(A2 * t[u]) * g + s[u];
+                }
+        }
+        a.R[(int64_t)c0 * DN + e] = g;
+    }
+}
+
+// Every gradient of a chunk of kGradQ tokens.  The states at the start of each SC tokens first
+// (into LDS); then, from the last SC tokens to the first, the states in between again and the
+// way back through them,
+//
+//   g_t = e^{Delta_t+1 A} g_t+1 + C_t dy_t,   dB_t = sum over d of Delta x g_t,  dC_t = sum over d of dy h_t,
+//   dx = Delta (B . g) + D dy,  dDelta = x (B . g) + sum_n A e^{Delta A} g h_t-1,  dA = sum_t Delta e^{Delta A} g h_t-1
+//
+// with dy the gradient before the gate.  dB and dC are summed over the workgroup's channels
+// here and over tiles of channels by k_scan_keys.
+template <typename E, int LN, bool GATE>
+__global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
+{
+    constexpr int NP = 4 * LN, SC = LN <= 8 ? 8 : 16, GS = SC / LN, NSUB = kGradQ / SC, CB = kThreads / LN;
+    constexpr int NL = (kGradQ * NP + kThreads - 1) / kThreads;
+    __shared__ float keys[2][kGradQ * NP];
+    __shared__ floatx4 hs[NSUB][kThreads];
+    __shared__ float red[4][SC][2][NP];
+    const int c = blockIdx.x / a.nblk, blk = blockIdx.x - c * a.nblk;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    (void)CB;
+    const Slot s = slot_at(a, c);
+    const Place p = place_of<LN>(a, blk);
+    const int n0 = 4 * p.j;
+    const int64_t dn = (int64_t)p.d * a.N, DN = (int64_t)a.D * a.N;
+    if (s.count <= 0) {
+        const float none[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!p.live) return;
+        // a segment without tokens hands its gradient on; a slot without tokens adds nothing
+        if (s.len <= 0 && s.j == 0 && a.d0) {
+            float g[4] = {0.f, 0.f, 0.f, 0.f};
+            if (a.d1) load_state(a.d1 + s.row * DN + dn, n0, a.N, g);
+            store_state(a.d0 + s.row * DN + dn, n0, a.N, g);
+        }
+        store_state(a.S + c * DN + dn, n0, a.N, none);
+        if (p.j == 0) a.pD[(int64_t)c * a.D + p.d] = a.pbias[(int64_t)c * a.D + p.d] = 0.f;
+        return;
+    }
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, g[4] = {0.f, 0.f, 0.f, 0.f}, A2[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.live) {
+        if (s.j > 0) load_state(a.S + c * DN + dn, n0, a.N, h);
+        else if (a.s0) load_state(a.s0 + s.row * DN + dn, n0, a.N, h);
+        if (!s.last) load_state(a.R + c * DN + dn, n0, a.N, g);
+        else if (a.d1) load_state(a.d1 + s.row * DN + dn, n0, a.N, g);
+        load_state(a.A + dn, n0, a.N, A2);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
+    const float bias = a.bias ? a.bias[p.d] : 0.f, skip = a.D_ ? a.D_[p.d] : 0.f;
+    {
+        float kb[NL], kc[NL];
+        fetch_keys<E, LN, NL>(a.B, s.t0, a.Bs, p.g, a.N, s.count, kb);
+        fetch_keys<E, LN, NL>(a.C, s.t0, a.Cs, p.g, a.N, s.count, kc);
+        put_keys<LN, NL>(keys[0], kb, kGradQ * NP);
+        put_keys<LN, NL>(keys[1], kc, kGradQ * NP);
+    }
+    const __amdgpu_buffer_rsrc_t rx = token_rsrc<E>(a.x, s.t0, a.xs, s.count, a.D),
+                                 rd = token_rsrc<E>(a.dt, s.t0, a.dts, s.count, a.D),
+                                 rz = token_rsrc<E>(GATE ? a.z : a.x, s.t0, GATE ? a.zs : a.xs, s.count, a.D),
+                                 rg = token_rsrc<E>(a.dy, s.t0, a.D, s.count, a.D);
+    const int nsub = (s.count + SC - 1) / SC;
+    __syncthreads();
+    const float *kB = keys[0] + n0, *kC = keys[1] + n0;
+    // a token's Delta and x of this lane (none for a lane without a channel, none past the chunk)
+    auto step_of = [&](int t, float &raw, float &x, float &dl) {
+        const bool in = t < s.count && p.live;
+        raw = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + p.d) * (int)sizeof(E))) + bias;
+        x = bload_el<E>(rx, in ? (uint32_t)((t * (int)a.xs + p.d) * (int)sizeof(E)) : kOffNone);
+        dl = in ? step_size(raw, a.softplus) : 0.f;
+    };
+    for (int u = 0; u < nsub; ++u) {
+        hs[u][tid] = floatx4{h[0], h[1], h[2], h[3]};
+        if (u == nsub - 1) break;
+        float raw, x[GS], dl[GS];
+#pragma unroll
+        for (int q = 0; q < GS; ++q) step_of(u * SC + q * LN + p.j, raw, x[q], dl[q]);
+#pragma unroll
+        for (int q = 0; q < GS; ++q) {
+            const float dx = dl[q] * x[q];
+            unrolled<LN>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dx);
+                const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + q * LN + i) * NP);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = exp2_(di * A2[k]) * h[k] + dxi * B[k];
+            });
+        }
+    }
+    float dA[4] = {0.f, 0.f, 0.f, 0.f}, sD = 0.f, sb = 0.f;
+    for (int u = nsub - 1; u >= 0; --u) {
+        float raw[GS], x[GS], dl[GS], zv[GS], go[GS], dy[GS], dxs[GS], ys[GS];
+#pragma unroll
+        for (int q = 0; q < GS; ++q) {
+            const int t = u * SC + q * LN + p.j;
+            step_of(t, raw[q], x[q], dl[q]);
+            go[q] = bload_el<E>(rg, p.live ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone);
+            if constexpr (GATE) zv[q] = bload_el<E>(rz, (uint32_t)((t * (int)a.zs + p.d) * (int)sizeof(E)));
+            dy[q] = GATE ? go[q] * silu(zv[q]) : go[q];
+            if (!p.live) dy[q] = 0.f;
+            dxs[q] = dl[q] * x[q];
+            ys[q] = 0.f;
+        }
+        float hh[SC + 1][4], ee[SC][4];
+        {
+            const floatx4 v = hs[u][tid];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) hh[0][k] = v[k];
+        }
+        unrolled<SC>([&](auto tc) {
+            constexpr int t = decltype(tc)::value, q = t / LN, i = t % LN;
+            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]);
+            const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
+            float acc = 0.f;
+            floatx4 C;
+            if constexpr (GATE) C = *reinterpret_cast<const floatx4 *>(kC + (u * SC + t) * NP);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ee[t][k] = exp2_(di * A2[k]);
+                hh[t + 1][k] = ee[t][k] * hh[t][k] + dxi * B[k];
+                if constexpr (GATE) acc += hh[t + 1][k] * C[k];
+            }
+            if constexpr (GATE) {
+                acc = lane_sum<LN>(acc);
+                ys[q] = p.j == i ? acc : ys[q];
+            }
+        });
+        float along[GS], dd[GS];
+        unrolled<SC>([&](auto tc) {
+            constexpr int t = SC - 1 - decltype(tc)::value, q = t / LN, i = t % LN;
+            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]), dyi = from_lane<LN, i>(dy[q]);
+            const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
+            const floatx4 C = *reinterpret_cast<const floatx4 *>(kC + (u * SC + t) * NP);
+            float al = 0.f, de = 0.f, vB[4], vC[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[k] += dyi * C[k];
+                vC[k] = dyi * hh[t + 1][k];
+                vB[k] = dxi * g[k];
+                al += g[k] * B[k];
+                g[k] *= ee[t][k];
+                const float gh = g[k] * hh[t][k];
+                de += gh * A2[k];
+                dA[k] += gh * di;
+            }
+            al = lane_sum<LN>(al);
+            de = lane_sum<LN>(de);
+            along[q] = i == LN - 1 || p.j == i ? al : along[q];
+            dd[q] = i == LN - 1 || p.j == i ? de : dd[q];
+            // over the wave's channels
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int m = LN; m < 64; m <<= 1) {
+                    vB[k] += __shfl_xor(vB[k], m);
+                    vC[k] += __shfl_xor(vC[k], m);
+                }
+            }
+            if (lane < LN) {
+                *reinterpret_cast<floatx4 *>(&red[wv][t][0][n0]) = floatx4{vB[0], vB[1], vB[2], vB[3]};
+                *reinterpret_cast<floatx4 *>(&red[wv][t][1][n0]) = floatx4{vC[0], vC[1], vC[2], vC[3]};
+            }
+        });
+        __syncthreads();
+        for (int e = tid; e < SC * 2 * NP; e += kThreads) {
+            const int t = u * SC + e / (2 * NP);
+            const float *r = &red[0][0][0][0] + e;
+            constexpr int W = SC * 2 * NP;
+            if (t < s.count) a.part[((s.t0 + t) * a.nblk + blk) * (2 * NP) + e % (2 * NP)] = (r[0] + r[W]) + (r[2 * W] + r[3 * W]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < GS; ++q) {
+            const int t = u * SC + q * LN + p.j;
+            if (t >= s.count || !p.live) continue;
+            const int64_t at = (s.t0 + t) * a.D + p.d;
+            float dd_ = x[q] * along[q] + kLn2 * dd[q];
+            if (a.softplus) dd_ *= __builtin_amdgcn_rcpf(1.f + exp2_(-raw[q] * kLog2e));
+            static_cast<E *>(a.dx)[at] = from_float<E>(dl[q] * along[q] + dy[q] * skip);
+            static_cast<E *>(a.ddt)[at] = from_float<E>(dd_);
+            sD += dy[q] * x[q];
+            sb += dd_;
+            if constexpr (GATE) {
+                const float sg = __builtin_amdgcn_rcpf(1.f + exp2_(-zv[q] * kLog2e));
+                static_cast<E *>(a.dz)[at] = from_float<E>(go[q] * (ys[q] + skip * x[q]) * (sg * (1.f + zv[q] * (1.f - sg))));
+            }
+        }
+    }
+    if (!p.live) return;
+    if (s.j == 0 && a.d0) store_state(a.d0 + s.row * DN + dn, n0, a.N, g);
+    store_state(a.S + c * DN + dn, n0, a.N, dA);   // this workgroup alone has read it
+    sD = lane_sum<LN>(sD);
+    sb = lane_sum<LN>(sb);
+    if (p.j == 0) {
+        a.pD[(int64_t)c * a.D + p.d] = sD;
+        a.pbias[(int64_t)c * a.D + p.d] = sb;
+    }
+}
+
+// dB and dC: the sums of a token's and group's tiles of channels.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void k_scan_keys(const float *__restrict__ part, E *__restrict__ dB, E *__restrict__ dC,
+                                                        int64_t items, int bpg, int N, int NP)
+{
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= items) return;
+    const int n = (int)(i % (2 * NP));
+    const int64_t tg = i / (2 * NP);
+    const float *p = part + tg * bpg * (2 * NP) + n;
+    float s = 0.f;
+    for (int b = 0; b < bpg; ++b) s += p[(int64_t)b * 2 * NP];
+    const int k = n % NP;
+    if (k < N) (n < NP ? dB : dC)[tg * N + k] = from_float<E>(s);
+}
+
+// out[e] = the sum over the slots of part[slot][e]: 32 values and 32 slices of the slots a workgroup.
+__global__ __launch_bounds__(1024) void k_scan_sum(const float *__restrict__ part, float *__restrict__ out, int slots, int64_t n)
+{
+    __shared__ float s[32][33];
+    const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int64_t e = (int64_t)blockIdx.x * 32 + cl;
+    float v = 0.f;
+    if (e < n)
+        for (int c = sl; c < slots; c += 32) v += part[c * n + e];
+    s[sl][cl] = v;
+    __syncthreads();
+    if (sl == 0 && e < n) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t += s[r][cl];
+        out[e] = t;
+    }
+}
+
+// One token of every batch row: the state is read and written once, 16 bytes a lane, and that
+// is what bounds it.
+struct StepArgs {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *bias;
+    int64_t xs, dts, Bs, Cs, zs;
+    float *state;
+    void *y;
+    int dim, N, G, per, bpg, nblk, softplus;
+};
+template <typename E, int LN>
+__global__ __launch_bounds__(kThreads) void k_scan_step(StepArgs a)
+{
+    constexpr int CB = kThreads / LN;
+    const int b = blockIdx.x / a.nblk, blk = blockIdx.x - b * a.nblk;
+    const int g = blk / a.bpg, c = (blk - g * a.bpg) * CB + threadIdx.x / LN, j = threadIdx.x % LN, n0 = 4 * j;
+    if (c >= a.per) return;   // all lanes of the channel
+    const int d = g * a.per + c;
+    const E *Bp = static_cast<const E *>(a.B) + b * a.Bs + (int64_t)g * a.N, *Cp = static_cast<const E *>(a.C) + b * a.Cs + (int64_t)g * a.N;
+    float *sp = a.state + ((int64_t)b * a.dim + d) * a.N;
+    float h[4], A[4], B[4], C[4];
+    load_state(sp, n0, a.N, h);
+    load_state(a.A + (int64_t)d * a.N, n0, a.N, A);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        B[k] = n0 + k < a.N ? to_float(Bp[n0 + k]) : 0.f;
+        C[k] = n0 + k < a.N ? to_float(Cp[n0 + k]) : 0.f;
+    }
+    const float x = to_float(static_cast<const E *>(a.x)[b * a.xs + d]);
+    const float dl = step_size(to_float(static_cast<const E *>(a.dt)[b * a.dts + d]) + (a.bias ? a.bias[d] : 0.f), a.softplus);
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = exp2_(dl * (A[k] * kLog2e)) * h[k] + dl * x * B[k];
+        y += h[k] * C[k];
+    }
+    store_state(sp, n0, a.N, h);
+    y = lane_sum<LN>(y);
+    if (j) return;
+    if (a.D) y += a.D[d] * x;
+    if (a.z) y *= silu(to_float(static_cast<const E *>(a.z)[b * a.zs + d]));
+    static_cast<E *>(a.y)[(int64_t)b * a.dim + d] = from_float<E>(y);
+}
+
+
+}  // namespace sscan
+}  // namespace ssd

@@ -50,6 +50,19 @@ template <int CTRL> __device__ __forceinline__ float dpp_mov(float v)
 // divide.  v -> -inf gives -0 (the reciprocal of inf is 0).
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + exp2_(-v * kLog2e)); }
 
+// softplus(z) = log(1 + e^z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1],
+// from the hardware base-2 exponential and logarithm.  log1p(u) is taken as
+// log(w) u / (w - 1) with w = fl(1 + u): w - 1 is exact, and the quotient
+// cancels the rounding of 1 + u, so the result keeps a few-ulp relative error
+// however small u is (w == 1 means u is below half an ulp of 1: log1p(u) = u).
+__device__ __forceinline__ float softplus_f(float z)
+{
+    const float u = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
+    const float w = 1.f + u;
+    const float l1p = w == 1.f ? u : __builtin_amdgcn_logf(w) * 0.6931471805599453f * (u / (w - 1.f));
+    return fmaxf(z, 0.f) + l1p;
+}
+
 template <typename E> struct Frag;
 template <> struct Frag<bf16> { using type = bf16x8; };
 template <> struct Frag<float> { using type = floatx8; };

@@ -44,19 +44,6 @@ __device__ __forceinline__ void chunk_rows(int c, int Q, int T, const int2 *cmap
 // ---------------------------------------------------------------------------
 constexpr int kCumsumHeads = 4;   // one wave per head
 
-// softplus(z) = log(1 + e^z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1],
-// from the hardware base-2 exponential and logarithm.  log1p(u) is taken as
-// log(w) u / (w - 1) with w = fl(1 + u): w - 1 is exact, and the quotient
-// cancels the rounding of 1 + u, so the result keeps a few-ulp relative error
-// however small u is (w == 1 means u is below half an ulp of 1: log1p(u) = u).
-__device__ __forceinline__ float softplus_f(float z)
-{
-    const float u = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
-    const float w = 1.f + u;
-    const float l1p = w == 1.f ? u : __builtin_amdgcn_logf(w) * 0.6931471805599453f * (u / (w - 1.f));
-    return fmaxf(z, 0.f) + l1p;
-}
-
 // Inclusive segmented scan over the 64 lanes of a wave: lane i ends with the
 // sum of v over lanes j <= i back to (and including) the nearest lane whose
 // flag is set, and f = whether any lane in 0..i has it.  Hillis-Steele steps

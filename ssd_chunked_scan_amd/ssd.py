@@ -11,7 +11,11 @@ Names follow the C ABI: ``fwd`` (= ``ssd_fwd``), the per-step entry points
 ``seq_final_states``, ``chunk_scan``, the decode step ``step`` (= ``ssd_step``)
 and the backward ``bwd`` (= ``ssd_bwd``); the gated delta rule ``gdr_fwd``,
 ``gdr_bwd`` and ``gdr_step``; layer norm ``layer_norm_fwd`` and
-``layer_norm_bwd``.
+``layer_norm_bwd``; the selective scan ``selective_scan_fwd``,
+``selective_scan_bwd`` and ``selective_scan_step`` with its convolution
+``causal_conv_fwd``, ``causal_conv_bwd`` and ``causal_conv_step``; RMS norm
+``rms_norm_fwd``, ``rms_norm_quant`` and ``rms_norm_bwd``; the 8-bit product
+``matmul_fp8``.
 """
 from __future__ import annotations
 
@@ -33,7 +37,11 @@ EXPORTED = ["ssd_abi_version", "ssd_status_string", "ssd_fwd_workspace_size", "s
             "ssd_seq_final_states", "ssd_chunk_scan", "ssd_step", "ssd_bwd_workspace_size", "ssd_bwd",
             "ssd_fwd_gated", "ssd_conv1d_silu", "ssd_fwd_noalloc", "ssd_bwd_stage_times", "ssd_check_seq_idx",
             "ssd_gdr_fwd_workspace_size", "ssd_gdr_bwd_workspace_size", "ssd_gdr_fwd", "ssd_gdr_bwd", "ssd_gdr_step",
-            "ssd_layer_norm_fwd", "ssd_layer_norm_bwd_workspace_size", "ssd_layer_norm_bwd"]
+            "ssd_layer_norm_fwd", "ssd_layer_norm_bwd_workspace_size", "ssd_layer_norm_bwd",
+            "ssd_selective_scan_fwd_workspace_size", "ssd_selective_scan_bwd_workspace_size", "ssd_selective_scan_fwd",
+            "ssd_selective_scan_bwd", "ssd_selective_scan_step", "ssd_causal_conv_fwd", "ssd_causal_conv_bwd_workspace_size",
+            "ssd_causal_conv_bwd", "ssd_causal_conv_step", "ssd_rms_norm_fwd", "ssd_rms_norm_bwd_workspace_size", "ssd_rms_norm_bwd",
+            "ssd_matmul_fp8_workspace_size", "ssd_matmul_fp8"]
 
 # SSD_BWD_MAX_STAGES in include/ssd.h
 BWD_MAX_STAGES = 24
@@ -142,6 +150,103 @@ class NormBwdArgs(ctypes.Structure):
     ]
 
 
+class SelectiveScanArgs(ctypes.Structure):
+    """Mirror of ``ssd_selective_scan_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("dt", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+        ("C", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("z", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64), ("B_stride", ctypes.c_int64),
+        ("C_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("initial_states", ctypes.c_void_p),
+        ("seq_idx", ctypes.c_void_p), ("nseq", ctypes.c_int64), ("y", ctypes.c_void_p),
+        ("final_states", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SelectiveScanBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_selective_scan_bwd_args``."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("dfinal_states", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("ddt", ctypes.c_void_p), ("dA", ctypes.c_void_p), ("dB", ctypes.c_void_p), ("dC", ctypes.c_void_p),
+        ("dD", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p), ("dz", ctypes.c_void_p),
+        ("dinitial_states", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SelectiveScanStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_selective_scan_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32), ("x", ctypes.c_void_p), ("dt", ctypes.c_void_p),
+        ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("C", ctypes.c_void_p), ("D", ctypes.c_void_p),
+        ("dt_bias", ctypes.c_void_p), ("z", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+        ("dt_stride", ctypes.c_int64), ("B_stride", ctypes.c_int64), ("C_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64), ("state", ctypes.c_void_p), ("y", ctypes.c_void_p),
+    ]
+
+
+class CausalConvArgs(ctypes.Structure):
+    """Mirror of ``ssd_causal_conv_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64), ("width", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("initial_window", ctypes.c_void_p),
+        ("seq_idx", ctypes.c_void_p), ("nseq", ctypes.c_int64), ("y", ctypes.c_void_p),
+        ("final_window", ctypes.c_void_p),
+    ]
+
+
+class CausalConvBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_causal_conv_bwd_args``."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("dfinal_window", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("dinitial_window", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class CausalConvStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_causal_conv_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("silu", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("window", ctypes.c_void_p), ("y", ctypes.c_void_p),
+    ]
+
+
+class RmsNormArgs(ctypes.Structure):
+    """Mirror of ``ssd_rms_norm_args``."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p), ("q", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class RmsNormBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_rms_norm_bwd_args``."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32), ("r", ctypes.c_void_p), ("dy", ctypes.c_void_p),
+        ("dresidual_out", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MatmulFp8Args(ctypes.Structure):
+    """Mirror of ``ssd_matmul_fp8_args``."""
+    _fields_ = [
+        ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("a", ctypes.c_void_p), ("a_scales", ctypes.c_void_p), ("w", ctypes.c_void_p),
+        ("w_scales", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class SSDError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -188,6 +293,8 @@ def load_library(path: str = LIB_PATH):
     lib.ssd_layer_norm_fwd.argtypes = [vp, vp]
     lib.ssd_layer_norm_bwd_workspace_size.argtypes = [vp, vp]
     lib.ssd_layer_norm_bwd.argtypes = [vp, vp]
+    for name in EXPORTED[EXPORTED.index("ssd_selective_scan_fwd_workspace_size"):]:
+        getattr(lib, name).argtypes = [vp, vp, vp] if name in ("ssd_selective_scan_bwd", "ssd_causal_conv_bwd") else [vp, vp]
     for name in EXPORTED[2:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -899,3 +1006,432 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, grads=None, workspace=None, s
         return load_library().ssd_layer_norm_bwd(a, st), out
 
     return _launch("ssd_layer_norm_bwd", dev, stream, call)
+
+
+# ---------------------------------------------------------------------------
+# the selective scan and its convolution
+# ---------------------------------------------------------------------------
+
+_SCAN = struct.Struct("5q2i8P5q2Pq4P")      # ssd_selective_scan_args
+_SCAN_BWD = struct.Struct("13P")            # ssd_selective_scan_bwd_args
+_SCAN_STEP = struct.Struct("4q2i8P5q2P")    # ssd_selective_scan_step_args
+_CCONV = struct.Struct("4q2iPq4Pq2P")       # ssd_causal_conv_args
+_CCONV_BWD = struct.Struct("8P")            # ssd_causal_conv_bwd_args
+_CCONV_STEP = struct.Struct("3q2iPq4P")     # ssd_causal_conv_step_args
+_RMS = struct.Struct("2q2ifi8P")            # ssd_rms_norm_args
+_RMS_BWD = struct.Struct("2q2i10P")         # ssd_rms_norm_bwd_args
+_MM = struct.Struct("3q2i8P")               # ssd_matmul_fp8_args
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _token_stride(t, name, dtype, shape, dev, lead):
+    """Elements from one token of ``t`` to the next, 0 if nothing lies between them.  The first
+    ``lead`` axes count tokens; a token's elements are contiguous, tokens may be columns of
+    wider rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    st, width = t.stride(), 1
+    for n, s in zip(reversed(shape[lead:]), reversed(st[lead:])):
+        if n != 1 and s != width:
+            raise ValueError(f"{name}: the elements of a token must be contiguous (no silent copies)")
+        width *= n
+    step = None
+    for n, s in zip(reversed(shape[:lead]), reversed(st[:lead])):   # the last of them first
+        if n == 1:
+            continue
+        if step is None:
+            step, expect = s, s * n
+        elif s != expect:
+            raise ValueError(f"{name}: batch rows must follow each other (no silent copies)")
+    if step is None:
+        return 0
+    if step < width:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return step
+
+
+def _on_gpu(t, name, dims, what):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be {what}")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+
+
+def _given(t, name, dtype, shape, dev):
+    """An optional dense tensor."""
+    if t is not None:
+        _same(t, name, dtype, shape, dev)
+
+
+def _made(t, name, dtype, shape, dev):
+    """An output: the caller's, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _same(t, name, dtype, shape, dev)
+    return t
+
+
+def _packed_rows(seq_idx, nseq, batch, T, dev):
+    """(address of the ids, nseq, rows of the states)."""
+    if seq_idx is None:
+        return 0, 0, batch
+    _same(seq_idx, "seq_idx", torch.int32, (T,), dev)
+    if nseq is None:
+        raise ValueError("nseq is required with seq_idx (no device->host read)")
+    return _ids(seq_idx), int(nseq), int(nseq)
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
+    """Checked inputs of a scan: (sizes, dtype flags and input pointers and strides, N, G)."""
+    _on_gpu(x, "x", lead + 1, "[batch, seqlen, dim]" if lead == 2 else "[batch, dim]")
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError("B must be [batch, seqlen, ngroups, dstate]" if lead == 2 else "B must be [batch, ngroups, dstate]")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    dim, (G, N) = shape[-1], B.shape[lead:]
+    keys = shape[:lead] + B.shape[lead:]
+    strides = (_token_stride(x, "x", dtype, shape, dev, lead), _token_stride(dt, "dt", dtype, shape, dev, lead),
+               _token_stride(B, "B", dtype, keys, dev, lead), _token_stride(C, "C", dtype, keys, dev, lead),
+               0 if z is None else _token_stride(z, "z", dtype, shape, dev, lead))
+    _same(A, "A", torch.float32, (dim, N), dev)
+    _given(D, "D", torch.float32, (dim,), dev)
+    _given(dt_bias, "dt_bias", torch.float32, (dim,), dev)
+    ptrs = (x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z))
+    return (*shape, N, G, _DTYPES[dtype], 1 if dt_softplus else 0), ptrs, strides
+
+
+def _scan_pack(head, ptrs, strides, s0, ids, n, y=0, final_states=0, workspace=0, nbytes=0):
+    return _SCAN.pack(*head, *ptrs, *strides, s0, ids, n, y, final_states, workspace, nbytes)
+
+
+def _scan_workspace(name, head, ids, n):
+    # only the sizes matter, and whether there is a seq_idx
+    return _workspace_bytes(name, _scan_pack(head, (0,) * 8, (0,) * 5, 0, _NO_IDS if ids else 0, n))
+
+
+def selective_scan_fwd_workspace_bytes(x, dt, A, B, C, seq_idx=None, nseq=None) -> int:
+    """Bytes of the ``workspace`` that ``selective_scan_fwd`` takes for these shapes."""
+    head, _, _ = _scan_args(x, dt, A, B, C, None, None, None, True, 2)
+    ids, n, _ = _packed_rows(seq_idx, nseq, x.shape[0], x.shape[1], x.device)
+    return _scan_workspace("ssd_selective_scan_fwd_workspace_size", head, ids, n)
+
+
+def selective_scan_bwd_workspace_bytes(x, dt, A, B, C, seq_idx=None, nseq=None) -> int:
+    """Bytes of the ``workspace`` that ``selective_scan_bwd`` takes for these shapes."""
+    head, _, _ = _scan_args(x, dt, A, B, C, None, None, None, True, 2)
+    ids, n, _ = _packed_rows(seq_idx, nseq, x.shape[0], x.shape[1], x.device)
+    return _scan_workspace("ssd_selective_scan_bwd_workspace_size", head, ids, n)
+
+
+def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, initial_states=None, seq_idx=None,
+                       nseq=None, y=None, final_states=None, workspace=None, stream=None, want_final=True):
+    """y, final_states = the selective scan over whole sequences (``ssd_selective_scan_fwd``):
+    x, dt, z [b,T,dim], B, C [b,T,G,N], all fp32 or bf16, A [dim,N], D and dt_bias [dim]
+    fp32; y = (C.h + D x) SiLU(z).  x, dt, z, B and C may be columns of wider rows (a
+    projection's output, sliced).  States are [b,dim,N] fp32, with ``seq_idx`` (packed
+    streams, batch 1) [nseq,dim,N], one per segment.  ``y``, ``final_states`` and
+    ``workspace`` (uint8) may be passed pre-allocated."""
+    head, ptrs, strides = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    b, T, dim, N = head[:4]
+    dev = x.device
+    ids, n, rows = _packed_rows(seq_idx, nseq, b, T, dev)
+    states = (rows, dim, N)
+    _given(initial_states, "initial_states", torch.float32, states, dev)
+
+    def call(st):
+        yy = _made(y, "y", x.dtype, (b, T, dim), dev)
+        fin = _made(final_states, "final_states", torch.float32, states, dev) if want_final or final_states is not None else None
+        need = _scan_workspace("ssd_selective_scan_fwd_workspace_size", head, ids, n) if workspace is None else 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else workspace
+        _given(ws, "workspace", torch.uint8, None if ws is None else ws.shape, dev)
+        a = _scan_pack(head, ptrs, strides, _at(initial_states), ids, n, yy.data_ptr(), _at(fin), _at(ws),
+                       0 if ws is None else ws.numel())
+        return load_library().ssd_selective_scan_fwd(a, st), (yy, fin)
+
+    return _launch("ssd_selective_scan_fwd", dev, stream, call)
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=True, initial_states=None,
+                       dfinal_states=None, seq_idx=None, nseq=None, grads=None, workspace=None, stream=None, want_dinit=True):
+    """Gradients of sum(y * dy) + sum(final_states * dfinal_states) (``ssd_selective_scan_bwd``):
+    a dict with dx, ddt, dA, dB, dC, dD (None without D), dz (None without z), ddt_bias
+    (None without dt_bias) and dinitial_states (None unless ``want_dinit``); ``grads`` may
+    pass those tensors pre-allocated."""
+    head, ptrs, strides = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    b, T, dim, N = head[:4]
+    dtype, dev = x.dtype, x.device
+    ids, n, rows = _packed_rows(seq_idx, nseq, b, T, dev)
+    states = (rows, dim, N)
+    _given(initial_states, "initial_states", torch.float32, states, dev)
+    _given(dfinal_states, "dfinal_states", torch.float32, states, dev)
+    _same(dy, "dy", dtype, x.shape, dev)
+
+    def call(st):
+        out = dict(grads or {})
+        f32 = torch.float32
+        for name, kind, shape, want in (("dx", dtype, x.shape, True), ("ddt", dtype, x.shape, True), ("dA", f32, A.shape, True),
+                                        ("dB", dtype, B.shape, True), ("dC", dtype, B.shape, True), ("dD", f32, (dim,), D is not None),
+                                        ("ddt_bias", f32, (dim,), dt_bias is not None), ("dz", dtype, x.shape, z is not None),
+                                        ("dinitial_states", f32, states, want_dinit)):
+            given = out.get(name)
+            out[name] = _made(given, name, kind, shape, dev) if want or given is not None else None
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(_scan_workspace("ssd_selective_scan_bwd_workspace_size", head, ids, n), dtype=torch.uint8, device=dev)
+        else:
+            _check(ws, "workspace", torch.uint8, None, dev)
+        g = _SCAN_BWD.pack(dy.data_ptr(), _at(dfinal_states), *(_at(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dz",
+                                                                                      "dinitial_states")), ws.data_ptr(), ws.numel())
+        return load_library().ssd_selective_scan_bwd(_scan_pack(head, ptrs, strides, _at(initial_states), ids, n), g, st), out
+
+    return _launch("ssd_selective_scan_bwd", dev, stream, call)
+
+
+def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, y=None, stream=None):
+    """y = one token of every batch row (``ssd_selective_scan_step``): x, dt, z [b,dim], B, C
+    [b,G,N]; ``state`` [b,dim,N] fp32 is updated in place."""
+    head, ptrs, strides = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 1)
+    b, dim, N = head[:3]
+    dev = x.device
+    _same(state, "state", torch.float32, (b, dim, N), dev)
+
+    def call(st):
+        yy = _made(y, "y", x.dtype, (b, dim), dev)
+        a = _SCAN_STEP.pack(*head, *ptrs, *strides, state.data_ptr(), yy.data_ptr())
+        return load_library().ssd_selective_scan_step(a, st), yy
+
+    return _launch("ssd_selective_scan_step", dev, stream, call)
+
+
+def _conv_args(x, weight, bias, silu, window, seq_idx, nseq):
+    """Checked inputs of the convolution: (packed head and input pointers, shape of the windows)."""
+    _on_gpu(x, "x", 3, "[batch, seqlen, dim]")
+    (b, T, dim), dtype, dev = x.shape, x.dtype, x.device
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [dim, width]")
+    K = weight.shape[1]
+    stride = _token_stride(x, "x", dtype, x.shape, dev, 2)
+    _same(weight, "weight", torch.float32, (dim, K), dev)
+    _given(bias, "bias", torch.float32, (dim,), dev)
+    ids, n, rows = _packed_rows(seq_idx, nseq, b, T, dev)
+    windows = (rows, K - 1, dim)
+    _given(window, "initial_window", dtype, windows, dev)
+    return (b, T, dim, K, _DTYPES[dtype], 1 if silu else 0, x.data_ptr(), stride, weight.data_ptr(), _at(bias), _at(window), ids, n), windows
+
+
+def causal_conv_fwd(x, weight, bias=None, silu=True, initial_window=None, seq_idx=None, nseq=None, y=None, final_window=None,
+                    stream=None, want_window=True):
+    """y, final_window = the causal convolution of every channel with its own taps
+    (``ssd_causal_conv_fwd``): x [b,T,dim] fp32 or bf16 (it may be columns of wider rows), weight
+    [dim,width] and bias [dim] fp32.  Windows hold the width - 1 inputs before a sequence's
+    first token, or its last ones: [b,width-1,dim] in x's dtype, with ``seq_idx`` (packed
+    streams, batch 1) [nseq,width-1,dim]."""
+    head, windows = _conv_args(x, weight, bias, silu, initial_window, seq_idx, nseq)
+    dev = x.device
+
+    def call(st):
+        yy = _made(y, "y", x.dtype, x.shape, dev)
+        fin = _made(final_window, "final_window", x.dtype, windows, dev) if want_window or final_window is not None else None
+        return load_library().ssd_causal_conv_fwd(_CCONV.pack(*head, yy.data_ptr(), _at(fin)), st), (yy, fin)
+
+    return _launch("ssd_causal_conv_fwd", dev, stream, call)
+
+
+def causal_conv_bwd(x, weight, dy, bias=None, silu=True, initial_window=None, dfinal_window=None, seq_idx=None, nseq=None, grads=None,
+                    workspace=None, stream=None, want_dinit=True):
+    """Gradients of sum(y * dy) + sum(final_window * dfinal_window) (``ssd_causal_conv_bwd``): a
+    dict with dx, dweight, dbias (None without bias) and dinitial_window (None unless
+    ``want_dinit``); ``grads`` may pass those tensors pre-allocated."""
+    head, windows = _conv_args(x, weight, bias, silu, initial_window, seq_idx, nseq)
+    dtype, dev = x.dtype, x.device
+    _same(dy, "dy", dtype, x.shape, dev)
+    _given(dfinal_window, "dfinal_window", dtype, windows, dev)
+
+    def call(st):
+        out = dict(grads or {})
+        for name, kind, shape, want in (("dx", dtype, x.shape, True), ("dweight", torch.float32, weight.shape, True),
+                                        ("dbias", torch.float32, weight.shape[:1], bias is not None),
+                                        ("dinitial_window", dtype, windows, want_dinit)):
+            given = out.get(name)
+            out[name] = _made(given, name, kind, shape, dev) if want or given is not None else None
+        ws = workspace
+        if ws is None:
+            # neither addresses nor strides change the size
+            size = _CCONV.pack(*head[:6], 0, 0, 0, 0, 0, _NO_IDS if head[11] else 0, head[12], 0, 0)
+            ws = torch.empty(_workspace_bytes("ssd_causal_conv_bwd_workspace_size", size), dtype=torch.uint8, device=dev)
+        else:
+            _check(ws, "workspace", torch.uint8, None, dev)
+        g = _CCONV_BWD.pack(dy.data_ptr(), _at(dfinal_window), out["dx"].data_ptr(), out["dweight"].data_ptr(), _at(out["dbias"]),
+                            _at(out["dinitial_window"]), ws.data_ptr(), ws.numel())
+        return load_library().ssd_causal_conv_bwd(_CCONV.pack(*head, 0, 0), g, st), out
+
+    return _launch("ssd_causal_conv_bwd", dev, stream, call)
+
+
+def causal_conv_step(x, window, weight, bias=None, silu=True, y=None, stream=None):
+    """y = one token of every batch row (``ssd_causal_conv_step``): x [b,dim]; ``window``
+    [b,width-1,dim] in x's dtype is moved on by this token in place."""
+    _on_gpu(x, "x", 2, "[batch, dim]")
+    (b, dim), dtype, dev = x.shape, x.dtype, x.device
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [dim, width]")
+    K = weight.shape[1]
+    stride = _token_stride(x, "x", dtype, x.shape, dev, 1)
+    _same(weight, "weight", torch.float32, (dim, K), dev)
+    _given(bias, "bias", torch.float32, (dim,), dev)
+    _same(window, "window", dtype, (b, K - 1, dim), dev)
+
+    def call(st):
+        yy = _made(y, "y", dtype, (b, dim), dev)
+        a = _CCONV_STEP.pack(b, dim, K, _DTYPES[dtype], 1 if silu else 0, x.data_ptr(), stride, weight.data_ptr(), _at(bias),
+                             window.data_ptr(), yy.data_ptr())
+        return load_library().ssd_causal_conv_step(a, st), yy
+
+    return _launch("ssd_causal_conv_step", dev, stream, call)
+
+
+# ---------------------------------------------------------------------------
+# RMS norm with the residual's addition, and the 8-bit product that reads it
+# ---------------------------------------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+
+
+def _rms_fwd(x, weight, residual, eps, residual_out, y, q, scales, rstd, stream, want_y, want_q, want_rstd):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    lead, dim = shape[:-1], shape[-1]
+    if dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16")
+    _check(x, "x")   # on the GPU, contiguous
+    _given(weight, "weight", torch.float32, (dim,), dev)
+    rtype = dtype
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.dtype not in _DTYPES:
+            raise TypeError("residual must be a float32 or bfloat16 tensor")
+        rtype = residual.dtype
+        _same(residual, "residual", rtype, shape, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+
+    def call(st):
+        yy = _made(y, "y", dtype, shape, dev) if want_y else None
+        ro = _made(residual_out, "residual_out", rtype, shape, dev) if residual is not None else None
+        qq = _made(q, "q", _F8, shape, dev) if want_q else None
+        ss = _made(scales, "scales", torch.float32, (*lead, -(-dim // 128)), dev) if want_q else None
+        rr = _made(rstd, "rstd", torch.float32, lead, dev) if want_rstd else None
+        a = _RMS.pack(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], _DTYPES[rtype], eps, 0, x.data_ptr(), _at(residual), _at(weight),
+                      _at(ro), _at(yy), _at(qq), _at(ss), _at(rr))
+        return load_library().ssd_rms_norm_fwd(a, st), (yy, ro, rr, qq, ss)
+
+    return _launch("ssd_rms_norm_fwd", dev, stream, call)
+
+
+def rms_norm_fwd(x, weight=None, residual=None, eps=1e-5, y=None, residual_out=None, rstd=None, stream=None, want_rstd=True):
+    """y, residual_out, rstd = RMS norm over the last axis of x + residual (``ssd_rms_norm_fwd``):
+    x [..., dim] and residual fp32 or bf16, each of its own type, weight [dim] fp32 or None.
+    residual_out is the sum in the residual's type (None without a residual), and what the norm and
+    its backward read; it may be ``residual``, ``y`` may be ``x``.  rstd is fp32, the leading
+    shape of x."""
+    yy, ro, rr, _, _ = _rms_fwd(x, weight, residual, eps, residual_out, y, None, None, rstd, stream, True, False, want_rstd)
+    return yy, ro, rr
+
+
+def rms_norm_quant(x, weight=None, residual=None, eps=1e-5, q=None, scales=None, residual_out=None, stream=None):
+    """q, scales, residual_out = the same norm in 8 bits (``ssd_rms_norm_fwd``): q [..., dim]
+    float8_e4m3fn and scales [..., ceil(dim/128)] fp32, y being about q times the scale of its 128
+    values: what ``matmul_fp8`` reads."""
+    _, ro, _, qq, ss = _rms_fwd(x, weight, residual, eps, residual_out, None, q, scales, None, stream, False, True, False)
+    return qq, ss, ro
+
+
+def rms_norm_bwd(r, dy, rstd, weight=None, dresidual=None, grads=None, workspace=None, stream=None, want_dweight=None):
+    """Gradients of sum(y * dy) + sum(residual_out * dresidual) through ``rms_norm_fwd``
+    (``ssd_rms_norm_bwd``): r is its residual_out (x, where there was no residual), dresidual
+    the gradient of residual_out in r's type or None.  A dict with dx in dy's type, dresidual (the
+    gradient of the residual: the same in r's type, the same tensor where the types are the same;
+    None without a dresidual) and, when ``want_dweight`` (default: if a weight is given), dweight
+    [dim] fp32; ``grads`` may pass those tensors pre-allocated (dx may be ``dy``, dresidual of another
+    type than dx's ``dresidual``)."""
+    if not isinstance(r, torch.Tensor) or r.dim() < 1:
+        raise ValueError("r must be [..., dim]")
+    if not isinstance(dy, torch.Tensor) or r.dtype not in _DTYPES or dy.dtype not in _DTYPES:
+        raise TypeError("r and dy must be float32 or bfloat16 tensors")
+    shape, rtype, dtype, dev = r.shape, r.dtype, dy.dtype, r.device
+    lead, dim = shape[:-1], shape[-1]
+    _check(r, "r")   # on the GPU, contiguous
+    _same(dy, "dy", dtype, shape, dev)
+    _same(rstd, "rstd", torch.float32, lead, dev)
+    _given(weight, "weight", torch.float32, (dim,), dev)
+    _given(dresidual, "dresidual", rtype, shape, dev)
+    params = weight is not None if want_dweight is None else want_dweight
+    rows = r.numel() // dim if dim else 0
+
+    def call(st):
+        out, ws = dict(grads or {}), workspace
+        out["dx"] = _made(out.get("dx"), "dx", dtype, shape, dev)
+        other = out.get("dresidual")
+        if other is not None or (dresidual is not None and rtype is not dtype):
+            out["dresidual"] = other = _made(other, "dresidual", rtype, shape, dev)
+        else:
+            out["dresidual"] = out["dx"] if dresidual is not None else None
+        dw = out.get("dweight")
+        out["dweight"] = dw = _made(dw, "dweight", torch.float32, (dim,), dev) if params or dw is not None else None
+        if ws is not None:
+            _check(ws, "workspace", torch.uint8, None, dev)
+        elif dw is not None:
+            size = _workspace_bytes("ssd_rms_norm_bwd_workspace_size", _RMS_BWD.pack(rows, dim, _DTYPES[dtype], _DTYPES[rtype], *(0,) * 10))
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        a = _RMS_BWD.pack(rows, dim, _DTYPES[dtype], _DTYPES[rtype], r.data_ptr(), dy.data_ptr(), _at(dresidual), rstd.data_ptr(),
+                          _at(weight), out["dx"].data_ptr(), _at(other), _at(dw), _at(ws), 0 if ws is None else ws.numel())
+        return load_library().ssd_rms_norm_bwd(a, st), out
+
+    return _launch("ssd_rms_norm_bwd", dev, stream, call)
+
+
+def matmul_fp8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """out = a w^T + bias of 8-bit numbers with a scale for each block of 128 (``ssd_matmul_fp8``): a
+    [..., k] and w [n, k] float8_e4m3fn, a_scale [..., ceil(k/128)] (as ``rms_norm_quant`` leaves
+    them) and w_scale [ceil(n/128), ceil(k/128)] fp32, bias [n] fp32 or None; out [..., n] fp32 or
+    bf16.  k is a multiple of 16."""
+    if not isinstance(a, torch.Tensor) or a.dim() < 1 or a.dtype is not _F8:
+        raise TypeError("a must be a float8_e4m3fn tensor [..., k]")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be [n, k]")
+    if out_dtype not in _DTYPES:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    dev, lead, k = a.device, a.shape[:-1], a.shape[-1]
+    n, kb = w.shape[0], -(-k // 128)
+    _check(a, "a")   # on the GPU, contiguous
+    _same(a_scale, "a_scale", torch.float32, (*lead, kb), dev)
+    _same(w, "w", _F8, (n, k), dev)
+    _same(w_scale, "w_scale", torch.float32, (-(-n // 128), kb), dev)
+    _given(bias, "bias", torch.float32, (n,), dev)
+    m = a.numel() // k if k else 0
+
+    def call(st):
+        oo = _made(out, "out", out_dtype, (*lead, n), dev)
+        ws = workspace
+        if ws is not None:
+            _check(ws, "workspace", torch.uint8, None, dev)
+        else:
+            need = _workspace_bytes("ssd_matmul_fp8_workspace_size", _MM.pack(m, n, k, _DTYPES[out_dtype], 0, *(0,) * 8))
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        args = _MM.pack(m, n, k, _DTYPES[out_dtype], 0, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _at(bias),
+                        oo.data_ptr(), _at(ws), 0 if ws is None else ws.numel())
+        return load_library().ssd_matmul_fp8(args, st), oo
+
+    return _launch("ssd_matmul_fp8", dev, stream, call)
