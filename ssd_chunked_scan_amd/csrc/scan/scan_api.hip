@@ -63,7 +63,7 @@ Chunking fwd_chunks(const Shape &s)
     Chunking c{};
     const int64_t waves = s.nblk * 4, want = 4096;
     int lq = 6;
-    while (lq < 30 && waves * (s.packed ? ceil_div(s.T, (int64_t)1 << lq) : s.b * ceil_div(s.T, (int64_t)1 << lq)) > want) ++lq;
+    while (lq < 28 && waves * (s.packed ? ceil_div(s.T, (int64_t)1 << lq) : s.b * ceil_div(s.T, (int64_t)1 << lq)) > want) ++lq;
     c.lq = lq;
     if (s.packed) {
         c.cut = s.T > ((int64_t)1 << lq);
@@ -73,20 +73,20 @@ Chunking fwd_chunks(const Shape &s)
     } else {
         c.cut = s.b * waves < 1024 && s.T > 128 && s.T > ((int64_t)1 << lq);
     }
-    if (!c.cut) c.lq = s.packed ? 30 : 31;
+    if (!c.cut) c.lq = kUncut;
     c.nch = s.T > 0 ? ceil_div(s.T, (int64_t)1 << c.lq) : 1;
-    c.slots = s.packed ? (s.T >> c.lq) + s.nseq : s.b * c.nch;
+    c.slots = s.packed ? (c.cut ? (s.T >> c.lq) : 0) + s.nseq : s.b * c.nch;
     return c;
 }
 Chunking bwd_chunks(const Shape &s)
 {
     Chunking c{};
-    c.lq = 6;
-    static_assert(kGradQ == 64, "");
+    c.lq = grad_log2(s.LN);
+    const int64_t q = (int64_t)1 << c.lq;
     c.limit = -1;
     c.cut = true;
-    c.nch = s.T > 0 ? ceil_div(s.T, kGradQ) : 1;
-    c.slots = s.packed ? s.T / kGradQ + s.nseq : s.b * c.nch;
+    c.nch = s.T > 0 ? ceil_div(s.T, q) : 1;
+    c.slots = s.packed ? s.T / q + s.nseq : s.b * c.nch;
     return c;
 }
 
@@ -115,7 +115,7 @@ ssd_status parse_shape(const ssd_selective_scan_args *a, Shape *s)
 }
 
 struct Workspace {
-    size_t plan, S, sum, R, pD, pbias, part, total;
+    size_t plan, order, S, sum, R, pD, pbias, part, total;
 };
 Workspace layout(const Shape &s, const Chunking &c, bool bwd)
 {
@@ -123,7 +123,8 @@ Workspace layout(const Shape &s, const Chunking &c, bool bwd)
     size_t o = 0;
     auto take = [&](size_t n) { const size_t at = o; o = align256(o + n); return at; };
     const size_t states = (size_t)(c.slots * s.D * s.N) * 4, chans = (size_t)(c.slots * s.D) * 4;
-    if (s.packed) w.plan = take((size_t)(s.nseq + 2) * 4);
+    if (s.packed) w.plan = take((size_t)(s.nseq + 1) * 4);
+    if (s.packed && !bwd) w.order = take((size_t)(s.nseq + 1) * 4);
     if (c.cut) {
         w.S = take(states);
         w.sum = take(chans);
@@ -226,10 +227,15 @@ template <typename F> void with_lanes(int LN, F &&f)
     else f(Int<16>{});
 }
 
-void plan(const Shape &s, const Chunking &c, const ssd_selective_scan_args *a, char *ws, const Workspace &w, hipStream_t st)
+// The segments' first tokens; for the forward also their order and whether they are cut.
+void plan(const Shape &s, const Chunking &c, const ssd_selective_scan_args *a, ScanArgs &k, char *ws, const Workspace &w, bool order, hipStream_t st)
 {
-    hipLaunchKernelGGL(k_scan_plan, dim3(1), dim3(kPlanThreads), 0, st, a->seq_idx, reinterpret_cast<int32_t *>(ws + w.plan),
-                       (int)s.T, (int)s.nseq, c.lq, (int)(c.limit < INT32_MAX ? c.limit : INT32_MAX));
+    hipLaunchKernelGGL(k_scan_starts, dim3((unsigned)(s.T > 0 ? ceil_div(s.T, 4 * kThreads) : 1)), dim3(s.T > 0 ? kThreads : 1), 0, st, a->seq_idx,
+                       reinterpret_cast<int32_t *>(ws + w.plan), (int)s.T, (int)s.nseq);
+    if (!order) return;
+    int32_t *o = reinterpret_cast<int32_t *>(ws + w.order);
+    hipLaunchKernelGGL(k_scan_plan, dim3(1), dim3(kPlanThreads), 0, st, k, o, c.lq, (int)(c.limit < INT32_MAX ? c.limit : INT32_MAX));
+    k.order = o;
 }
 
 template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_selective_scan_args *a, hipStream_t st)
@@ -240,7 +246,7 @@ template <typename E> ssd_status fwd_typed(const Shape &s, const ssd_selective_s
     ScanArgs k = scan_args(s, c, a, ws, w);
     k.y = a->y;
     k.s1 = a->final_states;
-    if (s.packed) plan(s, c, a, ws, w, st);
+    if (s.packed) plan(s, c, a, k, ws, w, true, st);
     const dim3 grid((unsigned)(c.slots * s.nblk)), block(kThreads);
     with_lanes(s.LN, [&](auto ln) {
         constexpr int LN = decltype(ln)::value;
@@ -272,7 +278,7 @@ ssd_status bwd_typed(const Shape &s, const ssd_selective_scan_args *a, const ssd
     k.pD = reinterpret_cast<float *>(ws + w.pD);
     k.pbias = reinterpret_cast<float *>(ws + w.pbias);
     k.part = reinterpret_cast<float *>(ws + w.part);
-    if (s.packed) plan(s, c, a, ws, w, st);
+    if (s.packed) plan(s, c, a, k, ws, w, false, st);
     const dim3 grid((unsigned)(c.slots * s.nblk)), block(kThreads);
     const int blocks = (int)ceil_div(s.D * s.N, kThreads);
     with_lanes(s.LN, [&](auto ln) {

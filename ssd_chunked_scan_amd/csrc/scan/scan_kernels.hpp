@@ -28,7 +28,12 @@ namespace ssd {
 namespace sscan {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kGradQ = 64;    // tokens of a chunk of the backward
+// Tokens of a chunk of the backward (their Delta and x are in LDS, for 256 / LN channels).
+constexpr int grad_log2(int LN) { return LN == 1 ? 4 : LN == 2 || LN == 16 ? 5 : 6; }
+template <int LN> constexpr int kGradQ = 1 << grad_log2(LN);
+
+constexpr int kUncut = 31;      // log2 of the chunk of rows that are not cut
+constexpr int kRanked = 1024;   // rows that are put in order
 
 struct ScanArgs {
     const void *x, *dt, *B, *C, *z;
@@ -37,7 +42,8 @@ struct ScanArgs {
     const float *s0;               // initial states
     float *s1;                     // final states
     void *y;
-    const int32_t *plan;           // packed streams: first token of every segment and of none, log2 of the chunk
+    const int32_t *plan;           // packed streams: first token of every segment, T
+    const int32_t *order;          // rows by length, then log2 of the chunk (NULL: lq), where the device decides
     float *S, *sum;                // chunk states [slots][D][N], sums of Delta [slots][D]
     const void *dy;
     const float *d1;               // gradient of the final states
@@ -62,7 +68,7 @@ template <int LN, int I> __device__ __forceinline__ float from_lane(float v)
     }
 }
 // The sum over the LN lanes of a channel, in all of them.
-constexpr int kDppRowMirror = 0x140;
+constexpr int kDppRowMirror = 0x140, kDppRowRor4 = 0x124;
 template <int LN> __device__ __forceinline__ float lane_sum(float v)
 {
     if constexpr (LN >= 2) v += dpp_mov<kDppQuadXor1>(v);
@@ -79,12 +85,27 @@ template <int N, typename F> __device__ __forceinline__ void unrolled(F &&f)
     }
 }
 
+// A barrier for what is in LDS: accesses of global memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 // One element of a row's buffer, zero past its end.
 template <typename E> __device__ __forceinline__ float bload_el(__amdgpu_buffer_rsrc_t r, uint32_t off)
 {
     if constexpr (sizeof(E) == 2)
         return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0) << 16);
     else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+// The same to memory, rounded; lost past the buffer's end.  Stores without branches around them leave
+// the number of outstanding accesses known, so a wait for loads issued before them is not one for the stores.
+template <typename E> __device__ __forceinline__ void bstore_el(__amdgpu_buffer_rsrc_t r, uint32_t off, float v)
+{
+    if constexpr (sizeof(E) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, from_float<E>(v)), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
 }
 // `tokens` tokens of a tensor from token t0 on, `width` elements each.
 template <typename E>
@@ -106,22 +127,30 @@ struct Slot {
     int len;             // tokens of the row
     bool last;
 };
+// The first token of segment i; in [0, T] whatever an invalid stream has left there.
+__device__ __forceinline__ int start_of(const ScanArgs &a, int i)
+{
+    const int v = a.plan[i];
+    return v < 0 ? 0 : v > a.T ? a.T : v;
+}
 __device__ __forceinline__ Slot slot_at(const ScanArgs &a, int c)
 {
     Slot s;
     int lq = a.lq, start = 0;
     if (a.plan) {
-        lq = a.plan[a.rows + 1];
+        if (a.order) lq = a.order[a.rows];
         int lo = 0, hi = a.rows - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)(a.plan[mid] >> lq) + mid <= c) lo = mid;
-            else hi = mid - 1;
-        }
+        if (lq == kUncut) lo = c < a.rows && a.rows <= kRanked ? a.order[c] : c < a.rows ? c : hi;
+        else
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((int64_t)(start_of(a, mid) >> lq) + mid <= c) lo = mid;
+                else hi = mid - 1;
+            }
         s.row = lo;
-        start = a.plan[lo];
-        s.len = a.plan[lo + 1] - start;
-        s.j = c - ((start >> lq) + lo);
+        start = start_of(a, lo);
+        s.len = start_of(a, lo + 1) - start;
+        s.j = lq == kUncut ? (c < a.rows ? 0 : -1) : c - ((start >> lq) + lo);
         s.t0 = start;
     } else {
         s.row = c / a.nch;
@@ -136,47 +165,52 @@ __device__ __forceinline__ Slot slot_at(const ScanArgs &a, int c)
     return s;
 }
 
-// start[i]: the first token of segment i, start[nseq] = T, for non-decreasing ids; the chunk
-// length.  Any stream leaves start in [0, T] (and what it cannot mean out).  One workgroup, 16
-// tokens a thread in flight.
-constexpr int kPlanThreads = 1024;
-__global__ __launch_bounds__(kPlanThreads) void k_scan_plan(const int32_t *__restrict__ seq_idx, int32_t *__restrict__ start,
-                                                            int T, int nseq, int lq_long, int limit)
+// start[i]: the first token of segment i (or of the next one that has any), start[nseq] = T, for non-decreasing
+// ids; four tokens a thread.
+__global__ __launch_bounds__(kThreads) void k_scan_starts(const int32_t *__restrict__ seq_idx, int32_t *__restrict__ start, int T, int nseq)
 {
-    __shared__ int most;
+    const int t0 = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc_n(seq_idx, T * 4);
+    int id[5];
+    id[0] = t0 > 0 && t0 < T ? (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * t0 - 4, 0, 0) : -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) id[e + 1] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * (t0 + e), 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = t0 + e;
+        if (t >= T) break;
+        const int hi = id[e + 1] < nseq ? id[e + 1] : nseq - 1;
+        for (int i = id[e] < -1 ? 0 : id[e] + 1; i <= hi; ++i) start[i] = t;   // this id's, and those of ids left out
+        if (t == T - 1)
+            for (int i = hi < -1 ? 0 : hi + 1; i <= nseq; ++i) start[i] = T;
+    }
+    if (T == 0)
+        for (int64_t i = t0; i <= nseq; i += 1) start[i] = 0;
+}
+// Where the device decides: rows in the order of their lengths, the longest first (a long one that starts last
+// would run alone at the end), and whether any is long enough beside the whole to be cut.
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void k_scan_plan(ScanArgs a, int32_t *__restrict__ order, int lq_long, int limit)
+{
+    __shared__ int most, len[kRanked];
     const int tid = threadIdx.x;
     if (tid == 0) most = 0;
-    // ids above the last one start at T; the others are written over below
-    for (int i = tid; i <= nseq; i += kPlanThreads) start[i] = T;
-    __syncthreads();
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc_n(seq_idx, T * 4);   // past the end: 0, not used
-    constexpr int U = 4;
-    for (int tb = 0; tb < T; tb += U * 4 * kPlanThreads) {
-        int id[U][5];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = tb + (u * kPlanThreads + tid) * 4;
-            id[u][0] = t > 0 && t < T ? (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * t - 4, 0, 0) : -1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) id[u][e + 1] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, 4u * (t + e), 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = tb + (u * kPlanThreads + tid) * 4 + e;
-                if (t >= T) continue;
-                const int lo = id[u][e] < -1 ? -1 : id[u][e], hi = id[u][e + 1] < nseq ? id[u][e + 1] : nseq - 1;
-                for (int i = lo + 1; i <= hi; ++i) start[i] = t;   // this id's, and those of ids left out
-            }
-    }
     __syncthreads();
     int m = 0;
-    for (int i = tid; i < nseq; i += kPlanThreads) m = max(m, start[i + 1] - start[i]);
+    for (int i = tid; i < a.rows; i += kPlanThreads) {
+        const int n = start_of(a, i + 1) - start_of(a, i);
+        m = max(m, n);
+        if (a.rows <= kRanked) len[i] = n;
+    }
     atomicMax(&most, m);
     __syncthreads();
-    // rows that are short beside the whole need no cutting
-    if (tid == 0) start[nseq + 1] = most <= limit ? 30 : lq_long;
+    if (a.rows <= kRanked && tid < a.rows) {
+        const int n = len[tid];
+        int rank = 0;
+        for (int o = 0; o < a.rows; ++o) rank += len[o] > n || (len[o] == n && o < tid) ? 1 : 0;
+        order[rank] = tid;
+    }
+    if (tid == 0) order[a.rows] = most <= limit ? kUncut : lq_long;
 }
 
 // ---------------------------------------------------------------------------
@@ -236,7 +270,14 @@ template <int LN, int NL> __device__ __forceinline__ void put_keys(float *dst, c
     }
 }
 
-__device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplus_f(raw) : raw; }
+// softplus as softplus_f, with the hardware's reciprocal (1 ulp) for its quotient: once for every channel and token.
+__device__ __forceinline__ float step_size(float raw, int softplus)
+{
+    if (!softplus) return raw;
+    const float u = exp2_(-fabsf(raw) * kLog2e), w = 1.f + u;
+    const float l1p = w == 1.f ? u : __builtin_amdgcn_logf(w) * kLn2 * (u * __builtin_amdgcn_rcpf(w - 1.f));
+    return fmaxf(raw, 0.f) + l1p;
+}
 
 // Forward over a chunk.  MODE 0: y and the final states, from the state that enters the chunk.
 // MODE 1: the chunk's end state from a zero start into S, and the sum of its Delta.  MODE 2:
@@ -293,7 +334,6 @@ __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
         if constexpr (HASC) fetch_keys<E, LN, NL>(a.C, t, a.Cs, p.g, a.N, left, kc);
     };
     if (s.count > 0) fetch(0);
-    E *yp = static_cast<E *>(a.y);
     for (int t1 = 0, b = 0; t1 < s.count; t1 += TT, b ^= 1) {
         put_keys<LN, NL>(keys[b][0], kb, TT * NP);
         if constexpr (HASC) put_keys<LN, NL>(keys[b][HASC ? 1 : 0], kc, TT * NP);
@@ -308,7 +348,9 @@ __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
             if constexpr (HASG) gv[q] = HASZ ? gr[q] * silu(zv[q]) : gr[q];
         }
         if (t1 + TT < s.count) fetch(t1 + TT);
-        __syncthreads();   // the tile's keys are there, and the tile before last is done with
+        const __amdgpu_buffer_rsrc_t ry =
+            token_rsrc<E>(MODE == 0 ? a.y : a.x, s.t0 + t1, a.D, MODE != 0 ? 0 : s.count - t1 < TT ? s.count - t1 : TT, a.D);
+        lds_barrier();   // the tile's keys are there, and the tile before last is done with
         const float *kB = keys[b][0] + n0, *kC = keys[b][HASC ? 1 : 0] + n0;
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
@@ -338,10 +380,9 @@ __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
                 }
             });
             if constexpr (MODE == 0) {
-                const int t = t1 + q * LN + p.j;
                 y += skip * xv[q];
                 if constexpr (HASZ) y *= silu(zv[q]);
-                if (t < s.count && p.live) yp[(s.t0 + t) * a.D + p.d] = from_float<E>(y);
+                bstore_el<E>(ry, p.live ? (uint32_t)(((q * LN + p.j) * a.D + p.d) * (int)sizeof(E)) : kOffNone, y);
             } else total += dl[q];
         }
     }
@@ -366,9 +407,9 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
     const int64_t DN = (int64_t)a.D * a.N, e = (int64_t)(blockIdx.x - row * blocks) * kThreads + threadIdx.x;
     int lq = a.lq, len = a.T, c0 = row * a.nch;
     if (a.plan) {
-        lq = a.plan[a.rows + 1];
-        const int start = a.plan[row];
-        len = a.plan[row + 1] - start;
+        if (a.order) lq = a.order[a.rows];
+        const int start = start_of(a, row);
+        len = start_of(a, row + 1) - start;
         c0 = (start >> lq) + row;
     }
     const int n = len <= 0 ? 0 : (int)(((int64_t)len + ((int64_t)1 << lq) - 1) >> lq);
@@ -413,29 +454,31 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
     }
 }
 
-// Every gradient of a chunk of kGradQ tokens.  The states at the start of each SC tokens first
-// (into LDS); then, from the last SC tokens to the first, the states in between again and the
-// way back through them,
+// Every gradient of a chunk.  Delta and x of the whole chunk go to LDS first, then the states at the start
+// of each 8 tokens; then, from the last 8 tokens to the first, the states in between again and the way back
+// through them,
 //
 //   g_t = e^{Delta_t+1 A} g_t+1 + C_t dy_t,   dB_t = sum over d of Delta x g_t,  dC_t = sum over d of dy h_t,
 //   dx = Delta (B . g) + D dy,  dDelta = x (B . g) + sum_n A e^{Delta A} g h_t-1,  dA = sum_t Delta e^{Delta A} g h_t-1
 //
-// with dy the gradient before the gate.  dB and dC are summed over the workgroup's channels
-// here and over tiles of channels by k_scan_keys.
+// with dy the gradient before the gate.  Over the four rows of 16 lanes the sum over channels of dB and dC is a
+// product with a one-hot row on the matrix cores, which are idle here: v_mfma_f32_16x16x4 adds the four
+// lanes of a column into row t (dB) or 8 + t (dC) of an accumulator that 8 tokens share; over the lanes of a
+// row and over the waves it is taken once for the 8 tokens.  Over tiles of channels k_scan_keys adds it up.
 template <typename E, int LN, bool GATE>
-__global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
+__global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
 {
-    constexpr int NP = 4 * LN, SC = LN <= 8 ? 8 : 16, GS = SC / LN, NSUB = kGradQ / SC, CB = kThreads / LN;
-    constexpr int NL = (kGradQ * NP + kThreads - 1) / kThreads;
-    __shared__ float keys[2][kGradQ * NP];
+    constexpr int Q = kGradQ<LN>, NP = 4 * LN, SC = 8, TL = LN < SC ? LN : SC, GS = SC / TL, NSUB = Q / SC, SL = kThreads / LN;
+    constexpr int NL = (Q * NP + kThreads - 1) / kThreads, NT = Q * SL / kThreads;
+    __shared__ float keys[2][Q * NP];
     __shared__ floatx4 hs[NSUB][kThreads];
-    __shared__ float red[4][SC][2][NP];
+    __shared__ float red[2][4][SC][2][NP];
+    __shared__ float sdl[Q * SL], sx[Q * SL];
     const int c = blockIdx.x / a.nblk, blk = blockIdx.x - c * a.nblk;
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    (void)CB;
     const Slot s = slot_at(a, c);
     const Place p = place_of<LN>(a, blk);
-    const int n0 = 4 * p.j;
+    const int n0 = 4 * p.j, jt = p.j % TL, slot = tid / LN;
     const int64_t dn = (int64_t)p.d * a.N, DN = (int64_t)a.D * a.N;
     if (s.count <= 0) {
         const float none[4] = {0.f, 0.f, 0.f, 0.f};
@@ -450,6 +493,12 @@ __global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
         if (p.j == 0) a.pD[(int64_t)c * a.D + p.d] = a.pbias[(int64_t)c * a.D + p.d] = 0.f;
         return;
     }
+    const __amdgpu_buffer_rsrc_t rd = token_rsrc<E>(a.dt, s.t0, a.dts, s.count, a.D),
+                                 rz = token_rsrc<E>(GATE ? a.z : a.x, s.t0, GATE ? a.zs : a.xs, s.count, a.D),
+                                 rg = token_rsrc<E>(a.dy, s.t0, a.D, s.count, a.D), wx = token_rsrc<E>(a.dx, s.t0, a.D, s.count, a.D),
+                                 wd = token_rsrc<E>(a.ddt, s.t0, a.D, s.count, a.D),
+                                 wz = token_rsrc<E>(GATE ? a.dz : a.dx, s.t0, a.D, s.count, a.D),
+                                 wp = token_rsrc<float>(a.part + blk * (2 * NP), s.t0, (int64_t)a.nblk * (2 * NP), s.count, 2 * NP);
     float h[4] = {0.f, 0.f, 0.f, 0.f}, g[4] = {0.f, 0.f, 0.f, 0.f}, A2[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.live) {
         if (s.j > 0) load_state(a.S + c * DN + dn, n0, a.N, h);
@@ -461,59 +510,80 @@ __global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
 #pragma unroll
     for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
     const float bias = a.bias ? a.bias[p.d] : 0.f, skip = a.D_ ? a.D_[p.d] : 0.f;
+    const int nsub = (s.count + SC - 1) / SC;
+    const float *kB = keys[0] + n0, *kC = keys[1] + n0;
+    // the first tokens of the way back are on their way meanwhile
+    float nraw[GS], nz[GS], ng[GS];
+    auto fetch = [&](int u) {
+#pragma unroll
+        for (int q = 0; q < GS; ++q) {
+            const int t = u * SC + q * TL + jt;
+            nraw[q] = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + p.d) * (int)sizeof(E)));
+            ng[q] = bload_el<E>(rg, p.live ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone);
+            nz[q] = GATE ? bload_el<E>(rz, p.live ? (uint32_t)((t * (int)a.zs + p.d) * (int)sizeof(E)) : kOffNone) : 0.f;
+        }
+    };
+    fetch(nsub - 1);
+    // LDS position of a token and channel: the TL tokens that a wave's lanes read together lie in different banks
+    auto place = [&](int t, int ch) { return t * SL + (ch ^ ((t % TL) * (64 / LN) & (SL - 1))); };
     {
-        float kb[NL], kc[NL];
+        const __amdgpu_buffer_rsrc_t rx = token_rsrc<E>(a.x, s.t0, a.xs, s.count, a.D);
+        const int ch = tid % SL, cc = (blk - p.g * a.bpg) * SL + ch, dd = p.g * a.per + (cc < a.per ? cc : a.per - 1);
+        const float b = a.bias ? a.bias[dd] : 0.f;
+        float xr[NT], dr[NT], kb[NL], kc[NL];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int t = i * LN + tid / SL;
+            xr[i] = bload_el<E>(rx, cc < a.per ? (uint32_t)((t * (int)a.xs + dd) * (int)sizeof(E)) : kOffNone);
+            dr[i] = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + dd) * (int)sizeof(E)));
+        }
         fetch_keys<E, LN, NL>(a.B, s.t0, a.Bs, p.g, a.N, s.count, kb);
         fetch_keys<E, LN, NL>(a.C, s.t0, a.Cs, p.g, a.N, s.count, kc);
-        put_keys<LN, NL>(keys[0], kb, kGradQ * NP);
-        put_keys<LN, NL>(keys[1], kc, kGradQ * NP);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int t = i * LN + tid / SL;
+            // none for a lane without a channel, none past the chunk
+            sdl[place(t, ch)] = t < s.count && cc < a.per ? step_size(dr[i] + b, a.softplus) : 0.f;
+            sx[place(t, ch)] = xr[i];
+        }
+        put_keys<LN, NL>(keys[0], kb, Q * NP);
+        put_keys<LN, NL>(keys[1], kc, Q * NP);
     }
-    const __amdgpu_buffer_rsrc_t rx = token_rsrc<E>(a.x, s.t0, a.xs, s.count, a.D),
-                                 rd = token_rsrc<E>(a.dt, s.t0, a.dts, s.count, a.D),
-                                 rz = token_rsrc<E>(GATE ? a.z : a.x, s.t0, GATE ? a.zs : a.xs, s.count, a.D),
-                                 rg = token_rsrc<E>(a.dy, s.t0, a.D, s.count, a.D);
-    const int nsub = (s.count + SC - 1) / SC;
-    __syncthreads();
-    const float *kB = keys[0] + n0, *kC = keys[1] + n0;
-    // a token's Delta and x of this lane (none for a lane without a channel, none past the chunk)
-    auto step_of = [&](int t, float &raw, float &x, float &dl) {
-        const bool in = t < s.count && p.live;
-        raw = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + p.d) * (int)sizeof(E))) + bias;
-        x = bload_el<E>(rx, in ? (uint32_t)((t * (int)a.xs + p.d) * (int)sizeof(E)) : kOffNone);
-        dl = in ? step_size(raw, a.softplus) : 0.f;
-    };
+    lds_barrier();
     for (int u = 0; u < nsub; ++u) {
         hs[u][tid] = floatx4{h[0], h[1], h[2], h[3]};
         if (u == nsub - 1) break;
-        float raw, x[GS], dl[GS];
-#pragma unroll
-        for (int q = 0; q < GS; ++q) step_of(u * SC + q * LN + p.j, raw, x[q], dl[q]);
+        float dxs[GS], dl[GS];
 #pragma unroll
         for (int q = 0; q < GS; ++q) {
-            const float dx = dl[q] * x[q];
-            unrolled<LN>([&](auto ic) {
-                constexpr int i = decltype(ic)::value;
-                const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dx);
-                const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + q * LN + i) * NP);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = exp2_(di * A2[k]) * h[k] + dxi * B[k];
-            });
+            const int at = place(u * SC + q * TL + jt, slot);
+            dl[q] = sdl[at];
+            dxs[q] = dl[q] * sx[at];
         }
+        unrolled<SC>([&](auto tc) {
+            constexpr int t = decltype(tc)::value, q = t / TL, i = t % TL;
+            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]);
+            const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = exp2_(di * A2[k]) * h[k] + dxi * B[k];
+        });
     }
     float dA[4] = {0.f, 0.f, 0.f, 0.f}, sD = 0.f, sb = 0.f;
     for (int u = nsub - 1; u >= 0; --u) {
         float raw[GS], x[GS], dl[GS], zv[GS], go[GS], dy[GS], dxs[GS], ys[GS];
 #pragma unroll
         for (int q = 0; q < GS; ++q) {
-            const int t = u * SC + q * LN + p.j;
-            step_of(t, raw[q], x[q], dl[q]);
-            go[q] = bload_el<E>(rg, p.live ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone);
-            if constexpr (GATE) zv[q] = bload_el<E>(rz, (uint32_t)((t * (int)a.zs + p.d) * (int)sizeof(E)));
+            const int at = place(u * SC + q * TL + jt, slot);
+            dl[q] = sdl[at];
+            x[q] = sx[at];
+            raw[q] = nraw[q] + bias;
+            go[q] = ng[q];
+            zv[q] = nz[q];
             dy[q] = GATE ? go[q] * silu(zv[q]) : go[q];
-            if (!p.live) dy[q] = 0.f;
             dxs[q] = dl[q] * x[q];
             ys[q] = 0.f;
         }
+        fetch(u > 0 ? u - 1 : 0);
         float hh[SC + 1][4], ee[SC][4];
         {
             const floatx4 v = hs[u][tid];
@@ -521,12 +591,12 @@ __global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
             for (int k = 0; k < 4; ++k) hh[0][k] = v[k];
         }
         unrolled<SC>([&](auto tc) {
-            constexpr int t = decltype(tc)::value, q = t / LN, i = t % LN;
-            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]);
+            constexpr int t = decltype(tc)::value, q = t / TL, i = t % TL;
             const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
-            float acc = 0.f;
             floatx4 C;
             if constexpr (GATE) C = *reinterpret_cast<const floatx4 *>(kC + (u * SC + t) * NP);
+            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]);
+            float acc = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 ee[t][k] = exp2_(di * A2[k]);
@@ -535,21 +605,25 @@ __global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
             }
             if constexpr (GATE) {
                 acc = lane_sum<LN>(acc);
-                ys[q] = p.j == i ? acc : ys[q];
+                ys[q] = jt == i ? acc : ys[q];
             }
         });
         float along[GS], dd[GS];
+        floatx4 keysum[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) keysum[k] = floatx4{0.f, 0.f, 0.f, 0.f};
         unrolled<SC>([&](auto tc) {
-            constexpr int t = SC - 1 - decltype(tc)::value, q = t / LN, i = t % LN;
-            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]), dyi = from_lane<LN, i>(dy[q]);
+            constexpr int t = SC - 1 - decltype(tc)::value, q = t / TL, i = t % TL;
             const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
             const floatx4 C = *reinterpret_cast<const floatx4 *>(kC + (u * SC + t) * NP);
-            float al = 0.f, de = 0.f, vB[4], vC[4];
+            const float di = from_lane<LN, i>(dl[q]), dxi = from_lane<LN, i>(dxs[q]), dyi = from_lane<LN, i>(dy[q]);
+            const float to = (lane & 15) == t + (lane < 32 ? 0 : 8) ? 1.f : 0.f;
+            float al = 0.f, de = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 g[k] += dyi * C[k];
-                vC[k] = dyi * hh[t + 1][k];
-                vB[k] = dxi * g[k];
+                const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(dxi * g[k]), __float_as_uint(dyi * hh[t + 1][k]), false, false);
+                keysum[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(to, __uint_as_float(v[0]) + __uint_as_float(v[1]), keysum[k], 0, 0, 0);
                 al += g[k] * B[k];
                 g[k] *= ee[t][k];
                 const float gh = g[k] * hh[t][k];
@@ -558,52 +632,54 @@ __global__ __launch_bounds__(kThreads) void k_scan_grad(ScanArgs a)
             }
             al = lane_sum<LN>(al);
             de = lane_sum<LN>(de);
-            along[q] = i == LN - 1 || p.j == i ? al : along[q];
-            dd[q] = i == LN - 1 || p.j == i ? de : dd[q];
-            // over the wave's channels
+            along[q] = i == TL - 1 || jt == i ? al : along[q];
+            dd[q] = i == TL - 1 || jt == i ? de : dd[q];
+        });
+        // keysum[k][r]: row 4 (lane / 16) + r of column lane % 16; over the columns of one state
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int m = LN; m < 64; m <<= 1) {
-                    vB[k] += __shfl_xor(vB[k], m);
-                    vC[k] += __shfl_xor(vC[k], m);
-                }
+                v[k] = keysum[k][r];
+                if constexpr (LN <= 8) v[k] += dpp_mov<kDppRowRor8>(v[k]);
+                if constexpr (LN <= 4) v[k] += dpp_mov<kDppRowRor4>(v[k]);
+                if constexpr (LN <= 2) v[k] += dpp_mov<kDppQuadXor2>(v[k]);
+                if constexpr (LN == 1) v[k] += dpp_mov<kDppQuadXor1>(v[k]);
             }
-            if (lane < LN) {
-                *reinterpret_cast<floatx4 *>(&red[wv][t][0][n0]) = floatx4{vB[0], vB[1], vB[2], vB[3]};
-                *reinterpret_cast<floatx4 *>(&red[wv][t][1][n0]) = floatx4{vC[0], vC[1], vC[2], vC[3]};
-            }
-        });
-        __syncthreads();
-        for (int e = tid; e < SC * 2 * NP; e += kThreads) {
-            const int t = u * SC + e / (2 * NP);
-            const float *r = &red[0][0][0][0] + e;
-            constexpr int W = SC * 2 * NP;
-            if (t < s.count) a.part[((s.t0 + t) * a.nblk + blk) * (2 * NP) + e % (2 * NP)] = (r[0] + r[W]) + (r[2 * W] + r[3 * W]);
+            const int row = 4 * (lane >> 4) + r;
+            if ((lane & 15) < LN) *reinterpret_cast<floatx4 *>(&red[u & 1][wv][row & 7][row >> 3][n0]) = floatx4{v[0], v[1], v[2], v[3]};
         }
-        __syncthreads();
 #pragma unroll
         for (int q = 0; q < GS; ++q) {
-            const int t = u * SC + q * LN + p.j;
-            if (t >= s.count || !p.live) continue;
-            const int64_t at = (s.t0 + t) * a.D + p.d;
+            const int t = u * SC + q * TL + jt;
+            const uint32_t at = p.live && p.j < TL ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone;
             float dd_ = x[q] * along[q] + kLn2 * dd[q];
             if (a.softplus) dd_ *= __builtin_amdgcn_rcpf(1.f + exp2_(-raw[q] * kLog2e));
-            static_cast<E *>(a.dx)[at] = from_float<E>(dl[q] * along[q] + dy[q] * skip);
-            static_cast<E *>(a.ddt)[at] = from_float<E>(dd_);
-            sD += dy[q] * x[q];
-            sb += dd_;
+            bstore_el<E>(wx, at, dl[q] * along[q] + dy[q] * skip);
+            bstore_el<E>(wd, at, dd_);
+            // tokens past the chunk have neither
+            const bool in = t < s.count && p.j < TL;
+            sD += in ? dy[q] * x[q] : 0.f;
+            sb += in ? dd_ : 0.f;
             if constexpr (GATE) {
                 const float sg = __builtin_amdgcn_rcpf(1.f + exp2_(-zv[q] * kLog2e));
-                static_cast<E *>(a.dz)[at] = from_float<E>(go[q] * (ys[q] + skip * x[q]) * (sg * (1.f + zv[q] * (1.f - sg))));
+                bstore_el<E>(wz, at, go[q] * (ys[q] + skip * x[q]) * (sg * (1.f + zv[q] * (1.f - sg))));
             }
         }
+        lds_barrier();   // once for 8 tokens: the next ones' sums go to the other half
+        for (int e = tid; e < SC * 2 * NP; e += kThreads) {
+            const int t = u * SC + e / (2 * NP);
+            const float *r = &red[u & 1][0][0][0][0] + e;
+            constexpr int W = SC * 2 * NP;
+            bstore_el<float>(wp, (uint32_t)(t * a.nblk * (2 * NP) + e % (2 * NP)) * 4u, (r[0] + r[W]) + (r[2 * W] + r[3 * W]));
+        }
     }
+    sD = lane_sum<LN>(sD);
+    sb = lane_sum<LN>(sb);
     if (!p.live) return;
     if (s.j == 0 && a.d0) store_state(a.d0 + s.row * DN + dn, n0, a.N, g);
     store_state(a.S + c * DN + dn, n0, a.N, dA);   // this workgroup alone has read it
-    sD = lane_sum<LN>(sD);
-    sb = lane_sum<LN>(sb);
     if (p.j == 0) {
         a.pD[(int64_t)c * a.D + p.d] = sD;
         a.pbias[(int64_t)c * a.D + p.d] = sb;
