@@ -31,10 +31,11 @@ FLAGS = [
 ]
 
 
-# The gated delta rule's kernels and the selective scan's gradients hold their products' accumulators in the general
-# registers; given a whole register file the compiler would put them into the
-# accumulation registers and copy them out for every use.
-EXTRA = {"gdr_api.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "scan_api.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# These kernels hold their products' accumulators in the general registers; given a
+# whole register file the compiler would put them into the accumulation registers and
+# copy them out for every use.
+_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"gdr_api.hip": _IN_VGPRS, "scan_api.hip": _IN_VGPRS, "mm_api.hip": _IN_VGPRS}
 
 
 def _run(cmd, verbose: bool) -> None:

@@ -21,7 +21,7 @@ constexpr int64_t kMaxInner = (int64_t)1 << 22;   // a tile's rows are addressed
 constexpr int64_t kMaxSide = ((int64_t)1 << 31) - 512;
 
 struct Plan {
-    int bm, bn;          // tile; bn 128 with few rows
+    int bm, bn;          // tile
     bool few;
     int64_t tm, tn, kb, per, shares;
 };
@@ -43,9 +43,10 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int dtype)
     if (dtype == SSD_DTYPE_BF16 && m > 64 && tiles(256, 256) >= 256) return p;
     if (m > 64 && tiles(128, 128) >= 192) return p;
     p.few = true;
-    tiles(m <= 16 ? 16 : m <= 32 ? 32 : 64, 128);
-    // two workgroups a CU, at least four blocks each
-    const int64_t want = ceil_div(512, p.tm * p.tn), most = ceil_div(p.kb, 4);
+    const int64_t groups = tiles(m <= 16 ? 16 : m <= 32 ? 32 : 64, 64);
+    // where the tiles are too few to keep half of the CUs loading, k is shared out over workgroups, at least four blocks
+    // each
+    const int64_t want = groups >= 128 ? 1 : ceil_div(256, groups), most = ceil_div(p.kb, 4);
     const int64_t shares = want < most ? want : most;
     p.per = ceil_div(p.kb, shares);
     p.shares = ceil_div(p.kb, p.per);
@@ -61,9 +62,12 @@ ssd_status check_dims(const ssd_matmul_fp8_args *a, Plan *p)
     if (a->m < 0 || a->n < 0 || a->k < 1 || a->k % 16 != 0 || a->m > kMaxSide || a->n > kMaxSide || a->k > kMaxInner) return SSD_ERR_BAD_SHAPE;
     if (a->m * a->k > most || a->n * a->k > most || (a->m > 0 && a->n > most / a->m)) return SSD_ERR_BAD_SHAPE;
     *p = plan_of(a->m, a->n, a->k, a->dtype);
-    if (p->tm > 0 && p->tn > 0 && p->tm > (kMaxGroups / 2) / p->tn / p->shares) return SSD_ERR_BAD_SHAPE;
+    if (p->tm > 0 && p->tn > 0 && p->tm > (p->few ? kMaxGroups / 2 / p->shares : INT32_MAX / 2) / p->tn) return SSD_ERR_BAD_SHAPE;
     return SSD_OK;
 }
+
+// Workgroups of a tiled product: what the card holds at a time (LDS: one of 256 a CU, two of 128).
+unsigned resident(const Plan &p, int64_t most) { return (unsigned)(p.tm * p.tn < most ? p.tm * p.tn : most); }
 
 template <typename O> void run(const ssd_matmul_fp8_args *a, const Plan &p, hipStream_t st)
 {
@@ -86,10 +90,10 @@ template <typename O> void run(const ssd_matmul_fp8_args *a, const Plan &p, hipS
     if (!p.few) {
         if constexpr (std::is_same<O, bf16>::value)
             if (p.bm == 256) {
-                hipLaunchKernelGGL((k_mm_tile<O, 256, 256, 2, 4>), grid, dim3(512), 0, st, k);
+                hipLaunchKernelGGL((k_mm_tile<O, 256, 256, 2, 4>), dim3(resident(p, 256)), dim3(512), 0, st, k);
                 return;
             }
-        hipLaunchKernelGGL((k_mm_tile<O, 128, 128, 2, 2>), grid, dim3(256), 0, st, k);
+        hipLaunchKernelGGL((k_mm_tile<O, 128, 128, 2, 2>), dim3(resident(p, 512)), dim3(256), 0, st, k);
         return;
     }
     auto few = [&](auto mi) {

@@ -55,7 +55,7 @@ def check(case, dtype="fp32", bias=False):
 
 
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 100])
-@pytest.mark.parametrize("n,k", [(128, 128), (200, 400), (1531, 1040), (2560, 2560)])
+@pytest.mark.parametrize("n,k", [(128, 128), (200, 400), (1531, 1040), (2560, 2560), (8200, 3840)])
 def test_few_rows(m, n, k):
     check(draw(m + n, m, n, k), "bf16" if m % 2 else "fp32")
 
@@ -68,7 +68,8 @@ def test_odd_columns_and_short_inner(n, k):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("m,n,k", [(2048, 2048, 256), (2000, 2049, 400), (1999, 1999, 16), (4096, 4096, 128), (4100, 3999, 272), (4095, 4097, 1040)])
+@pytest.mark.parametrize("m,n,k", [(2048, 2048, 256), (2000, 2049, 400), (1999, 1999, 16), (4096, 4096, 128), (4100, 3999, 272), (4095, 4097, 1040), (4000, 4104, 272),
+                                   (2050, 2056, 128), (4608, 4608, 384), (20000, 300, 512)])
 def test_tiles(dtype, m, n, k):
     check(draw(m, m, n, k), dtype, True)
 
