@@ -262,13 +262,12 @@ ssd_status ssd_causal_conv_step(const ssd_causal_conv_step_args *a, void *stream
             hipLaunchKernelGGL((k_conv_step<E, V, K>), dim3((unsigned)ceil_div(items, kThreads)), dim3(kThreads), 0, st,
                                (const E *)a->x, xs, a->weight, a->bias, (E *)a->window, (E *)a->y, items, (int)s.C, a->silu != 0);
         };
-        if (s.dtype == SSD_DTYPE_BF16) {
-            if (vec) launch(bf16{}, Int<8>{});
-            else launch(bf16{}, Int<1>{});
-        } else {
-            if (vec) launch(float{}, Int<4>{});
-            else launch(float{}, Int<1>{});
-        }
+        auto typed = [&](auto e) {
+            if (vec) launch(e, Int<4>{});
+            else launch(e, Int<1>{});
+        };
+        if (s.dtype == SSD_DTYPE_BF16) typed(bf16{});
+        else typed(float{});
     });
     return launched();
 }
