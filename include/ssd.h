@@ -542,10 +542,11 @@ ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args *args, void *stream);
  * Every pointer needs the alignment of its elements only.
  *
  * Supported: batch >= 1, seqlen >= 0, 1 <= N <= 64, any D with D % G == 0, D <= 2^20,
- * G*N <= 2^20, batch * seqlen < 2^31 - 64, strides below 2^31; a launch has fewer
- * than 2^32 threads (chunks of 64 tokens times tiles of 64 channels below 2^24 or so),
- * larger sizes are SSD_ERR_BAD_SHAPE.  Results do not change from call to call: every
- * sum has a fixed order.
+ * G*N <= 2^20, batch * seqlen < 2^31 - 64 (2^28 tokens of a packed stream), strides up
+ * to 2^22; a launch has fewer than 2^32 threads, which limits batch * seqlen * D to
+ * about 2^36; larger sizes are SSD_ERR_BAD_SHAPE.  Results do not change from call to
+ * call: every sum has a fixed order.  Outputs and the workspace may overlap neither
+ * each other nor an input (SSD_ERR_ALIASING).
  *
  * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0, nseq),
  * not checked here: see ssd_check_seq_idx; an invalid stream gives wrong results and
@@ -639,10 +640,12 @@ ssd_status ssd_selective_scan_step(const ssd_selective_scan_step_args *args, voi
  * ssd_causal_conv_bwd the gradients, ssd_causal_conv_step one token per batch row.  x may be columns
  * of a wider row, x_stride elements from token to token (0: no gaps); the rest has
  * no gaps.  Sums are in fp32; outputs are rounded once.  Every pointer needs the alignment
- * of its elements only; 16-byte aligned tensors with a dim and stride that are multiples
- * of 8 are moved in wider accesses.
+ * of its elements only; tensors that start at a multiple of four elements, with a dim and
+ * stride that are multiples of four, are moved in wider accesses.
  * Supported: batch >= 1, seqlen >= 0, any dim up to 2^22, width 1..4, batch * seqlen <
- * 2^31 - 64.  Packed streams as for ssd_selective_scan_fwd.
+ * 2^31 - 64, x_stride below 2^31, batch * seqlen * dim below about 2^36 (a launch has fewer
+ * than 2^32 threads); larger sizes are SSD_ERR_BAD_SHAPE.  Outputs and the workspace may
+ * overlap neither each other nor an input.  Packed streams as for ssd_selective_scan_fwd.
  */
 typedef struct {
     int64_t batch, seqlen, dim, width;
@@ -764,10 +767,15 @@ ssd_status ssd_rms_norm_bwd(const ssd_rms_norm_bwd_args *args, void *stream);
  *                           sum_{k in block i} a[m][k] w[n][k]
  *
  * Products and sums inside a block go through the matrix cores, their scaling and the
- * sum over blocks are in fp32.  Supported: m, n >= 0, any n, k >= 1 a multiple of 16,
+ * sum over blocks are in fp32.  The matrix cores add 8-bit products to about 13 bits below
+ * the largest of them, so before its rounding a bf16 output is good to some 1.5e-5 of the
+ * sum's size; for fp32 outputs both operands become bf16 first, exactly, which is good to
+ * fp32 and takes at least twice as long.  Supported: m, n >= 0, any n, k >= 1 a multiple of 16,
  * k <= 2^22, each of m * k, n * k and m * n up to 2^40, m and n < 2^31 - 512.  a, w, out and the
- * workspace need 16-byte alignment, the scales and bias 4-byte.
- * Few rows are shared out along k; the parts are added in a fixed order.
+ * workspace need 16-byte alignment, the scales and bias 4-byte.  Outputs and the workspace
+ * may overlap neither each other nor an input.  Where the outputs are too few to fill the
+ * card, k is shared out over workgroups and the parts, in the workspace, are added in a
+ * fixed order.
  */
 typedef struct {
     int64_t m, n, k;

@@ -92,13 +92,14 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
-// One element of a row's buffer, zero past its end.
-template <typename E> __device__ __forceinline__ float bload_el(__amdgpu_buffer_rsrc_t r, uint32_t off)
+// One element of a row's buffer, zero past its end, as it is in memory: what is loaded ahead is turned into a
+// float where it is used, since that waits for the load.
+template <typename E> __device__ __forceinline__ uint32_t bload_raw(__amdgpu_buffer_rsrc_t r, uint32_t off)
 {
-    if constexpr (sizeof(E) == 2)
-        return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0) << 16);
-    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    if constexpr (sizeof(E) == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
+template <typename E> __device__ __forceinline__ float float_of(uint32_t raw) { return __uint_as_float(sizeof(E) == 2 ? raw << 16 : raw); }
 // The same to memory, rounded; lost past the buffer's end.  Stores without branches around them leave
 // the number of outstanding accesses known, so a wait for loads issued before them is not one for the stores.
 template <typename E> __device__ __forceinline__ void bstore_el(__amdgpu_buffer_rsrc_t r, uint32_t off, float v)
@@ -266,22 +267,22 @@ __device__ __forceinline__ void store_state(float *p, int n0, int N, const float
 
 // B or C of `tokens` tokens from t0 on for LDS: element e of a tile is token e / NP, state e % NP.
 template <typename E, int LN, int NL>
-__device__ __forceinline__ void fetch_keys(const void *p, int64_t t0, int64_t stride, int g, int N, int tokens, float (&v)[NL])
+__device__ __forceinline__ void fetch_keys(const void *p, int64_t t0, int64_t stride, int g, int N, int tokens, uint32_t (&v)[NL])
 {
     constexpr int NP = Lanes<LN>::NP;
     const __amdgpu_buffer_rsrc_t r = token_rsrc<E>(static_cast<const E *>(p) + (int64_t)g * N, t0, stride, tokens, N);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const int e = i * kThreads + threadIdx.x, t = e / NP, n = e % NP;
-        v[i] = bload_el<E>(r, n < N && t < tokens ? (uint32_t)((t * stride + n) * sizeof(E)) : kOffNone);
+        v[i] = bload_raw<E>(r, n < N && t < tokens ? (uint32_t)((t * stride + n) * sizeof(E)) : kOffNone);
     }
 }
-template <int LN, int NL> __device__ __forceinline__ void put_keys(float *dst, const float (&v)[NL], int elems)
+template <typename E, int LN, int NL> __device__ __forceinline__ void put_keys(float *dst, const uint32_t (&v)[NL], int elems)
 {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const int e = i * kThreads + threadIdx.x;
-        if (e < elems) dst[e] = v[i];
+        if (e < elems) dst[e] = float_of<E>(v[i]);
     }
 }
 
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
     float total = 0.f;
 
     // the next tile's values are on their way while this one is computed
-    float xr[NG], dr[NG], zr[HASZ ? NG : 1], gr[HASG ? NG : 1], kb[NL], kc[HASC ? NL : 1];
+    uint32_t xr[NG], dr[NG], zr[HASZ ? NG : 1], gr[HASG ? NG : 1], kb[NL], kc[HASC ? NL : 1];
     auto fetch = [&](int t1) {
         const int64_t t = s.t0 + t1;
         const int left = s.count - t1 < TT ? s.count - t1 : TT;
@@ -332,35 +333,35 @@ __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
             const int at = q * LN + p.j;
-            xr[q] = bload_el<E>(rx, (uint32_t)((at * (int)a.xs + p.d) * (int)sizeof(E)));
-            dr[q] = bload_el<E>(rd, (uint32_t)((at * (int)a.dts + p.d) * (int)sizeof(E)));
+            xr[q] = bload_raw<E>(rx, (uint32_t)((at * (int)a.xs + p.d) * (int)sizeof(E)));
+            dr[q] = bload_raw<E>(rd, (uint32_t)((at * (int)a.dts + p.d) * (int)sizeof(E)));
         }
         if constexpr (HASZ) {
             const __amdgpu_buffer_rsrc_t rz = token_rsrc<E>(a.z, t, a.zs, left, a.D);
 #pragma unroll
-            for (int q = 0; q < NG; ++q) zr[q] = bload_el<E>(rz, (uint32_t)(((q * LN + p.j) * (int)a.zs + p.d) * (int)sizeof(E)));
+            for (int q = 0; q < NG; ++q) zr[q] = bload_raw<E>(rz, (uint32_t)(((q * LN + p.j) * (int)a.zs + p.d) * (int)sizeof(E)));
         }
         if constexpr (HASG) {
             const __amdgpu_buffer_rsrc_t rg = token_rsrc<E>(a.dy, t, a.D, left, a.D);
 #pragma unroll
-            for (int q = 0; q < NG; ++q) gr[q] = bload_el<E>(rg, (uint32_t)(((q * LN + p.j) * a.D + p.d) * (int)sizeof(E)));
+            for (int q = 0; q < NG; ++q) gr[q] = bload_raw<E>(rg, (uint32_t)(((q * LN + p.j) * a.D + p.d) * (int)sizeof(E)));
         }
         fetch_keys<E, LN, NL>(a.B, t, a.Bs, p.g, a.N, left, kb);
         if constexpr (HASC) fetch_keys<E, LN, NL>(a.C, t, a.Cs, p.g, a.N, left, kc);
     };
     if (s.count > 0) fetch(0);
     for (int t1 = 0, b = 0; t1 < s.count; t1 += TT, b ^= 1) {
-        put_keys<LN, NL>(keys[b][0], kb, TT * NP);
-        if constexpr (HASC) put_keys<LN, NL>(keys[b][HASC ? 1 : 0], kc, TT * NP);
+        put_keys<E, LN, NL>(keys[b][0], kb, TT * NP);
+        if constexpr (HASC) put_keys<E, LN, NL>(keys[b][HASC ? 1 : 0], kc, TT * NP);
         float xv[NG], dl[NG], zv[HASZ ? NG : 1], gv[HASG ? NG : 1];
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
             // tokens past the chunk: no step, so that the state stays
             const bool in = t1 + q * LN + p.j < s.count;
-            xv[q] = xr[q];
-            dl[q] = in ? step_size(dr[q] + bias, a.softplus) : 0.f;
-            if constexpr (HASZ) zv[q] = zr[q];
-            if constexpr (HASG) gv[q] = HASZ ? gr[q] * silu(zv[q]) : gr[q];
+            xv[q] = float_of<E>(xr[q]);
+            dl[q] = in ? step_size(float_of<E>(dr[q]) + bias, a.softplus) : 0.f;
+            if constexpr (HASZ) zv[q] = float_of<E>(zr[q]);
+            if constexpr (HASG) gv[q] = HASZ ? float_of<E>(gr[q]) * silu(zv[q]) : float_of<E>(gr[q]);
         }
         if (t1 + TT < s.count) fetch(t1 + TT);
         const __amdgpu_buffer_rsrc_t ry =
@@ -528,14 +529,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
     const int nsub = (s.count + SC - 1) / SC;
     const float *kB = keys[0] + n0, *kC = keys[1] + n0;
     // the first tokens of the way back are on their way meanwhile
-    float nraw[GS], nz[GS], ng[GS];
+    uint32_t nraw[GS], nz[GS], ng[GS];
     auto fetch = [&](int u) {
 #pragma unroll
         for (int q = 0; q < GS; ++q) {
             const int t = u * SC + q * TL + jt;
-            nraw[q] = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + p.d) * (int)sizeof(E)));
-            ng[q] = bload_el<E>(rg, p.live ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone);
-            nz[q] = GATE ? bload_el<E>(rz, p.live ? (uint32_t)((t * (int)a.zs + p.d) * (int)sizeof(E)) : kOffNone) : 0.f;
+            nraw[q] = bload_raw<E>(rd, (uint32_t)((t * (int)a.dts + p.d) * (int)sizeof(E)));
+            ng[q] = bload_raw<E>(rg, p.live ? (uint32_t)((t * a.D + p.d) * (int)sizeof(E)) : kOffNone);
+            nz[q] = GATE ? bload_raw<E>(rz, p.live ? (uint32_t)((t * (int)a.zs + p.d) * (int)sizeof(E)) : kOffNone) : 0u;
         }
     };
     fetch(nsub - 1);
@@ -545,12 +546,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
         const __amdgpu_buffer_rsrc_t rx = token_rsrc<E>(a.x, s.t0, a.xs, s.count, a.D);
         const int ch = tid % SL, cc = (blk - p.g * a.bpg) * SL + ch, dd = p.g * a.per + (cc < a.per ? cc : a.per - 1);
         const float b = a.bias ? a.bias[dd] : 0.f;
-        float xr[NT], dr[NT], kb[NL], kc[NL];
+        uint32_t xr[NT], dr[NT], kb[NL], kc[NL];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int t = i * LN + tid / SL;
-            xr[i] = bload_el<E>(rx, cc < a.per ? (uint32_t)((t * (int)a.xs + dd) * (int)sizeof(E)) : kOffNone);
-            dr[i] = bload_el<E>(rd, (uint32_t)((t * (int)a.dts + dd) * (int)sizeof(E)));
+            xr[i] = bload_raw<E>(rx, cc < a.per ? (uint32_t)((t * (int)a.xs + dd) * (int)sizeof(E)) : kOffNone);
+            dr[i] = bload_raw<E>(rd, (uint32_t)((t * (int)a.dts + dd) * (int)sizeof(E)));
         }
         fetch_keys<E, LN, NL>(a.B, s.t0, a.Bs, p.g, a.N, s.count, kb);
         fetch_keys<E, LN, NL>(a.C, s.t0, a.Cs, p.g, a.N, s.count, kc);
@@ -558,11 +559,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
         for (int i = 0; i < NT; ++i) {
             const int t = i * LN + tid / SL;
             // none for a lane without a channel, none past the chunk
-            sdl[place(t, ch)] = t < s.count && cc < a.per ? step_size(dr[i] + b, a.softplus) : 0.f;
-            sx[place(t, ch)] = xr[i];
+            sdl[place(t, ch)] = t < s.count && cc < a.per ? step_size(float_of<E>(dr[i]) + b, a.softplus) : 0.f;
+            sx[place(t, ch)] = float_of<E>(xr[i]);
         }
-        put_keys<LN, NL>(keys[0], kb, Q * NP);
-        put_keys<LN, NL>(keys[1], kc, Q * NP);
+        put_keys<E, LN, NL>(keys[0], kb, Q * NP);
+        put_keys<E, LN, NL>(keys[1], kc, Q * NP);
     }
     lds_barrier();
     for (int u = 0; u < nsub; ++u) {
@@ -591,9 +592,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
             const int at = place(u * SC + q * TL + jt, slot);
             dl[q] = sdl[at];
             x[q] = sx[at];
-            raw[q] = nraw[q] + bias;
-            go[q] = ng[q];
-            zv[q] = nz[q];
+            raw[q] = float_of<E>(nraw[q]) + bias;
+            go[q] = float_of<E>(ng[q]);
+            zv[q] = float_of<E>(nz[q]);
             dy[q] = GATE ? go[q] * silu(zv[q]) : go[q];
             dxs[q] = dl[q] * x[q];
             ys[q] = 0.f;

@@ -1076,9 +1076,12 @@ def _given(t, name, dtype, shape, dev):
         _same(t, name, dtype, shape, dev)
 
 
-def _made(t, name, dtype, shape, dev):
-    """An output: the caller's, or a new one."""
+def _made(t, name, dtype, shape, dev, like=None):
+    """An output: the caller's, or a new one.  ``like``: an input of this shape (torch allocates
+    in 1.2 us after a dense one, in 2.1 us from a shape)."""
     if t is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
         return torch.empty(shape, dtype=dtype, device=dev)
     _same(t, name, dtype, shape, dev)
     return t
@@ -1151,7 +1154,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     _given(initial_states, "initial_states", torch.float32, states, dev)
 
     def call(st):
-        yy = _made(y, "y", x.dtype, (b, T, dim), dev)
+        yy = _made(y, "y", x.dtype, (b, T, dim), dev, x)
         fin = _made(final_states, "final_states", torch.float32, states, dev) if want_final or final_states is not None else None
         need = _scan_workspace("ssd_selective_scan_fwd_workspace_size", head, ids, n) if workspace is None else 0
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else workspace
@@ -1208,7 +1211,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     _same(state, "state", torch.float32, (b, dim, N), dev)
 
     def call(st):
-        yy = _made(y, "y", x.dtype, (b, dim), dev)
+        yy = _made(y, "y", x.dtype, (b, dim), dev, x)
         a = _SCAN_STEP.pack(*head, *ptrs, *strides, state.data_ptr(), yy.data_ptr())
         return load_library().ssd_selective_scan_step(a, st), yy
 
@@ -1242,7 +1245,7 @@ def causal_conv_fwd(x, weight, bias=None, silu=True, initial_window=None, seq_id
     dev = x.device
 
     def call(st):
-        yy = _made(y, "y", x.dtype, x.shape, dev)
+        yy = _made(y, "y", x.dtype, x.shape, dev, x)
         fin = _made(final_window, "final_window", x.dtype, windows, dev) if want_window or final_window is not None else None
         return load_library().ssd_causal_conv_fwd(_CCONV.pack(*head, yy.data_ptr(), _at(fin)), st), (yy, fin)
 
@@ -1294,7 +1297,7 @@ def causal_conv_step(x, window, weight, bias=None, silu=True, y=None, stream=Non
     _same(window, "window", dtype, (b, K - 1, dim), dev)
 
     def call(st):
-        yy = _made(y, "y", dtype, (b, dim), dev)
+        yy = _made(y, "y", dtype, (b, dim), dev, x)
         a = _CCONV_STEP.pack(b, dim, K, _DTYPES[dtype], 1 if silu else 0, x.data_ptr(), stride, weight.data_ptr(), _at(bias),
                              window.data_ptr(), yy.data_ptr())
         return load_library().ssd_causal_conv_step(a, st), yy
@@ -1328,9 +1331,9 @@ def _rms_fwd(x, weight, residual, eps, residual_out, y, q, scales, rstd, stream,
         raise ValueError("residual_out needs a residual")
 
     def call(st):
-        yy = _made(y, "y", dtype, shape, dev) if want_y else None
-        ro = _made(residual_out, "residual_out", rtype, shape, dev) if residual is not None else None
-        qq = _made(q, "q", _F8, shape, dev) if want_q else None
+        yy = _made(y, "y", dtype, shape, dev, x) if want_y else None
+        ro = _made(residual_out, "residual_out", rtype, shape, dev, x) if residual is not None else None
+        qq = _made(q, "q", _F8, shape, dev, x) if want_q else None
         ss = _made(scales, "scales", torch.float32, (*lead, -(-dim // 128)), dev) if want_q else None
         rr = _made(rstd, "rstd", torch.float32, lead, dev) if want_rstd else None
         a = _RMS.pack(x.numel() // dim if dim else 0, dim, _DTYPES[dtype], _DTYPES[rtype], eps, 0, x.data_ptr(), _at(residual), _at(weight),
@@ -1382,7 +1385,7 @@ def rms_norm_bwd(r, dy, rstd, weight=None, dresidual=None, grads=None, workspace
 
     def call(st):
         out, ws = dict(grads or {}), workspace
-        out["dx"] = _made(out.get("dx"), "dx", dtype, shape, dev)
+        out["dx"] = _made(out.get("dx"), "dx", dtype, shape, dev, dy)
         other = out.get("dresidual")
         if other is not None or (dresidual is not None and rtype is not dtype):
             out["dresidual"] = other = _made(other, "dresidual", rtype, shape, dev)
