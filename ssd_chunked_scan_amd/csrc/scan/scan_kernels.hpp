@@ -6,7 +6,8 @@
 //
 // The decays differ in every channel d and state n, so no product of matrices forms the
 // scan: it is an exponential and a few multiply-adds for each (t, d, n), and these bound
-// it, not the bytes (N = 16: 16 exponentials for 8 bytes of x, dt, z and y).
+// it, not the bytes (N = 16: 16 exponentials for 8 bytes of x, dt, z and y).  A wave issues an
+// fp32 instruction in 4 cycles and an exponential in 9.
 //
 // Layout.  LN neighbouring lanes share a channel, each holding 4 of its states (LN = N / 4
 // rounded up to a power of two), so a wave has 64 / LN channels.  The LN lanes also share
@@ -299,6 +300,10 @@ __device__ __forceinline__ float step_size(float raw, int softplus)
 // MODE 1: the chunk's end state from a zero start into S, and the sum of its Delta.  MODE 2:
 // that, and what the chunk's dy add to the gradient of the state that enters it, R = sum over
 // t of (product of the decays up to t's) C_t dy_t SiLU(z_t).
+//
+// 16 prompts of 18 K tokens in all, 5120 channels, 16 states, bf16: 518 us (MODE 0), of which the recurrence
+// and its output (per 4 states and token 4 exponentials and 17 other instructions) are 360 and the loads, softplus, SiLU and
+// the sum over lanes the rest; the bytes would take 140.  Workgroups of longer rows start first: 690 without that.
 template <typename E, int LN, bool GATE, int MODE>
 __global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
 {
@@ -481,6 +486,10 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
 // product with a one-hot row on the matrix cores, which are idle here: v_mfma_f32_16x16x4 adds the four
 // lanes of a column into row t (dB) or 8 + t (dC) of an accumulator that 8 tokens share; over the lanes of a
 // row and over the waves it is taken once for the 8 tokens.  Over tiles of channels k_scan_keys adds it up.
+//
+// 16384 tokens of 5120 channels, 16 states, bf16: 1634 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
+// 248 registers a thread: two waves a SIMD (three spill: 2890 us).  Sums over channels by DPP and LDS alone, and Delta and x formed where
+// they are used instead of staged, took 3045.  Chunks of 64 tokens: a shorter one rebuilds its states more often.
 template <typename E, int LN, bool GATE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
 {
