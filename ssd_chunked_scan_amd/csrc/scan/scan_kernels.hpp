@@ -301,11 +301,15 @@ __device__ __forceinline__ float step_size(float raw, int softplus)
 // that, and what the chunk's dy add to the gradient of the state that enters it, R = sum over
 // t of (product of the decays up to t's) C_t dy_t SiLU(z_t).
 //
-// 16 prompts of 18 K tokens in all, 5120 channels, 16 states, bf16: 518 us (MODE 0), of which the recurrence
+// 16 prompts of 18 K tokens in all, 5120 channels, 16 states, bf16: 495 us (MODE 0), of which the recurrence
 // and its output (per 4 states and token 4 exponentials and 17 other instructions) are 360 and the loads, softplus, SiLU and
-// the sum over lanes the rest; the bytes would take 140.  Workgroups of longer rows start first: 690 without that.
+// the sum over lanes the rest; the bytes would take 140.  Workgroups of longer rows start first: 690 without that and with four waves.
+// Three waves a SIMD keep it busy; with four, which the registers would let in, the longest rows share a SIMD with
+// more of the others and end later (532 against 505 us; 555 with two).  Forms that need more registers have their own limit.
+template <int LN, int MODE> constexpr bool kThree = MODE == 0 && LN > 1 && LN < 16;
 template <typename E, int LN, bool GATE, int MODE>
-__global__ __launch_bounds__(kThreads) void k_scan(ScanArgs a)
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kThree<LN, MODE> ? 3 : 1, kThree<LN, MODE> ? 3 : 8)))
+void k_scan(ScanArgs a)
 {
     using L = Lanes<LN>;
     constexpr int TT = L::TT, NP = L::NP, NG = L::NG, NL = L::NL;
@@ -488,7 +492,7 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
 // row and over the waves it is taken once for the 8 tokens.  Over tiles of channels k_scan_keys adds it up.
 //
 // 16384 tokens of 5120 channels, 16 states, bf16: 1634 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
-// 248 registers a thread: two waves a SIMD (three spill: 2890 us).  Sums over channels by DPP and LDS alone, and Delta and x formed where
+// 244 registers a thread: two waves a SIMD (three spill: 2890 us).  Sums over channels by DPP and LDS alone, and Delta and x formed where
 // they are used instead of staged, took 3045.  Chunks of 64 tokens: a shorter one rebuilds its states more often.
 template <typename E, int LN, bool GATE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
