@@ -88,12 +88,19 @@ template <typename O> void run(const ssd_matmul_fp8_args *a, const Plan &p, hipS
     k.tn = (int)p.tn;
     const dim3 grid((unsigned)(p.tm * p.tn * p.shares));
     if (!p.few) {
-        if constexpr (std::is_same<O, bf16>::value)
-            if (p.bm == 256) {
-                hipLaunchKernelGGL((k_mm_tile<O, 256, 256, 2, 4>), dim3(resident(p, 256)), dim3(512), 0, st, k);
-                return;
-            }
-        hipLaunchKernelGGL((k_mm_tile<O, 128, 128, 2, 2>), dim3(resident(p, 512)), dim3(256), 0, st, k);
+        auto tile = [&](auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            if constexpr (std::is_same<O, bf16>::value)
+                if (p.bm == 256) {
+                    hipLaunchKernelGGL((k_mm_tile<O, 256, 256, 2, 4, WHOLE>), dim3(resident(p, 256)), dim3(512), 0, st, k);
+                    return;
+                }
+            hipLaunchKernelGGL((k_mm_tile<O, 128, 128, 2, 2, WHOLE>), dim3(resident(p, 512)), dim3(256), 0, st, k);
+        };
+        // such a tile is addressed in 31 bits
+        if (std::is_same<O, bf16>::value && a->n % 8 == 0 && a->n <= (int64_t)1 << 21) {
+            if constexpr (std::is_same<O, bf16>::value) tile(std::true_type{});
+        } else tile(std::false_type{});
         return;
     }
     auto few = [&](auto mi) {

@@ -100,13 +100,13 @@ __device__ __forceinline__ void stage_done()
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");   // nothing is read ahead of the barrier
 }
+// Vectors in memory that are aligned to an element only: rows of n values start anywhere.
+template <typename T, int N> using any_t = T __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 // 4 neighbouring n of row m, to the output's type (or as fp32 sums).
-template <typename O> __device__ __forceinline__ void store4(O *row, int n, int N, const floatx4 &v, bool vec)
+template <typename O> __device__ __forceinline__ void store4(O *row, int n, int N, const floatx4 &v)
 {
-    if (vec && n + 3 < N) {
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        store4_f32(row + n, f);
-    } else
+    if (n + 3 < N) *reinterpret_cast<any_t<O, 4> *>(row + n) = __builtin_convertvector(v, any_t<O, 4>);   // to nearest even
+    else
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (n + i < N) row[n + i] = from_float<O>(v[i]);
@@ -116,11 +116,12 @@ template <typename O> __device__ __forceinline__ void store4(O *row, int n, int 
 // group g hold n 4 g .. of each; the halves that are in the wrong lanes swap.  A store then writes 64 bytes of each of 16
 // rows (32 with 4 values a lane: 16384 x 10240 of k = 2560 in 444 us, 411 so), past the caches, which would write
 // them all back at once when every workgroup's tile ends (400 us; 350 without any stores).
+// Rows that are not whole vectors take ordinary stores, aligned to an element, and single elements at their ends.
 constexpr int kCpolPast = 18;   // streaming, written through
-template <int MI, int NI>
+template <bool WHOLE, int MI, int NI>
 __device__ __forceinline__ void store_wide(const float (&acc)[MI][NI][4], bf16 *tile, int row, int col, int g, int rows, int cols, int stride)
 {
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(tile, ((int64_t)(rows - 1) * stride + cols) * 2);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(tile, WHOLE ? ((int64_t)(rows - 1) * stride + cols) * 2 : 0);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -133,16 +134,27 @@ __device__ __forceinline__ void store_wide(const float (&acc)[MI][NI][4], bf16 *
             typedef unsigned int u32x4 __attribute__((__vector_size__(16)));
             const u32x4 o = {u[0], v[0], u[1], v[1]};
             const int c = col + 16 * j + 8 * g;   // groups 0 and 1 have the first tile's, 2 and 3 the second's
-            __builtin_amdgcn_raw_buffer_store_b128(o, r, c < cols ? ((uint32_t)(row + 16 * i) * (uint32_t)stride + (uint32_t)c) * 2u : kOffNone, 0,
-                                                   kCpolPast);
+            if constexpr (WHOLE)
+                __builtin_amdgcn_raw_buffer_store_b128(o, r, c < cols ? ((uint32_t)(row + 16 * i) * (uint32_t)stride + (uint32_t)c) * 2u : kOffNone, 0,
+                                                       kCpolPast);
+            else if (row + 16 * i < rows) {
+                bf16 *to = tile + (int64_t)(row + 16 * i) * stride + c;
+                const any_t<bf16, 8> e = __builtin_bit_cast(bf16x8, o);
+                if (c + 8 <= cols) *reinterpret_cast<any_t<bf16, 8> *>(to) = e;
+                else
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (c + q < cols) to[q] = e[q];
+            }
         }
 }
 
 // Tile of BM rows of a and BN rows of w, WM x WN waves.  Two stages of LDS, filled straight from memory:
 // the next block of both operands is on its way while this one is multiplied.  The stages are arrays of their
 // own, so that a read of one does not wait for the loads into the other.  A workgroup stays for tile after
-// tile: the next one's first block comes while this one's last is multiplied and its values are stored.
-template <typename O, int BM, int BN, int WM, int WN>
+// tile: the next one's first block comes while this one's last is multiplied and its values are stored.  WHOLE: rows of
+// whole 16-byte vectors of bf16 (11844 x 5154 of k = 112, not so: 121 us with single elements, 42 with vectors).
+template <typename O, int BM, int BN, int WM, int WN, bool WHOLE>
 __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
 {
     constexpr bool BF = std::is_same<O, float>::value;
@@ -221,8 +233,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
             __builtin_amdgcn_sched_barrier(0);   // further ahead the scheduler runs out of registers
         }
     };
-    // bf16 rows of whole 16-byte vectors, whose tile is addressed in 31 bits
-    const bool vec = (p.n & 3) == 0, wide = (p.n & 7) == 0 && p.n <= 1 << 21;
     Tile t = tile_at(blockIdx.x);
     stage(sa0, sw0, sc0, t, 0);
     for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
@@ -255,21 +265,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
                     for (int i = 0; i < MI; ++i) acc[i][j][e] += b;
                 }
         if constexpr (!BF) {
-            if (wide) {
-                store_wide(acc, static_cast<O *>(p.out) + (int64_t)t.m0 * p.n + t.n0, wm + lr, wn, g, p.m - t.m0 < BM ? p.m - t.m0 : BM,
-                           p.n - t.n0 < BN ? p.n - t.n0 : BN, p.n);
-                t = next;
-                continue;
+            O *tile = static_cast<O *>(p.out) + (int64_t)t.m0 * p.n + t.n0;
+            const int rows = p.m - t.m0 < BM ? p.m - t.m0 : BM, cols = p.n - t.n0 < BN ? p.n - t.n0 : BN;
+            store_wide<WHOLE>(acc, tile, wm + lr, wn, g, rows, cols, p.n);
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int m = t.m0 + wm + 16 * i + lr;
+                if (m >= p.m) continue;
+                O *row = static_cast<O *>(p.out) + (int64_t)m * p.n;
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+                    store4(row, t.n0 + wn + 16 * j + 4 * g, p.n, floatx4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]});
             }
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int m = t.m0 + wm + 16 * i + lr;
-            if (m >= p.m) continue;
-            O *row = static_cast<O *>(p.out) + (int64_t)m * p.n;
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                store4(row, t.n0 + wn + 16 * j + 4 * g, p.n, floatx4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]}, vec);
         }
         t = next;
     }
@@ -396,7 +404,6 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs p)
         for (int i = 0; i < MI; ++i) store4_f32(sums + i * 256, acc[i]);
     stage_done();
     if (half) return;
-    const bool vec = (p.n & 3) == 0;
     const int n = n0 + 4 * g;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -405,12 +412,12 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs p)
         float o[4];
         load4_f32(sums + i * 256, o);
         floatx4 v = {acc[i][0] + o[0], acc[i][1] + o[1], acc[i][2] + o[2], acc[i][3] + o[3]};
-        if constexpr (SHARED) store4(p.part + ((int64_t)share * p.m + m) * p.n, n, p.n, v, vec);
+        if constexpr (SHARED) store4(p.part + ((int64_t)share * p.m + m) * p.n, n, p.n, v);
         else {
             if (p.bias)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] += p.bias[n + e < p.n ? n + e : 0];
-            store4(static_cast<O *>(p.out) + (int64_t)m * p.n, n, p.n, v, vec);
+            store4(static_cast<O *>(p.out) + (int64_t)m * p.n, n, p.n, v);
         }
     }
 }
