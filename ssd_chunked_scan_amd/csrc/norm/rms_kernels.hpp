@@ -7,7 +7,8 @@
 // Bound by bytes: a row is read once into registers, summed there and written once.  L lanes share a
 // row, each with IT runs of 8 neighbouring values (16 bytes of bf16, 32 of fp32), so that a block
 // of 128 values, which shares a scale, lies in 16 lanes: one DPP row.  Rows whose length is not a
-// multiple of 8 are moved by single elements in the same places.
+// multiple of 8 start at any element: the same vectors, not aligned (8000 rows of 2561, fp32: 66 us; by single
+// elements 186 us), and single elements where the row's end cuts a run.
 //
 // The backward's sum over rows: every workgroup keeps its lanes' columns in registers over a strip of
 // rows, joins its row groups through LDS and writes one fp32 row of partial sums; a second kernel
@@ -26,30 +27,42 @@ constexpr float kMax8 = 448.f;     // largest e4m3 value
 constexpr float kLeastScale = 0x1p-126f;
 constexpr int kDppRowMirror = 0x140;
 
-// A run of 8 values as it is in memory.  AL: in vectors of 16 bytes.
-template <typename T, bool AL> struct Run {
-    typename std::conditional<AL, uint4, T>::type v[AL ? (int)sizeof(T) / 2 : kRun];
+// A run of 8 values as it is in memory.
+template <typename T> struct Run {
+    uint4 v[(int)sizeof(T) / 2];
 };
+// Vectors in memory that are aligned to an element only.
+template <typename T, typename V, int N> using any_t = V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 // Loads the run at column c of a row; past the row's end its first values are loaded instead
-// (`clear` drops them).
-template <typename T, bool AL> __device__ __forceinline__ void load_run(Run<T, AL> &r, const T *row, int c, int dim)
+// (`unpack_run` drops them).  AL: rows are whole runs, which start at 16 bytes; otherwise vectors start
+// at any element, and a run that the row's end cuts is loaded by single elements.
+template <bool AL, typename T> __device__ __forceinline__ void load_run(Run<T> &r, const T *row, int c, int dim)
 {
-    typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
     if constexpr (AL) {
+        typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
         const uint4v *p = reinterpret_cast<const uint4v *>(row + (c < dim ? c : 0));
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(p + i));   // read once
-    } else {
+    } else if (c + kRun <= dim) {
+        typedef any_t<T, unsigned int, 4> uint4v;
+        const uint4v *p = reinterpret_cast<const uint4v *>(row + c);
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) r.v[e] = row[c + e < dim ? c + e : 0];
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = uint4{p[i].x, p[i].y, p[i].z, p[i].w};
+    } else {
+        typedef T tv __attribute__((ext_vector_type(16 / sizeof(T))));
+        constexpr int W = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < kRun / W; ++i) {
+            tv t;
+#pragma unroll
+            for (int e = 0; e < W; ++e) t[e] = row[c + i * W + e < dim ? c + i * W + e : 0];
+            r.v[i] = __builtin_bit_cast(uint4, t);
+        }
     }
 }
-template <typename T, bool AL> __device__ __forceinline__ void unpack_run(const Run<T, AL> &r, float (&o)[kRun], int c, int dim)
+template <bool AL, typename T> __device__ __forceinline__ void unpack_run(const Run<T> &r, float (&o)[kRun], int c, int dim)
 {
-    if constexpr (!AL) {
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) o[e] = to_float(r.v[e]);
-    } else if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
         const floatx8 f = __builtin_convertvector(__builtin_bit_cast(bf16x8, r.v[0]), floatx8);
 #pragma unroll
         for (int e = 0; e < kRun; ++e) o[e] = f[e];
@@ -66,22 +79,28 @@ template <typename T, bool AL> __device__ __forceinline__ void unpack_run(const 
     for (int e = 0; e < kRun; ++e)
         if ((AL ? c : c + e) >= dim) o[e] = 0.f;
 }
-template <typename T, bool AL> __device__ __forceinline__ void store_run(T *row, const float (&v)[kRun], int c, int dim)
+template <bool AL, typename T> __device__ __forceinline__ void store_run(T *row, const float (&v)[kRun], int c, int dim)
 {
-    if constexpr (!AL) {
-#pragma unroll
-        for (int e = 0; e < kRun; ++e)
-            if (c + e < dim) row[c + e] = from_float<T>(v[e]);
-    } else if (c < dim) {
+    if (AL ? c < dim : c + kRun <= dim) {
         if constexpr (sizeof(T) == 2) {
             floatx8 f;
 #pragma unroll
             for (int e = 0; e < kRun; ++e) f[e] = v[e];
-            *reinterpret_cast<bf16x8 *>(row + c) = __builtin_convertvector(f, bf16x8);
-        } else {
+            const bf16x8 o = __builtin_convertvector(f, bf16x8);
+            if constexpr (AL) *reinterpret_cast<bf16x8 *>(row + c) = o;
+            else *reinterpret_cast<any_t<T, T, 8> *>(row + c) = o;
+        } else if constexpr (AL) {
             store4_f32(row + c, v);
             store4_f32(row + c + 4, v + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun; i += 4)
+                *reinterpret_cast<any_t<T, T, 4> *>(row + c + i) = any_t<T, T, 4>{v[i], v[i + 1], v[i + 2], v[i + 3]};
         }
+    } else if constexpr (!AL) {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            if (c + e < dim) row[c + e] = from_float<T>(v[e]);
     }
 }
 template <bool AL> __device__ __forceinline__ void load_weight(const float *w, float (&o)[kRun], int c, int dim)
@@ -89,7 +108,8 @@ template <bool AL> __device__ __forceinline__ void load_weight(const float *w, f
 #pragma unroll
     for (int e = 0; e < kRun; ++e) o[e] = 1.f;
     if (!w) return;
-    if constexpr (AL) {
+    // weights start at 16 bytes, and so do a row's runs of them
+    if (AL || c + kRun <= dim) {
         const int cc = c < dim ? c : 0;
         load4_f32(w + cc, o);
         load4_f32(w + cc + 4, o + 4);
@@ -133,6 +153,7 @@ template <bool AL> __device__ __forceinline__ void put_8bit(uint8_t *q, const fl
         b[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(w[4 * h + 2] * inv, w[4 * h + 3] * inv, p, true);
     }
     if constexpr (AL) *reinterpret_cast<uint2 *>(q) = uint2{b[0], b[1]};
+    else if (left >= kRun) *reinterpret_cast<any_t<uint8_t, unsigned int, 2> *>(q) = any_t<uint8_t, unsigned int, 2>{b[0], b[1]};
     else
 #pragma unroll
         for (int e = 0; e < kRun; ++e)
@@ -160,25 +181,25 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_fwd(FwdArgs
     if (L <= 64 && row >= a.rows) return;   // longer rows: one a workgroup, always there
     const E *x = static_cast<const E *>(a.x) + row * a.dim;
     const R *res = static_cast<const R *>(a.res) + row * a.dim;
-    Run<E, AL> rx[IT];
-    Run<R, AL> rr[RES ? IT : 1];
+    Run<E> rx[IT];
+    Run<R> rr[RES ? IT : 1];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int c = (i * L + ln) * kRun;
-        load_run(rx[i], x, c, a.dim);
-        if constexpr (RES) load_run(rr[i], res, c, a.dim);
+        load_run<AL>(rx[i], x, c, a.dim);
+        if constexpr (RES) load_run<AL>(rr[i], res, c, a.dim);
     }
     float v[IT][kRun], s = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int c = (i * L + ln) * kRun;
-        unpack_run(rx[i], v[i], c, a.dim);
+        unpack_run<AL>(rx[i], v[i], c, a.dim);
         if constexpr (RES) {
             float o[kRun];
-            unpack_run(rr[i], o, c, a.dim);
+            unpack_run<AL>(rr[i], o, c, a.dim);
 #pragma unroll
             for (int e = 0; e < kRun; ++e) v[i][e] = to_float(from_float<R>(v[i][e] + o[e]));   // what the stream holds
-            store_run<R, AL>(static_cast<R *>(a.res_out) + row * a.dim, v[i], c, a.dim);
+            store_run<AL>(static_cast<R *>(a.res_out) + row * a.dim, v[i], c, a.dim);
         }
 #pragma unroll
         for (int e = 0; e < kRun; ++e) s += v[i][e] * v[i][e];
@@ -197,7 +218,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_fwd(FwdArgs
             w[e] = v[i][e] * rs * w[e];
             m = fmaxf(m, fabsf(w[e]));
         }
-        if (a.y) store_run<E, AL>(static_cast<E *>(a.y) + row * a.dim, w, c, a.dim);
+        if (a.y) store_run<AL>(static_cast<E *>(a.y) + row * a.dim, w, c, a.dim);
         if (!a.q) continue;
         const float scale = fmaxf(max16(m) / kMax8, kLeastScale), inv = 1.f / scale;
         if (c >= a.dim) continue;
@@ -246,7 +267,7 @@ template <typename E, typename R, bool RES> __global__ __launch_bounds__(kLong) 
         }
         const float scale = fmaxf(max16(m) / kMax8, kLeastScale), inv = 1.f / scale;
         if (c >= a.dim) continue;
-        if (a.y) store_run<E, false>(static_cast<E *>(a.y) + at, w, c, a.dim);
+        if (a.y) store_run<false>(static_cast<E *>(a.y) + at, w, c, a.dim);
         if (!a.q) continue;
         if ((threadIdx.x & 15) == 0) a.scales[(int64_t)blockIdx.x * nb + c / 128] = scale;
         put_8bit<false>(a.q + at + c, w, inv, a.dim - c);
@@ -279,8 +300,8 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_bwd(BwdArgs
     }
     const int64_t r0 = (int64_t)blockIdx.x * a.strip, r1 = r0 + a.strip < a.rows ? r0 + a.strip : a.rows;
     // the next row is on its way while this one is summed; rows past the strip load its first
-    Run<R, AL> nr[IT], nd[DRES ? IT : 1];
-    Run<E, AL> ng[IT];
+    Run<R> nr[IT], nd[DRES ? IT : 1];
+    Run<E> ng[IT];
     float nrs;
     auto fetch = [&](int64_t row) {
         const int64_t rr = row < r1 ? row : r0, at = rr * a.dim;
@@ -288,9 +309,9 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_bwd(BwdArgs
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * L + ln) * kRun;
-            load_run(nr[i], static_cast<const R *>(a.r) + at, c, a.dim);
-            load_run(ng[i], static_cast<const E *>(a.dy) + at, c, a.dim);
-            if constexpr (DRES) load_run(nd[i], static_cast<const R *>(a.dres) + at, c, a.dim);
+            load_run<AL>(nr[i], static_cast<const R *>(a.r) + at, c, a.dim);
+            load_run<AL>(ng[i], static_cast<const E *>(a.dy) + at, c, a.dim);
+            if constexpr (DRES) load_run<AL>(nd[i], static_cast<const R *>(a.dres) + at, c, a.dim);
         }
     };
     const float inv = 1.f / (float)a.dim;
@@ -300,13 +321,13 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_bwd(BwdArgs
         const int64_t row = rb + rg, at = row * a.dim;
         const bool live = row < r1;   // the whole row group agrees
         float h[IT][kRun], g[IT][kRun];
-        Run<R, AL> cd[DRES ? IT : 1];
+        Run<R> cd[DRES ? IT : 1];
         const float rs = nrs;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = live ? (i * L + ln) * kRun : a.dim;
-            unpack_run(nr[i], h[i], c, a.dim);
-            unpack_run(ng[i], g[i], c, a.dim);
+            unpack_run<AL>(nr[i], h[i], c, a.dim);
+            unpack_run<AL>(ng[i], g[i], c, a.dim);
             if constexpr (DRES) cd[i] = nd[i];
         }
         if (rb + G < r1) fetch(row + G);
@@ -326,11 +347,11 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void k_rms_bwd(BwdArgs
         for (int i = 0; i < IT; ++i) {
             const int c = (i * L + ln) * kRun;
             float o[kRun];
-            if constexpr (DRES) unpack_run(cd[i], o, c, a.dim);
+            if constexpr (DRES) unpack_run<AL>(cd[i], o, c, a.dim);
 #pragma unroll
             for (int e = 0; e < kRun; ++e) o[e] = rs * (g[i][e] - h[i][e] * s) + (DRES ? o[e] : 0.f);
-            store_run<E, AL>(static_cast<E *>(a.dx) + at, o, c, a.dim);
-            if (a.dr) store_run<R, AL>(static_cast<R *>(a.dr) + at, o, c, a.dim);
+            store_run<AL>(static_cast<E *>(a.dx) + at, o, c, a.dim);
+            if (a.dr) store_run<AL>(static_cast<R *>(a.dr) + at, o, c, a.dim);
         }
     }
     if (!a.parts) return;
