@@ -640,8 +640,7 @@ ssd_status ssd_selective_scan_step(const ssd_selective_scan_step_args *args, voi
  * ssd_causal_conv_bwd the gradients, ssd_causal_conv_step one token per batch row.  x may be columns
  * of a wider row, x_stride elements from token to token (0: no gaps); the rest has
  * no gaps.  Sums are in fp32; outputs are rounded once.  Every pointer needs the alignment
- * of its elements only; tensors that start at a multiple of four elements, with a dim and
- * stride that are multiples of four, are moved in wider accesses.
+ * of its elements only.
  * Supported: batch >= 1, seqlen >= 0, any dim up to 2^22, width 1..4, batch * seqlen <
  * 2^31 - 64, x_stride below 2^31, batch * seqlen * dim below about 2^36 (a launch has fewer
  * than 2^32 threads); larger sizes are SSD_ERR_BAD_SHAPE.  Outputs and the workspace may

@@ -95,19 +95,10 @@ template <typename F> void with_width(int64_t K, F &&f)
     else if (K == 3) f(Int<3>{});
     else f(Int<4>{});
 }
-// Whether every row of these tensors may be moved in vectors of four elements.
-template <size_t N> bool wide(const Shape &s, int64_t stride, const void *const (&ptrs)[N])
-{
-    if (s.C % 4 != 0 || stride % 4 != 0) return false;
-    for (const void *p : ptrs)
-        if (!aligned_to(p, 4 * s.esz)) return false;
-    return true;
-}
-
 // E, vector width, taps and packing of a call.  Four elements to a thread in both types: 16
 // bytes of bf16 take twice the registers (packed prompts of 18 K tokens, 5120 channels: 110
 // against 97 us; gradients of 16384 tokens: 283 against 141 us, at one wave a SIMD).
-template <typename F> void dispatch(const Shape &s, bool vec, F &&f)
+template <typename F> void dispatch(const Shape &s, F &&f)
 {
     with_width(s.K, [&](auto kw) {
         auto typed = [&](auto e) {
@@ -116,7 +107,7 @@ template <typename F> void dispatch(const Shape &s, bool vec, F &&f)
                 if (s.packed) f(e, v, kw, std::true_type{});
                 else f(e, v, kw, std::false_type{});
             };
-            if (vec) packed(Int<4>{});
+            if (s.C >= 4) packed(Int<4>{});
             else packed(Int<1>{});
         };
         if (s.dtype == SSD_DTYPE_BF16) typed(bf16{});
@@ -167,10 +158,9 @@ ssd_status ssd_causal_conv_fwd(const ssd_causal_conv_args *a, void *stream)
     ConvArgs k = conv_args(s, a, kFwdStrip);
     k.y = a->y;
     k.win1 = s.K > 1 ? a->final_window : nullptr;
-    const void *const ptrs[] = {a->x, a->initial_window, a->y, a->final_window};
-    dispatch(s, wide(s, k.xs, ptrs), [&](auto e, auto v, auto kw, auto packed) {
+    dispatch(s, [&](auto e, auto v, auto kw, auto packed) {
         constexpr int V = decltype(v)::value;
-        k.items = s.b * k.nb * (s.C / V);
+        k.items = s.b * k.nb * ceil_div(s.C, V);
         hipLaunchKernelGGL((k_conv_fwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>),
                            dim3((unsigned)ceil_div(k.items, kThreads)), dim3(kThreads), 0, st, k);
     });
@@ -217,10 +207,9 @@ ssd_status ssd_causal_conv_bwd(const ssd_causal_conv_args *a, const ssd_causal_c
     k.parts = static_cast<float *>(g->workspace);
     if (s.T == 0) keep(s, g->dfinal_window, g->dinitial_window, st);
     else {
-        const void *const ptrs[] = {a->x, a->initial_window, g->dy, g->dx, g->dfinal_window, g->dinitial_window};
-        dispatch(s, wide(s, k.xs, ptrs), [&](auto e, auto v, auto kw, auto packed) {
+        dispatch(s, [&](auto e, auto v, auto kw, auto packed) {
             constexpr int V = decltype(v)::value;
-            k.items = s.b * k.nb * (s.C / V);
+            k.items = s.b * k.nb * ceil_div(s.C, V);
             hipLaunchKernelGGL((k_conv_bwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>),
                                dim3((unsigned)ceil_div(k.items, kThreads)), dim3(kThreads), 0, st, k);
         });
@@ -251,8 +240,7 @@ ssd_status ssd_causal_conv_step(const ssd_causal_conv_step_args *a, void *stream
     if (!apart(ins, outs)) return SSD_ERR_ALIASING;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t xs = a->x_stride ? a->x_stride : s.C;
-    const void *const ptrs[] = {a->x, a->window, a->y};
-    const bool vec = wide(s, xs, ptrs);
+    const bool vec = s.C % 4 == 0;   // the window is moved in place: no element may be two threads'
     with_width(s.K, [&](auto kw) {
         constexpr int K = decltype(kw)::value;
         auto launch = [&](auto e, auto v) {

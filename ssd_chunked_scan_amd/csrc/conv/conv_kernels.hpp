@@ -4,8 +4,8 @@
 //   v_t = bias + sum_k w[k] x_{t-K+1+k},  y_t = SiLU(v_t) or v_t        for every channel
 //   dv_t = dy_t SiLU'(v_t),  dx_t = sum_d w[K-1-d] dv_{t+d},  dw[k] = sum_t dv_t x_{t-K+1+k}
 //
-// Bound by its bytes: a thread has V neighbouring channels (four; single elements where rows
-// do not start at a multiple of them) and walks a strip of tokens with the last K-1 inputs in
+// Bound by its bytes: a thread has V neighbouring channels (four, at any element; one where there
+// are fewer) and walks a strip of tokens with the last K-1 inputs in
 // registers, so that every row is read once, but for the K-1 rows around a strip.  The inputs
 // before a sequence's first token are its window's.
 #pragma once
@@ -32,8 +32,7 @@ struct ConvArgs {
 };
 
 // V elements of E as they are in memory, and as floats.
-template <typename E, int V>
-using vec_t = typename std::conditional<V * sizeof(E) == 16, uint4, typename std::conditional<V * sizeof(E) == 8, uint2, E>::type>::type;
+template <typename E, int V> using vec_t = typename std::conditional<V * sizeof(E) == 16, uint4, typename std::conditional<V * sizeof(E) == 8, uint2, E>::type>::type;
 template <typename E, int V> __device__ __forceinline__ void to_floats(const vec_t<E, V> &r, float (&o)[V])
 {
     if constexpr (V == 1) o[0] = to_float(r);
@@ -57,13 +56,28 @@ template <typename E, int V> __device__ __forceinline__ vec_t<E, V> from_floats(
         return __builtin_bit_cast(vec_t<E, V>, __builtin_convertvector(f, ev));   // to nearest even
     }
 }
+// In memory they are aligned to an element only.
+template <typename E, int V> using any_t = E __attribute__((ext_vector_type(V), aligned(sizeof(E))));
 template <typename E, int V> __device__ __forceinline__ vec_t<E, V> load_vec(const void *p, int64_t at)
 {
-    return *reinterpret_cast<const vec_t<E, V> *>(static_cast<const E *>(p) + at);
+    if constexpr (V == 1) return static_cast<const E *>(p)[at];
+    else {
+        typedef E ev __attribute__((ext_vector_type(V)));
+        const ev v = *reinterpret_cast<const any_t<E, V> *>(static_cast<const E *>(p) + at);
+        return __builtin_bit_cast(vec_t<E, V>, v);
+    }
+}
+template <typename E, int V> __device__ __forceinline__ void store_raw(void *p, int64_t at, const vec_t<E, V> &v)
+{
+    if constexpr (V == 1) static_cast<E *>(p)[at] = v;
+    else {
+        typedef E ev __attribute__((ext_vector_type(V)));
+        *reinterpret_cast<any_t<E, V> *>(static_cast<E *>(p) + at) = __builtin_bit_cast(ev, v);
+    }
 }
 template <typename E, int V> __device__ __forceinline__ void store_vec(void *p, int64_t at, const float (&v)[V])
 {
-    *reinterpret_cast<vec_t<E, V> *>(static_cast<E *>(p) + at) = from_floats<E, V>(v);
+    store_raw<E, V>(p, at, from_floats<E, V>(v));
 }
 
 // A thread's place: its channels c .., its sequence row b and first token.
@@ -78,9 +92,11 @@ template <int V> __device__ __forceinline__ bool strip_of(const ConvArgs &a, Str
     // XCD-aware order: strips that share rows run on one XCD
     const int64_t it = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * kThreads + threadIdx.x;
     if (it >= a.items) return false;
-    const int gv = a.C / V;
+    // the last channels of a number that V does not divide are two threads', which write the same values
+    const int gv = (a.C + V - 1) / V;
     s.index = it / gv;
     s.c = (int)(it - s.index * gv) * V;
+    if (s.c > a.C - V) s.c = a.C - V;
     s.b = (int)(s.index / a.nb);
     s.t0 = (int)(s.index - (int64_t)s.b * a.nb) * a.strip;
     s.t1 = a.T - s.t0 < a.strip ? a.T : s.t0 + a.strip;
@@ -411,7 +427,7 @@ __global__ __launch_bounds__(kThreads) void k_conv_step(const E *__restrict__ x,
         for (int e = 0; e < V; ++e) o[e] = silu(o[e]);
     store_vec<E, V>(y, b * C + c, o);
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) *reinterpret_cast<vec_t<E, V> *>(window + (b * (K - 1) + i) * C + c) = raw[i + 1];
+    for (int i = 0; i < K - 1; ++i) store_raw<E, V>(window, (b * (K - 1) + i) * C + c, raw[i + 1]);
 }
 
 }  // namespace conv
