@@ -765,13 +765,10 @@ ssd_status ssd_rms_norm_bwd(const ssd_rms_norm_bwd_args *args, void *stream);
  *     out[m][n] = bias[n] + sum_i a_scales[m][i] w_scales[n/128][i]
  *                           sum_{k in block i} a[m][k] w[n][k]
  *
- * Products and sums inside a block go through the matrix cores, their scaling and the
- * sum over blocks are in fp32.  The matrix cores add 8-bit products to about 13 bits below
- * the largest of them, so before its rounding a bf16 output is good to some 1.5e-5 of the
- * sum's size; for fp32 outputs both operands become bf16 first, exactly, which is good to
- * fp32 and takes at least twice as long.  Supported: m, n >= 0, any n, k >= 1 a multiple of 16,
- * k <= 2^22, each of m * k, n * k and m * n up to 2^40, m and n < 2^31 - 512.  a, w, out and the
- * workspace need 16-byte alignment, the scales and bias 4-byte.  Outputs and the workspace
+ * The operands become bf16 on their way to the matrix cores, exactly, and every sum and
+ * scaling is in fp32, whatever the output's type; the output is rounded once.
+ * Supported: m, n >= 0, any n, k >= 1 a multiple of 16, k <= 2^22, each of m * k, n * k
+ * and m * n up to 2^40, m and n < 2^31 - 512.  a, w, out and the workspace need 16-byte alignment, the scales and bias 4-byte.  Outputs and the workspace
  * may overlap neither each other nor an input.  Where the outputs are too few to fill the
  * card, k is shared out over workgroups and the parts, in the workspace, are added in a
  * fixed order.

@@ -21,11 +21,11 @@ constexpr int64_t kMaxInner = (int64_t)1 << 22;   // a tile's rows are addressed
 constexpr int64_t kMaxSide = ((int64_t)1 << 31) - 512;
 
 struct Plan {
-    int bm, bn;          // tile
+    int bm;              // rows of a tile
     bool few;
     int64_t tm, tn, kb, per, shares;
 };
-Plan plan_of(int64_t m, int64_t n, int64_t k, int dtype)
+Plan plan_of(int64_t m, int64_t n, int64_t k)
 {
     Plan p{};
     p.kb = ceil_div(k, kBlock);
@@ -34,14 +34,13 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int dtype)
     if (m == 0 || n == 0) return p;   // no tiles
     auto tiles = [&](int bm, int bn) {
         p.bm = bm;
-        p.bn = bn;
         p.tm = ceil_div(m, bm);
         p.tn = ceil_div(n, bn);
         return p.tm * p.tn;
     };
-    // fp32 outputs have no tile of 256: their operands take twice the registers
-    if (dtype == SSD_DTYPE_BF16 && m > 64 && tiles(256, 256) >= 256) return p;
-    if (m > 64 && tiles(128, 128) >= 192) return p;
+    // tiles of 128 where they keep a quarter of the CUs busy, or where the other form could not share k out further.  400 x 2560
+    // of k = 2560, 80 tiles: 25 us so, 36 in the other form; 640 x 1280, 50 tiles: 24 against 19, and of k = 512 8 against 11
+    if (m > 64 && (tiles(128, 128) >= 64 || p.kb <= 4)) return p;
     p.few = true;
     const int64_t groups = tiles(m <= 16 ? 16 : m <= 32 ? 32 : 64, 64);
     // where the tiles are too few to keep half of the CUs loading, k is shared out over workgroups, at least four blocks
@@ -61,13 +60,10 @@ ssd_status check_dims(const ssd_matmul_fp8_args *a, Plan *p)
     constexpr int64_t most = (int64_t)1 << 40;
     if (a->m < 0 || a->n < 0 || a->k < 1 || a->k % 16 != 0 || a->m > kMaxSide || a->n > kMaxSide || a->k > kMaxInner) return SSD_ERR_BAD_SHAPE;
     if (a->m * a->k > most || a->n * a->k > most || (a->m > 0 && a->n > most / a->m)) return SSD_ERR_BAD_SHAPE;
-    *p = plan_of(a->m, a->n, a->k, a->dtype);
+    *p = plan_of(a->m, a->n, a->k);
     if (p->tm > 0 && p->tn > 0 && p->tm > (p->few ? kMaxGroups / 2 / p->shares : INT32_MAX / 2) / p->tn) return SSD_ERR_BAD_SHAPE;
     return SSD_OK;
 }
-
-// Workgroups of a tiled product: what the card holds at a time (LDS: one of 256 a CU, two of 128).
-unsigned resident(const Plan &p, int64_t most) { return (unsigned)(p.tm * p.tn < most ? p.tm * p.tn : most); }
 
 template <typename O> void run(const ssd_matmul_fp8_args *a, const Plan &p, hipStream_t st)
 {
@@ -90,12 +86,8 @@ template <typename O> void run(const ssd_matmul_fp8_args *a, const Plan &p, hipS
     if (!p.few) {
         auto tile = [&](auto whole) {
             constexpr bool WHOLE = decltype(whole)::value;
-            if constexpr (std::is_same<O, bf16>::value)
-                if (p.bm == 256) {
-                    hipLaunchKernelGGL((k_mm_tile<O, 256, 256, 2, 4, WHOLE>), dim3(resident(p, 256)), dim3(512), 0, st, k);
-                    return;
-                }
-            hipLaunchKernelGGL((k_mm_tile<O, 128, 128, 2, 2, WHOLE>), dim3(resident(p, 512)), dim3(256), 0, st, k);
+            // workgroups: what the card holds at a time (LDS: two a CU)
+            hipLaunchKernelGGL((k_mm_tile<O, WHOLE>), dim3((unsigned)(p.tm * p.tn < 512 ? p.tm * p.tn : 512)), dim3(256), 0, st, k);
         };
         // such a tile is addressed in 31 bits
         if (std::is_same<O, bf16>::value && a->n % 8 == 0 && a->n <= (int64_t)1 << 21) {

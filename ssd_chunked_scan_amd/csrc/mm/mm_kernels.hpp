@@ -3,12 +3,10 @@
 //
 //   out[m][n] = bias[n] + sum_i a_scales[m][i] w_scales[n/128][i] sum_{k in block i} a[m][k] w[n][k]
 //
-// For bf16 outputs one v_mfma_f32_16x16x128 takes a whole block of 128, so its result (from a zero
-// accumulator) is the block's sum, which one multiply-add per value scales into the fp32 total.  The matrix
-// cores add e4m3 products to about 13 bits below the largest of them: 1.5e-5 of the result in norm with
-// normal values, 5e-5 with a few large ones among them, whatever the instruction's length; far inside bf16's
-// rounding (1.7e-3), but not fp32's.  fp32 outputs therefore turn both operands to bf16, exactly, and take
-// four v_mfma_f32_16x16x32_bf16 a block (1e-8), at half the rate or less.
+// Both operands become bf16 in registers, which is exact, and four v_mfma_f32_16x16x32_bf16 form a block's sum in
+// fp32; one multiply-add per value scales it into the total.  The matrix cores' own e4m3 products run at twice the rate
+// (410 against 780 us for 16384 x 10240 of k = 2560), but add to about 13 bits below the largest product: where a channel
+// stands out of a block, what is beside it is lost, 1.4e-4 of the terms' sizes where two such channels cancel.
 //
 // The weights are the first operand and the rows of a the second: a lane then holds 4 neighbouring n of one
 // m, so a lane has one scale for a 16 x 16 tile and stores its 4 values together.  What a lane group
@@ -23,8 +21,6 @@
 namespace ssd {
 namespace mm {
 
-typedef int intx8 __attribute__((ext_vector_type(8)));
-
 constexpr int kBlock = 128;   // bytes of a row that share a scale
 
 struct MmArgs {
@@ -37,9 +33,9 @@ struct MmArgs {
     int tm, tn;         // tiles along m and n
 };
 
-// What a lane feeds of 16 rows of a block: 32 numbers as they are, or as bf16.
-template <bool BF> struct Operand {
-    typename std::conditional<BF, bf16x8, intx8>::type v[BF ? 4 : 1];
+// What a lane feeds of 16 rows of a block: 32 numbers.
+struct Operand {
+    bf16x8 v[4];
 };
 __device__ __forceinline__ bf16x8 bf16_of(uint32_t a, uint32_t b)
 {
@@ -47,24 +43,15 @@ __device__ __forceinline__ bf16x8 bf16_of(uint32_t a, uint32_t b)
                  r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false), t = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
     return bf16x8{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
-template <bool BF> __device__ __forceinline__ Operand<BF> operand(const uint4 &lo, const uint4 &hi)
+__device__ __forceinline__ Operand operand(const uint4 &lo, const uint4 &hi)
 {
-    Operand<BF> o;
-    if constexpr (BF) {
-        o.v[0] = bf16_of(lo.x, lo.y);
-        o.v[1] = bf16_of(lo.z, lo.w);
-        o.v[2] = bf16_of(hi.x, hi.y);
-        o.v[3] = bf16_of(hi.z, hi.w);
-    } else o.v[0] = intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    return o;
+    return Operand{{bf16_of(lo.x, lo.y), bf16_of(lo.z, lo.w), bf16_of(hi.x, hi.y), bf16_of(hi.z, hi.w)}};
 }
-template <bool BF> __device__ __forceinline__ floatx4 block_product(const Operand<BF> &a, const Operand<BF> &b)
+__device__ __forceinline__ floatx4 block_product(const Operand &a, const Operand &b)
 {
     floatx4 t = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (BF) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma(t, a.v[i], b.v[i]);
-    } else t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v[0], b.v[0], t, 0, 0, 0, 0, 0, 0);   // scales of zero: the form without
+    for (int i = 0; i < 4; ++i) mma(t, a.v[i], b.v[i]);
     return t;
 }
 
@@ -78,9 +65,9 @@ __device__ __forceinline__ Places places_of(int lane)
     const int r = lane & 15, g = lane >> 4;
     return Places{r * kBlock + 16 * (g ^ (r & 7)), r * kBlock + 16 * ((g + 4) ^ (r & 7))};
 }
-template <bool BF> __device__ __forceinline__ Operand<BF> lds_operand(const uint8_t *rows16, const Places &p)
+__device__ __forceinline__ Operand lds_operand(const uint8_t *rows16, const Places &p)
 {
-    return operand<BF>(*reinterpret_cast<const uint4 *>(rows16 + p.lo), *reinterpret_cast<const uint4 *>(rows16 + p.hi));
+    return operand(*reinterpret_cast<const uint4 *>(rows16 + p.lo), *reinterpret_cast<const uint4 *>(rows16 + p.hi));
 }
 typedef __attribute__((address_space(3))) void *lds_t;
 // The byte of a row's block that this lane brings to LDS (8 lanes a row, 8 rows an access).
@@ -114,8 +101,8 @@ template <typename O> __device__ __forceinline__ void store4(O *row, int n, int 
 
 // A wave's values as bf16, 8 neighbouring n a lane: of two 16 x 16 tiles next to each other along n the lanes of
 // group g hold n 4 g .. of each; the halves that are in the wrong lanes swap.  A store then writes 64 bytes of each of 16
-// rows (32 with 4 values a lane: 16384 x 10240 of k = 2560 in 444 us, 411 so), past the caches, which would write
-// them all back at once when every workgroup's tile ends (400 us; 350 without any stores).
+// rows (32 with 4 values a lane: 16384 x 10240 of k = 2560 in 813 us, 780 so), past the caches, which would write
+// them all back at once when every workgroup's tile ends (791 us).
 // Rows that are not whole vectors take ordinary stores, aligned to an element, and single elements at their ends.
 constexpr int kCpolPast = 18;   // streaming, written through
 template <bool WHOLE, int MI, int NI>
@@ -149,16 +136,18 @@ __device__ __forceinline__ void store_wide(const float (&acc)[MI][NI][4], bf16 *
         }
 }
 
-// Tile of BM rows of a and BN rows of w, WM x WN waves.  Two stages of LDS, filled straight from memory:
+// Tile of BM rows of a and BN rows of w, WM x WN waves.  16384 x 10240 of k = 2560 to bf16: 780 us, 1.10 PFLOP/s, where a large library
+// product of bf16 numbers reaches 1.13 to 1.22: the matrix cores bound it.  (Tiles of 256 x 128 and 8 waves took 754
+// there, 388 for 2560 columns of k = 5120 either way, and for 4096 rows of those 142 instead of 100.)
+// Two stages of LDS, filled straight from memory:
 // the next block of both operands is on its way while this one is multiplied.  The stages are arrays of their
 // own, so that a read of one does not wait for the loads into the other.  A workgroup stays for tile after
 // tile: the next one's first block comes while this one's last is multiplied and its values are stored.  WHOLE: rows of
-// whole 16-byte vectors of bf16 (11844 x 5154 of k = 112, not so: 121 us with single elements, 42 with vectors).
-template <typename O, int BM, int BN, int WM, int WN, bool WHOLE>
-__global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
+// whole 16-byte vectors of bf16 (11844 x 5154 of k = 112, not so: 138 us with single elements, 43 with vectors).
+template <typename O, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void k_mm_tile(MmArgs p)
 {
-    constexpr bool BF = std::is_same<O, float>::value;
-    constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
+    constexpr int BM = 128, BN = 128, WM = 2, WN = 2, NW = WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
     static_assert(128 % TN == 0 && BN % 128 == 0, "a wave's columns share a scale");
     static_assert(BM < 64 * NW && BM % 64 == 0, "a wave loads the scales of 64 rows, the last one those of w");
     __shared__ __attribute__((aligned(128))) uint8_t sa0[BM * kBlock], sw0[BN * kBlock], sa1[BM * kBlock], sw1[BN * kBlock];
@@ -206,11 +195,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
     auto multiply = [&](const uint8_t *sa, const uint8_t *sw, const float *sc) {
         sa += wm * kBlock;
         sw += wn * kBlock;
-        Operand<BF> fw[NI];
+        Operand fw[NI];
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fw[j] = lds_operand<BF>(sw + 16 * j * kBlock, at);
-        Operand<BF> fa[2];
-        fa[0] = lds_operand<BF>(sa, at);
+        for (int j = 0; j < NI; ++j) fw[j] = lds_operand(sw + 16 * j * kBlock, at);
+        Operand fa[2];
+        fa[0] = lds_operand(sa, at);
         floatx4 t[AHEAD + 1];
         float f[MI];
         const float ws = sc[BM + wn / kBlock];
@@ -220,8 +209,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
         for (int n = 0; n < MI * NI + AHEAD; ++n) {
             const int i = n / NI, j = n % NI;
             if (n < MI * NI) {
-                if (j == 0 && i + 1 < MI) fa[(i + 1) & 1] = lds_operand<BF>(sa + 16 * (i + 1) * kBlock, at);
-                t[n % (AHEAD + 1)] = block_product<BF>(fw[j], fa[i & 1]);
+                if (j == 0 && i + 1 < MI) fa[(i + 1) & 1] = lds_operand(sa + 16 * (i + 1) * kBlock, at);
+                t[n % (AHEAD + 1)] = block_product(fw[j], fa[i & 1]);
             }
             if (n >= AHEAD) {
                 const int pi = (n - AHEAD) / NI, pj = (n - AHEAD) % NI;
@@ -264,7 +253,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_tile(MmArgs p)
 #pragma unroll
                     for (int i = 0; i < MI; ++i) acc[i][j][e] += b;
                 }
-        if constexpr (!BF) {
+        if constexpr (std::is_same<O, bf16>::value) {
             O *tile = static_cast<O *>(p.out) + (int64_t)t.m0 * p.n + t.n0;
             const int rows = p.m - t.m0 < BM ? p.m - t.m0 : BM, cols = p.n - t.n0 < BN ? p.n - t.n0 : BN;
             store_wide<WHOLE>(acc, tile, wm + lr, wn, g, rows, cols, p.n);
@@ -302,13 +291,14 @@ template <int N, typename F> __device__ __forceinline__ void unrolled(F &&f)
 
 // Few rows: bound by the weights' bytes.  A workgroup has 16 MI rows of a and 64 rows of w, in 4 waves of 16 twice: each
 // half takes half of the workgroup's blocks, and the halves are added in LDS.  A wave reads its weights straight
-// into registers, 8 blocks ahead, since they come from memory (two halves of every line, so not past the caches: 64
-// rows of 10240 x 2560 in 15.3 us, 19.2 past them); the rows of a, which the 4 waves share, come through
+// into registers, up to 8 blocks ahead, since they come from memory (two halves of every line, so not past the caches).  Where
+// its loop of 8 blocks ends the compiler moves what is on its way to other registers, which waits for it: a wave with
+// more than 8 blocks sees the memory's latency once more every 8.  The rows of a, which the 4 waves share, come through
 // LDS a phase of U blocks ahead.  SHARED: the blocks are shared out over workgroups too, and k_mm_join adds their sums.
+// 64 rows of 10240 x 2560: 18.7 us, 16 rows 11.0; the weights' bytes would take 5.2.
 template <typename O, int MI, bool SHARED>
 __global__ __launch_bounds__(512) void k_mm_few(MmArgs p)
 {
-    constexpr bool BF = std::is_same<O, float>::value;
     constexpr int BM = 16 * MI, U = MI == 4 ? 2 : 4, R = 8 / U;
     __shared__ __attribute__((aligned(128))) uint8_t sa0[2 * U * BM * kBlock], sa1[2 * U * BM * kBlock];
     __shared__ float ss0[2 * U * 64], ss1[2 * U * 64];   // scales of the rows of a
@@ -375,11 +365,11 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs p)
         const float *ss = (S & 1 ? ss1 : ss0) + half * U * 64 + lr;
         loads_done<NF>();
         stage(S & 1 ? sa0 : sa1, S & 1 ? ss0 : ss1, ph + 1);
-        Operand<BF> w[U];
+        Operand w[U];
         float ws[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            w[u] = operand<BF>(lo[S][u], hi[S][u]);
+            w[u] = operand(lo[S][u], hi[S][u]);
             ws[u] = fw[S][u];
         }
         fetch(set, ph + R);
@@ -387,7 +377,7 @@ __global__ __launch_bounds__(512) void k_mm_few(MmArgs p)
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                const floatx4 t = block_product<BF>(w[u], lds_operand<BF>(sa + ((half * U + u) * BM + 16 * i) * kBlock, at));
+                const floatx4 t = block_product(w[u], lds_operand(sa + ((half * U + u) * BM + 16 * i) * kBlock, at));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][e] += ss[u * 64 + 16 * i] * ws[u] * t[e];
             }
