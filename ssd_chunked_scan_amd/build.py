@@ -19,7 +19,7 @@ HEADERS = [os.path.join(ROOT, "include", "ssd.h"), os.path.join(CSRC, "ssd_devic
            os.path.join(CSRC, "ssd_kernels.hpp"), os.path.join(CSRC, "gdr", "gdr_kernels.hpp"),
            os.path.join(CSRC, "norm", "norm_kernels.hpp"), os.path.join(CSRC, "norm", "rms_kernels.hpp"),
            os.path.join(CSRC, "scan", "scan_kernels.hpp"), os.path.join(CSRC, "conv", "conv_kernels.hpp"),
-           os.path.join(CSRC, "mm", "mm_kernels.hpp"), os.path.join(CSRC, "api_checks.hpp")]
+           os.path.join(CSRC, "mm", "mm_kernels.hpp"), os.path.join(CSRC, "api_checks.hpp"), os.path.join(CSRC, "segment_ids.hpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -23,6 +23,7 @@
 
 #include <type_traits>
 
+#include "segment_ids.hpp"
 #include "ssd_device.hpp"
 
 namespace ssd {
@@ -168,7 +169,7 @@ __device__ __forceinline__ Slot slot_at(const ScanArgs &a, int c)
 }
 
 // start[i]: the first token of segment i (or of the next one that has any), start[nseq] = T, for non-decreasing
-// ids; four tokens a thread.
+// ids; four tokens a thread.  Whatever the ids, i is in [0, nseq].
 __global__ __launch_bounds__(kThreads) void k_scan_starts(const int32_t *__restrict__ seq_idx, int32_t *__restrict__ start, int T, int nseq)
 {
     const int t0 = (blockIdx.x * kThreads + threadIdx.x) * 4;
@@ -181,10 +182,10 @@ __global__ __launch_bounds__(kThreads) void k_scan_starts(const int32_t *__restr
     for (int e = 0; e < 4; ++e) {
         const int t = t0 + e;
         if (t >= T) break;
-        const int hi = id[e + 1] < nseq ? id[e + 1] : nseq - 1;
-        for (int i = id[e] < -1 ? 0 : id[e] + 1; i <= hi; ++i) start[i] = t;   // this id's, and those of ids left out
+        const Segments here = segments_through(id[e], id[e + 1], nseq);   // this id's, and those of ids left out
+        for (int i = here.from; i < here.to; ++i) start[i] = t;
         if (t == T - 1)
-            for (int i = hi < -1 ? 0 : hi + 1; i <= nseq; ++i) start[i] = T;
+            for (int i = here.to; i <= nseq; ++i) start[i] = T;
     }
     if (T == 0)
         for (int64_t i = t0; i <= nseq; i += 1) start[i] = 0;

@@ -1,0 +1,67 @@
+"""Packed streams whose ids are the largest and smallest 32-bit numbers: whatever comes out, nothing outside the
+outputs and the workspace is written, and the calls end."""
+import numpy as np
+import pytest
+import torch
+
+from ssd_chunked_scan_amd import ssd
+
+pytestmark = pytest.mark.gpu
+
+LEAST, MOST = -2 ** 31, 2 ** 31 - 1
+PAD = 4096
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ssd.load_library()
+    torch.cuda.set_device(0)
+
+
+class Guarded:
+    """Tensors with `PAD` elements in front and behind that have to stay as they are."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, *shape, dtype=torch.float32):
+        n = int(np.prod(shape))
+        self.bufs.append(torch.full((n + 2 * PAD,), 7, device="cuda", dtype=dtype))
+        return self.bufs[-1][PAD:PAD + n].view(shape)
+
+    def whole(self):
+        torch.cuda.synchronize()
+        return all((b[:PAD] == 7).all() and (b[-PAD:] == 7).all() for b in self.bufs)
+
+
+def streams(T, nseq):
+    half = torch.arange(T) * nseq // (2 * T)
+    some = torch.tensor([LEAST, -1, 0, nseq - 1, nseq, MOST])
+    return {"largest": torch.full((T,), MOST), "smallest": torch.full((T,), LEAST), "pads": torch.where(torch.arange(T) < T - 2, half, MOST),
+            "one pad": torch.where(torch.arange(T) < T - 1, half, MOST), "from least": torch.where(torch.arange(T) < 5, LEAST, half),
+            "falls": torch.where(torch.arange(T) < T // 2, MOST, half), "any": some[torch.randint(0, 6, (T,), generator=torch.Generator().manual_seed(0))]}
+
+
+KINDS = list(streams(8, 2))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,dim,nseq", [(150, 20, 4), (1, 3, 1), (1030, 8, 2)])
+def test_scan(kind, T, dim, nseq):
+    N, rnd = 16, lambda *s: torch.randn(s, device="cuda")
+    x, dt, z, dy, B, C = rnd(1, T, dim), rnd(1, T, dim), rnd(1, T, dim), rnd(1, T, dim), rnd(1, T, 1, N), rnd(1, T, 1, N)
+    A, s0 = -torch.rand(dim, N, device="cuda"), rnd(nseq, dim, N)
+    ids = streams(T, nseq)[kind].int().cuda()
+    kw = dict(D=rnd(dim), z=z, dt_bias=rnd(dim), initial_states=s0, seq_idx=ids, nseq=nseq)
+    out = Guarded()
+    byte = dict(dtype=torch.uint8)
+    ssd.selective_scan_fwd(x, dt, A, B, C, y=out(1, T, dim), final_states=out(nseq, dim, N),
+                           workspace=out(ssd.selective_scan_fwd_workspace_bytes(x, dt, A, B, C, seq_idx=ids, nseq=nseq), **byte), **kw)
+    assert out.whole()
+    shapes = dict(dx=(1, T, dim), ddt=(1, T, dim), dz=(1, T, dim), dA=(dim, N), dB=(1, T, 1, N), dC=(1, T, 1, N), dD=(dim,), ddt_bias=(dim,),
+                  dinitial_states=(nseq, dim, N))
+    ssd.selective_scan_bwd(x, dt, A, B, C, dy, dfinal_states=rnd(nseq, dim, N), grads={n: out(*s) for n, s in shapes.items()},
+                           workspace=out(ssd.selective_scan_bwd_workspace_bytes(x, dt, A, B, C, seq_idx=ids, nseq=nseq), **byte), **kw)
+    assert out.whole()
