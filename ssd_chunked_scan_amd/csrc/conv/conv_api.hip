@@ -50,9 +50,8 @@ ssd_status parse_shape(const ssd_causal_conv_args *a, Shape *s)
     s->tokens = s->b * s->T;
     s->dtype = a->dtype;
     s->esz = elem_size(a->dtype);
-    // a thread an element of a strip of 16 tokens at least, and one a window's element
-    if (s->b * ceil_div(s->T, kFwdStrip) > kMaxGroups * kThreads / s->C || s->rows * (s->K - 1) > kMaxGroups * kThreads / s->C)
-        return SSD_ERR_BAD_SHAPE;
+    // a thread an element of a strip of 16 tokens at least, and one a window's element, in one launch
+    if (s->b * ceil_div(s->T, kFwdStrip) + s->rows * (s->K - 1) > (kMaxGroups - 2) * kThreads / s->C) return SSD_ERR_BAD_SHAPE;
     return SSD_OK;
 }
 size_t span(int64_t tokens, int64_t stride, int64_t width, size_t esz)
@@ -115,6 +114,16 @@ template <typename F> void dispatch(const Shape &s, F &&f)
     });
 }
 
+// Workgroups of a launch for V channels a thread: the strips', and in front of them, if windows go out, those of the windows of a packed
+// stream's segments without tokens.
+unsigned groups_of(const Shape &s, ConvArgs &k, int V, bool windows)
+{
+    const int64_t gv = ceil_div(s.C, V);
+    k.items = s.b * k.nb * gv;
+    k.ahead = s.packed && windows ? (int)ceil_div(s.rows * gv, kThreads) : 0;
+    return (unsigned)(k.ahead + ceil_div(k.items, kThreads));
+}
+
 void keep(const Shape &s, const void *from, void *to, hipStream_t st)
 {
     const int64_t n = s.rows * (s.K - 1) * s.C;
@@ -160,9 +169,8 @@ ssd_status ssd_causal_conv_fwd(const ssd_causal_conv_args *a, void *stream)
     k.win1 = s.K > 1 ? a->final_window : nullptr;
     dispatch(s, [&](auto e, auto v, auto kw, auto packed) {
         constexpr int V = decltype(v)::value;
-        k.items = s.b * k.nb * ceil_div(s.C, V);
-        hipLaunchKernelGGL((k_conv_fwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>),
-                           dim3((unsigned)ceil_div(k.items, kThreads)), dim3(kThreads), 0, st, k);
+        const unsigned groups = groups_of(s, k, V, k.win1 != nullptr);
+        hipLaunchKernelGGL((k_conv_fwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>), dim3(groups), dim3(kThreads), 0, st, k);
     });
     return launched();
 }
@@ -209,9 +217,8 @@ ssd_status ssd_causal_conv_bwd(const ssd_causal_conv_args *a, const ssd_causal_c
     else {
         dispatch(s, [&](auto e, auto v, auto kw, auto packed) {
             constexpr int V = decltype(v)::value;
-            k.items = s.b * k.nb * ceil_div(s.C, V);
-            hipLaunchKernelGGL((k_conv_bwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>),
-                               dim3((unsigned)ceil_div(k.items, kThreads)), dim3(kThreads), 0, st, k);
+            const unsigned groups = groups_of(s, k, V, k.dwin0 != nullptr);
+            hipLaunchKernelGGL((k_conv_bwd<decltype(e), V, decltype(kw)::value, decltype(packed)::value>), dim3(groups), dim3(kThreads), 0, st, k);
         });
     }
     hipLaunchKernelGGL(k_conv_sum, dim3((unsigned)ceil_div((s.K + 1) * s.C, 32)), dim3(1024), 0, st, (const float *)k.parts, g->dweight,

@@ -12,6 +12,7 @@
 
 #include <type_traits>
 
+#include "segment_ids.hpp"
 #include "ssd_device.hpp"
 
 namespace ssd {
@@ -28,6 +29,7 @@ struct ConvArgs {
     void *dx, *dwin0;
     float *parts;            // dweight, dbias of every strip [strips][K+1][C]
     int T, C, rows, nb, strip, silu;
+    int ahead;               // workgroups in front of the strips': windows of segments without tokens
     int64_t items;           // threads: rows of strips times vectors of a row
 };
 
@@ -90,7 +92,7 @@ struct Strip {
 template <int V> __device__ __forceinline__ bool strip_of(const ConvArgs &a, Strip &s)
 {
     // XCD-aware order: strips that share rows run on one XCD
-    const int64_t it = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * kThreads + threadIdx.x;
+    const int64_t it = (int64_t)xcd_remap(blockIdx.x - a.ahead, gridDim.x - a.ahead) * kThreads + threadIdx.x;
     if (it >= a.items) return false;
     // the last channels of a number that V does not divide are two threads', which write the same values
     const int gv = (a.C + V - 1) / V;
@@ -116,16 +118,24 @@ __device__ __forceinline__ void put_window_row(const ConvArgs &a, void *win, int
 {
     if ((unsigned)seq < (unsigned)a.rows) store_vec<E, V>(win, ((int64_t)seq * (K - 1) + i) * a.C + c, v);
 }
-// The segments between ids `lo` and `hi` (neither of them): from -> to.
-template <typename E, int V, int K>
-__device__ __forceinline__ void pass_windows(const ConvArgs &a, const void *from, void *to, int lo, int hi, int c)
+// Windows of the segments without tokens: from -> to (zeros without a `from`), V channels of one segment a thread, in workgroups
+// of their own, the launch's first (64 tokens and 65536 segments, 16 channels, bf16: 11 us; with a segment after
+// another in the thread of the strip in front of them 43 ms).
+template <typename E, int V, int K> __device__ __forceinline__ void pass_windows(const ConvArgs &a, const void *from, void *to)
 {
-    for (int q = lo < -1 ? 0 : lo + 1; q < (hi < a.rows ? hi : a.rows); ++q)
-        for (int i = 0; i < K - 1; ++i) {
-            float v[V];
-            window_row<E, V, K>(a, from, q, i, c, v);
-            put_window_row<E, V, K>(a, to, q, i, c, v);
-        }
+    const int gv = (a.C + V - 1) / V;
+    const int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x, q = it / gv;
+    if (q >= a.rows) return;
+    const int at = first_from(a.ids, a.T, (int)q);
+    if (at < a.T && a.ids[at] == (int)q) return;
+    int c = (int)(it - q * gv) * V;
+    if (c > a.C - V) c = a.C - V;
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        float v[V];
+        window_row<E, V, K>(a, from, (int)q, i, c, v);
+        put_window_row<E, V, K>(a, to, (int)q, i, c, v);
+    }
 }
 // The last K-1 inputs before the strip's first token, and how many of them (up to K-1) are of
 // its sequence.
@@ -164,6 +174,10 @@ constexpr int kFwdStrip = 16;
 template <typename E, int V, int K, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs a)
 {
+    if (PACKED && (int)blockIdx.x < a.ahead) {
+        pass_windows<E, V, K>(a, a.win0, a.win1);
+        return;
+    }
     Strip s;
     if (!strip_of<V>(a, s)) return;
     vec_t<E, V> raw[kFwdStrip];
@@ -178,8 +192,6 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs a)
     float w[K][V], bias[V], hist[K][V];
     load_taps<V, K>(a, s.c, w, bias);
     history<E, V, K, PACKED>(a, s, PACKED ? id[0] : s.b, hist);
-    if constexpr (PACKED)
-        if (s.t0 == 0 && a.win1) pass_windows<E, V, K>(a, a.win0, a.win1, -1, id[0], s.c);
 #pragma unroll
     for (int j = 0; j < kFwdStrip; ++j) {
         const int t = s.t0 + j;
@@ -208,11 +220,9 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs a)
         // the id behind the last token of the strip is the next strip's
         const int next = PACKED ? (t == s.t1 - 1 ? id[PACKED ? kFwdStrip : 0] : id[PACKED ? j + 1 : 0]) : 0;
         const bool end = PACKED ? t == a.T - 1 || next != seq : t == a.T - 1;
-        if (a.win1 && end) {
+        if (a.win1 && end)
 #pragma unroll
             for (int i = 0; i < K - 1; ++i) put_window_row<E, V, K>(a, a.win1, seq, i, s.c, hist[i]);
-            if constexpr (PACKED) pass_windows<E, V, K>(a, a.win0, a.win1, seq, next, s.c);
-        }
     }
 }
 
@@ -225,6 +235,10 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs a)
 template <typename E, int V, int K, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs a)
 {
+    if (PACKED && (int)blockIdx.x < a.ahead) {
+        pass_windows<E, V, K>(a, a.dwin1, a.dwin0);
+        return;
+    }
     Strip s;
     if (!strip_of<V>(a, s)) return;
     constexpr int U = 4;   // tokens in flight
@@ -252,8 +266,6 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs a)
     int seq = idr[0];
     int q = history<E, V, K, PACKED>(a, s, seq, hist);   // tokens of the sequence before this one, up to K - 1
     bool own = q == 0;   // the sequence's first token is in this strip
-    if constexpr (PACKED)
-        if (s.t0 == 0 && a.dwin0) pass_windows<E, V, K>(a, a.dwin1, a.dwin0, -1, seq, s.c);
     for (int tb = s.t0; tb < stop; tb += U) {
         vec_t<E, V> xc[U], gc[U];
         int ic[U + 1];
@@ -346,8 +358,6 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs a)
 #pragma unroll
                 for (int i = 0; i < K - 1; ++i) put_window_row<E, V, K>(a, a.dwin0, seq, i, s.c, dwin[i]);
             }
-            if (PACKED && end && a.dwin0 && t < s.t1)
-                pass_windows<E, V, K>(a, a.dwin1, a.dwin0, seq, t == a.T - 1 ? a.rows : ic[u + 1], s.c);
             const int done = t - (K - 1);
             if (done >= s.t0 && done < s.t1) store_vec<E, V>(a.dx, (s.row0 + done) * a.C + s.c, pend[0]);
 #pragma unroll

@@ -1,4 +1,4 @@
-// segment_ids.hpp -- which segments lie between two neighbouring ids of a packed stream, for any 32-bit ids
+// segment_ids.hpp -- where a packed stream's segments are, in range for any 32-bit ids
 // (plain C++: the host's tests compile it too).
 #pragma once
 
@@ -24,6 +24,17 @@ SSD_HOST_DEVICE Segments segments_through(int32_t prev, int32_t id, int32_t nseq
 {
     const int32_t p = clamp_id(prev, nseq), i = clamp_id(id, nseq);
     return Segments{p < nseq ? p + 1 : nseq, i < nseq ? i + 1 : nseq};
+}
+// The first of T tokens whose id is not below `q`, T if there is none.
+SSD_HOST_DEVICE int32_t first_from(const int32_t *ids, int32_t T, int32_t q)
+{
+    int32_t lo = 0, hi = T;
+    while (lo < hi) {
+        const int32_t mid = lo + (hi - lo) / 2;
+        if (ids[mid] < q) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
 }
 
 }  // namespace ssd

@@ -65,3 +65,40 @@ def test_scan(kind, T, dim, nseq):
     ssd.selective_scan_bwd(x, dt, A, B, C, dy, dfinal_states=rnd(nseq, dim, N), grads={n: out(*s) for n, s in shapes.items()},
                            workspace=out(ssd.selective_scan_bwd_workspace_bytes(x, dt, A, B, C, seq_idx=ids, nseq=nseq), **byte), **kw)
     assert out.whole()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,dim,K,nseq", [(90, 16, 4, 3), (1, 3, 2, 1), (700, 7, 3, 5)])
+def test_conv(kind, T, dim, K, nseq):
+    rnd = lambda *s: torch.randn(s, device="cuda")
+    x, dy, w, b, win = rnd(1, T, dim), rnd(1, T, dim), rnd(dim, K), rnd(dim), rnd(nseq, K - 1, dim)
+    kw = dict(bias=b, initial_window=win, seq_idx=streams(T, nseq)[kind].int().cuda(), nseq=nseq)
+    out = Guarded()
+    ssd.causal_conv_fwd(x, w, y=out(1, T, dim), final_window=out(nseq, K - 1, dim), **kw)
+    assert out.whole()
+    grads = dict(dx=out(1, T, dim), dweight=out(dim, K), dbias=out(dim), dinitial_window=out(nseq, K - 1, dim))
+    ssd.causal_conv_bwd(x, w, dy, dfinal_window=rnd(nseq, K - 1, dim), grads=grads, **kw)
+    assert out.whole()
+
+
+@pytest.mark.parametrize("dim", [3, 18])
+def test_conv_with_many_segments_without_tokens(dim):
+    """Their windows, and the gradients of those, pass through; the others are what they are by themselves."""
+    nseq, K, at = 3000, 4, torch.tensor([7, 8, 8, 8, 8, 1500, 1500, 2998])
+    rnd = lambda *s: torch.randn(s, device="cuda")
+    x, dy, w, win, dwin = rnd(1, len(at), dim), rnd(1, len(at), dim), rnd(dim, K), rnd(nseq, K - 1, dim), rnd(nseq, K - 1, dim)
+    y, fin = ssd.causal_conv_fwd(x, w, initial_window=win, seq_idx=at.int().cuda(), nseq=nseq)
+    g = ssd.causal_conv_bwd(x, w, dy, initial_window=win, dfinal_window=dwin, seq_idx=at.int().cuda(), nseq=nseq)
+    used = at.unique()
+    few = torch.searchsorted(used, at).int().cuda()
+    part = dict(initial_window=win[used].contiguous(), seq_idx=few, nseq=len(used))
+    y1, fin1 = ssd.causal_conv_fwd(x, w, **part)
+    g1 = ssd.causal_conv_bwd(x, w, dy, dfinal_window=dwin[used].contiguous(), **part)
+    torch.cuda.synchronize()
+    none = torch.ones(nseq, dtype=torch.bool)
+    none[used] = False
+    assert torch.equal(fin[none], win[none]) and torch.equal(g["dinitial_window"][none], dwin[none])
+    assert torch.equal(fin[used], fin1) and torch.equal(g["dinitial_window"][used], g1["dinitial_window"])
+    assert torch.equal(y, y1) and all(torch.equal(g[k], g1[k]) for k in ("dx", "dweight"))
+    zeros, _ = ssd.causal_conv_fwd(x, w, seq_idx=at.int().cuda(), nseq=nseq, final_window=fin)
+    assert torch.equal(fin[none], torch.zeros_like(fin[none]))

@@ -14,7 +14,8 @@ PROGRAM = r"""
 #include <cstdio>
 #include <vector>
 #include "segment_ids.hpp"
-// stdin: T nseq ids...; stdout: the starts as the device fills them (-7: never written), or "out" if an index leaves [0, nseq].
+// stdin: T nseq ids...; stdout: the starts as the device fills them (-7: never written), then every segment's first token by a
+// search, or "out" if an index leaves [0, nseq].
 int main()
 {
     int T, nseq;
@@ -29,8 +30,10 @@ int main()
             else for (int i = here.from; i < here.to; ++i) put(i, t);
             if (t == T - 1) for (int i = here.to; i <= nseq; ++i) put(i, T);
         }
+        std::vector<int> first;
+        for (int q = 0; q < nseq; ++q) first.push_back(ssd::first_from(id.data(), T, q));
         if (out) printf("out\n");
-        else { for (int v : start) printf("%d ", v); printf("\n"); }
+        else { for (int v : start) printf("%d ", v); for (int v : first) printf("%d ", v); printf("\n"); }
     }
 }
 """
@@ -62,11 +65,12 @@ def test_any_ids_stay_in_range(starts):
     assert len(got) == len(streams)
     for (ids, nseq), s in zip(streams, got):
         assert s != "out" and all(v == -7 or 0 <= v <= len(ids) for v in s), (ids, nseq, s)
+        assert len(s) == 2 * nseq + 1 and -7 not in s[nseq + 1:]
 
 
 def test_valid_streams(starts):
     rng = np.random.default_rng(1)
     streams = [(sorted(int(v) for v in rng.integers(0, n, T)), n) for T in (1, 2, 7, 40) for n in (1, 2, 5, 60) for _ in range(5)]
     for (ids, nseq), s in zip(streams, starts(streams)):
-        assert s == [int(np.searchsorted(ids, i)) for i in range(nseq + 1)]
+        assert s == [int(np.searchsorted(ids, i)) for i in [*range(nseq + 1), *range(nseq)]]
 
