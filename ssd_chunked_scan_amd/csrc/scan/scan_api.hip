@@ -230,8 +230,8 @@ template <typename F> void with_lanes(int LN, F &&f)
 // The segments' first tokens; for the forward also their order and whether they are cut.
 void plan(const Shape &s, const Chunking &c, const ssd_selective_scan_args *a, ScanArgs &k, char *ws, const Workspace &w, bool order, hipStream_t st)
 {
-    hipLaunchKernelGGL(k_scan_starts, dim3((unsigned)(s.T > 0 ? ceil_div(s.T, 4 * kThreads) : 1)), dim3(s.T > 0 ? kThreads : 1), 0, st, a->seq_idx,
-                       reinterpret_cast<int32_t *>(ws + w.plan), (int)s.T, (int)s.nseq);
+    hipLaunchKernelGGL(k_scan_starts, dim3((unsigned)(s.T > 0 ? ceil_div(s.T, 4 * kThreads) : ceil_div(s.nseq + 1, kThreads))), dim3(kThreads), 0, st,
+                       a->seq_idx, reinterpret_cast<int32_t *>(ws + w.plan), (int)s.T, (int)s.nseq);
     if (!order) return;
     int32_t *o = reinterpret_cast<int32_t *>(ws + w.order);
     hipLaunchKernelGGL(k_scan_plan, dim3(1), dim3(kPlanThreads), 0, st, k, o, c.lq, (int)(c.limit < INT32_MAX ? c.limit : INT32_MAX));

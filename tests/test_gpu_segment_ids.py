@@ -102,3 +102,40 @@ def test_conv_with_many_segments_without_tokens(dim):
     assert torch.equal(y, y1) and all(torch.equal(g[k], g1[k]) for k in ("dx", "dweight"))
     zeros, _ = ssd.causal_conv_fwd(x, w, seq_idx=at.int().cuda(), nseq=nseq, final_window=fin)
     assert torch.equal(fin[none], torch.zeros_like(fin[none]))
+
+
+@pytest.mark.parametrize("nseq,at", [(3000, [7, 8, 8, 8, 8, 1500, 1500, 2998]), (1100, [0, 1, 9, 10, 27, 1099]), (5000, [4999]), (700, [0, 0, 3]),
+                                     (2000, sorted([5, 5, 900, 1999] * 300))])
+def test_scan_with_many_segments_without_tokens(nseq, at):
+    """Their states, and the gradients of those, pass through; the others are what they are by themselves."""
+    dim, N, at = 6, 5, torch.tensor(at)
+    T, rnd = len(at), lambda *s: torch.randn(s, device="cuda")
+    x, dt, dy, B, C = rnd(1, T, dim), rnd(1, T, dim), rnd(1, T, dim), rnd(1, T, 1, N), rnd(1, T, 1, N)
+    A, s0, ds = -torch.rand(dim, N, device="cuda"), rnd(nseq, dim, N), rnd(nseq, dim, N)
+    used = at.unique()
+    few = torch.searchsorted(used, at).int().cuda()
+
+    def both(states, dstates, ids, n):
+        y, fin = ssd.selective_scan_fwd(x, dt, A, B, C, initial_states=states, seq_idx=ids, nseq=n)
+        return y, fin, ssd.selective_scan_bwd(x, dt, A, B, C, dy, initial_states=states, dfinal_states=dstates, seq_idx=ids, nseq=n)
+
+    y, fin, g = both(s0, ds, at.int().cuda(), nseq)
+    y1, fin1, g1 = both(s0[used].contiguous(), ds[used].contiguous(), few, len(used))
+    torch.cuda.synchronize()
+    none = torch.ones(nseq, dtype=torch.bool)
+    none[used] = False
+    assert torch.equal(fin[none], s0[none]) and torch.equal(g["dinitial_states"][none], ds[none])
+    near = lambda a, b: (a - b).norm() <= 1e-5 * b.norm()   # more segments, other chunks: sums in another order, 1e-6 or less
+    assert near(y, y1) and near(fin[used], fin1) and near(g["dinitial_states"][used], g1["dinitial_states"])
+    assert all(near(g[k], g1[k]) for k in ("dx", "ddt", "dA", "dB", "dC"))
+
+
+def test_scan_without_tokens_hands_on_many_states():
+    nseq, dim, N = 5000, 3, 4
+    e = lambda *s: torch.empty(s, device="cuda")
+    s0 = torch.randn(nseq, dim, N, device="cuda")
+    ids = torch.empty(0, dtype=torch.int32, device="cuda")
+    _, fin = ssd.selective_scan_fwd(e(1, 0, dim), e(1, 0, dim), -torch.ones(dim, N, device="cuda"), e(1, 0, 1, N), e(1, 0, 1, N), initial_states=s0,
+                                    seq_idx=ids, nseq=nseq)
+    torch.cuda.synchronize()
+    assert torch.equal(fin, s0)
