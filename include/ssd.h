@@ -545,7 +545,8 @@ ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args *args, void *stream);
  * G*N <= 2^20, batch * seqlen < 2^31 - 64 (2^28 tokens of a packed stream), strides up
  * to 2^22; a launch has fewer than 2^32 threads, which limits batch * seqlen * D to
  * about 2^36; larger sizes are SSD_ERR_BAD_SHAPE.  Results do not change from call to
- * call: every sum has a fixed order.  Outputs and the workspace may overlap neither
+ * call: every sum has a fixed order.  A value that is not finite makes only those results
+ * not finite that the formulas compute from it; the dA of its channel is undefined.  Outputs and the workspace may overlap neither
  * each other nor an input (SSD_ERR_ALIASING).
  *
  * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0, nseq),

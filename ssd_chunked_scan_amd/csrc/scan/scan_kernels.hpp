@@ -507,8 +507,14 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
 // lanes of a column into row t (dB) or 8 + t (dC) of an accumulator that 8 tokens share; over the lanes of a
 // row and over the waves it is taken once for the 8 tokens.  Over tiles of channels k_scan_keys adds it up.
 //
-// 16384 tokens of 5120 channels, 16 states, bf16: 1634 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
-// 244 registers a thread: two waves a SIMD (three spill: 2890 us).  Sums over channels by DPP and LDS alone, and Delta and x formed where
+// 0 x inf is NaN, so such a product spreads what is not finite over all 8 tokens; where a sum is not finite, the wave takes
+// the 8 tokens' sums one by one from the states at their start and the gradient at their end (that check and its registers
+// take 0.4 % of the time for N = 16, 4 % for N = 64).
+//
+// 16384 tokens of 5120 channels, 16 states, bf16: 1640 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
+// 256 registers a thread, 6 more in scratch: two waves a SIMD (three spill more: 2890 us).  In scratch are also, of the gated forms, some 160
+// for N <= 4 and 13 for N = 5 to 8, and 50 of the ungated one for N <= 4 (all gradients of these tokens: 1990 us for N = 4 gated, 790
+// ungated, 1485 and 1150 for N = 8).  Sums over channels by DPP and LDS alone, and Delta and x formed where
 // they are used instead of staged, took 3045.  Chunks of 64 tokens: a shorter one rebuilds its states more often.
 template <typename E, int LN, bool GATE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
@@ -545,13 +551,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
                                  wz = token_rsrc<E>(GATE ? a.dz : a.dx, s.t0, a.D, s.count, a.D),
                                  wp = token_rsrc<float>(a.part + blk * (2 * NP), s.t0, (int64_t)a.nblk * (2 * NP), s.count, 2 * NP);
     float h[4] = {0.f, 0.f, 0.f, 0.f}, g[4] = {0.f, 0.f, 0.f, 0.f}, A2[4] = {0.f, 0.f, 0.f, 0.f};
+    // the gradient of the state that leaves the chunk
+    auto load_end = [&](float(&v)[4]) {
+        if (!p.live) return;
+        if (!s.last) load_state(a.R + c * DN + dn, n0, a.N, v);
+        else if (a.d1) load_state(a.d1 + s.row * DN + dn, n0, a.N, v);
+    };
     if (p.live) {
         if (s.j > 0) load_state(a.S + c * DN + dn, n0, a.N, h);
         else if (a.s0) load_state(a.s0 + s.row * DN + dn, n0, a.N, h);
-        if (!s.last) load_state(a.R + c * DN + dn, n0, a.N, g);
-        else if (a.d1) load_state(a.d1 + s.row * DN + dn, n0, a.N, g);
         load_state(a.A + dn, n0, a.N, A2);
     }
+    load_end(g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
     const float bias = a.bias ? a.bias[p.d] : 0.f, skip = a.D_ ? a.D_[p.d] : 0.f;
@@ -632,6 +643,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
         float hh[SC + 1][4], ee[SC][4];
         {
             const floatx4 v = hs[u][tid];
+            if (u < nsub - 1) hs[u + 1][tid] = floatx4{g[0], g[1], g[2], g[3]};   // for the sums token by token below
 #pragma unroll
             for (int k = 0; k < 4; ++k) hh[0][k] = v[k];
         }
@@ -680,6 +692,69 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
             along[q] = i == TL - 1 || jt == i ? al : along[q];
             dd[q] = i == TL - 1 || jt == i ? de : dd[q];
         });
+        // a product with a row of zeros and a one spreads what is not finite over all 8 tokens: such sums are taken token by token
+        float odd = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd += keysum[k][r] * 0.f;
+        if (__builtin_expect(__any(odd != 0.f), 0)) {
+            float As[4], xs[GS], ds[GS], gy[GS], v[4];
+            // formed again, not kept in registers from above
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                As[k] = A2[k];
+                asm volatile("" : "+v"(As[k]));
+            }
+#pragma unroll
+            for (int q = 0; q < GS; ++q) {
+                ds[q] = dl[q];
+                xs[q] = x[q];
+                gy[q] = dy[q];
+                asm volatile("" : "+v"(ds[q]), "+v"(xs[q]), "+v"(gy[q]));
+                xs[q] *= ds[q];
+            }
+            // v, summed over the wave's channels, as token t's dB (0) or dC (1)
+            auto put = [&](int t, int which) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int d = LN; d < 64; d <<= 1) v[k] += __shfl_xor(v[k], d);
+                if (lane < LN) *reinterpret_cast<floatx4 *>(&red[u & 1][wv][t][which][n0]) = floatx4{v[0], v[1], v[2], v[3]};
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            floatx4 st = hs[u][tid];
+            unrolled<SC>([&](auto tc) {
+                constexpr int t = decltype(tc)::value, q = t / TL, i = t % TL;
+                const floatx4 B = *reinterpret_cast<const floatx4 *>(kB + (u * SC + t) * NP);
+                const float di = from_lane<LN, i>(ds[q]), dxi = from_lane<LN, i>(xs[q]), dyi = from_lane<LN, i>(gy[q]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    st[k] = exp2_(di * As[k]) * st[k] + dxi * B[k];
+                    v[k] = dyi * st[k];
+                }
+                put(t, 1);
+            });
+            float gs[4] = {0.f, 0.f, 0.f, 0.f};
+            if (u == nsub - 1) load_end(gs);
+            else {
+                const floatx4 w = hs[u + 1][tid];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gs[k] = w[k];
+            }
+            unrolled<SC>([&](auto tc) {
+                constexpr int t = SC - 1 - decltype(tc)::value, q = t / TL, i = t % TL;
+                const floatx4 C = *reinterpret_cast<const floatx4 *>(kC + (u * SC + t) * NP);
+                const float di = from_lane<LN, i>(ds[q]), dxi = from_lane<LN, i>(xs[q]), dyi = from_lane<LN, i>(gy[q]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    gs[k] += dyi * C[k];
+                    v[k] = dxi * gs[k];
+                    gs[k] *= exp2_(di * As[k]);
+                }
+                put(t, 0);
+            });
+        } else
         // keysum[k][r]: row 4 (lane / 16) + r of column lane % 16; over the columns of one state
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
