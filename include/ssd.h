@@ -543,11 +543,16 @@ ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args *args, void *stream);
  *
  * Supported: batch >= 1, seqlen >= 0, 1 <= N <= 64, any D with D % G == 0, D <= 2^20,
  * G*N <= 2^20, batch * seqlen < 2^31 - 64 (2^28 tokens of a packed stream), strides up
- * to 2^22; a launch has fewer than 2^32 threads, which limits batch * seqlen * D to
- * about 2^36; larger sizes are SSD_ERR_BAD_SHAPE.  Results do not change from call to
- * call: every sum has a fixed order.  A value that is not finite makes only those results
- * not finite that the formulas compute from it; the dA of its channel is undefined.  Outputs and the workspace may overlap neither
- * each other nor an input (SSD_ERR_ALIASING).
+ * to 2^22 (of ssd_selective_scan_step 2^36), the states, (batch or nseq) * D * N, up to
+ * about 2^32 numbers.  batch * seqlen * D is up to 2^40 in the forward; in the backward a
+ * launch, which has fewer than 2^32 threads, limits it to about 2^36 for N <= 16, 2^35 for
+ * N <= 32 and 2^33 above, and batch * seqlen * G to about 2^31 / N.  A group's channels count
+ * as whole 256, 128, 64, 32 or 16 (N <= 4, 8, 16, 32, 64) in the backward's limit, and so
+ * counted (batch or nseq) * D is up to 2^32 to 2^28.  Larger sizes are SSD_ERR_BAD_SHAPE.
+ * Results do not change from call to call: every sum has a fixed order.  A value that is
+ * not finite makes only those results not finite that the formulas compute from it; the dA
+ * of its channel is undefined.  Outputs and the workspace may overlap neither each other
+ * nor an input (SSD_ERR_ALIASING).
  *
  * Packed streams: seq_idx as for ssd_fwd (batch 1, non-decreasing ids in [0, nseq),
  * not checked here: see ssd_check_seq_idx; an invalid stream gives wrong results and

@@ -18,7 +18,9 @@ namespace {
 
 ssd_status launched() { return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
-constexpr int64_t kMaxWidth = (int64_t)1 << 20, kMaxStride = (int64_t)1 << 22;
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;       // tiles of tokens are addressed in 31 bits
+constexpr int64_t kMaxStepStride = (int64_t)1 << 36;   // single tokens in 64
 
 struct Shape {
     int64_t b, T, D, N, G, nseq;
@@ -90,7 +92,7 @@ Chunking bwd_chunks(const Shape &s)
     return c;
 }
 
-ssd_status parse_shape(const ssd_selective_scan_args *a, Shape *s)
+ssd_status parse_shape(const ssd_selective_scan_args *a, bool bwd, Shape *s)
 {
     if (!a) return SSD_ERR_NULL_POINTER;
     const ssd_status r = check_dims(a->batch, a->dim, a->dstate, a->ngroups, a->dtype, s);
@@ -104,11 +106,11 @@ ssd_status parse_shape(const ssd_selective_scan_args *a, Shape *s)
     s->rows = s->packed ? s->nseq : s->b;
     s->tokens = s->b * s->T;
     if (s->packed && s->T > ((int64_t)1 << 28)) return SSD_ERR_BAD_SHAPE;   // ids are read with 31-bit byte offsets
-    // grids, of the finest chunks, and of one thread a state or a key's gradient
-    const int64_t slots = bwd_chunks(*s).slots;
-    if (slots > kMaxGroups / s->nblk || s->rows > kMaxGroups / ceil_div(s->D * s->N, kThreads) ||
-        s->tokens * s->G > kMaxGroups * kThreads / (8 * s->LN))
-        return SSD_ERR_BAD_SHAPE;
+    if (s->tokens > ((int64_t)1 << 40) / s->D) return SSD_ERR_BAD_SHAPE;
+    // grids: a direction's own chunks, a thread a state from chunk to chunk, and in the backward one a key's gradient
+    const int64_t slots = (bwd ? bwd_chunks(*s) : fwd_chunks(*s)).slots;
+    if (slots > kMaxGroups / s->nblk || s->rows > kMaxGroups / ceil_div(s->D * s->N, kThreads)) return SSD_ERR_BAD_SHAPE;
+    if (bwd && s->tokens * s->G > kMaxGroups * kThreads / (8 * s->LN)) return SSD_ERR_BAD_SHAPE;
     // byte counts stay far below 2^63
     if (slots * s->D > ((int64_t)1 << 52) / s->N || s->rows * s->D > ((int64_t)1 << 52) / s->N) return SSD_ERR_BAD_SHAPE;
     return SSD_OK;
@@ -139,13 +141,13 @@ Workspace layout(const Shape &s, const Chunking &c, bool bwd)
     return w;
 }
 
-bool strides_ok(const Shape &s, int64_t xs, int64_t dts, int64_t Bs, int64_t Cs, int64_t zs)
+bool strides_ok(const Shape &s, int64_t xs, int64_t dts, int64_t Bs, int64_t Cs, int64_t zs, int64_t most)
 {
     const int64_t d[] = {xs, dts, zs}, k[] = {Bs, Cs};
     for (int64_t v : d)
-        if (v != 0 && (v < s.D || v > kMaxStride)) return false;
+        if (v != 0 && (v < s.D || v > most)) return false;
     for (int64_t v : k)
-        if (v != 0 && (v < s.G * s.N || v > kMaxStride)) return false;
+        if (v != 0 && (v < s.G * s.N || v > most)) return false;
     return true;
 }
 size_t span(int64_t tokens, int64_t stride, int64_t width, size_t esz)
@@ -155,7 +157,7 @@ size_t span(int64_t tokens, int64_t stride, int64_t width, size_t esz)
 
 ssd_status check_inputs(const Shape &s, const ssd_selective_scan_args *a)
 {
-    if (!strides_ok(s, a->x_stride, a->dt_stride, a->B_stride, a->C_stride, a->z_stride)) return SSD_ERR_BAD_SHAPE;
+    if (!strides_ok(s, a->x_stride, a->dt_stride, a->B_stride, a->C_stride, a->z_stride, kMaxStride)) return SSD_ERR_BAD_SHAPE;
     if (!a->A) return SSD_ERR_NULL_POINTER;
     if (s.tokens > 0 && (!a->x || !a->dt || !a->B || !a->C)) return SSD_ERR_NULL_POINTER;
     const void *els[] = {a->x, a->dt, a->B, a->C, a->z}, *f[] = {a->A, a->D, a->dt_bias, a->initial_states, a->seq_idx};
@@ -312,7 +314,7 @@ extern "C" {
 ssd_status ssd_selective_scan_fwd_workspace_size(const ssd_selective_scan_args *a, size_t *bytes)
 {
     Shape s;
-    const ssd_status r = parse_shape(a, &s);
+    const ssd_status r = parse_shape(a, false, &s);
     if (r != SSD_OK) return r;
     if (!bytes) return SSD_ERR_NULL_POINTER;
     *bytes = layout(s, fwd_chunks(s), false).total;
@@ -322,7 +324,7 @@ ssd_status ssd_selective_scan_fwd_workspace_size(const ssd_selective_scan_args *
 ssd_status ssd_selective_scan_bwd_workspace_size(const ssd_selective_scan_args *a, size_t *bytes)
 {
     Shape s;
-    const ssd_status r = parse_shape(a, &s);
+    const ssd_status r = parse_shape(a, true, &s);
     if (r != SSD_OK) return r;
     if (!bytes) return SSD_ERR_NULL_POINTER;
     *bytes = layout(s, bwd_chunks(s), true).total;
@@ -332,7 +334,7 @@ ssd_status ssd_selective_scan_bwd_workspace_size(const ssd_selective_scan_args *
 ssd_status ssd_selective_scan_fwd(const ssd_selective_scan_args *a, void *stream)
 {
     Shape s;
-    ssd_status r = parse_shape(a, &s);
+    ssd_status r = parse_shape(a, false, &s);
     if (r != SSD_OK) return r;
     if ((r = check_inputs(s, a)) != SSD_OK) return r;
     if (s.tokens > 0 && !a->y) return SSD_ERR_NULL_POINTER;
@@ -352,7 +354,7 @@ ssd_status ssd_selective_scan_fwd(const ssd_selective_scan_args *a, void *stream
 ssd_status ssd_selective_scan_bwd(const ssd_selective_scan_args *a, const ssd_selective_scan_bwd_args *g, void *stream)
 {
     Shape s;
-    ssd_status r = parse_shape(a, &s);
+    ssd_status r = parse_shape(a, true, &s);
     if (r != SSD_OK) return r;
     if (!g) return SSD_ERR_NULL_POINTER;
     if ((r = check_inputs(s, a)) != SSD_OK) return r;
@@ -389,7 +391,7 @@ ssd_status ssd_selective_scan_step(const ssd_selective_scan_step_args *a, void *
     const ssd_status r = check_dims(a->batch, a->dim, a->dstate, a->ngroups, a->dtype, &s);
     if (r != SSD_OK) return r;
     if (s.b > kMaxGroups / s.nblk) return SSD_ERR_BAD_SHAPE;
-    if (!strides_ok(s, a->x_stride, a->dt_stride, a->B_stride, a->C_stride, a->z_stride)) return SSD_ERR_BAD_SHAPE;
+    if (!strides_ok(s, a->x_stride, a->dt_stride, a->B_stride, a->C_stride, a->z_stride, kMaxStepStride)) return SSD_ERR_BAD_SHAPE;
     if (!a->x || !a->dt || !a->A || !a->B || !a->C || !a->state || !a->y) return SSD_ERR_NULL_POINTER;
     const void *els[] = {a->x, a->dt, a->B, a->C, a->z, a->y}, *f[] = {a->A, a->D, a->dt_bias, a->state};
     for (const void *p : els)
