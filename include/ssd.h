@@ -715,10 +715,11 @@ ssd_status ssd_causal_conv_step(const ssd_causal_conv_step_args *args, void *str
  *
  * A value that is not finite makes its row (of y and q) and the scales of its row
  * undefined; other rows are not touched.  Sums are in fp32.
- * Supported: rows >= 0, 1 <= dim <= 65536, rows * dim <= 2^40, any dim (rows of
- * one that is not a multiple of 8 start at any element).  Tensors [rows,dim] need 16-byte alignment;
- * rstd and scales 4-byte.  residual_out may be residual (or x, of the same type)
- * itself, y may be x; no other overlap.
+ * Supported: 0 <= rows < 2^31, 1 <= dim <= 65536, rows * dim <= 2^40; mean(r^2) has to be
+ * finite in fp32.  Tensors [rows,dim] need 16-byte alignment where dim is a multiple of 8 and
+ * their elements' otherwise, weight, dweight and the workspace 16-byte, rstd and scales
+ * 4-byte.  residual_out may be residual (or x, of the same type) itself, y may be x; no
+ * other overlap.
  */
 typedef struct {
     int64_t rows, dim;

@@ -29,8 +29,11 @@ ssd_status check_dims(int64_t rows, int64_t dim, int dtype, int res_dtype)
     return SSD_OK;
 }
 
-// How a row of `dim` is held: lanes of a row and runs of 8 values a lane.  Rows that are moved by
-// single elements have fewer forms.  The backward's rows take up to four times the registers, so
+// Rows of whole runs start at 16 bytes, others at any element.
+bool rows_aligned(const void *p, int64_t dim, size_t esz) { return aligned_to(p, dim % kRun == 0 ? 16 : esz); }
+
+// How a row of `dim` is held: lanes of a row and runs of 8 values a lane.  Rows that are not whole
+// runs have fewer forms.  The backward's rows take up to four times the registers, so
 // they have more lanes.
 struct Plan {
     int L, IT;
@@ -159,11 +162,12 @@ ssd_status ssd_rms_norm_fwd(const ssd_rms_norm_args *a, void *stream)
     if (a->rows == 0) return SSD_OK;
     if (!a->x || (!a->y && !a->q) || (a->residual && !a->residual_out) || (!a->residual && a->residual_out) || (a->q && !a->scales))
         return SSD_ERR_NULL_POINTER;
-    const void *ptrs[] = {a->x, a->residual, a->weight, a->residual_out, a->y, a->q};
-    for (const void *p : ptrs)
-        if (!aligned_to(p, 16)) return SSD_ERR_MISALIGNED;
+    const size_t e = elem_size(a->dtype), re = elem_size(a->residual_dtype);
+    if (!rows_aligned(a->x, a->dim, e) || !rows_aligned(a->y, a->dim, e) || !rows_aligned(a->residual, a->dim, re) ||
+        !rows_aligned(a->residual_out, a->dim, re) || !rows_aligned(a->q, a->dim, 1) || !aligned_to(a->weight, 16))
+        return SSD_ERR_MISALIGNED;
     if (!aligned_to(a->scales, 4) || !aligned_to(a->rstd, 4)) return SSD_ERR_MISALIGNED;
-    const size_t n = (size_t)(a->rows * a->dim), e = elem_size(a->dtype), re = elem_size(a->residual_dtype);
+    const size_t n = (size_t)(a->rows * a->dim);
     const Range ins[] = {{a->x, n * e}, {a->residual, n * re}, {a->weight, (size_t)a->dim * 4}};
     const Range outs[] = {{a->residual_out, n * re}, {a->y, n * e}, {a->q, n},
                           {a->q ? a->scales : nullptr, (size_t)(a->rows * ceil_div(a->dim, 128)) * 4}, {a->rstd, (size_t)a->rows * 4}};
@@ -207,7 +211,11 @@ ssd_status ssd_rms_norm_bwd(const ssd_rms_norm_bwd_args *a, void *stream)
     const ssd_status r = ssd_rms_norm_bwd_workspace_size(a, &need);
     if (r != SSD_OK) return r;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const void *ptrs[] = {a->r, a->dy, a->dresidual_out, a->weight, a->dx, a->dresidual, a->dweight, a->workspace};
+    const size_t e = elem_size(a->dtype), re = elem_size(a->residual_dtype);
+    if (!rows_aligned(a->dy, a->dim, e) || !rows_aligned(a->dx, a->dim, e) || !rows_aligned(a->r, a->dim, re) ||
+        !rows_aligned(a->dresidual_out, a->dim, re) || !rows_aligned(a->dresidual, a->dim, re))
+        return SSD_ERR_MISALIGNED;
+    const void *ptrs[] = {a->weight, a->dweight, a->workspace};
     for (const void *p : ptrs)
         if (!aligned_to(p, 16)) return SSD_ERR_MISALIGNED;
     if (!aligned_to(a->rstd, 4)) return SSD_ERR_MISALIGNED;
@@ -216,7 +224,7 @@ ssd_status ssd_rms_norm_bwd(const ssd_rms_norm_bwd_args *a, void *stream)
         if (a->dweight && !a->workspace) return SSD_ERR_NULL_POINTER;
         if (a->dweight && a->workspace_bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
     }
-    const size_t n = (size_t)(a->rows * a->dim), e = elem_size(a->dtype), re = elem_size(a->residual_dtype), d = (size_t)a->dim * 4;
+    const size_t n = (size_t)(a->rows * a->dim), d = (size_t)a->dim * 4;
     const Range ins[] = {{a->dy, n * e}, {a->dresidual_out, n * re}, {a->r, n * re}, {a->rstd, (size_t)a->rows * 4}, {a->weight, d}};
     const Range outs[] = {{a->dx, n * e}, {a->dresidual, n * re}, {a->dweight, d}, {a->dweight ? a->workspace : nullptr, need}};
     for (int i = 0; i < 4; ++i) {

@@ -1,5 +1,5 @@
-"""Which sizes the selective scan's entry points take: each direction by its own launches, single tokens by their own
-strides (host only: sizes that are taken end at a missing pointer or in the workspace's size)."""
+"""Which sizes and alignments the newer operators' entry points take: each direction of the selective scan by its own launches, single
+tokens by their own strides, rows of the norm by their length (host only: what is taken ends at a missing pointer, an overlap or in the workspace's size)."""
 import ctypes
 import os
 
@@ -44,3 +44,17 @@ def test_single_tokens_of_long_rows(lib, name):
         return lib.ssd_selective_scan_step(ctypes.addressof(a), None)
     assert ask(1 << 22) == ask((1 << 22) + 64) == ask(1 << 36) == NULLP
     assert ask((1 << 36) + 1) == ask(15 if name in "BC" else 63) == ask(-1) == SHAPE
+
+
+def test_norm_s_alignment(lib):
+    """Rows of whole runs of 8 start at 16 bytes, others at an element; weights at 16 bytes."""
+    at = {n: (i + 1) << 34 for i, n in enumerate(("x", "residual", "weight", "residual_out", "y", "q", "scales", "rstd"))}
+
+    def ask(dim, **kw):
+        a = ssd.RmsNormArgs(rows=100, dim=dim, dtype=1, residual_dtype=0, eps=1e-5, reserved=0, **{**at, **kw})
+        a.residual_out = a.y   # past the alignment checks it ends here
+        return lib.ssd_rms_norm_fwd(ctypes.addressof(a), None)
+    MISAL, ALIAS = 8, 9
+    for name, size in (("x", 2), ("residual", 4), ("q", 1)):
+        assert ask(321, **{name: at[name] + size}) == ALIAS and ask(320, **{name: at[name] + size}) == MISAL
+    assert ask(321, x=at["x"] + 1) == ask(321, residual=at["residual"] + 2) == ask(321, weight=at["weight"] + 4) == MISAL
