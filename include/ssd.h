@@ -711,10 +711,11 @@ ssd_status ssd_causal_conv_step(const ssd_causal_conv_step_args *args, void *str
  * mantissa, largest value 448), or both: block i of a row is its values 128 i to
  * 128 i + 127,
  *
- *     scales[row][i] = max(max|y| / 448, 2^-126),   q = y / scales, to nearest even.
+ *     scales[row][i] = max(max|y| / 448, 2^-126),   q = y / scales, to nearest even
  *
- * A value that is not finite makes its row (of y and q) and the scales of its row
- * undefined; other rows are not touched.  Sums are in fp32.
+ * (as y times the scale's reciprocal, both in fp32).  A value that is not finite makes its
+ * row (of y and q) and the scales of its row undefined; other rows are not touched.  Sums
+ * are in fp32.
  * Supported: 0 <= rows < 2^31, 1 <= dim <= 65536, rows * dim <= 2^40; mean(r^2) has to be
  * finite in fp32.  Tensors [rows,dim] need 16-byte alignment where dim is a multiple of 8 and
  * their elements' otherwise, weight, dweight and the workspace 16-byte, rstd and scales

@@ -101,7 +101,6 @@ template <typename F> void dispatch(const Shape &s, F &&f)
 {
     with_width(s.K, [&](auto kw) {
         auto typed = [&](auto e) {
-            using E = decltype(e);
             auto packed = [&](auto v) {
                 if (s.packed) f(e, v, kw, std::true_type{});
                 else f(e, v, kw, std::false_type{});

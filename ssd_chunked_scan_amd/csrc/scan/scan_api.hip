@@ -208,7 +208,6 @@ ScanArgs scan_args(const Shape &s, const Chunking &c, const ssd_selective_scan_a
     k.T = (int)s.T;
     k.D = (int)s.D;
     k.N = (int)s.N;
-    k.G = (int)s.G;
     k.per = (int)s.per;
     k.bpg = (int)s.bpg;
     k.nblk = (int)s.nblk;
@@ -422,7 +421,6 @@ ssd_status ssd_selective_scan_step(const ssd_selective_scan_step_args *a, void *
     k.y = a->y;
     k.dim = (int)s.D;
     k.N = (int)s.N;
-    k.G = (int)s.G;
     k.per = (int)s.per;
     k.bpg = (int)s.bpg;
     k.nblk = (int)s.nblk;

@@ -54,7 +54,7 @@ struct ScanArgs {
     float *R;                      // gradients of the chunk states [slots][D][N]
     float *part;                   // dB, dC of every tile of channels [tokens][nblk][2][4 LN]
     float *pD, *pbias;             // dD, ddt_bias of every chunk [slots][D]
-    int T, D, N, G, per, bpg, nblk, rows, lq, nch, softplus;
+    int T, D, N, per, bpg, nblk, rows, lq, nch, softplus;
 };
 
 // The LN lanes of a channel, lane I's value in all of them.
@@ -321,7 +321,9 @@ __device__ __forceinline__ float step_size(float raw, int softplus)
 // and its output (per 4 states and token 4 exponentials and 17 other instructions) are 360 and the loads, softplus, SiLU and
 // the sum over lanes the rest; the bytes would take 140.  Workgroups of longer rows start first: 690 without that and with four waves.
 // Three waves a SIMD keep it busy; with four, which the registers would let in, the longest rows share a SIMD with
-// more of the others and end later (532 against 505 us; 555 with two).  Forms that need more registers have their own limit.
+// more of the others and end later (532 against 505 us; 555 with two; the same tokens of N = 8 456 either way, of N = 32, where four do
+// not fit, 828 told so and 850 without).  For N <= 4 a limit of three would put 19 registers into scratch (636 against 430 us), for N > 32 two
+// fit (1735 either way).  Forms that need more registers have their own limit.
 template <int LN, int MODE> constexpr bool kThree = MODE == 0 && LN > 1 && LN < 16;
 template <typename E, int LN, bool GATE, int MODE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kThree<LN, MODE> ? 3 : 1, kThree<LN, MODE> ? 3 : 8)))
@@ -329,7 +331,7 @@ void k_scan(ScanArgs a)
 {
     using L = Lanes<LN>;
     constexpr int TT = L::TT, NP = L::NP, NG = L::NG, NL = L::NL;
-    constexpr bool HASX = true, HASC = MODE != 1, HASZ = GATE && MODE != 1, HASG = MODE == 2;
+    constexpr bool HASC = MODE != 1, HASZ = GATE && MODE != 1, HASG = MODE == 2;
     __shared__ float keys[2][HASC ? 2 : 1][TT * NP];
     const int c = blockIdx.x / a.nblk, blk = blockIdx.x - c * a.nblk;
     const Slot s = slot_at(a, c);
@@ -849,7 +851,7 @@ struct StepArgs {
     int64_t xs, dts, Bs, Cs, zs;
     float *state;
     void *y;
-    int dim, N, G, per, bpg, nblk, softplus;
+    int dim, N, per, bpg, nblk, softplus;
 };
 template <typename E, int LN>
 __global__ __launch_bounds__(kThreads) void k_scan_step(StepArgs a)
