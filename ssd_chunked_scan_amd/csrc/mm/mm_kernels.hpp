@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_wide(const float (&acc)[MI][NI][4], bf16 *
 }
 
 // Tile of BM rows of a and BN rows of w, WM x WN waves.  16384 x 10240 of k = 2560 to bf16: 780 us, 1.10 PFLOP/s, where a large library
-// product of bf16 numbers reaches 1.13 to 1.22: the matrix cores bound it.  (Tiles of 256 x 128 and 8 waves took 754
+// product of bf16 numbers reaches 1.13 to 1.27: the matrix cores bound it.  (Tiles of 256 x 128 and 8 waves took 754
 // there, 388 for 2560 columns of k = 5120 either way, and for 4096 rows of those 142 instead of 100.)
 // Two stages of LDS, filled straight from memory:
 // the next block of both operands is on its way while this one is multiplied.  The stages are arrays of their

@@ -513,7 +513,7 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
 // the 8 tokens' sums one by one from the states at their start and the gradient at their end (that check and its registers
 // take 0.4 % of the time for N = 16, 4 % for N = 64).
 //
-// 16384 tokens of 5120 channels, 16 states, bf16: 1640 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
+// 16384 tokens of 5120 channels, 16 states, bf16: 1660 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
 // 256 registers a thread, 6 more in scratch: two waves a SIMD (three spill more: 2890 us).  In scratch are also, of the gated forms, some 160
 // for N <= 4 and 13 for N = 5 to 8, and 50 of the ungated one for N <= 4 (all gradients of these tokens: 1990 us for N = 4 gated, 790
 // ungated, 1485 and 1150 for N = 8).  Sums over channels by DPP and LDS alone, and Delta and x formed where
@@ -844,7 +844,8 @@ __global__ __launch_bounds__(1024) void k_scan_sum(const float *__restrict__ par
 }
 
 // One token of every batch row: the state is read and written once, 16 bytes a lane, and that
-// is what bounds it.  64 rows of 5120 channels and 16 states: 42 MB in 13 us (single elements 23).
+// is what should bound it.  64 rows of 5120 channels and 16 states: 42 MB in 13 us (single elements 23; a copy of as
+// many bytes, in the last cache, takes 5.5).
 struct StepArgs {
     const void *x, *dt, *B, *C, *z;
     const float *A, *D, *bias;
