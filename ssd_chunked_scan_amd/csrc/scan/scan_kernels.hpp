@@ -514,7 +514,7 @@ template <bool BWD> __global__ __launch_bounds__(kThreads) void k_scan_pass(Scan
 // take 0.4 % of the time for N = 16, 4 % for N = 64).
 //
 // 16384 tokens of 5120 channels, 16 states, bf16: 1660 us, of k_scan's MODE 2 before it 433; the bytes would take 230.
-// 256 registers a thread, 6 more in scratch: two waves a SIMD (three spill more: 2890 us).  In scratch are also, of the gated forms, some 160
+// 256 registers a thread, 8 more in scratch: two waves a SIMD (three spill more: 2890 us).  In scratch are also, of the gated forms, some 160
 // for N <= 4 and 13 for N = 5 to 8, and 50 of the ungated one for N <= 4 (all gradients of these tokens: 1990 us for N = 4 gated, 790
 // ungated, 1485 and 1150 for N = 8).  Sums over channels by DPP and LDS alone, and Delta and x formed where
 // they are used instead of staged, took 3045.  Chunks of 64 tokens: a shorter one rebuilds its states more often.
@@ -694,13 +694,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_grad(ScanArgs a)
             along[q] = i == TL - 1 || jt == i ? al : along[q];
             dd[q] = i == TL - 1 || jt == i ? de : dd[q];
         });
-        // a product with a row of zeros and a one spreads what is not finite over all 8 tokens: such sums are taken token by token
-        float odd = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) odd += keysum[k][r] * 0.f;
-        if (__builtin_expect(__any(odd != 0.f), 0)) {
+        // a product with a row of zeros and a one spreads what is not finite over all 8 tokens, so that one of a column's rows shows
+        // it: such sums are taken token by token
+        const float odd = (keysum[0][0] + keysum[1][0]) + (keysum[2][0] + keysum[3][0]);
+        if (__builtin_expect(__any(!__builtin_isfinite(odd)), 0)) {
             float As[4], xs[GS], ds[GS], gy[GS], v[4];
             // formed again, not kept in registers from above
 #pragma unroll
